@@ -15,7 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libssscan.so")
-SOURCES = [os.path.join(CSRC, n) for n in ("ss_kernels.hip", "ss_bwd.hip", "ss_conv.hip", "ss_ssd.hip", "ss_api.cpp")]
+SOURCES = [os.path.join(CSRC, n) for n in ("ss_kernels.hip", "ss_bwd.hip", "ss_conv.hip", "ss_ssd.hip", "ss_glr.hip",
+                                               "ss_glu.hip", "ss_xent.hip", "ss_api.cpp", "ss_lm_api.cpp")]
 # the measurement probes (stream and ALU-issue kernels), a library of their own
 PROBE_DIR = os.path.join(PKG, "probe")
 PROBE_SOURCES = [os.path.join(PROBE_DIR, "ss_probe.hip")]

@@ -4,6 +4,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "ss_check.h"
 #include "ss_internal.h"
 #include "ss_scan.h"
 
@@ -36,24 +37,6 @@ constexpr int64_t kMaxGridYZ = 65535;
 // lanes use offsets at and above 2^31: one chunk of rows must stay below 2^31
 // bytes at 4 bytes per element.
 constexpr int64_t kMaxChunkBytes = int64_t(1) << 31;
-
-bool mul(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
-
-int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi); empty when the pointer is NULL
-};
-
-Range span(const void* p, int64_t bytes)
-{
-    if (!p) return {0, 0};
-    return {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-bool aligned(const void* p, uintptr_t al) { return (reinterpret_cast<uintptr_t>(p) % al) == 0; }
 
 struct Sizes {
     int64_t rows;    // batch*seqlen*dim
@@ -272,6 +255,8 @@ ss_status scan_fwd_impl(const void* u, const void* delta, const float* A, const 
                         int64_t chunk_len_request, ss_dtype dtype, hipStream_t stream, bool use_scratch = false);
 
 }  // namespace
+
+void ssk::note_hip_error(hipError_t e) { g_last_hip_error = static_cast<int>(e); }
 
 extern "C" {
 

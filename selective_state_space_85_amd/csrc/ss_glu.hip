@@ -1,0 +1,532 @@
+// gfx950 kernels of the gated feed-forward projection
+//   g = x Wg^T, u = x Wu^T, h = act(g) u          x (m, k), Wg and Wu (f, k), h (m, f)
+// and its gradients
+//   dg = dh u act'(g), du = dh act(g)
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x.
+//
+// Forward: one kernel.  A tile's B rows are 32 rows of Wg and the same 32 of Wu in turn for
+// each wave column, so that one wave holds g and u of the same elements in its accumulators
+// and the product never leaves the registers; g and u are not stored.
+// Backward: the same product again with dh in the epilogue gives dg and du (rounded once to
+// the operands' type, as the next product's operands must be), side by side in one (m, 2 f)
+// workspace matrix; the second launch holds the tiles of dx (contraction over the 2 f columns
+// of that matrix against the rows of Wg, then of Wu) and those of dWg and dWu (its transpose
+// against x) together, so that one set's last tiles run beside the other's first.
+// All three are bound by the matrix cores at training sizes.
+#include "ss_gemm.h"
+#include "ss_lm_internal.h"
+
+namespace ssk {
+namespace {
+
+// ---- the activation ----------------------------------------------------------------------
+
+constexpr float kGeluA = 0.79788456f;   // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+__device__ __forceinline__ float sigmoidf(float v) { return __builtin_amdgcn_rcpf(1.0f + exp2_hw(-v * kLog2e)); }
+
+// gelu's tanh form: 0.5 g (1 + tanh(s)) = g sigmoid(2 s), s = sqrt(2/pi) (g + 0.044715 g^3)
+template <int ACT>
+__device__ __forceinline__ float act_of(float g)
+{
+    if constexpr (ACT == kActSilu) return g * sigmoidf(g);
+    const float s2 = 2.0f * kGeluA * fmaf(kGeluB * g * g, g, g);
+    return g * sigmoidf(s2);
+}
+
+// act and its derivative
+template <int ACT>
+__device__ __forceinline__ void act_grad(float g, float* act, float* slope)
+{
+    if constexpr (ACT == kActSilu) {
+        const float s = sigmoidf(g);
+        *act = g * s;
+        *slope = fmaf(g * s, 1.0f - s, s);
+    } else {
+        const float s2 = 2.0f * kGeluA * fmaf(kGeluB * g * g, g, g);
+        const float s = sigmoidf(s2);
+        *act = g * s;
+        *slope = fmaf(g * s * (1.0f - s), 2.0f * kGeluA * fmaf(3.0f * kGeluB * g, g, 1.0f), s);
+    }
+}
+
+template <int DT>
+struct Vec4;
+template <>
+struct Vec4<0> {
+    using V = f32x4;
+};
+template <>
+struct Vec4<1> {
+    using V = bf16x4;
+};
+
+// 4 neighbouring elements of a row whose first `left` exist; vec: 4-element accesses are aligned
+template <int DT>
+__device__ __forceinline__ void load4(const typename MM<DT>::T* p, int64_t left, bool vec, float (&v)[4])
+{
+    if (vec && left >= 4) {
+        const auto q = *reinterpret_cast<const typename Vec4<DT>::V*>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = MM<DT>::widen(q[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = e < left ? MM<DT>::widen(p[e]) : 0.0f;
+    }
+}
+template <int DT>
+__device__ __forceinline__ void store4(typename MM<DT>::T* p, int64_t left, bool vec, const float (&v)[4])
+{
+    if (vec && left >= 4) {
+        typename Vec4<DT>::V q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = MM<DT>::narrow(v[e]);
+        *reinterpret_cast<typename Vec4<DT>::V*>(p) = q;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left) p[e] = MM<DT>::narrow(v[e]);
+    }
+}
+
+// ---- g and u of a tile, and what is made of them ------------------------------------------
+
+// BACK: dg and du into the workspace instead of h
+template <int DT, int ACT, bool BACK>
+struct GluProb {
+    using T = typename MM<DT>::T;
+    const GluArgs& a;
+    int64_t m0, f0;  // the tile's first token and first feature
+    int tiles;
+    bool vec;        // rows of h (dh) are aligned for 4-element accesses
+
+    __device__ const char* a_chunk(int row, int k) const
+    {
+        int64_t r = m0 + row;
+        r = r < a.m ? r : a.m - 1;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + r * a.x_ld + k);
+    }
+    __device__ const char* b_chunk(int row, int k) const
+    {
+        // 64 tile rows per wave column: 32 of Wg, then the same 32 of Wu
+        int64_t r = f0 + (row >> 6) * 32 + (row & 31);
+        r = r < a.f ? r : a.f - 1;
+        return reinterpret_cast<const char*>(static_cast<const T*>((row & 32) ? a.wu : a.wg) + r * a.w_ld + k);
+    }
+    __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
+    __device__ int64_t b_off(int t) const { return int64_t(t) * 128; }
+    __device__ int valid(int t) const { return int(a.k_pad - int64_t(t) * (8 * MM<DT>::kEpc)); }
+
+    template <class G>
+    __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
+    {
+        static_assert(G::FN == 4, "a wave column holds 32 + 32 tile rows of B");
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int64_t m = m0 + (wm * G::FM + i) * 16 + (lane & 15);
+            if (m >= a.m) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t f = f0 + wn * 32 + j * 16 + (lane >> 4) * 4;
+                const f32x4 g = acc[i][j], u = acc[i][j + 2];
+                if constexpr (!BACK) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = act_of<ACT>(g[e]) * u[e];
+                    if (f < a.f) store4<DT>(static_cast<T*>(a.h) + m * a.f + f, a.f - f, vec, v);
+                } else {
+                    if (f >= a.f_pad) continue;
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dg[4], du[4];
+                    if (f < a.f) load4<DT>(static_cast<const T*>(a.dh) + m * a.f + f, a.f - f, vec, d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float act, slope;
+                        act_grad<ACT>(g[e], &act, &slope);
+                        // the pad columns f..f_pad hold zeros: later products read them
+                        const bool in = f + e < a.f;
+                        dg[e] = in ? d[e] * u[e] * slope : 0.0f;
+                        du[e] = in ? d[e] * act : 0.0f;
+                    }
+                    // f_pad is a multiple of 4: whole groups, aligned
+                    T* const row = static_cast<T*>(a.dgu) + m * 2 * a.f_pad + f;
+                    store4<DT>(row, 4, true, dg);
+                    store4<DT>(row + a.f_pad, 4, true, du);
+                }
+            }
+        }
+    }
+};
+
+template <class G, int ACT, bool BACK>
+__global__ __launch_bounds__(G::NT) void glu_tile_kernel(GluArgs a, uint32_t ntm, uint32_t ntf, bool vec)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
+    uint32_t tm, tf;
+    tile_of(blockIdx.x, ntm, ntf, &tm, &tf);
+    const GluProb<G::DT, ACT, BACK> p{a, int64_t(tm) * G::BM, int64_t(tf) * (G::BN / 2),
+                                      int((a.k_pad + G::BK - 1) / G::BK), vec};
+    mm_tile<G>(p, lds);
+}
+
+// ---- dx = [dg du] [Wg; Wu] -----------------------------------------------------------------
+
+template <int DT>
+struct GluDxProb {
+    using T = typename MM<DT>::T;
+    static constexpr int BK = 8 * MM<DT>::kEpc;
+    const GluArgs& a;
+    int64_t m0, n0;
+    int half;   // k tiles per half
+    int tiles;
+    bool vec;
+
+    __device__ const char* a_chunk(int row, int k) const
+    {
+        int64_t r = m0 + row;
+        r = r < a.m ? r : a.m - 1;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.dgu) + r * 2 * a.f_pad + k);
+    }
+    __device__ const char* b_chunk(int col, int k) const
+    {
+        int64_t c = n0 + col;
+        c = c < a.k_pad ? c : a.k_pad - MM<DT>::kEpc;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.wg) + int64_t(k) * a.w_ld + c);
+    }
+    __device__ int64_t a_off(int t) const
+    {
+        return t < half ? int64_t(t) * 128 : int64_t(t - half) * 128 + a.f_pad * int64_t(sizeof(T));
+    }
+    __device__ int64_t b_off(int t) const
+    {
+        const int64_t second = reinterpret_cast<intptr_t>(a.wu) - reinterpret_cast<intptr_t>(a.wg);
+        const int64_t row = int64_t(BK) * a.w_ld * int64_t(sizeof(T));
+        return t < half ? t * row : (t - half) * row + second;
+    }
+    __device__ int valid(int t) const { return int(a.f - int64_t(t < half ? t : t - half) * BK); }
+
+    template <class G>
+    __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int64_t m = m0 + (wm * G::FM + i) * 16 + (lane & 15);
+            if (m >= a.m) continue;
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const int64_t n = n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
+                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                if (n < a.k) store4<DT>(static_cast<T*>(a.dx) + m * a.k + n, a.k - n, vec, v);
+            }
+        }
+    }
+};
+
+// ---- [dWg; dWu] = [dg du]^T x ----------------------------------------------------------------
+
+template <int DT>
+struct GluDwProb {
+    using T = typename MM<DT>::T;
+    static constexpr int BK = 8 * MM<DT>::kEpc;
+    const GluArgs& a;
+    int64_t m0, n0;  // m0: first column of dgu (of its 2 f_pad), n0: first column of x
+    int tiles;
+    bool vec;
+
+    __device__ const char* a_chunk(int col, int k) const
+    {
+        int64_t c = m0 + col;
+        c = c < 2 * a.f_pad ? c : 2 * a.f_pad - MM<DT>::kEpc;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.dgu) + int64_t(k) * 2 * a.f_pad + c);
+    }
+    __device__ const char* b_chunk(int col, int k) const
+    {
+        int64_t c = n0 + col;
+        c = c < a.k_pad ? c : a.k_pad - MM<DT>::kEpc;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + int64_t(k) * a.x_ld + c);
+    }
+    __device__ int64_t a_off(int t) const { return int64_t(t) * BK * 2 * a.f_pad * int64_t(sizeof(T)); }
+    __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
+    __device__ int valid(int t) const
+    {
+        const int64_t left = a.m - int64_t(t) * BK;
+        return left < BK ? int(left) : BK;
+    }
+
+    template <class G>
+    __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int64_t c = m0 + (wm * G::FM + i) * 16 + (lane & 15);
+            const bool up = c >= a.f_pad;
+            const int64_t f = up ? c - a.f_pad : c;
+            if (f >= a.f) continue;
+            T* const row = static_cast<T*>(up ? a.dwu : a.dwg) + f * a.k;
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const int64_t n = n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
+                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                if (n < a.k) store4<DT>(row + n, a.k - n, vec, v);
+            }
+        }
+    }
+};
+
+// Both sets of tiles; ids below n_dx are dx's.
+template <class GX, class GW>
+__global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, uint32_t n_dx, uint32_t xm, uint32_t xn,
+                                                          uint32_t wm, uint32_t wn, bool vec_x, bool vec_w)
+{
+    static_assert(GX::NT == GW::NT, "one launch");
+    __shared__ __attribute__((aligned(1024))) char lds[GX::LDS > GW::LDS ? GX::LDS : GW::LDS];
+    uint32_t tm, tn;
+    if (blockIdx.x < n_dx) {
+        tile_of(blockIdx.x, xm, xn, &tm, &tn);
+        const int half = int((a.f + GX::BK - 1) / GX::BK);
+        const GluDxProb<GX::DT> p{a, int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, half, 2 * half, vec_x};
+        mm_tile<GX>(p, lds);
+    } else {
+        tile_of(blockIdx.x - n_dx, wm, wn, &tm, &tn);
+        const GluDwProb<GW::DT> p{a, int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, int((a.m + GW::BK - 1) / GW::BK),
+                                  vec_w};
+        mm_tile<GW>(p, lds);
+    }
+}
+
+// ---- few tokens: the weights stream past them -------------------------------------------------
+
+// A workgroup forms the outputs of 16 features for all tokens (MT x 16 of them).  Its waves
+// split k; a wave reads its part of the 16 rows of Wg and of Wu straight into MFMA operands
+// (lane: row l % 16, 16 bytes of k per step), the tokens' rows likewise (they are shared by
+// every workgroup and stay in the caches), and the waves' sums are joined in LDS.
+constexpr int kStreamWaves = 4;
+constexpr int kStreamUnroll = 4;  // steps whose loads are in flight together
+
+template <int DT, int MT, int ACT>
+__global__ __launch_bounds__(64 * kStreamWaves) void glu_stream_kernel(GluArgs a, bool vec)
+{
+    using M = MM<DT>;
+    using T = typename M::T;
+    using Frag = typename M::Frag;
+    constexpr int KS = 4 * M::kEpc;  // k per step
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t f0 = int64_t(blockIdx.x) * 16;
+    int64_t fr = f0 + (lane & 15);
+    fr = fr < a.f ? fr : a.f - 1;
+    const int kq = (lane >> 4) * M::kEpc;
+    const T* const pg = static_cast<const T*>(a.wg) + fr * a.w_ld + kq;
+    const T* const pu = static_cast<const T*>(a.wu) + fr * a.w_ld + kq;
+    const T* px[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        int64_t m = i * 16 + (lane & 15);
+        m = m < a.m ? m : a.m - 1;
+        px[i] = static_cast<const T*>(a.x) + m * a.x_ld + kq;
+    }
+    f32x4 g[MT], u[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) g[i] = u[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int64_t steps = a.k_pad / KS;  // whole steps
+    int64_t s = wave;
+    for (; s + (kStreamUnroll - 1) * kStreamWaves < steps; s += kStreamUnroll * kStreamWaves) {
+        Frag wg[kStreamUnroll], wu[kStreamUnroll], xf[kStreamUnroll][MT];
+#pragma unroll
+        for (int q = 0; q < kStreamUnroll; ++q) {
+            const int64_t k = (s + q * kStreamWaves) * KS;
+            wg[q] = *reinterpret_cast<const Frag*>(pg + k);
+            wu[q] = *reinterpret_cast<const Frag*>(pu + k);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xf[q][i] = *reinterpret_cast<const Frag*>(px[i] + k);
+        }
+#pragma unroll
+        for (int q = 0; q < kStreamUnroll; ++q)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                g[i] = M::mul(wg[q], xf[q][i], g[i]);
+                u[i] = M::mul(wu[q], xf[q][i], u[i]);
+            }
+    }
+    for (; s < (a.k_pad + KS - 1) / KS; s += kStreamWaves) {
+        const int64_t k = s * KS;
+        const bool in = k + kq < a.k_pad;  // the last step may be partial: whole chunks
+        Frag zero{};
+        const Frag wg = in ? *reinterpret_cast<const Frag*>(pg + k) : zero;
+        const Frag wu = in ? *reinterpret_cast<const Frag*>(pu + k) : zero;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const Frag xf = in ? *reinterpret_cast<const Frag*>(px[i] + k) : zero;
+            g[i] = M::mul(wg, xf, g[i]);
+            u[i] = M::mul(wu, xf, u[i]);
+        }
+    }
+    __shared__ f32x4 part[kStreamWaves][2 * MT][64];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        part[wave][2 * i][lane] = g[i];
+        part[wave][2 * i + 1][lane] = u[i];
+    }
+    __syncthreads();
+    for (int i = wave; i < MT; i += kStreamWaves) {
+        f32x4 gs = part[0][2 * i][lane], us = part[0][2 * i + 1][lane];
+#pragma unroll
+        for (int w = 1; w < kStreamWaves; ++w) {
+            gs += part[w][2 * i][lane];
+            us += part[w][2 * i + 1][lane];
+        }
+        const int64_t m = i * 16 + (lane & 15), f = f0 + (lane >> 4) * 4;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_of<ACT>(gs[e]) * us[e];
+        if (m < a.m && f < a.f) store4<DT>(static_cast<T*>(a.h) + m * a.f + f, a.f - f, vec, v);
+    }
+}
+
+// ---- padded copy ------------------------------------------------------------------------------
+
+template <int DT>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const typename MM<DT>::T* src, int64_t ld,
+                                                       typename MM<DT>::T* dst, int64_t rows, int64_t cols,
+                                                       int64_t cols_pad)
+{
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+        if (c < cols_pad) dst[r * cols_pad + c] = c < cols ? src[r * ld + c] : MM<DT>::narrow(0.0f);
+    }
+}
+
+// ---- launches -----------------------------------------------------------------------------------
+
+template <int DT>
+struct Tiles;
+template <>
+struct Tiles<1> {
+    template <bool AM, bool BM_>
+    using Large = Geo<1, 256, 256, 2, 4, AM, BM_>;
+    template <bool AM, bool BM_>
+    using Small = Geo<1, 128, 128, 2, 2, AM, BM_>;
+};
+template <>
+struct Tiles<0> {
+    template <bool AM, bool BM_>
+    using Large = Geo<0, 128, 128, 2, 2, AM, BM_>;
+    template <bool AM, bool BM_>
+    using Small = Geo<0, 128, 128, 2, 2, AM, BM_>;
+};
+
+uint32_t up(int64_t a, int64_t b) { return uint32_t((a + b - 1) / b); }
+
+// Which tile: 256x256 (one workgroup per CU) or 128x128 (two per CU).  A round of the chip is
+// 256 large tiles or 512 small ones; the small tile does a quarter of the work at 0.88 of the
+// large one's rate, so a small round costs 0.57 of a large one.
+bool large_tile(int64_t large, int64_t small)
+{
+    const double rl = double((large + 255) / 256), rs = double((small + 511) / 512);
+    return rl <= 0.57 * rs;
+}
+
+template <class G, int ACT, bool BACK>
+hipError_t launch_glu_tile(const GluArgs& a, bool vec, hipStream_t s)
+{
+    const uint32_t ntm = up(a.m, G::BM), ntf = up(BACK ? a.f_pad : a.f, G::BN / 2);
+    glu_tile_kernel<G, ACT, BACK><<<dim3(ntm * ntf), dim3(G::NT), 0, s>>>(a, ntm, ntf, vec);
+    return hipGetLastError();
+}
+
+template <int DT, int ACT, bool BACK>
+hipError_t launch_glu_gu(const GluArgs& a, bool vec, hipStream_t s)
+{
+    using L = typename Tiles<DT>::template Large<false, false>;
+    using S = typename Tiles<DT>::template Small<false, false>;
+    if (DT == 1 && large_tile(int64_t(up(a.m, 256)) * up(a.f, 128), int64_t(up(a.m, 128)) * up(a.f, 64)))
+        return launch_glu_tile<L, ACT, BACK>(a, vec, s);
+    return launch_glu_tile<S, ACT, BACK>(a, vec, s);
+}
+
+template <int DT, int ACT>
+hipError_t launch_glu_stream(const GluArgs& a, bool vec, hipStream_t s)
+{
+    const dim3 grid(up(a.f, 16)), block(64 * kStreamWaves);
+    if (a.m <= 16)
+        glu_stream_kernel<DT, 1, ACT><<<grid, block, 0, s>>>(a, vec);
+    else if (a.m <= 32)
+        glu_stream_kernel<DT, 2, ACT><<<grid, block, 0, s>>>(a, vec);
+    else
+        glu_stream_kernel<DT, 4, ACT><<<grid, block, 0, s>>>(a, vec);
+    return hipGetLastError();
+}
+
+bool vec_rows(const void* p, int64_t row, int dtype)
+{
+    return row % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (dtype == 0 ? 16 : 8) == 0;
+}
+
+template <int DT>
+hipError_t glu_fwd_dt(const GluArgs& a, hipStream_t s)
+{
+    const bool vec = vec_rows(a.h, a.f, DT);
+    if (a.m <= kGluStreamRows)
+        return a.act == kActSilu ? launch_glu_stream<DT, kActSilu>(a, vec, s)
+                                 : launch_glu_stream<DT, kActGelu>(a, vec, s);
+    return a.act == kActSilu ? launch_glu_gu<DT, kActSilu, false>(a, vec, s)
+                             : launch_glu_gu<DT, kActGelu, false>(a, vec, s);
+}
+
+template <class GX, class GW>
+hipError_t launch_glu_grad(const GluArgs& a, hipStream_t s)
+{
+    const uint32_t xm = up(a.m, GX::BM), xn = up(a.k, GX::BN);
+    const uint32_t wm = up(2 * a.f_pad, GW::BM), wn = up(a.k, GW::BN);
+    const uint32_t n_dx = a.dx ? xm * xn : 0, n_dw = a.dwg ? wm * wn : 0;
+    const bool vx = vec_rows(a.dx, a.k, GX::DT), vw = vec_rows(a.dwg, a.k, GX::DT) && vec_rows(a.dwu, a.k, GX::DT);
+    glu_grad_kernel<GX, GW><<<dim3(n_dx + n_dw), dim3(GX::NT), 0, s>>>(a, n_dx, xm, xn, wm, wn, vx, vw);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
+{
+    const bool vec = vec_rows(a.dh, a.f, DT);
+    const hipError_t e = a.act == kActSilu ? launch_glu_gu<DT, kActSilu, true>(a, vec, s)
+                                           : launch_glu_gu<DT, kActGelu, true>(a, vec, s);
+    if (e != hipSuccess) return e;
+    using T = Tiles<DT>;
+    const int64_t large = (a.dx ? int64_t(up(a.m, 256)) * up(a.k, 256) : 0) +
+                          (a.dwg ? int64_t(up(2 * a.f_pad, 256)) * up(a.k, 256) : 0);
+    const int64_t small = (a.dx ? int64_t(up(a.m, 128)) * up(a.k, 128) : 0) +
+                          (a.dwg ? int64_t(up(2 * a.f_pad, 128)) * up(a.k, 128) : 0);
+    if (DT == 1 && large_tile(large, small))
+        return launch_glu_grad<typename T::template Large<false, true>, typename T::template Large<true, true>>(a, s);
+    return launch_glu_grad<typename T::template Small<false, true>, typename T::template Small<true, true>>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_pad_rows(const void* src, int64_t ld, void* dst, int64_t rows, int64_t cols, int64_t cols_pad,
+                           int dtype, hipStream_t stream)
+{
+    (void)hipGetLastError();
+    const dim3 grid(up(cols_pad, 256), unsigned(rows < 65535 ? rows : 65535));
+    if (dtype == 0)
+        pad_rows_kernel<0><<<grid, dim3(256), 0, stream>>>(static_cast<const float*>(src), ld, static_cast<float*>(dst),
+                                                          rows, cols, cols_pad);
+    else
+        pad_rows_kernel<1><<<grid, dim3(256), 0, stream>>>(static_cast<const __bf16*>(src), ld,
+                                                          static_cast<__bf16*>(dst), rows, cols, cols_pad);
+    return hipGetLastError();
+}
+
+hipError_t launch_glu_fwd(const GluArgs& a, int dtype, hipStream_t stream)
+{
+    (void)hipGetLastError();
+    return dtype == 0 ? glu_fwd_dt<0>(a, stream) : glu_fwd_dt<1>(a, stream);
+}
+
+hipError_t launch_glu_bwd(const GluArgs& a, int dtype, hipStream_t stream)
+{
+    (void)hipGetLastError();
+    return dtype == 0 ? glu_bwd_dt<0>(a, stream) : glu_bwd_dt<1>(a, stream);
+}
+
+}  // namespace ssk

@@ -7,6 +7,9 @@
 
 namespace ssk {
 
+// Records the HIP error behind an SS_ERR_HIP of this thread for ss_last_hip_error (ss_api.cpp).
+void note_hip_error(hipError_t e);
+
 constexpr int kDState = 16;  // the state width the kernels are built for
 
 // Option bits of a scan or step call (the same values as the C ABI's).

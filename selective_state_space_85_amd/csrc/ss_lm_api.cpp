@@ -1,0 +1,635 @@
+// C ABI of the language-model operators (ss_lm.h): argument validation, plans, workspace
+// sizing and kernel dispatch.  Validation runs on the host before anything is enqueued.
+#include <math.h>
+#include <stdint.h>
+
+#include "ss_check.h"
+#include "ss_internal.h"
+#include "ss_lm.h"
+#include "ss_lm_internal.h"
+
+namespace {
+
+constexpr size_t kBad = static_cast<size_t>(-1);
+
+int64_t elem_size(ss_dtype dtype) { return dtype == SS_F32 ? 4 : 2; }
+bool known(ss_dtype dtype) { return dtype == SS_F32 || dtype == SS_BF16; }
+
+ss_status done(hipError_t e)
+{
+    if (e == hipSuccess) return SS_OK;
+    ssk::note_hip_error(e);
+    return SS_ERR_HIP;
+}
+
+// Regions of a workspace, each from a 256-byte boundary.
+struct Regions {
+    int64_t at = 0;
+    bool ok = true;
+    int64_t add(int64_t count, int64_t size)
+    {
+        int64_t bytes, from;
+        if (!ok || !mul(count, size, &bytes) || __builtin_add_overflow(at, int64_t(255), &from)) {
+            ok = false;
+            return 0;
+        }
+        from &= ~int64_t(255);
+        if (__builtin_add_overflow(from, bytes, &at)) ok = false;
+        return from;
+    }
+};
+
+// Bytes that `rows` rows of `cols` elements, ld elements apart, span.
+bool strided_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t es, int64_t* bytes)
+{
+    int64_t n;
+    return mul(rows - 1, ld, &n) && !__builtin_add_overflow(n, cols, &n) && mul(n, es, bytes);
+}
+
+// Whether two tensors of the same rows, row length and stride (bytes) share an element.
+// Column slices of one tensor interleave without sharing any.
+bool strided_overlap(const void* p, const void* q, int64_t bytes, int64_t row, int64_t stride)
+{
+    if (!overlap(span(p, bytes), span(q, bytes))) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    const int64_t off = static_cast<int64_t>((a < b ? b - a : a - b) % static_cast<uintptr_t>(stride));
+    return off < row || off + row > stride;
+}
+
+ss_status check_workspace(void* workspace, size_t given, int64_t need, const Range* others, size_t count)
+{
+    if (need == 0) return SS_OK;
+    if (!workspace || given < static_cast<size_t>(need)) return SS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SS_ERR_INVALID_ARG;
+    const Range w = span(workspace, need);
+    for (size_t i = 0; i < count; ++i)
+        if (overlap(w, others[i])) return SS_ERR_INVALID_ARG;
+    return SS_OK;
+}
+
+bool any_overlap(const Range* outputs, size_t n_out, const Range* inputs, size_t n_in)
+{
+    for (size_t i = 0; i < n_out; ++i) {
+        for (size_t k = 0; k < n_in; ++k)
+            if (overlap(outputs[i], inputs[k])) return true;
+        for (size_t k = i + 1; k < n_out; ++k)
+            if (overlap(outputs[i], outputs[k])) return true;
+    }
+    return false;
+}
+
+// ---- gated linear recurrence ------------------------------------------------------------
+
+constexpr int64_t kGlrCols = 64;          // channels per workgroup
+// Fewer one-chunk workgroups than kGlrWhole leave CUs idle: the rows are then cut until there
+// are kGlrTarget workgroups, in chunks of at least kGlrMinChunk rows (the cut costs a pass over
+// the operands) and at most kGlrMaxChunks of them (a chunk joins its predecessors' maps itself).
+constexpr int64_t kGlrWhole = 256, kGlrTarget = 512, kGlrMinChunk = 512, kGlrMaxChunks = 64;
+
+void glr_plan(int64_t batch, int64_t seqlen, int64_t dim, int64_t* len, int64_t* chunks)
+{
+    const int64_t unit = ssk::kGlrChunkUnit;
+    const int64_t blocks = batch * ceil_div(dim, kGlrCols);
+    int64_t k = 1;
+    if (blocks < kGlrWhole) {
+        k = ceil_div(kGlrTarget, blocks);
+        const int64_t most = seqlen / kGlrMinChunk;
+        k = k < most ? k : most;
+        k = k < kGlrMaxChunks ? k : kGlrMaxChunks;
+        k = k > 1 ? k : 1;
+    }
+    *len = ceil_div(ceil_div(seqlen, k), unit) * unit;
+    *chunks = ceil_div(seqlen, *len);
+}
+
+struct GlrLayout {
+    int64_t len, chunks, prod, end, part, ckpt, total;
+};
+
+bool glr_sizes(int64_t batch, int64_t seqlen, int64_t dim)
+{
+    int64_t n;
+    return batch > 0 && seqlen > 0 && dim > 0 && mul(batch, seqlen, &n) && mul(n, dim, &n) && mul(n, 4, &n);
+}
+
+bool glr_layout(int64_t batch, int64_t seqlen, int64_t dim, bool back, bool with_ckpt, GlrLayout* w)
+{
+    if (!glr_sizes(batch, seqlen, dim)) return false;
+    glr_plan(batch, seqlen, dim, &w->len, &w->chunks);
+    Regions r;
+    const int64_t maps = w->chunks > 1 ? w->chunks * batch * dim : 0;
+    w->prod = r.add(maps, 4);
+    w->end = r.add(maps, 4);
+    w->part = r.add(back ? w->chunks * batch * dim : 0, 4);
+    w->ckpt = r.add(back && !with_ckpt ? ceil_div(seqlen, ssk::kGlrRows) * batch * dim : 0, 4);
+    w->total = r.at;
+    return r.ok;
+}
+
+bool glr_grid_ok(int64_t batch, int64_t dim, int64_t chunks)
+{
+    int64_t n;
+    return mul(batch, ceil_div(dim, kGlrCols / 2), &n) && mul(n, chunks, &n) && n <= INT32_MAX;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ss_glr_ckpt_bytes(int64_t batch, int64_t seqlen, int64_t dim)
+{
+    int64_t n;
+    if (!glr_sizes(batch, seqlen, dim)) return kBad;
+    if (!mul(ceil_div(seqlen, ssk::kGlrRows), batch, &n) || !mul(n, dim, &n) || !mul(n, 4, &n)) return kBad;
+    return static_cast<size_t>(n);
+}
+
+size_t ss_glr_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim)
+{
+    GlrLayout w;
+    return glr_layout(batch, seqlen, dim, false, true, &w) ? static_cast<size_t>(w.total) : kBad;
+}
+
+size_t ss_glr_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int with_ckpt)
+{
+    GlrLayout w;
+    return glr_layout(batch, seqlen, dim, true, with_ckpt != 0, &w) ? static_cast<size_t>(w.total) : kBad;
+}
+
+ss_status ss_glr_fwd(const void* x, int64_t x_row_stride, const void* r, int64_t r_row_stride, const void* i,
+                     int64_t i_row_stride, const float* decay, float c, const float* h0, const uint8_t* reset,
+                     void* y, float* h_last, float* ckpt, void* workspace, size_t workspace_bytes, int64_t batch,
+                     int64_t seqlen, int64_t dim, ss_dtype dtype, hipStream_t stream)
+{
+    if (!x || !r || !i || !decay || !y) return SS_ERR_INVALID_ARG;
+    GlrLayout w;
+    if (!glr_layout(batch, seqlen, dim, false, true, &w)) return SS_ERR_INVALID_ARG;
+    if (x_row_stride < dim || r_row_stride < dim || i_row_stride < dim) return SS_ERR_INVALID_ARG;
+    if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
+    if (!known(dtype)) return SS_ERR_UNSUPPORTED;
+    if (!glr_grid_ok(batch, dim, w.chunks)) return SS_ERR_UNSUPPORTED;
+    const int64_t es = elem_size(dtype), rows = batch * seqlen;
+    const void* elems[] = {x, r, i, y};
+    for (const void* p : elems)
+        if (!aligned(p, uintptr_t(es))) return SS_ERR_INVALID_ARG;
+    const void* words[] = {decay, h0, h_last, ckpt};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return SS_ERR_INVALID_ARG;
+    int64_t xb, rb, ib;
+    if (!strided_bytes(rows, dim, x_row_stride, es, &xb) || !strided_bytes(rows, dim, r_row_stride, es, &rb) ||
+        !strided_bytes(rows, dim, i_row_stride, es, &ib))
+        return SS_ERR_INVALID_ARG;
+    const int64_t state = batch * dim * 4;
+    const Range all[] = {span(x, xb), span(r, rb), span(i, ib), span(decay, dim * 4), span(reset, rows),
+                         span(h0, state), span(y, rows * dim * es),
+                         span(ckpt, static_cast<int64_t>(ss_glr_ckpt_bytes(batch, seqlen, dim))),
+                         span(h_last == h0 ? nullptr : h_last, state)};
+    if (any_overlap(all + 6, 3, all, 6)) return SS_ERR_INVALID_ARG;
+    const ss_status st = check_workspace(workspace, workspace_bytes, w.total, all, 9);
+    if (st != SS_OK) return st;
+
+    char* const ws = static_cast<char*>(workspace);
+    ssk::GlrArgs a{};
+    a.x = x;
+    a.r = r;
+    a.i = i;
+    a.x_ld = x_row_stride;
+    a.r_ld = r_row_stride;
+    a.i_ld = i_row_stride;
+    a.decay = decay;
+    a.c = c;
+    a.h0 = h0;
+    a.reset = reset;
+    a.y = y;
+    a.h_last = h_last;
+    a.ckpt = ckpt;
+    if (w.chunks > 1) {
+        a.ws_prod = reinterpret_cast<float*>(ws + w.prod);
+        a.ws_end = reinterpret_cast<float*>(ws + w.end);
+    }
+    a.batch = batch;
+    a.seqlen = seqlen;
+    a.dim = dim;
+    a.chunk_len = w.len;
+    a.n_chunks = w.chunks;
+    return done(ssk::launch_glr_fwd(a, dtype == SS_F32 ? 0 : 1, stream));
+}
+
+ss_status ss_glr_bwd(const void* x, int64_t x_row_stride, const void* r, int64_t r_row_stride, const void* i,
+                     int64_t i_row_stride, const float* decay, float c, const float* h0, const uint8_t* reset,
+                     const void* dy, const float* dh_last, const float* ckpt, void* dx, void* dr, void* di,
+                     int64_t grad_row_stride, float* ddecay, float* dh0, void* workspace, size_t workspace_bytes,
+                     int64_t batch, int64_t seqlen, int64_t dim, ss_dtype dtype, hipStream_t stream)
+{
+    if (!x || !r || !i || !decay || !dy || !dx || !dr || !di || !ddecay) return SS_ERR_INVALID_ARG;
+    GlrLayout w;
+    if (!glr_layout(batch, seqlen, dim, true, ckpt != nullptr, &w)) return SS_ERR_INVALID_ARG;
+    if (x_row_stride < dim || r_row_stride < dim || i_row_stride < dim || grad_row_stride < dim)
+        return SS_ERR_INVALID_ARG;
+    if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
+    if (!known(dtype)) return SS_ERR_UNSUPPORTED;
+    if (!glr_grid_ok(batch, dim, w.chunks)) return SS_ERR_UNSUPPORTED;
+    const int64_t es = elem_size(dtype), rows = batch * seqlen;
+    const void* elems[] = {x, r, i, dy, dx, dr, di};
+    for (const void* p : elems)
+        if (!aligned(p, uintptr_t(es))) return SS_ERR_INVALID_ARG;
+    const void* words[] = {decay, h0, dh_last, ckpt, ddecay, dh0};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return SS_ERR_INVALID_ARG;
+    int64_t xb, rb, ib, gb;
+    if (!strided_bytes(rows, dim, x_row_stride, es, &xb) || !strided_bytes(rows, dim, r_row_stride, es, &rb) ||
+        !strided_bytes(rows, dim, i_row_stride, es, &ib) || !strided_bytes(rows, dim, grad_row_stride, es, &gb))
+        return SS_ERR_INVALID_ARG;
+    const int64_t state = batch * dim * 4;
+    const Range all[] = {span(x, xb), span(r, rb), span(i, ib), span(decay, dim * 4), span(reset, rows),
+                         span(h0, state), span(dy, rows * dim * es), span(dh_last, state),
+                         span(ckpt, static_cast<int64_t>(ss_glr_ckpt_bytes(batch, seqlen, dim))),
+                         span(dx, gb), span(dr, gb), span(di, gb), span(ddecay, dim * 4), span(dh0, state)};
+    for (int k = 9; k < 12; ++k) {
+        if (any_overlap(all + k, 1, all, 9)) return SS_ERR_INVALID_ARG;
+        if (overlap(all[k], all[12]) || overlap(all[k], all[13])) return SS_ERR_INVALID_ARG;
+    }
+    if (any_overlap(all + 12, 2, all, 9)) return SS_ERR_INVALID_ARG;
+    const int64_t row = dim * es, stride = grad_row_stride * es;
+    if (strided_overlap(dx, dr, gb, row, stride) || strided_overlap(dx, di, gb, row, stride) ||
+        strided_overlap(dr, di, gb, row, stride))
+        return SS_ERR_INVALID_ARG;
+    const ss_status st = check_workspace(workspace, workspace_bytes, w.total, all, 14);
+    if (st != SS_OK) return st;
+
+    char* const ws = static_cast<char*>(workspace);
+    ssk::GlrArgs a{};
+    a.x = x;
+    a.r = r;
+    a.i = i;
+    a.x_ld = x_row_stride;
+    a.r_ld = r_row_stride;
+    a.i_ld = i_row_stride;
+    a.decay = decay;
+    a.c = c;
+    a.h0 = h0;
+    a.reset = reset;
+    if (w.chunks > 1) {
+        a.ws_prod = reinterpret_cast<float*>(ws + w.prod);
+        a.ws_end = reinterpret_cast<float*>(ws + w.end);
+    }
+    a.batch = batch;
+    a.seqlen = seqlen;
+    a.dim = dim;
+    a.chunk_len = w.len;
+    a.n_chunks = w.chunks;
+    // the kept states: only read from here on when they are the caller's
+    a.ckpt = ckpt ? const_cast<float*>(ckpt) : reinterpret_cast<float*>(ws + w.ckpt);
+    const int dt = dtype == SS_F32 ? 0 : 1;
+    if (!ckpt) {
+        const hipError_t e = ssk::launch_glr_fwd(a, dt, stream);  // y is null: the states alone
+        if (e != hipSuccess) return done(e);
+    }
+    a.dy = dy;
+    a.dh_last = dh_last;
+    a.dx = dx;
+    a.dr = dr;
+    a.di = di;
+    a.g_ld = grad_row_stride;
+    a.dh0 = dh0;
+    a.part_decay = reinterpret_cast<float*>(ws + w.part);
+    a.ddecay = ddecay;
+    return done(ssk::launch_glr_bwd(a, dt, stream));
+}
+
+ss_status ss_glr_step(float* h, const void* x, int64_t x_row_stride, const void* r, int64_t r_row_stride,
+                      const void* i, int64_t i_row_stride, const float* decay, float c, void* y, int64_t batch,
+                      int64_t dim, ss_dtype dtype, hipStream_t stream)
+{
+    if (!h || !x || !r || !i || !decay || !y) return SS_ERR_INVALID_ARG;
+    if (!glr_sizes(batch, 1, dim)) return SS_ERR_INVALID_ARG;
+    if (x_row_stride < dim || r_row_stride < dim || i_row_stride < dim) return SS_ERR_INVALID_ARG;
+    if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
+    if (!known(dtype)) return SS_ERR_UNSUPPORTED;
+    if (ceil_div(dim, 256) > INT32_MAX) return SS_ERR_UNSUPPORTED;
+    const int64_t es = elem_size(dtype);
+    const void* elems[] = {x, r, i, y};
+    for (const void* p : elems)
+        if (!aligned(p, uintptr_t(es))) return SS_ERR_INVALID_ARG;
+    if (!aligned(h, 4) || !aligned(decay, 4)) return SS_ERR_INVALID_ARG;
+    int64_t xb, rb, ib;
+    if (!strided_bytes(batch, dim, x_row_stride, es, &xb) || !strided_bytes(batch, dim, r_row_stride, es, &rb) ||
+        !strided_bytes(batch, dim, i_row_stride, es, &ib))
+        return SS_ERR_INVALID_ARG;
+    const Range all[] = {span(x, xb), span(r, rb), span(i, ib), span(decay, dim * 4), span(h, batch * dim * 4),
+                         span(y, batch * dim * es)};
+    if (any_overlap(all + 4, 2, all, 4)) return SS_ERR_INVALID_ARG;
+    const ssk::GlrStepArgs a{h, x, r, i, x_row_stride, r_row_stride, i_row_stride, decay, c, y, batch, dim};
+    return done(ssk::launch_glr_step(a, dtype == SS_F32 ? 0 : 1, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- the two matrix operators: x (rows, dim) against weights (cols, dim) ------------------
+
+// Elements per 16 bytes: rows are read in whole 16-byte chunks.
+int64_t chunk_elems(ss_dtype dtype) { return 16 / elem_size(dtype); }
+int64_t padded(int64_t n, ss_dtype dtype) { return ceil_div(n, chunk_elems(dtype)) * chunk_elems(dtype); }
+
+// Sizes whose products are formed unchecked below.
+bool mat_sizes(int64_t rows, int64_t dim, int64_t cols)
+{
+    if (rows <= 0 || dim <= 0 || cols <= 0) return false;
+    // room for the padding to 16-byte chunks and to tiles
+    if (rows > (INT64_MAX >> 16) || dim > (INT64_MAX >> 16) || cols > (INT64_MAX >> 16)) return false;
+    const int64_t r = rows + 256, d = dim + 256, c = cols + 256;
+    int64_t n;
+    return mul(r, d, &n) && mul(n, 16, &n) && mul(c, d, &n) && mul(n, 16, &n) && mul(r, c, &n) && mul(n, 16, &n);
+}
+
+// A grid of 128 x 128 tiles (the smaller kind) has to fit one launch.
+bool mat_grid_ok(int64_t rows, int64_t cols)
+{
+    int64_t n;
+    return mul(ceil_div(rows, 128), ceil_div(cols, 64), &n) && n <= INT32_MAX / 2;
+}
+
+// x's checks: its stride and alignment; *pack: it has to be copied to padded rows
+ss_status mat_operand(const void* p, int64_t ld, int64_t dim, ss_dtype dtype, bool* pack)
+{
+    if (ld < dim) return SS_ERR_INVALID_ARG;
+    *pack = dim % chunk_elems(dtype) != 0;
+    if (*pack) return aligned(p, uintptr_t(elem_size(dtype))) ? SS_OK : SS_ERR_INVALID_ARG;
+    if (!aligned(p, 16) || ld % chunk_elems(dtype) != 0) return SS_ERR_INVALID_ARG;
+    return SS_OK;
+}
+
+struct GluLayout {
+    int64_t k_pad, f_pad;
+    bool pack;
+    int64_t x, wg, wu, dgu, total;
+};
+
+bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluLayout* w)
+{
+    if (!mat_sizes(m, k, f) || !known(dtype)) return false;
+    const int64_t es = elem_size(dtype);
+    w->k_pad = padded(k, dtype);
+    w->f_pad = padded(f, dtype);
+    w->pack = w->k_pad != k;
+    Regions r;
+    w->x = r.add(w->pack ? m * w->k_pad : 0, es);
+    w->wg = r.add(w->pack ? f * w->k_pad : 0, es);
+    w->wu = r.add(w->pack ? f * w->k_pad : 0, es);
+    w->dgu = r.add(back ? m * 2 * w->f_pad : 0, es);
+    w->total = r.at;
+    return r.ok;
+}
+
+struct XentLayout {
+    int64_t d_pad, piece;
+    bool pack;
+    int64_t x, w, pmax, psum, tl, dl, lo, tokens, counts, acc, total;
+};
+
+// Columns per piece of the backward: as many as keep the piece's gradient of the logits within
+// kXentPieceBytes (it is written once and read twice, so it had better stay in the last-level
+// cache), but no fewer than kXentMinPiece (each piece reads and writes the fp32 sums of dx).
+// Pieces are evened out, in whole tiles of 256 columns.
+constexpr int64_t kXentPieceBytes = int64_t(256) << 20, kXentMinPiece = 4096;
+
+int64_t xent_piece(int64_t n, int64_t v, int64_t es)
+{
+    int64_t most = kXentPieceBytes / (n * es);
+    most = most > kXentMinPiece ? most : kXentMinPiece;
+    const int64_t count = ceil_div(v, most);
+    const int64_t even = ceil_div(ceil_div(v, count), 256) * 256;
+    return even < v ? even : v;
+}
+
+bool xent_layout(int64_t n, int64_t d, int64_t v, ss_dtype dtype, bool back, XentLayout* w)
+{
+    if (!mat_sizes(n, d, v) || !known(dtype)) return false;
+    const int64_t es = elem_size(dtype);
+    w->d_pad = padded(d, dtype);
+    w->pack = w->d_pad != d;
+    w->piece = xent_piece(n, v, es);
+    Regions r;
+    w->x = r.add(w->pack ? n * w->d_pad : 0, es);
+    w->w = r.add(w->pack ? v * w->d_pad : 0, es);
+    const int64_t parts = back ? 0 : ceil_div(v, ssk::kXentCols) * n;
+    w->pmax = r.add(parts, 4);
+    w->psum = r.add(parts, 4);
+    w->tl = r.add(back ? 0 : n, 4);
+    w->dl = r.add(back ? n * (ceil_div(w->piece, 16) * 16) : 0, es);
+    const bool listed = back && dtype == SS_BF16;
+    const int64_t groups = ceil_div(v, ssk::kXentCols);
+    w->lo = r.add(listed ? n : 0, 4);
+    w->tokens = r.add(listed ? groups * n : 0, 4);
+    w->counts = r.add(listed ? groups : 0, 4);
+    w->acc = r.add(back && w->piece < v ? n * d : 0, 4);
+    w->total = r.at;
+    return r.ok;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ss_glu_workspace_bytes(int64_t tokens, int64_t dim, int64_t features, ss_dtype dtype)
+{
+    GluLayout w;
+    return glu_layout(tokens, dim, features, dtype, false, &w) ? static_cast<size_t>(w.total) : kBad;
+}
+
+size_t ss_glu_bwd_workspace_bytes(int64_t tokens, int64_t dim, int64_t features, ss_dtype dtype)
+{
+    GluLayout w;
+    return glu_layout(tokens, dim, features, dtype, true, &w) ? static_cast<size_t>(w.total) : kBad;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Both directions: h for the forward; dh, dx, dwg and dwu for the backward.
+ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, void* h, const void* dh, void* dx,
+                   void* dwg, void* dwu, bool back, ss_activation act, void* workspace, size_t workspace_bytes,
+                   int64_t m, int64_t k, int64_t f, ss_dtype dtype, hipStream_t stream)
+{
+    if (!x || !wg || !wu || (back ? !dh : !h)) return SS_ERR_INVALID_ARG;
+    if (back && ((dwg == nullptr) != (dwu == nullptr) || (!dx && !dwg))) return SS_ERR_INVALID_ARG;
+    if (!mat_sizes(m, k, f)) return SS_ERR_INVALID_ARG;
+    if (!known(dtype) || (act != SS_ACT_SILU && act != SS_ACT_GELU)) return SS_ERR_UNSUPPORTED;
+    GluLayout w;
+    if (!glu_layout(m, k, f, dtype, back, &w)) return SS_ERR_INVALID_ARG;
+    if (!mat_grid_ok(m, f) || !mat_grid_ok(m, k) || !mat_grid_ok(2 * w.f_pad, k)) return SS_ERR_UNSUPPORTED;
+    const int64_t es = elem_size(dtype);
+    bool pack;
+    ss_status st = mat_operand(x, x_ld, k, dtype, &pack);
+    if (st != SS_OK) return st;
+    const void* weights[] = {wg, wu};
+    for (const void* p : weights) {
+        st = mat_operand(p, k, k, dtype, &pack);
+        if (st != SS_OK) return st;
+    }
+    const void* elems[] = {h, dh, dx, dwg, dwu};
+    for (const void* p : elems)
+        if (!aligned(p, uintptr_t(es))) return SS_ERR_INVALID_ARG;
+    int64_t xb;
+    if (!strided_bytes(m, k, x_ld, es, &xb)) return SS_ERR_INVALID_ARG;
+    const Range all[] = {span(x, xb), span(wg, f * k * es), span(wu, f * k * es), span(dh, m * f * es),
+                         span(h, m * f * es), span(dx, m * k * es), span(dwg, f * k * es), span(dwu, f * k * es)};
+    if (any_overlap(all + 4, 4, all, 4)) return SS_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, w.total, all, 8);
+    if (st != SS_OK) return st;
+
+    char* const ws = static_cast<char*>(workspace);
+    const int dt = dtype == SS_F32 ? 0 : 1;
+    ssk::GluArgs a{};
+    a.x = x;
+    a.x_ld = x_ld;
+    a.wg = wg;
+    a.wu = wu;
+    a.w_ld = k;
+    a.h = h;
+    a.dh = dh;
+    a.dgu = ws ? ws + w.dgu : nullptr;
+    a.dx = dx;
+    a.dwg = dwg;
+    a.dwu = dwu;
+    a.m = m;
+    a.k = k;
+    a.f = f;
+    a.f_pad = w.f_pad;
+    a.k_pad = w.k_pad;
+    a.act = act == SS_ACT_SILU ? ssk::kActSilu : ssk::kActGelu;
+    if (w.pack) {
+        hipError_t e = ssk::launch_pad_rows(x, x_ld, ws + w.x, m, k, w.k_pad, dt, stream);
+        if (e == hipSuccess) e = ssk::launch_pad_rows(wg, k, ws + w.wg, f, k, w.k_pad, dt, stream);
+        if (e == hipSuccess) e = ssk::launch_pad_rows(wu, k, ws + w.wu, f, k, w.k_pad, dt, stream);
+        if (e != hipSuccess) return done(e);
+        a.x = ws + w.x;
+        a.wg = ws + w.wg;
+        a.wu = ws + w.wu;
+        a.x_ld = a.w_ld = w.k_pad;
+    }
+    return done(back ? ssk::launch_glu_bwd(a, dt, stream) : ssk::launch_glu_fwd(a, dt, stream));
+}
+
+ss_status xent_impl(const void* x, int64_t x_ld, const void* weight, const int64_t* target, int64_t ignore_index,
+                    float* loss, float* lse_out, const float* lse_in, const float* dloss, void* dx, void* dw,
+                    bool back, void* workspace, size_t workspace_bytes, int64_t n, int64_t d, int64_t v,
+                    ss_dtype dtype, hipStream_t stream)
+{
+    if (!x || !weight || !target) return SS_ERR_INVALID_ARG;
+    if (back ? (!lse_in || !dloss || (!dx && !dw)) : (!loss || !lse_out)) return SS_ERR_INVALID_ARG;
+    if (!mat_sizes(n, d, v)) return SS_ERR_INVALID_ARG;
+    if (!known(dtype)) return SS_ERR_UNSUPPORTED;
+    XentLayout w;
+    if (!xent_layout(n, d, v, dtype, back, &w)) return SS_ERR_INVALID_ARG;
+    if (!mat_grid_ok(n, v) || !mat_grid_ok(n, d) || !mat_grid_ok(v, d) || n > INT32_MAX) return SS_ERR_UNSUPPORTED;
+    const int64_t es = elem_size(dtype);
+    bool pack;
+    ss_status st = mat_operand(x, x_ld, d, dtype, &pack);
+    if (st == SS_OK) st = mat_operand(weight, d, d, dtype, &pack);
+    if (st != SS_OK) return st;
+    if (!aligned(target, 8) || !aligned(dx, uintptr_t(es)) || !aligned(dw, uintptr_t(es))) return SS_ERR_INVALID_ARG;
+    const void* words[] = {loss, lse_out, lse_in, dloss};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return SS_ERR_INVALID_ARG;
+    int64_t xb;
+    if (!strided_bytes(n, d, x_ld, es, &xb)) return SS_ERR_INVALID_ARG;
+    const Range all[] = {span(x, xb), span(weight, v * d * es), span(target, n * 8), span(lse_in, n * 4),
+                         span(dloss, n * 4), span(loss, n * 4), span(lse_out, n * 4), span(dx, n * d * es),
+                         span(dw, v * d * es)};
+    if (any_overlap(all + 5, 4, all, 5)) return SS_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, w.total, all, 9);
+    if (st != SS_OK) return st;
+
+    char* const ws = static_cast<char*>(workspace);
+    const int dt = dtype == SS_F32 ? 0 : 1;
+    ssk::XentArgs a{};
+    a.x = x;
+    a.x_ld = x_ld;
+    a.w = weight;
+    a.w_ld = d;
+    a.target = target;
+    a.ignore_index = ignore_index;
+    a.loss = loss;
+    a.lse = back ? const_cast<float*>(lse_in) : lse_out;  // the backward only reads it
+    a.dloss = dloss;
+    a.dx = dx;
+    a.dw = dw;
+    a.n = n;
+    a.d = d;
+    a.v = v;
+    a.d_pad = w.d_pad;
+    a.piece = w.piece;
+    a.part_max = reinterpret_cast<float*>(ws + w.pmax);
+    a.part_sum = reinterpret_cast<float*>(ws + w.psum);
+    a.target_logit = reinterpret_cast<float*>(ws + w.tl);
+    a.dl = ws + w.dl;
+    a.lo = reinterpret_cast<float*>(ws + w.lo);
+    a.tokens = reinterpret_cast<int32_t*>(ws + w.tokens);
+    a.counts = reinterpret_cast<int32_t*>(ws + w.counts);
+    a.dx_acc = w.piece < v ? reinterpret_cast<float*>(ws + w.acc) : nullptr;
+    if (w.pack) {
+        hipError_t e = ssk::launch_pad_rows(x, x_ld, ws + w.x, n, d, w.d_pad, dt, stream);
+        if (e == hipSuccess) e = ssk::launch_pad_rows(weight, d, ws + w.w, v, d, w.d_pad, dt, stream);
+        if (e != hipSuccess) return done(e);
+        a.x = ws + w.x;
+        a.w = ws + w.w;
+        a.x_ld = a.w_ld = w.d_pad;
+    }
+    return done(back ? ssk::launch_xent_bwd(a, dt, stream) : ssk::launch_xent_fwd(a, dt, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+ss_status ss_glu_fwd(const void* x, int64_t x_row_stride, const void* w_gate, const void* w_up, void* h,
+                     ss_activation act, void* workspace, size_t workspace_bytes, int64_t tokens, int64_t dim,
+                     int64_t features, ss_dtype dtype, hipStream_t stream)
+{
+    return glu_impl(x, x_row_stride, w_gate, w_up, h, nullptr, nullptr, nullptr, nullptr, false, act, workspace,
+                    workspace_bytes, tokens, dim, features, dtype, stream);
+}
+
+ss_status ss_glu_bwd(const void* x, int64_t x_row_stride, const void* w_gate, const void* w_up, const void* dh,
+                     void* dx, void* dw_gate, void* dw_up, ss_activation act, void* workspace,
+                     size_t workspace_bytes, int64_t tokens, int64_t dim, int64_t features, ss_dtype dtype,
+                     hipStream_t stream)
+{
+    return glu_impl(x, x_row_stride, w_gate, w_up, nullptr, dh, dx, dw_gate, dw_up, true, act, workspace,
+                    workspace_bytes, tokens, dim, features, dtype, stream);
+}
+
+size_t ss_xent_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, ss_dtype dtype)
+{
+    XentLayout w;
+    return xent_layout(tokens, dim, vocab, dtype, false, &w) ? static_cast<size_t>(w.total) : kBad;
+}
+
+size_t ss_xent_bwd_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, ss_dtype dtype)
+{
+    XentLayout w;
+    return xent_layout(tokens, dim, vocab, dtype, true, &w) ? static_cast<size_t>(w.total) : kBad;
+}
+
+ss_status ss_xent_fwd(const void* x, int64_t x_row_stride, const void* w, const int64_t* target,
+                      int64_t ignore_index, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                      int64_t tokens, int64_t dim, int64_t vocab, ss_dtype dtype, hipStream_t stream)
+{
+    return xent_impl(x, x_row_stride, w, target, ignore_index, loss, lse, nullptr, nullptr, nullptr, nullptr, false,
+                     workspace, workspace_bytes, tokens, dim, vocab, dtype, stream);
+}
+
+ss_status ss_xent_bwd(const void* x, int64_t x_row_stride, const void* w, const int64_t* target,
+                      int64_t ignore_index, const float* lse, const float* dloss, void* dx, void* dw,
+                      void* workspace, size_t workspace_bytes, int64_t tokens, int64_t dim, int64_t vocab,
+                      ss_dtype dtype, hipStream_t stream)
+{
+    return xent_impl(x, x_row_stride, w, target, ignore_index, nullptr, nullptr, lse, dloss, dx, dw, true, workspace,
+                     workspace_bytes, tokens, dim, vocab, dtype, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,130 @@
+// Internal interface between the C-ABI layer of the language-model operators
+// (ss_lm_api.cpp) and their gfx950 kernels (ss_glr.hip, ss_glu.hip, ss_xent.hip).
+// Not installed, not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace ssk {
+
+// ---- gated feed-forward projection -----------------------------------------------------
+
+constexpr int kActSilu = 0, kActGelu = 1;
+
+// Tokens up to which the weight-streaming kernel is used instead of the tiled one.
+constexpr int64_t kGluStreamRows = 64;
+
+struct GluArgs {
+    const void* x;   // (m, k), rows x_ld elements apart
+    int64_t x_ld;
+    const void* wg;  // (f, k), rows w_ld elements apart
+    const void* wu;
+    int64_t w_ld;
+    void* h;         // (m, f); the backward: unused
+    const void* dh;  // backward: (m, f)
+    void* dgu;       // backward workspace: (m, 2 f_pad), dg in the first half of a row, du in the second
+    void* dx;        // (m, k), nullable
+    void* dwg;       // (f, k), nullable (both or neither)
+    void* dwu;
+    int64_t m, k, f, f_pad;
+    int64_t k_pad;   // k rounded up to whole 16-byte chunks; x and w rows hold zeros there
+    int act;
+};
+
+// Copy of `rows` rows of `cols` elements (ld apart) into rows of cols_pad elements, the pad zeroed.
+hipError_t launch_pad_rows(const void* src, int64_t ld, void* dst, int64_t rows, int64_t cols, int64_t cols_pad,
+                           int dtype, hipStream_t stream);
+hipError_t launch_glu_fwd(const GluArgs& a, int dtype, hipStream_t stream);
+// The backward's two launches: dgu from x, w, dh; then dx and dw from dgu.
+hipError_t launch_glu_bwd(const GluArgs& a, int dtype, hipStream_t stream);
+
+// ---- softmax cross entropy of a vocabulary projection -----------------------------------
+
+// Columns of the vocabulary behind one partial (maximum, sum) pair of a row.
+constexpr int64_t kXentCols = 128;
+
+struct XentArgs {
+    const void* x;  // (n, d), rows x_ld elements apart
+    int64_t x_ld;
+    const void* w;  // (v, d), rows w_ld elements apart
+    int64_t w_ld;
+    const int64_t* target;  // (n,)
+    int64_t ignore_index;
+    float* loss;        // forward output (n,)
+    float* lse;         // forward output, backward input (n,)
+    float* part_max;    // forward workspace: (ceil(v / kXentCols), n)
+    float* part_sum;
+    float* target_logit;  // forward workspace (n,)
+    const float* dloss;   // backward (n,)
+    void* dl;             // backward workspace: (n, piece_pad) gradient of one piece's logits
+    // bf16 backward workspace: what rounding took from each row's target entry of dl, and per
+    // 128 columns of the vocabulary the tokens whose targets lie there, in order, and their number
+    float* lo;            // (n,)
+    int32_t* tokens;      // (ceil(v / kXentCols), n)
+    int32_t* counts;      // (ceil(v / kXentCols),)
+    float* dx_acc;        // backward workspace: (n, d) fp32 sums over the pieces, null with one piece
+    void* dx;             // (n, d), nullable
+    void* dw;             // (v, d), nullable
+    int64_t n, d, v;
+    int64_t d_pad;        // d rounded up to whole 16-byte chunks
+    int64_t piece;        // columns of the vocabulary per piece (the backward)
+};
+
+hipError_t launch_xent_fwd(const XentArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_xent_bwd(const XentArgs& a, int dtype, hipStream_t stream);
+
+// ---- gated linear recurrence ------------------------------------------------------------
+
+// Rows between two kept states, which is also the backward's tile: it rebuilds a
+// tile's states from the one that enters it.
+constexpr int64_t kGlrRows = 64;
+// Chunks are whole forward tiles.
+constexpr int64_t kGlrChunkUnit = 128;
+
+struct GlrArgs {
+    const void* x;  // (batch, seqlen, dim), rows *_ld elements apart
+    const void* r;
+    const void* i;
+    int64_t x_ld, r_ld, i_ld;
+    const float* decay;    // (dim,)
+    float c;
+    const float* h0;       // (batch, dim), nullable
+    const uint8_t* reset;  // (batch, seqlen), nullable
+    void* y;               // (batch, seqlen, dim); null: only the states are wanted
+    float* h_last;         // (batch, dim), nullable
+    float* ckpt;           // (ceil(seqlen / kGlrRows), batch, dim) states entering each tile, nullable
+    // the split plan (n_chunks > 1): per chunk and channel the affine map of the chunk
+    float* ws_prod;        // (n_chunks, batch, dim)
+    float* ws_end;         // (n_chunks, batch, dim)
+    int64_t batch, seqlen, dim;
+    int64_t chunk_len, n_chunks;  // chunk_len a multiple of kGlrChunkUnit
+    // backward
+    const void* dy;        // (batch, seqlen, dim)
+    const float* dh_last;  // (batch, dim), nullable
+    void* dx;              // (batch, seqlen, dim), rows g_ld elements apart
+    void* dr;
+    void* di;
+    int64_t g_ld;
+    float* dh0;            // (batch, dim), nullable
+    float* part_decay;     // (n_chunks, batch, dim) sums over a chunk's rows
+    float* ddecay;         // (dim,)
+};
+
+hipError_t launch_glr_fwd(const GlrArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrArgs& a, int dtype, hipStream_t stream);
+
+struct GlrStepArgs {
+    float* h;  // (batch, dim)
+    const void* x;
+    const void* r;
+    const void* i;  // (batch, dim)
+    int64_t x_ld, r_ld, i_ld;
+    const float* decay;
+    float c;
+    void* y;
+    int64_t batch, dim;
+};
+hipError_t launch_glr_step(const GlrStepArgs& a, int dtype, hipStream_t stream);
+
+}  // namespace ssk

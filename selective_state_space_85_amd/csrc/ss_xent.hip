@@ -1,0 +1,530 @@
+// gfx950 kernels of the softmax cross entropy of a vocabulary projection
+//   l = x w^T (n, v),  lse_i = log sum_j exp(l_ij),  loss_i = lse_i - l_i,target
+// and its gradients
+//   dl_ij = (exp(l_ij - lse_i) - [j = target_i]) dloss_i,  dx = dl w,  dw = dl^T x.
+//
+// The logits are never stored.  Forward: each 128 columns' tile of logits is reduced, in the
+// accumulators that hold it, to a maximum and a sum of exponentials per row; a second kernel
+// joins the (maximum, sum) pairs of a row.  Backward: the vocabulary is taken in pieces; a
+// piece's logits are formed again and turned into dl in the epilogue (rounded once to the
+// operands' type, as the next products' operands must be) in a workspace that the next piece
+// reuses, and one launch forms the piece's part of dx (fp32 sums over the pieces, rounded
+// after the last) and its rows of dw.  Bound by the matrix cores at training sizes.
+//
+// bf16: a row's target entry of dl, (p - 1) dloss, is far larger than its others, and what
+// rounding takes from it would be the largest error of both gradients.  It is kept aside: dx
+// gets it times the target's row of w in the epilogue, and a dw tile takes one more k tile
+// (per BK tokens whose targets lie in it) of these remainders against those tokens' rows of x.
+//
+// A row whose target is ignore_index, or lies outside [0, v), has loss 0 and no gradient.
+#include "ss_gemm.h"
+#include "ss_lm_internal.h"
+
+namespace ssk {
+namespace {
+
+__device__ __forceinline__ bool live_target(int64_t t, const XentArgs& a)
+{
+    return t != a.ignore_index && t >= 0 && t < a.v;
+}
+
+// what both products over (x, w) share: rows of x against rows [v0, v0 + cols) of w
+template <int DT>
+struct XentLogits {
+    using T = typename MM<DT>::T;
+    const XentArgs& a;
+    int64_t m0, n0;  // first row, first column of the vocabulary
+    int tiles;
+
+    __device__ const char* a_chunk(int row, int k) const
+    {
+        int64_t r = m0 + row;
+        r = r < a.n ? r : a.n - 1;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + r * a.x_ld + k);
+    }
+    __device__ const char* b_chunk(int row, int k) const
+    {
+        int64_t r = n0 + row;
+        r = r < a.v ? r : a.v - 1;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.w) + r * a.w_ld + k);
+    }
+    __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
+    __device__ int64_t b_off(int t) const { return int64_t(t) * 128; }
+    __device__ int valid(int t) const { return int(a.d_pad - int64_t(t) * (8 * MM<DT>::kEpc)); }
+};
+
+// ---- forward -------------------------------------------------------------------------------
+
+// (m, s) stands for s exp(m): joins another pair.  An all -inf side leaves the other as it is.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
+{
+    const float top = fmaxf(m, m2);
+    // NaN: fmaxf drops it, but its sum is NaN and stays
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    s = s * exp2_hw((m - base) * kLog2e) + s2 * exp2_hw((m2 - base) * kLog2e);
+    m = top;
+}
+
+template <int DT>
+struct XentFwdProb : XentLogits<DT> {
+    template <class G>
+    __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char* lds, int wm, int wn, int lane) const
+    {
+        const XentArgs& a = this->a;
+        // waves of one kXentCols group of columns
+        constexpr int kGroup = int(kXentCols) / (G::FN * 16);
+        static_assert(kGroup >= 1 && G::BN % kXentCols == 0, "whole groups of columns per tile");
+        float* const pm = reinterpret_cast<float*>(lds);           // (WN, BM)
+        float* const ps = pm + G::WN * G::BM;
+        __syncthreads();  // every wave has read its last operands
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int r = (wm * G::FM + i) * 16 + (lane & 15);
+            const int64_t m = this->m0 + r;
+            const int64_t t = m < a.n ? a.target[m] : -1;
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const int64_t c = this->n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (c + e == t && t < a.v) a.target_logit[m] = acc[i][j][e];
+                    if (c + e < a.v) top = fmaxf(top, acc[i][j][e]);
+                }
+            }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float base = top == -__builtin_inff() ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const int64_t c = this->n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < a.v) sum += exp2_hw((acc[i][j][e] - base) * kLog2e);
+            }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (lane < 16) {
+                pm[wn * G::BM + r] = top;
+                ps[wn * G::BM + r] = sum;
+            }
+        }
+        __syncthreads();
+        for (int q = threadIdx.x; q < G::BM * (G::BN / int(kXentCols)); q += G::NT) {
+            const int r = q % G::BM, g = q / G::BM;
+            if (this->m0 + r >= a.n || this->n0 + g * kXentCols >= a.v) continue;
+            float m = pm[g * kGroup * G::BM + r], s = ps[g * kGroup * G::BM + r];
+#pragma unroll
+            for (int w = 1; w < kGroup; ++w) join(m, s, pm[(g * kGroup + w) * G::BM + r], ps[(g * kGroup + w) * G::BM + r]);
+            const int64_t at = (this->n0 / kXentCols + g) * a.n + this->m0 + r;
+            a.part_max[at] = m;
+            a.part_sum[at] = s;
+        }
+    }
+};
+
+template <class G>
+__global__ __launch_bounds__(G::NT) void xent_fwd_kernel(XentArgs a, uint32_t ntm, uint32_t ntn)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
+    uint32_t tm, tn;
+    tile_of(blockIdx.x, ntm, ntn, &tm, &tn);
+    const XentFwdProb<G::DT> p{{a, int64_t(tm) * G::BM, int64_t(tn) * G::BN, int((a.d_pad + G::BK - 1) / G::BK)}};
+    mm_tile<G>(p, lds);
+}
+
+// The pairs of a row, joined: 16 rows per workgroup, 16 threads a row.
+constexpr int kJoinRows = 16, kJoinLanes = 16;
+__global__ __launch_bounds__(kJoinRows * kJoinLanes) void xent_join_kernel(XentArgs a, int64_t groups)
+{
+    __shared__ float sm[kJoinLanes][kJoinRows], ss[kJoinLanes][kJoinRows];
+    const int r = threadIdx.x % kJoinRows, q = threadIdx.x / kJoinRows;
+    const int64_t row = int64_t(blockIdx.x) * kJoinRows + r;
+    float m = -__builtin_inff(), s = 0.0f;
+    if (row < a.n)
+        for (int64_t g = q; g < groups; g += kJoinLanes) join(m, s, a.part_max[g * a.n + row], a.part_sum[g * a.n + row]);
+    sm[q][r] = m;
+    ss[q][r] = s;
+    __syncthreads();
+    if (q != 0 || row >= a.n) return;
+    for (int w = 1; w < kJoinLanes; ++w) join(m, s, sm[w][r], ss[w][r]);
+    const float lse = m + __builtin_amdgcn_logf(s) * kLn2;
+    const int64_t t = a.target[row];
+    a.lse[row] = lse;
+    a.loss[row] = live_target(t, a) ? lse - a.target_logit[row] : 0.0f;
+}
+
+// ---- backward ------------------------------------------------------------------------------
+
+// dl of one piece: columns [v0, v0 + cols) of the vocabulary, rows of `pad` elements
+template <int DT>
+struct XentDlProb : XentLogits<DT> {
+    using T = typename MM<DT>::T;
+    int64_t v0, cols, pad;
+
+    template <class G>
+    __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
+    {
+        const XentArgs& a = this->a;
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int64_t m = this->m0 + (wm * G::FM + i) * 16 + (lane & 15);
+            if (m >= a.n) continue;
+            const int64_t t = a.target[m];
+            const bool live = live_target(t, a);
+            const float lse = a.lse[m], scale = a.dloss[m];
+            T* const row = static_cast<T*>(a.dl) + m * pad;
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const int64_t c = this->n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
+                if (c - v0 >= pad) continue;
+                typedef T T4 __attribute__((ext_vector_type(4)));
+                T4 q;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p = exp2_hw((acc[i][j][e] - lse) * kLog2e) - (c + e == t ? 1.0f : 0.0f);
+                    // the columns past the piece's end hold zeros: the products read them
+                    const float full = live && c + e - v0 < cols ? p * scale : 0.0f;
+                    q[e] = MM<DT>::narrow(full);
+                    if (DT == 1 && live && c + e == t && c + e - v0 < cols) a.lo[m] = full - MM<DT>::widen(q[e]);
+                }
+                *reinterpret_cast<T4*>(row + (c - v0)) = q;
+            }
+        }
+    }
+};
+
+template <class G>
+__global__ __launch_bounds__(G::NT) void xent_dl_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad,
+                                                        uint32_t ntm, uint32_t ntn)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
+    uint32_t tm, tn;
+    tile_of(blockIdx.x, ntm, ntn, &tm, &tn);
+    const XentDlProb<G::DT> p{
+        {a, int64_t(tm) * G::BM, v0 + int64_t(tn) * G::BN, int((a.d_pad + G::BK - 1) / G::BK)}, v0, cols, pad};
+    mm_tile<G>(p, lds);
+}
+
+// The tokens whose targets lie in each group of kXentCols columns, in order.
+__global__ __launch_bounds__(256) void xent_list_kernel(XentArgs a)
+{
+    const int64_t from = int64_t(blockIdx.x) * kXentCols;
+    int32_t* const list = a.tokens + int64_t(blockIdx.x) * a.n;
+    __shared__ int found[2][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int count = 0, buf = 0;
+    for (int64_t i = 0; i < a.n; i += 256, buf ^= 1) {
+        const int64_t tok = i + threadIdx.x;
+        const int64_t t = tok < a.n ? a.target[tok] : -1;
+        const bool in = t >= from && t < from + kXentCols && live_target(t, a);
+        const uint64_t mask = __ballot(in);
+        if (lane == 0) found[buf][wave] = __popcll(mask);
+        __syncthreads();
+        int at = count;
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) at += found[buf][w];
+            count += found[buf][w];
+        }
+        if (in) list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = int32_t(tok);
+    }
+    if (threadIdx.x == 0) a.counts[blockIdx.x] = count;
+}
+
+// dx += dl w over one piece
+template <int DT>
+struct XentDxProb {
+    using T = typename MM<DT>::T;
+    static constexpr int BK = 8 * MM<DT>::kEpc;
+    const XentArgs& a;
+    int64_t m0, n0, v0, cols, pad;
+    int tiles;
+    bool first, last, vec;
+
+    __device__ const char* a_chunk(int row, int k) const
+    {
+        int64_t r = m0 + row;
+        r = r < a.n ? r : a.n - 1;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.dl) + r * pad + k);
+    }
+    __device__ const char* b_chunk(int col, int k) const
+    {
+        int64_t c = n0 + col;
+        c = c < a.d_pad ? c : a.d_pad - MM<DT>::kEpc;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.w) + (v0 + k) * a.w_ld + c);
+    }
+    __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
+    __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.w_ld * int64_t(sizeof(T)); }
+    __device__ int valid(int t) const
+    {
+        const int64_t left = cols - int64_t(t) * BK;
+        return left < BK ? int(left) : BK;
+    }
+
+    template <class G>
+    __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int64_t m = m0 + (wm * G::FM + i) * 16 + (lane & 15);
+            if (m >= a.n) continue;
+            const int64_t t = a.target[m];
+            const bool add = DT == 1 && last && live_target(t, a);
+            const float lo = add ? a.lo[m] : 0.0f;
+            const T* const wt = static_cast<const T*>(a.w) + (add ? t : 0) * a.w_ld;
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const int64_t c = n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (c + e >= a.d) continue;
+                    float v = acc[i][j][e];
+                    if (!first) v += a.dx_acc[m * a.d + c + e];
+                    if (add) v = fmaf(lo, MM<DT>::widen(wt[c + e]), v);
+                    if (last)
+                        static_cast<T*>(a.dx)[m * a.d + c + e] = MM<DT>::narrow(v);
+                    else
+                        a.dx_acc[m * a.d + c + e] = v;
+                }
+            }
+        }
+    }
+};
+
+// rows [v0, v0 + cols) of dw = dl^T x
+template <int DT>
+struct XentDwProb {
+    using T = typename MM<DT>::T;
+    static constexpr int BK = 8 * MM<DT>::kEpc;
+    const XentArgs& a;
+    int64_t m0, n0, v0, cols, pad;
+    int tiles;
+    bool vec;
+
+    __device__ const char* a_chunk(int col, int k) const
+    {
+        int64_t c = m0 + col;
+        c = c < pad ? c : pad - MM<DT>::kEpc;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.dl) + int64_t(k) * pad + c);
+    }
+    __device__ const char* b_chunk(int col, int k) const
+    {
+        int64_t c = n0 + col;
+        c = c < a.d_pad ? c : a.d_pad - MM<DT>::kEpc;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + int64_t(k) * a.x_ld + c);
+    }
+    __device__ int64_t a_off(int t) const { return int64_t(t) * BK * pad * int64_t(sizeof(T)); }
+    __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
+    __device__ int valid(int t) const
+    {
+        const int64_t left = a.n - int64_t(t) * BK;
+        return left < BK ? int(left) : BK;
+    }
+
+    // the target entries' remainders
+    template <class G>
+    __device__ void remainders(f32x4 (&acc)[G::FM][G::FN], char* lds, int wm, int wn, int lane) const
+    {
+        using M = MM<DT>;
+        const int tid = threadIdx.x;
+#pragma unroll 1
+        for (int half = 0; half < G::BM / int(kXentCols); ++half) {
+            const int64_t from = v0 + m0 + half * kXentCols;
+            if (from >= v0 + cols) break;
+            const int32_t* const list = a.tokens + from / kXentCols * a.n;
+            const int count = a.counts[from / kXentCols];
+#pragma unroll 1
+            for (int at = 0; at < count; at += BK) {
+                __syncthreads();  // the stage's last readers are done
+                for (int q = tid; q < G::A_BYTES / 16; q += G::NT)
+                    reinterpret_cast<f32x4*>(lds)[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                int col, k;
+#pragma unroll
+                for (int i = 0; i < G::NB; ++i) {
+                    chunk_place<G, G::B_MC, G::BN>(i, tid, &col, &k);
+                    int64_t c = n0 + col;
+                    c = c < a.d_pad ? c : a.d_pad - M::kEpc;
+                    const char* src = reinterpret_cast<const char*>(g_zero_chunk);
+                    if (at + k < count) src = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + list[at + k] * a.x_ld + c);
+                    load_to_lds(src, lds + G::A_BYTES + (tid >> 6) * 1024 + i * (G::NT * 16));
+                }
+                __syncthreads();
+                if (tid < BK && at + tid < count) {
+                    const int tok = list[at + tid];
+                    const int m = int(a.target[tok] - v0 - m0);
+                    const int gran = (m >> 4) ^ (M::mc_idx(tid) & (G::BM / 16 - 1));
+                    reinterpret_cast<T*>(lds)[tid * G::BM + gran * 16 + (m & 15)] = M::narrow(a.lo[tok]);
+                }
+                __syncthreads();
+                mm_step<G>(lds, wm, wn, lane, acc);
+            }
+        }
+    }
+
+    template <class G>
+    __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char* lds, int wm, int wn, int lane) const
+    {
+        if constexpr (DT == 1) remainders<G>(acc, lds, wm, wn, lane);
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int64_t r = m0 + (wm * G::FM + i) * 16 + (lane & 15);
+            if (r >= cols) continue;
+            T* const row = static_cast<T*>(a.dw) + (v0 + r) * a.d;
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const int64_t c = n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
+                if (vec && c + 4 <= a.d) {
+                    typedef T T4 __attribute__((ext_vector_type(4)));
+                    T4 q;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q[e] = MM<DT>::narrow(acc[i][j][e]);
+                    *reinterpret_cast<T4*>(row + c) = q;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < a.d) row[c + e] = MM<DT>::narrow(acc[i][j][e]);
+                }
+            }
+        }
+    }
+};
+
+template <class GX, class GW>
+__global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad,
+                                                           uint32_t n_dx, uint32_t xm, uint32_t xn, uint32_t wm,
+                                                           uint32_t wn, bool first, bool last, bool vec_w)
+{
+    static_assert(GX::NT == GW::NT, "one launch");
+    __shared__ __attribute__((aligned(1024))) char lds[GX::LDS > GW::LDS ? GX::LDS : GW::LDS];
+    uint32_t tm, tn;
+    if (blockIdx.x < n_dx) {
+        tile_of(blockIdx.x, xm, xn, &tm, &tn);
+        const XentDxProb<GX::DT> p{a,   int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, v0,   cols,
+                                   pad, int((cols + GX::BK - 1) / GX::BK), first, last, false};
+        mm_tile<GX>(p, lds);
+    } else {
+        tile_of(blockIdx.x - n_dx, wm, wn, &tm, &tn);
+        const XentDwProb<GW::DT> p{a,   int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, v0, cols,
+                                   pad, int((a.n + GW::BK - 1) / GW::BK), vec_w};
+        mm_tile<GW>(p, lds);
+    }
+}
+
+// ---- launches --------------------------------------------------------------------------------
+
+template <int DT>
+struct Tiles;
+template <>
+struct Tiles<1> {
+    template <bool AM, bool BM_>
+    using Large = Geo<1, 256, 256, 2, 4, AM, BM_>;
+    template <bool AM, bool BM_>
+    using Small = Geo<1, 128, 128, 2, 2, AM, BM_>;
+};
+template <>
+struct Tiles<0> {
+    template <bool AM, bool BM_>
+    using Large = Geo<0, 128, 128, 2, 2, AM, BM_>;
+    template <bool AM, bool BM_>
+    using Small = Geo<0, 128, 128, 2, 2, AM, BM_>;
+};
+
+uint32_t up(int64_t a, int64_t b) { return uint32_t((a + b - 1) / b); }
+
+// as in ss_glu.hip: a round of 512 small tiles costs 0.57 of a round of 256 large ones
+bool large_tile(int64_t large, int64_t small)
+{
+    const double rl = double((large + 255) / 256), rs = double((small + 511) / 512);
+    return rl <= 0.57 * rs;
+}
+
+template <class G>
+hipError_t fwd_tiles(const XentArgs& a, hipStream_t s)
+{
+    const uint32_t ntm = up(a.n, G::BM), ntn = up(a.v, G::BN);
+    xent_fwd_kernel<G><<<dim3(ntm * ntn), dim3(G::NT), 0, s>>>(a, ntm, ntn);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t fwd_dt(const XentArgs& a, hipStream_t s)
+{
+    using T = Tiles<DT>;
+    hipError_t e;
+    if (DT == 1 && large_tile(int64_t(up(a.n, 256)) * up(a.v, 256), int64_t(up(a.n, 128)) * up(a.v, 128)))
+        e = fwd_tiles<typename T::template Large<false, false>>(a, s);
+    else
+        e = fwd_tiles<typename T::template Small<false, false>>(a, s);
+    if (e != hipSuccess) return e;
+    xent_join_kernel<<<dim3(up(a.n, kJoinRows)), dim3(kJoinRows * kJoinLanes), 0, s>>>(a, int64_t(up(a.v, kXentCols)));
+    return hipGetLastError();
+}
+
+template <class G>
+hipError_t dl_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
+{
+    const uint32_t ntm = up(a.n, G::BM), ntn = up(pad, G::BN);
+    xent_dl_kernel<G><<<dim3(ntm * ntn), dim3(G::NT), 0, s>>>(a, v0, cols, pad, ntm, ntn);
+    return hipGetLastError();
+}
+
+template <class GX, class GW>
+hipError_t grad_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
+{
+    const uint32_t xm = up(a.n, GX::BM), xn = up(a.d, GX::BN), wm = up(cols, GW::BM), wn = up(a.d, GW::BN);
+    const uint32_t n_dx = a.dx ? xm * xn : 0, n_dw = a.dw ? wm * wn : 0;
+    const bool vec = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dw) % (GX::DT == 0 ? 16 : 8) == 0;
+    xent_grad_kernel<GX, GW><<<dim3(n_dx + n_dw), dim3(GX::NT), 0, s>>>(a, v0, cols, pad, n_dx, xm, xn, wm, wn, v0 == 0,
+                                                                       v0 + cols == a.v, vec);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t bwd_dt(const XentArgs& a, hipStream_t s)
+{
+    using T = Tiles<DT>;
+    if (DT == 1 && a.dw) {
+        xent_list_kernel<<<dim3(up(a.v, kXentCols)), dim3(256), 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    for (int64_t v0 = 0; v0 < a.v; v0 += a.piece) {
+        const int64_t cols = a.v - v0 < a.piece ? a.v - v0 : a.piece;
+        const int64_t pad = (cols + 15) / 16 * 16;
+        hipError_t e;
+        if (DT == 1 && large_tile(int64_t(up(a.n, 256)) * up(pad, 256), int64_t(up(a.n, 128)) * up(pad, 128)))
+            e = dl_tiles<typename T::template Large<false, false>>(a, v0, cols, pad, s);
+        else
+            e = dl_tiles<typename T::template Small<false, false>>(a, v0, cols, pad, s);
+        if (e != hipSuccess) return e;
+        const int64_t large = (a.dx ? int64_t(up(a.n, 256)) * up(a.d, 256) : 0) +
+                              (a.dw ? int64_t(up(cols, 256)) * up(a.d, 256) : 0);
+        const int64_t small = (a.dx ? int64_t(up(a.n, 128)) * up(a.d, 128) : 0) +
+                              (a.dw ? int64_t(up(cols, 128)) * up(a.d, 128) : 0);
+        if (DT == 1 && large_tile(large, small))
+            e = grad_tiles<typename T::template Large<false, true>, typename T::template Large<true, true>>(a, v0, cols,
+                                                                                                         pad, s);
+        else
+            e = grad_tiles<typename T::template Small<false, true>, typename T::template Small<true, true>>(a, v0, cols,
+                                                                                                         pad, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_xent_fwd(const XentArgs& a, int dtype, hipStream_t stream)
+{
+    (void)hipGetLastError();
+    return dtype == 0 ? fwd_dt<0>(a, stream) : fwd_dt<1>(a, stream);
+}
+
+hipError_t launch_xent_bwd(const XentArgs& a, int dtype, hipStream_t stream)
+{
+    (void)hipGetLastError();
+    return dtype == 0 ? bwd_dt<0>(a, stream) : bwd_dt<1>(a, stream);
+}
+
+}  // namespace ssk

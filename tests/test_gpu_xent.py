@@ -1,0 +1,204 @@
+"""GPU parity of the vocabulary cross entropy (ss_xent_fwd, ss_xent_bwd) with its float64
+definition.  Losses and statistics are fp32 from exact products: <= 1e-4 in either type.
+Gradients: <= 1e-4 in fp32; <= 2e-2 in bf16, where the logits' gradient is rounded once before
+the products and each output once."""
+import numpy as np
+import pytest
+import torch
+
+import lm_ref
+import workloads as wl
+from gpu_util import TOL, dev, host64, rel_err, say
+from test_gpu_glr import check, rand, wide
+
+pytestmark = pytest.mark.gpu
+
+
+def ss():
+    import selective_state_space_85_amd as m
+
+    return m
+
+
+def make(n, d, v, dt, seed, extra=0, scale=2.0):
+    rng = np.random.default_rng(seed + 31 * n + 7 * d + v)
+    x = rand(rng, (n, d + extra), dt)
+    w = rand(rng, (v, d), dt, scale / np.sqrt(d))
+    t = rng.integers(0, v, n)
+    t[rng.random(n) < 0.1] = -100
+    dloss = rng.uniform(0.1, 1.0, n).astype(np.float32)
+    return x, w, t.astype(np.int64), dloss
+
+
+def run(x, w, t, dloss, d=None, **kw):
+    d = w.shape[1] if d is None else d
+    xt, wt, tt = dev(x)[:, :d], dev(w), torch.from_numpy(t).cuda()
+    loss, lse = ss().xent_fwd(xt, wt, tt, **kw)
+    g = ss().xent_bwd(xt, wt, tt, lse, dev(dloss), **kw)
+    torch.cuda.synchronize()
+    return loss, lse, g
+
+
+# tokens, dim, vocab, dtype, extra columns of x's rows
+CASES = [
+    (1, 1, 1, wl.F32, 0),
+    (1, 8, 2, wl.BF16, 0),
+    (3, 64, 127, wl.BF16, 0),
+    (17, 33, 128, wl.F32, 0),            # dim in no whole 16 bytes: padded copies
+    (16, 100, 129, wl.BF16, 8),
+    (128, 72, 500, wl.BF16, 8),
+    (129, 40, 1000, wl.F32, 4),
+    (200, 513, 300, wl.BF16, 1),
+    (333, 96, 3001, wl.F32, 0),
+    (70, 264, 5003, wl.BF16, 0),
+]
+IDS = ["N%dD%dV%d-%s%s" % (c[0], c[1], c[2], c[3], "-str" * (c[4] > 0)) for c in CASES]
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_loss_and_gradients(case):
+    n, d, v, dt, extra = case
+    x, w, t, dloss = make(n, d, v, dt, 1, extra)
+    say("xent", case)
+    loss, lse, g = run(x, w, t, dloss, d)
+    x64, w64 = wide(x)[:, :d], wide(w)
+    lr, zr, _, _ = lm_ref.xent(x64, w64, t)
+    check("loss", host64(loss), lr, TOL["f32"])
+    check("lse", host64(lse), zr, TOL["f32"])
+    ref = lm_ref.xent_bwd(x64, w64, t, dloss.astype(np.float64))
+    for k in ref:
+        check(k, host64(g[k]), ref[k], TOL[dt])
+
+
+@pytest.mark.parametrize("n,d,v", [(2304, 264, 20000), (40000, 32, 9001)], ids=["large-tiles", "pieces"])
+def test_large(n, d, v):
+    """256 x 256 tiles; and more tokens than one piece of the vocabulary holds, so that dx is
+    summed over pieces."""
+    x, w, t, dloss = make(n, d, v, wl.BF16, 2)
+    say("xent large", n, d, v)
+    loss, lse, g = run(x, w, t, dloss)
+    x64 = torch.from_numpy(wide(x)).cuda()
+    w64 = torch.from_numpy(wide(w)).cuda()
+    dx, dw = np.empty((n, d)), torch.zeros((v, d), dtype=torch.float64, device="cuda")
+    wt = w64.t().contiguous()
+    for r in range(0, n, 2304):
+        l = x64[r:r + 2304] @ wt
+        z = torch.logsumexp(l, 1)
+        tt = torch.from_numpy(t[r:r + 2304]).cuda()
+        live = tt >= 0
+        at = torch.arange(len(tt), device="cuda")
+        picked = l[at, tt.clamp(min=0)]
+        check("loss", host64(loss[r:r + 2304]), torch.where(live, z - picked, 0.0).cpu().numpy(), TOL["f32"])
+        p = (l - z[:, None]).exp()
+        p[at, tt.clamp(min=0)] -= 1.0
+        p *= (torch.from_numpy(dloss[r:r + 2304]).cuda().double() * live)[:, None]
+        dx[r:r + 2304] = (p @ w64).cpu().numpy()
+        dw += p.t().contiguous() @ x64[r:r + 2304]
+    check("dx", host64(g["dx"]), dx, TOL["bf16"])
+    check("dw", host64(g["dw"]), dw.cpu().numpy(), TOL["bf16"])
+
+
+def test_targets():
+    """Ignored and out-of-range targets: no loss and no gradient; the others are as without
+    them.  All rows ignored: every gradient is exactly zero."""
+    n, d, v = 40, 64, 300
+    x, w, t, dloss = make(n, d, v, wl.F32, 3)
+    t[:] = np.arange(n) * 7
+    t[3], t[5], t[9], t[11] = 7, -1, v, 2 ** 40
+    say("xent targets")
+    loss, lse, g = run(x, w, t, dloss, ignore_index=7)
+    dead = np.zeros(n, bool)
+    dead[[1, 3, 5, 9, 11]] = True  # row 1 has target 7 as well
+    lr, _, _, live = lm_ref.xent(wide(x), wide(w), t, 7)
+    assert np.array_equal(~live, dead)
+    assert np.all(host64(loss)[dead] == 0.0)
+    check("loss", host64(loss), lr, TOL["f32"])
+    ref = lm_ref.xent_bwd(wide(x), wide(w), t, dloss.astype(np.float64), 7)
+    for k in ref:
+        check(k, host64(g[k]), ref[k], TOL["f32"])
+    assert np.all(host64(g["dx"])[dead] == 0.0)
+    loss, _, g = run(x, w, np.full(n, -100), dloss)
+    assert not host64(loss).any() and not host64(g["dx"]).any() and not host64(g["dw"]).any()
+
+
+@pytest.mark.parametrize("scale", [1e-3, 60.0, 400.0])
+def test_logit_scales(scale):
+    """Flat logits and logits whose exponentials would overflow without the running maximum."""
+    n, d, v = 50, 64, 700
+    x, w, t, dloss = make(n, d, v, wl.F32, 4, scale=scale)
+    say("xent scale", scale)
+    loss, lse, g = run(x, w, t, dloss)
+    lr, zr, _, _ = lm_ref.xent(wide(x), wide(w), t)
+    check("loss", host64(loss), lr, TOL["f32"])
+    check("lse", host64(lse), zr, TOL["f32"])
+    if scale < 100:  # beyond, p's error is the logit's (|l| 2^-24 ~ 1e-4) and says nothing
+        ref = lm_ref.xent_bwd(wide(x), wide(w), t, dloss.astype(np.float64))
+        for k in ref:
+            check(k, host64(g[k]), ref[k], 5e-4 if scale > 1 else TOL["f32"])
+
+
+def test_nonfinite_rows():
+    """A NaN token's loss is NaN and no other row's changes; a row of weights at the type's
+    lowest value counts as nothing."""
+    n, d, v = 60, 64, 300
+    x, w, t, dloss = make(n, d, v, wl.F32, 5)
+    t = np.abs(t) % v
+    base, _, _ = run(x, w, t, dloss)
+    x2 = x.copy()
+    x2[7, 0] = np.nan
+    say("xent nan row")
+    loss, lse, _ = run(x2, w, t, dloss)
+    got, want = host64(loss), host64(base)
+    assert np.isnan(got[7]) and np.array_equal(np.delete(got, 7), np.delete(want, 7))
+
+
+def test_gradient_against_differences():
+    n, d, v = 4, 3, 6
+    x, w, t, dloss = make(n, d, v, wl.F32, 6)
+    t = np.array([0, 5, -100, 2])
+    say("xent differences")
+    _, _, g = run(x, w, t, dloss)
+    inp = {"dx": x, "dw": w}
+    for name, arr in inp.items():
+        num = np.zeros(arr.shape)
+        for at in np.ndindex(arr.shape):
+            val = []
+            for s in (1e-5, -1e-5):
+                q = {k: a.astype(np.float64) for k, a in inp.items()}
+                q[name][at] += s
+                val.append((lm_ref.xent(q["dx"], q["dw"], t)[0] * dloss).sum())
+            num[at] = (val[0] - val[1]) / 2e-5
+        check(name, host64(g[name]), num, TOL["f32"])
+
+
+def test_parts_alone_and_shapes():
+    """dx alone and dw alone are the same bits; a (batch, seqlen, dim) input keeps its axes."""
+    x, w, t, dloss = make(24, 64, 300, wl.BF16, 7)
+    xt, wt, tt = dev(x).view(2, 12, 64), dev(w), torch.from_numpy(t).cuda().view(2, 12)
+    dl = dev(dloss).view(2, 12)
+    say("xent parts")
+    loss, lse = ss().xent_fwd(xt, wt, tt)
+    assert loss.shape == (2, 12) and lse.shape == (2, 12)
+    g = ss().xent_bwd(xt, wt, tt, lse, dl)
+    assert g["dx"].shape == xt.shape
+    assert torch.equal(ss().xent_bwd(xt, wt, tt, lse, dl, want_dw=False)["dx"], g["dx"])
+    assert torch.equal(ss().xent_bwd(xt, wt, tt, lse, dl, want_dx=False)["dw"], g["dw"])
+
+
+def test_refusals():
+    m = ss()
+    x, w = torch.zeros((4, 64), device="cuda"), torch.zeros((32, 64), device="cuda")
+    t = torch.zeros((4,), dtype=torch.int64, device="cuda")
+    with pytest.raises(TypeError):
+        m.xent_fwd(x, w, t.int())
+    with pytest.raises(ValueError):
+        m.xent_fwd(x, w, t[:3])
+    with pytest.raises(TypeError):
+        m.xent_fwd(x.half(), w.half(), t)
+    with pytest.raises(ValueError):
+        m.xent_fwd(x, w[:, :32], t)
+    with pytest.raises(m.SSError):
+        m.xent_fwd(x, w, t, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    loss, lse = m.xent_fwd(x, w, t)
+    with pytest.raises(m.SSError):
+        m.xent_bwd(x, w, t, lse, loss, want_dx=False, want_dw=False)
