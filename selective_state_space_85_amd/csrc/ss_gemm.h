@@ -116,16 +116,18 @@ struct MM<0> {  // fp32 operands
     static __device__ __forceinline__ T narrow(float v) { return v; }
 };
 
-// Tile of workgroup `id` of ntm x ntn.  Workgroups go to the 8 XCDs in turn, each with an L2
-// of its own: each XCD gets one contiguous run of the tile order, and the order walks columns
-// of kGroupM tiles, so that the tiles an XCD works on together share their A and B rows.
-constexpr int kXcds = 8, kGroupM = 8;
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t ntm, uint32_t ntn, uint32_t* tm, uint32_t* tn)
+// The order of the tiles.  Workgroups go to the 8 XCDs in turn, each with an L2 of its own:
+// run_of gives each XCD one contiguous run of the order, and the order walks columns of kGroupM
+// tiles, so that the tiles an XCD works on together share their A and B rows.
+constexpr uint32_t kXcds = 8, kGroupM = 8;
+__device__ __forceinline__ uint32_t run_of(uint32_t id, uint32_t total)
 {
-    const uint32_t total = ntm * ntn;
     const uint32_t per = total / kXcds, rem = total % kXcds;
     const uint32_t x = id % kXcds, i = id / kXcds;
-    const uint32_t at = x * per + (x < rem ? x : rem) + i;
+    return x * per + (x < rem ? x : rem) + i;
+}
+__device__ __forceinline__ void tile_at(uint32_t at, uint32_t ntm, uint32_t ntn, uint32_t* tm, uint32_t* tn)
+{
     const uint32_t width = kGroupM * ntn;
     const uint32_t g = at / width, in = at % width;
     const uint32_t gm = ntm - g * kGroupM < kGroupM ? ntm - g * kGroupM : kGroupM;
@@ -133,7 +135,28 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t ntm, uint32_t ntn,
     *tn = in / gm;
 }
 
+// A launch's tiles: `whole` of them as they are, and the `split` last ones of the order as two
+// halves of BM / 2 rows each.  With one large tile per CU the last round of a launch leaves CUs
+// idle; when at most half of them are left with work, halves of its tiles take half the time.
+struct TilePlan {
+    uint32_t ntm, ntn, whole, split;
+    uint32_t blocks() const { return whole + 2 * split; }
+};
+// Workgroup id's tile, and which half of it (-1: all of it).
+__device__ __forceinline__ int tile_of(uint32_t id, const TilePlan& t, uint32_t* tm, uint32_t* tn)
+{
+    if (id < t.whole) {
+        tile_at(run_of(id, t.whole), t.ntm, t.ntn, tm, tn);
+        return -1;
+    }
+    const uint32_t q = run_of(id - t.whole, 2 * t.split);
+    tile_at(t.whole + q / 2, t.ntm, t.ntn, tm, tn);
+    return int(q & 1);
+}
+
 // Geometry of a tile.  DT: 0 fp32, 1 bf16.  BM x BN over WM x WN waves.
+// With 2 x 4 waves the A tile lies in LDS as one part per wave row (A_PART rows or columns),
+// each loaded by the waves that read it.
 template <int DT_, int BM_, int BN_, int WM_, int WN_, bool A_MC_, bool B_MC_>
 struct Geo {
     static constexpr int DT = DT_, BM = BM_, BN = BN_, WM = WM_, WN = WN_;
@@ -141,19 +164,22 @@ struct Geo {
     static constexpr int BK = 8 * MM<DT>::kEpc;  // 128 bytes of k
     static constexpr int NT = 64 * WM * WN;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments per wave
-    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
-    static constexpr int LDS = 2 * STAGE;
+    static constexpr bool GROUPS = WM == 2 && WN == 4;          // the two-group schedule (see mm_loop)
+    static constexpr int A_PARTS = GROUPS ? 2 : 1, A_PART = BM / A_PARTS, A_NT = NT / A_PARTS;
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+    static constexpr int B_STAGES = GROUPS ? 3 : 2;
+    static constexpr int LDS = 2 * A_BYTES + B_STAGES * B_BYTES;  // the A buffers, then the B buffers
     static constexpr int NA = A_BYTES / 16 / NT, NB = B_BYTES / 16 / NT;  // chunks per thread
     static_assert(A_BYTES % (16 * NT) == 0 && B_BYTES % (16 * NT) == 0, "whole loads per thread");
 };
 
-// Chunk i of a thread in a tile of ROWS rows (KC) or ROWS columns (MC): which row/column group
-// and which 16-byte chunk of k (KC) or which k and chunk of columns (MC) it has to load.
-template <class G, bool MC, int ROWS>
+// Chunk i of thread `tid` of THREADS in a tile of ROWS rows (KC) or ROWS columns (MC): which
+// row and which 16-byte chunk of k (KC) or which k and chunk of columns (MC) it has to load.
+template <int DT, bool MC, int ROWS, int THREADS>
 __device__ __forceinline__ void chunk_place(int i, int tid, int* row, int* k)
 {
-    using M = MM<G::DT>;
-    const int q = i * G::NT + tid;
+    using M = MM<DT>;
+    const int q = i * THREADS + tid;
     if constexpr (!MC) {
         *row = q >> 3;
         *k = ((q & 7) ^ (*row & 7)) * M::kEpc;
@@ -166,84 +192,233 @@ __device__ __forceinline__ void chunk_place(int i, int tid, int* row, int* k)
         *row = (gran * gch + c % gch) * M::kEpc;
     }
 }
-
-// acc += A B^T over the k tile in `stage`, for the wave at (wm, wn).
 template <class G>
-__device__ __forceinline__ void mm_step(const char* stage, int wm, int wn, int lane, f32x4 (&acc)[G::FM][G::FN])
+__device__ __forceinline__ void a_place(int i, int tid, int* row, int* k)
+{
+    chunk_place<G::DT, G::A_MC, G::A_PART, G::A_NT>(i, tid % G::A_NT, row, k);
+    *row += tid / G::A_NT * G::A_PART;
+}
+template <class G>
+__device__ __forceinline__ void b_place(int i, int tid, int* row, int* k)
+{
+    chunk_place<G::DT, G::B_MC, G::BN, G::NT>(i, tid, row, k);
+}
+// Byte offset of element (row m, k) of an MC A tile.
+template <class G>
+__device__ __forceinline__ int a_mc_offset(int m, int k)
 {
     using M = MM<G::DT>;
-    const char* const at = stage;
-    const char* const bt = at + G::A_BYTES;
+    const int in = m % G::A_PART, gran = (in >> 4) ^ (M::mc_idx(k) & (G::A_PART / 16 - 1));
+    return m / G::A_PART * (G::A_PART * 128) + (k * G::A_PART + gran * 16 + (in & 15)) * int(sizeof(typename M::T));
+}
+
+// How many of the `total` k lie in k tile t, or a negative number past the last tile.
+template <int DT>
+__device__ __forceinline__ int k_left(int64_t total, int t)
+{
+    constexpr int BK = 8 * MM<DT>::kEpc;
+    const int64_t left = total - int64_t(t) * BK;
+    return left < BK ? int(left) : BK;
+}
+
+// The wave's fragments of half `kk` of the k tile in a_tile and b_tile.
+template <class G>
+__device__ __forceinline__ void mm_read(const char* a_tile, const char* b_tile, int kk, int wm, int wn, int lane,
+                                        typename MM<G::DT>::Frag (&a)[G::FM], typename MM<G::DT>::Frag (&b)[G::FN])
+{
+    using M = MM<G::DT>;
+#pragma unroll
+    for (int i = 0; i < G::FN; ++i) {
+        const int r0 = (wn * G::FN + i) * 16;
+        if constexpr (G::B_MC)
+            b[i] = M::template read_mc<G::BN>(b_tile, r0, kk, lane);
+        else
+            b[i] = M::read_kc(b_tile, r0, kk, lane);
+    }
+    // with one part per wave row, rows count from the part's first
+    const char* const part = a_tile + (G::A_PARTS > 1 ? wm * (G::A_PART * 128) : 0);
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i) {
+        const int r0 = ((G::A_PARTS > 1 ? 0 : wm * G::FM) + i) * 16;
+        if constexpr (G::A_MC)
+            a[i] = M::template read_mc<G::A_PART>(part, r0, kk, lane);
+        else
+            a[i] = M::read_kc(part, r0, kk, lane);
+    }
+}
+
+struct NoWork {
+    __device__ void operator()(int) const {}
+};
+// acc += the fragments' product; beside(i) is issued after row i's products.
+template <class G, class Beside = NoWork>
+__device__ __forceinline__ void mm_mul(const typename MM<G::DT>::Frag (&a)[G::FM],
+                                       const typename MM<G::DT>::Frag (&b)[G::FN], f32x4 (&acc)[G::FM][G::FN],
+                                       Beside beside = Beside())
+{
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) acc[i][j] = MM<G::DT>::mul(b[j], a[i], acc[i][j]);
+        beside(i);
+    }
+}
+
+// acc += A B^T over the k tile in a_tile and b_tile, for the wave at (wm, wn).
+template <class G>
+__device__ __forceinline__ void mm_step(const char* a_tile, const char* b_tile, int wm, int wn, int lane, f32x4 (&acc)[G::FM][G::FN])
+{
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-        typename M::Frag a[G::FM], b[G::FN];
-#pragma unroll
-        for (int i = 0; i < G::FN; ++i) {
-            const int r0 = (wn * G::FN + i) * 16;
-            if constexpr (G::B_MC)
-                b[i] = M::template read_mc<G::BN>(bt, r0, kk, lane);
-            else
-                b[i] = M::read_kc(bt, r0, kk, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < G::FM; ++i) {
-            const int r0 = (wm * G::FM + i) * 16;
-            if constexpr (G::A_MC)
-                a[i] = M::template read_mc<G::BM>(at, r0, kk, lane);
-            else
-                a[i] = M::read_kc(at, r0, kk, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < G::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < G::FN; ++j) acc[i][j] = M::mul(b[j], a[i], acc[i][j]);
+        typename MM<G::DT>::Frag a[G::FM], b[G::FN];
+        mm_read<G>(a_tile, b_tile, kk, wm, wn, lane, a, b);
+        mm_mul<G>(a, b, acc);
     }
+}
+
+// One phase of the two-group schedule ends: nothing moves across, in the compiler or the wave.
+__device__ __forceinline__ void phase_end()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// all but the latest N loads of this wave have arrived
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 // The main loop: acc += A B^T over `tiles` k tiles.  a_lane / b_lane: this thread's chunk
 // addresses at k = 0; Prob::a_off(t) / b_off(t): bytes to add for k tile t; Prob::valid(t): how
-// many k of tile t exist (the others read zeros on both sides).
+// many k of tile t exist (none past the last tile); the others read zeros on both sides.
 template <class G, class Prob>
 __device__ __forceinline__ void mm_loop(const Prob& p, const char* const (&a_lane)[G::NA],
                                         const char* const (&b_lane)[G::NB], int tiles, char* lds,
                                         f32x4 (&acc)[G::FM][G::FN])
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform, and known to be
     const int wm = wave / G::WN, wn = wave % G::WN;
 
-    auto issue = [&](int t, char* stage) {
-        const int64_t ao = p.a_off(t), bo = p.b_off(t);
+    // this wave's first lane's place: the hardware adds 16 bytes per lane
+    char* const a_dst = lds + (G::A_PARTS > 1 ? wm * (G::A_PART * 128) + wn * 1024 : wave * 1024);
+    char* const b_dst = lds + 2 * G::A_BYTES + wave * 1024;
+    const char* const zero = reinterpret_cast<const char*>(g_zero_chunk);
+    // this thread's source addresses of k tile t
+    auto a_src = [&](int t, const char* (&src)[G::NA]) {
+        const int64_t off = p.a_off(t);
         const int valid = p.valid(t);
-        // this wave's first lane's place in the tile: the hardware adds 16 bytes per lane
-        char* const dst = stage + wave * 1024;
-        if (valid >= G::BK) {
 #pragma unroll
-            for (int i = 0; i < G::NA; ++i) load_to_lds(a_lane[i] + ao, dst + i * (G::NT * 16));
-#pragma unroll
-            for (int i = 0; i < G::NB; ++i) load_to_lds(b_lane[i] + bo, dst + G::A_BYTES + i * (G::NT * 16));
-        } else {
+        for (int i = 0; i < G::NA; ++i) src[i] = a_lane[i] + off;
+        if (valid < G::BK) {
             int row, k;
 #pragma unroll
             for (int i = 0; i < G::NA; ++i) {
-                chunk_place<G, G::A_MC, G::BM>(i, tid, &row, &k);
-                load_to_lds(k < valid ? a_lane[i] + ao : reinterpret_cast<const char*>(g_zero_chunk),
-                            dst + i * (G::NT * 16));
-            }
-#pragma unroll
-            for (int i = 0; i < G::NB; ++i) {
-                chunk_place<G, G::B_MC, G::BN>(i, tid, &row, &k);
-                load_to_lds(k < valid ? b_lane[i] + bo : reinterpret_cast<const char*>(g_zero_chunk),
-                            dst + G::A_BYTES + i * (G::NT * 16));
+                a_place<G>(i, tid, &row, &k);
+                if (k >= valid) src[i] = zero;
             }
         }
     };
+    auto b_src = [&](int t, const char* (&src)[G::NB]) {
+        const int64_t off = p.b_off(t);
+        const int valid = p.valid(t);
+#pragma unroll
+        for (int i = 0; i < G::NB; ++i) src[i] = b_lane[i] + off;
+        if (valid < G::BK) {
+            int row, k;
+#pragma unroll
+            for (int i = 0; i < G::NB; ++i) {
+                b_place<G>(i, tid, &row, &k);
+                if (k >= valid) src[i] = zero;
+            }
+        }
+    };
+    const char* as[G::NA];
+    const char* bs[G::NB];
+    auto load_a = [&](int buf, int i) { load_to_lds(as[i], a_dst + buf * G::A_BYTES + i * (G::A_NT * 16)); };
+    auto load_b = [&](int buf, int i) { load_to_lds(bs[i], b_dst + buf * G::B_BYTES + i * (G::NT * 16)); };
+    auto issue_a = [&](int t, int buf) {
+        a_src(t, as);
+#pragma unroll
+        for (int i = 0; i < G::NA; ++i) load_a(buf, i);
+    };
+    auto issue_b = [&](int t, int buf) {
+        b_src(t, bs);
+#pragma unroll
+        for (int i = 0; i < G::NB; ++i) load_b(buf, i);
+    };
 
-    issue(0, lds);
+    if constexpr (G::GROUPS) {
+        static_assert(G::FM == 2 * G::NA && G::NB <= G::FM, "the loads' places among the products");
+        // Two groups of four waves (one of each on every SIMD), one phase apart: while one reads
+        // its fragments, the other has the matrix cores.  A k tile is four phases of each group:
+        // fragments of its first half, products, fragments of its second half, products.  Loads
+        // are issued among the products.  In phases of the early group (the late one is a phase
+        // behind), tile t is read from phase 4t to 4t + 3, the late group's last, and every read
+        // has been waited for when its phase ends.
+        //   B has three buffers: tile t + 2's was last read, with tile t - 1, in phase 4t - 1, and
+        //   takes its loads in phase 4t + 1 (early) and 4t + 2 (late).
+        //   A has two: tile t + 2's was last read, with tile t, by the wave row that loads it, in
+        //   phase 4t + 2 (4t + 3), and takes its loads in phase 4t + 3 (4t + 4).
+        // Before the end of phase 4t + 3 each wave waits for its own loads of tile t + 1; those
+        // issued after them, of B (and A) of tile t + 2, stay under way.  Tile t + 1 is read from
+        // phase 4t + 4 on.
+        const bool late = wm != 0;
+        issue_b(0, 0);
+        issue_a(0, 0);
+        issue_b(1, 1);
+        issue_a(1, 1);
+        wait_loads<G::NA + G::NB>();
+        phase_end();
+        if (late) phase_end();
+        typename MM<G::DT>::Frag a[G::FM], b[G::FN];
+        int b_buf = 0, b_next = 2;
+        for (int t = 0; t < tiles; ++t) {
+            const char* const a_tile = lds + (t & 1) * G::A_BYTES;
+            const char* const b_tile = lds + 2 * G::A_BYTES + b_buf * G::B_BYTES;
+            mm_read<G>(a_tile, b_tile, 0, wm, wn, lane, a, b);
+            b_src(t + 2, bs);
+            wait_lds_reads();
+            phase_end();
+            __builtin_amdgcn_s_setprio(1);
+            mm_mul<G>(a, b, acc, [&](int i) {
+                constexpr int every = G::FM / G::NB;
+                if (i % every == every - 1) load_b(b_next, i / every);
+            });
+            __builtin_amdgcn_s_setprio(0);
+            phase_end();
+            mm_read<G>(a_tile, b_tile, 1, wm, wn, lane, a, b);
+            a_src(t + 2, as);
+            wait_lds_reads();
+            if (late) wait_loads<G::NB>();
+            phase_end();
+            __builtin_amdgcn_s_setprio(1);
+            mm_mul<G>(a, b, acc, [&](int i) {
+                if (i & 1) load_a(t & 1, i >> 1);
+            });
+            __builtin_amdgcn_s_setprio(0);
+            if (!late) wait_loads<G::NA + G::NB>();
+            phase_end();
+            b_buf = b_buf == 2 ? 0 : b_buf + 1;
+            b_next = b_next == 2 ? 0 : b_next + 1;
+        }
+        wait_loads<0>();  // the loads past the last tile: LDS is free after the loop
+        if (!late) phase_end();
+        return;
+    }
+    issue_a(0, 0);
+    issue_b(0, 0);
     for (int t = 0; t < tiles; ++t) {
         // tile t has arrived for every wave, and every wave has finished reading tile t-1
         __syncthreads();
-        if (t + 1 < tiles) issue(t + 1, lds + ((t + 1) & 1) * G::STAGE);
-        mm_step<G>(lds + (t & 1) * G::STAGE, wm, wn, lane, acc);
+        if (t + 1 < tiles) {
+            issue_a(t + 1, (t + 1) & 1);
+            issue_b(t + 1, (t + 1) & 1);
+        }
+        mm_step<G>(lds + (t & 1) * G::A_BYTES, lds + 2 * G::A_BYTES + (t & 1) * G::B_BYTES, wm, wn, lane, acc);
     }
 }
 
@@ -256,18 +431,19 @@ __device__ __forceinline__ void mm_loop(const Prob& p, const char* const (&a_lan
 template <class G, class Prob>
 __device__ __forceinline__ void mm_tile(const Prob& p, char* lds)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform, and known to be
     const char* a_lane[G::NA];
     const char* b_lane[G::NB];
     int row, k;
 #pragma unroll
     for (int i = 0; i < G::NA; ++i) {
-        chunk_place<G, G::A_MC, G::BM>(i, tid, &row, &k);
+        a_place<G>(i, tid, &row, &k);
         a_lane[i] = p.a_chunk(row, k);
     }
 #pragma unroll
     for (int i = 0; i < G::NB; ++i) {
-        chunk_place<G, G::B_MC, G::BN>(i, tid, &row, &k);
+        b_place<G>(i, tid, &row, &k);
         b_lane[i] = p.b_chunk(row, k);
     }
     f32x4 acc[G::FM][G::FN];
@@ -277,6 +453,52 @@ __device__ __forceinline__ void mm_tile(const Prob& p, char* lds)
         for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     mm_loop<G>(p, a_lane, b_lane, p.tiles, lds, acc);
     p.template finish<G>(acc, lds, wave / G::WN, wave % G::WN, lane);
+}
+
+// ---- choosing tiles (host) ---------------------------------------------------------------------
+
+// The tiles of each element type: bf16 has a large one (one workgroup of 8 waves per CU, LDS
+// full) and its half, and a small one (4 waves, two workgroups per CU) for launches with too
+// little work for the large ones.  fp32's products are a sixteenth as fast, so that the small
+// one feeds them at any size.
+template <int DT>
+struct Tiles;
+template <>
+struct Tiles<1> {
+    template <bool AM, bool BM_>
+    using Large = Geo<1, 256, 256, 2, 4, AM, BM_>;
+    template <bool AM, bool BM_>
+    using Half = Geo<1, 128, 256, 2, 4, AM, BM_>;
+    template <bool AM, bool BM_>
+    using Small = Geo<1, 128, 128, 2, 2, AM, BM_>;
+};
+template <>
+struct Tiles<0> {
+    template <bool AM, bool BM_>
+    using Small = Geo<0, 128, 128, 2, 2, AM, BM_>;
+};
+
+constexpr uint32_t kCUs = 256;
+
+inline uint32_t up(int64_t a, int64_t b) { return uint32_t((a + b - 1) / b); }
+
+// `before`: workgroups of the same launch ahead of these tiles.
+inline TilePlan plan_tiles(uint32_t ntm, uint32_t ntn, bool can_split, uint32_t before = 0)
+{
+    const uint32_t total = ntm * ntn, last = (before + total) % kCUs;
+    const uint32_t split = can_split && last <= kCUs / 2 && last < total ? last : 0;
+    return {ntm, ntn, total - split, split};
+}
+
+// Whether the large tile is the faster: a round of the chip is 256 large tiles or 512 small ones;
+// a small tile is a quarter of the work at 0.78 of the large one's rate (8192 x 8192 x 4096: 1006
+// against 1288 TFLOP/s), so a round of them takes 0.64 of a round of large ones.  A last round of
+// at most half the large tiles is taken in halves (see TilePlan).
+inline bool large_tile(int64_t large, int64_t small)
+{
+    const int64_t rest = large % kCUs;
+    const double rl = double(large / kCUs) + (rest == 0 ? 0.0 : rest <= kCUs / 2 ? 0.55 : 1.0);
+    return rl <= 0.64 * double((small + 511) / 512);
 }
 
 }  // namespace

@@ -116,7 +116,7 @@ struct GluProb {
     }
     __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
     __device__ int64_t b_off(int t) const { return int64_t(t) * 128; }
-    __device__ int valid(int t) const { return int(a.k_pad - int64_t(t) * (8 * MM<DT>::kEpc)); }
+    __device__ int valid(int t) const { return k_left<DT>(a.k_pad, t); }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -158,15 +158,21 @@ struct GluProb {
     }
 };
 
-template <class G, int ACT, bool BACK>
-__global__ __launch_bounds__(G::NT) void glu_tile_kernel(GluArgs a, uint32_t ntm, uint32_t ntf, bool vec)
+// H: the geometry of half a tile (G itself where tiles are never halved)
+template <class G, class H, int ACT, bool BACK>
+__global__ __launch_bounds__(G::NT) void glu_tile_kernel(GluArgs a, TilePlan plan, bool vec)
 {
     __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
     uint32_t tm, tf;
-    tile_of(blockIdx.x, ntm, ntf, &tm, &tf);
-    const GluProb<G::DT, ACT, BACK> p{a, int64_t(tm) * G::BM, int64_t(tf) * (G::BN / 2),
-                                      int((a.k_pad + G::BK - 1) / G::BK), vec};
-    mm_tile<G>(p, lds);
+    const int half = tile_of(blockIdx.x, plan, &tm, &tf);
+    GluProb<G::DT, ACT, BACK> p{a, int64_t(tm) * G::BM, int64_t(tf) * (G::BN / 2),
+                                int((a.k_pad + G::BK - 1) / G::BK), vec};
+    if (half < 0) {
+        mm_tile<G>(p, lds);
+        return;
+    }
+    p.m0 += half * H::BM;
+    if (p.m0 < a.m) mm_tile<H>(p, lds);
 }
 
 // ---- dx = [dg du] [Wg; Wu] -----------------------------------------------------------------
@@ -203,7 +209,7 @@ struct GluDxProb {
         const int64_t row = int64_t(BK) * a.w_ld * int64_t(sizeof(T));
         return t < half ? t * row : (t - half) * row + second;
     }
-    __device__ int valid(int t) const { return int(a.f - int64_t(t < half ? t : t - half) * BK); }
+    __device__ int valid(int t) const { return k_left<DT>(a.f, t < half ? t : t - half); }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -247,11 +253,7 @@ struct GluDwProb {
     }
     __device__ int64_t a_off(int t) const { return int64_t(t) * BK * 2 * a.f_pad * int64_t(sizeof(T)); }
     __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
-    __device__ int valid(int t) const
-    {
-        const int64_t left = a.m - int64_t(t) * BK;
-        return left < BK ? int(left) : BK;
-    }
+    __device__ int valid(int t) const { return k_left<DT>(a.m, t); }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -273,24 +275,32 @@ struct GluDwProb {
     }
 };
 
-// Both sets of tiles; ids below n_dx are dx's.
-template <class GX, class GW>
-__global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, uint32_t n_dx, uint32_t xm, uint32_t xn,
-                                                          uint32_t wm, uint32_t wn, bool vec_x, bool vec_w)
+// Both sets of tiles: dw's after dx's.  HX, HW: their halves.
+template <class GX, class HX, class GW, class HW>
+__global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, TilePlan px, TilePlan pw, bool vec_x, bool vec_w)
 {
-    static_assert(GX::NT == GW::NT, "one launch");
-    __shared__ __attribute__((aligned(1024))) char lds[GX::LDS > GW::LDS ? GX::LDS : GW::LDS];
+    static_assert(GX::NT == GW::NT && GX::LDS == GW::LDS, "one launch");
+    __shared__ __attribute__((aligned(1024))) char lds[GX::LDS];
     uint32_t tm, tn;
-    if (blockIdx.x < n_dx) {
-        tile_of(blockIdx.x, xm, xn, &tm, &tn);
+    if (blockIdx.x < px.whole + 2 * px.split) {
+        const int h = tile_of(blockIdx.x, px, &tm, &tn);
         const int half = int((a.f + GX::BK - 1) / GX::BK);
-        const GluDxProb<GX::DT> p{a, int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, half, 2 * half, vec_x};
-        mm_tile<GX>(p, lds);
+        GluDxProb<GX::DT> p{a, int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, half, 2 * half, vec_x};
+        if (h < 0) {
+            mm_tile<GX>(p, lds);
+            return;
+        }
+        p.m0 += h * HX::BM;
+        if (p.m0 < a.m) mm_tile<HX>(p, lds);
     } else {
-        tile_of(blockIdx.x - n_dx, wm, wn, &tm, &tn);
-        const GluDwProb<GW::DT> p{a, int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, int((a.m + GW::BK - 1) / GW::BK),
-                                  vec_w};
-        mm_tile<GW>(p, lds);
+        const int h = tile_of(blockIdx.x - (px.whole + 2 * px.split), pw, &tm, &tn);
+        GluDwProb<GW::DT> p{a, int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, int((a.m + GW::BK - 1) / GW::BK), vec_w};
+        if (h < 0) {
+            mm_tile<GW>(p, lds);
+            return;
+        }
+        p.m0 += h * HW::BM;
+        if (p.m0 < 2 * a.f_pad) mm_tile<HW>(p, lds);
     }
 }
 
@@ -398,50 +408,25 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const typename MM<DT>::T*
 
 // ---- launches -----------------------------------------------------------------------------------
 
-template <int DT>
-struct Tiles;
-template <>
-struct Tiles<1> {
-    template <bool AM, bool BM_>
-    using Large = Geo<1, 256, 256, 2, 4, AM, BM_>;
-    template <bool AM, bool BM_>
-    using Small = Geo<1, 128, 128, 2, 2, AM, BM_>;
-};
-template <>
-struct Tiles<0> {
-    template <bool AM, bool BM_>
-    using Large = Geo<0, 128, 128, 2, 2, AM, BM_>;
-    template <bool AM, bool BM_>
-    using Small = Geo<0, 128, 128, 2, 2, AM, BM_>;
-};
-
-uint32_t up(int64_t a, int64_t b) { return uint32_t((a + b - 1) / b); }
-
-// Which tile: 256x256 (one workgroup per CU) or 128x128 (two per CU).  A round of the chip is
-// 256 large tiles or 512 small ones; the small tile does a quarter of the work at 0.88 of the
-// large one's rate, so a small round costs 0.57 of a large one.
-bool large_tile(int64_t large, int64_t small)
-{
-    const double rl = double((large + 255) / 256), rs = double((small + 511) / 512);
-    return rl <= 0.57 * rs;
-}
-
-template <class G, int ACT, bool BACK>
+template <class G, class H, int ACT, bool BACK>
 hipError_t launch_glu_tile(const GluArgs& a, bool vec, hipStream_t s)
 {
-    const uint32_t ntm = up(a.m, G::BM), ntf = up(BACK ? a.f_pad : a.f, G::BN / 2);
-    glu_tile_kernel<G, ACT, BACK><<<dim3(ntm * ntf), dim3(G::NT), 0, s>>>(a, ntm, ntf, vec);
+    const TilePlan plan = plan_tiles(up(a.m, G::BM), up(BACK ? a.f_pad : a.f, G::BN / 2), H::BM < G::BM);
+    glu_tile_kernel<G, H, ACT, BACK><<<dim3(plan.blocks()), dim3(G::NT), 0, s>>>(a, plan, vec);
     return hipGetLastError();
 }
 
 template <int DT, int ACT, bool BACK>
 hipError_t launch_glu_gu(const GluArgs& a, bool vec, hipStream_t s)
 {
-    using L = typename Tiles<DT>::template Large<false, false>;
-    using S = typename Tiles<DT>::template Small<false, false>;
-    if (DT == 1 && large_tile(int64_t(up(a.m, 256)) * up(a.f, 128), int64_t(up(a.m, 128)) * up(a.f, 64)))
-        return launch_glu_tile<L, ACT, BACK>(a, vec, s);
-    return launch_glu_tile<S, ACT, BACK>(a, vec, s);
+    using T = Tiles<DT>;
+    if constexpr (DT == 1) {
+        if (large_tile(int64_t(up(a.m, 256)) * up(a.f, 128), int64_t(up(a.m, 128)) * up(a.f, 64)))
+            return launch_glu_tile<typename T::template Large<false, false>, typename T::template Half<false, false>, ACT,
+                                   BACK>(a, vec, s);
+    }
+    using S = typename T::template Small<false, false>;
+    return launch_glu_tile<S, S, ACT, BACK>(a, vec, s);
 }
 
 template <int DT, int ACT>
@@ -473,14 +458,15 @@ hipError_t glu_fwd_dt(const GluArgs& a, hipStream_t s)
                              : launch_glu_gu<DT, kActGelu, false>(a, vec, s);
 }
 
-template <class GX, class GW>
+template <class GX, class HX, class GW, class HW>
 hipError_t launch_glu_grad(const GluArgs& a, hipStream_t s)
 {
-    const uint32_t xm = up(a.m, GX::BM), xn = up(a.k, GX::BN);
-    const uint32_t wm = up(2 * a.f_pad, GW::BM), wn = up(a.k, GW::BN);
-    const uint32_t n_dx = a.dx ? xm * xn : 0, n_dw = a.dwg ? wm * wn : 0;
+    const bool can = HX::BM < GX::BM;
+    TilePlan px{0, 0, 0, 0}, pw{0, 0, 0, 0};
+    if (a.dx) px = plan_tiles(up(a.m, GX::BM), up(a.k, GX::BN), can && !a.dwg);  // only the last tiles are halved
+    if (a.dwg) pw = plan_tiles(up(2 * a.f_pad, GW::BM), up(a.k, GW::BN), can, px.whole);
     const bool vx = vec_rows(a.dx, a.k, GX::DT), vw = vec_rows(a.dwg, a.k, GX::DT) && vec_rows(a.dwu, a.k, GX::DT);
-    glu_grad_kernel<GX, GW><<<dim3(n_dx + n_dw), dim3(GX::NT), 0, s>>>(a, n_dx, xm, xn, wm, wn, vx, vw);
+    glu_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() + pw.blocks()), dim3(GX::NT), 0, s>>>(a, px, pw, vx, vw);
     return hipGetLastError();
 }
 
@@ -496,9 +482,14 @@ hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
                           (a.dwg ? int64_t(up(2 * a.f_pad, 256)) * up(a.k, 256) : 0);
     const int64_t small = (a.dx ? int64_t(up(a.m, 128)) * up(a.k, 128) : 0) +
                           (a.dwg ? int64_t(up(2 * a.f_pad, 128)) * up(a.k, 128) : 0);
-    if (DT == 1 && large_tile(large, small))
-        return launch_glu_grad<typename T::template Large<false, true>, typename T::template Large<true, true>>(a, s);
-    return launch_glu_grad<typename T::template Small<false, true>, typename T::template Small<true, true>>(a, s);
+    if constexpr (DT == 1) {
+        if (large_tile(large, small))
+            return launch_glu_grad<typename T::template Large<false, true>, typename T::template Half<false, true>,
+                                   typename T::template Large<true, true>, typename T::template Half<true, true>>(a, s);
+    }
+    using SX = typename T::template Small<false, true>;
+    using SW = typename T::template Small<true, true>;
+    return launch_glu_grad<SX, SX, SW, SW>(a, s);
 }
 
 }  // namespace

@@ -50,7 +50,7 @@ struct XentLogits {
     }
     __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
     __device__ int64_t b_off(int t) const { return int64_t(t) * 128; }
-    __device__ int valid(int t) const { return int(a.d_pad - int64_t(t) * (8 * MM<DT>::kEpc)); }
+    __device__ int valid(int t) const { return k_left<DT>(a.d_pad, t); }
 };
 
 // ---- forward -------------------------------------------------------------------------------
@@ -124,14 +124,20 @@ struct XentFwdProb : XentLogits<DT> {
     }
 };
 
-template <class G>
-__global__ __launch_bounds__(G::NT) void xent_fwd_kernel(XentArgs a, uint32_t ntm, uint32_t ntn)
+// H: the geometry of half a tile (G itself where tiles are never halved)
+template <class G, class H>
+__global__ __launch_bounds__(G::NT) void xent_fwd_kernel(XentArgs a, TilePlan plan)
 {
     __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
     uint32_t tm, tn;
-    tile_of(blockIdx.x, ntm, ntn, &tm, &tn);
-    const XentFwdProb<G::DT> p{{a, int64_t(tm) * G::BM, int64_t(tn) * G::BN, int((a.d_pad + G::BK - 1) / G::BK)}};
-    mm_tile<G>(p, lds);
+    const int half = tile_of(blockIdx.x, plan, &tm, &tn);
+    XentFwdProb<G::DT> p{{a, int64_t(tm) * G::BM, int64_t(tn) * G::BN, int((a.d_pad + G::BK - 1) / G::BK)}};
+    if (half < 0) {
+        mm_tile<G>(p, lds);
+        return;
+    }
+    p.m0 += half * H::BM;
+    if (p.m0 < a.n) mm_tile<H>(p, lds);
 }
 
 // The pairs of a row, joined: 16 rows per workgroup, 16 threads a row.
@@ -195,16 +201,20 @@ struct XentDlProb : XentLogits<DT> {
     }
 };
 
-template <class G>
-__global__ __launch_bounds__(G::NT) void xent_dl_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad,
-                                                        uint32_t ntm, uint32_t ntn)
+template <class G, class H>
+__global__ __launch_bounds__(G::NT) void xent_dl_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad, TilePlan plan)
 {
     __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
     uint32_t tm, tn;
-    tile_of(blockIdx.x, ntm, ntn, &tm, &tn);
-    const XentDlProb<G::DT> p{
+    const int half = tile_of(blockIdx.x, plan, &tm, &tn);
+    XentDlProb<G::DT> p{
         {a, int64_t(tm) * G::BM, v0 + int64_t(tn) * G::BN, int((a.d_pad + G::BK - 1) / G::BK)}, v0, cols, pad};
-    mm_tile<G>(p, lds);
+    if (half < 0) {
+        mm_tile<G>(p, lds);
+        return;
+    }
+    p.m0 += half * H::BM;
+    if (p.m0 < a.n) mm_tile<H>(p, lds);
 }
 
 // The tokens whose targets lie in each group of kXentCols columns, in order.
@@ -240,7 +250,7 @@ struct XentDxProb {
     const XentArgs& a;
     int64_t m0, n0, v0, cols, pad;
     int tiles;
-    bool first, last, vec;
+    bool first, last;
 
     __device__ const char* a_chunk(int row, int k) const
     {
@@ -256,11 +266,7 @@ struct XentDxProb {
     }
     __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
     __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.w_ld * int64_t(sizeof(T)); }
-    __device__ int valid(int t) const
-    {
-        const int64_t left = cols - int64_t(t) * BK;
-        return left < BK ? int(left) : BK;
-    }
+    __device__ int valid(int t) const { return k_left<DT>(cols, t); }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -316,11 +322,7 @@ struct XentDwProb {
     }
     __device__ int64_t a_off(int t) const { return int64_t(t) * BK * pad * int64_t(sizeof(T)); }
     __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
-    __device__ int valid(int t) const
-    {
-        const int64_t left = a.n - int64_t(t) * BK;
-        return left < BK ? int(left) : BK;
-    }
+    __device__ int valid(int t) const { return k_left<DT>(a.n, t); }
 
     // the target entries' remainders
     template <class G>
@@ -342,22 +344,21 @@ struct XentDwProb {
                 int col, k;
 #pragma unroll
                 for (int i = 0; i < G::NB; ++i) {
-                    chunk_place<G, G::B_MC, G::BN>(i, tid, &col, &k);
+                    b_place<G>(i, tid, &col, &k);
                     int64_t c = n0 + col;
                     c = c < a.d_pad ? c : a.d_pad - M::kEpc;
                     const char* src = reinterpret_cast<const char*>(g_zero_chunk);
                     if (at + k < count) src = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + list[at + k] * a.x_ld + c);
-                    load_to_lds(src, lds + G::A_BYTES + (tid >> 6) * 1024 + i * (G::NT * 16));
+                    load_to_lds(src, lds + 2 * G::A_BYTES + (tid >> 6) * 1024 + i * (G::NT * 16));
                 }
                 __syncthreads();
                 if (tid < BK && at + tid < count) {
                     const int tok = list[at + tid];
                     const int m = int(a.target[tok] - v0 - m0);
-                    const int gran = (m >> 4) ^ (M::mc_idx(tid) & (G::BM / 16 - 1));
-                    reinterpret_cast<T*>(lds)[tid * G::BM + gran * 16 + (m & 15)] = M::narrow(a.lo[tok]);
+                    *reinterpret_cast<T*>(lds + a_mc_offset<G>(m, tid)) = M::narrow(a.lo[tok]);
                 }
                 __syncthreads();
-                mm_step<G>(lds, wm, wn, lane, acc);
+                mm_step<G>(lds, lds + 2 * G::A_BYTES, wm, wn, lane, acc);
             }
         }
     }
@@ -390,100 +391,124 @@ struct XentDwProb {
     }
 };
 
-template <class GX, class GW>
-__global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad,
-                                                           uint32_t n_dx, uint32_t xm, uint32_t xn, uint32_t wm,
-                                                           uint32_t wn, bool first, bool last, bool vec_w)
+// Both sets of tiles: dw's after dx's.  HX, HW: their halves.
+template <class GX, class HX, class GW, class HW>
+__global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad, TilePlan px,
+                                                           TilePlan pw, bool first, bool last, bool vec_w)
 {
-    static_assert(GX::NT == GW::NT, "one launch");
-    __shared__ __attribute__((aligned(1024))) char lds[GX::LDS > GW::LDS ? GX::LDS : GW::LDS];
+    static_assert(GX::NT == GW::NT && GX::LDS == GW::LDS, "one launch");
+    __shared__ __attribute__((aligned(1024))) char lds[GX::LDS];
     uint32_t tm, tn;
-    if (blockIdx.x < n_dx) {
-        tile_of(blockIdx.x, xm, xn, &tm, &tn);
-        const XentDxProb<GX::DT> p{a,   int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, v0,   cols,
-                                   pad, int((cols + GX::BK - 1) / GX::BK), first, last, false};
-        mm_tile<GX>(p, lds);
+    if (blockIdx.x < px.whole + 2 * px.split) {
+        const int h = tile_of(blockIdx.x, px, &tm, &tn);
+        XentDxProb<GX::DT> p{a,   int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, v0,   cols,
+                             pad, int((cols + GX::BK - 1) / GX::BK), first, last};
+        if (h < 0) {
+            mm_tile<GX>(p, lds);
+            return;
+        }
+        p.m0 += h * HX::BM;
+        if (p.m0 < a.n) mm_tile<HX>(p, lds);
     } else {
-        tile_of(blockIdx.x - n_dx, wm, wn, &tm, &tn);
-        const XentDwProb<GW::DT> p{a,   int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, v0, cols,
-                                   pad, int((a.n + GW::BK - 1) / GW::BK), vec_w};
-        mm_tile<GW>(p, lds);
+        const int h = tile_of(blockIdx.x - (px.whole + 2 * px.split), pw, &tm, &tn);
+        XentDwProb<GW::DT> p{a,   int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, v0, cols,
+                             pad, int((a.n + GW::BK - 1) / GW::BK), vec_w};
+        if (h < 0) {
+            mm_tile<GW>(p, lds);
+            return;
+        }
+        p.m0 += h * HW::BM;
+        if (p.m0 < cols) mm_tile<HW>(p, lds);
     }
 }
 
 // ---- launches --------------------------------------------------------------------------------
 
-template <int DT>
-struct Tiles;
-template <>
-struct Tiles<1> {
-    template <bool AM, bool BM_>
-    using Large = Geo<1, 256, 256, 2, 4, AM, BM_>;
-    template <bool AM, bool BM_>
-    using Small = Geo<1, 128, 128, 2, 2, AM, BM_>;
-};
-template <>
-struct Tiles<0> {
-    template <bool AM, bool BM_>
-    using Large = Geo<0, 128, 128, 2, 2, AM, BM_>;
-    template <bool AM, bool BM_>
-    using Small = Geo<0, 128, 128, 2, 2, AM, BM_>;
-};
-
-uint32_t up(int64_t a, int64_t b) { return uint32_t((a + b - 1) / b); }
-
-// as in ss_glu.hip: a round of 512 small tiles costs 0.57 of a round of 256 large ones
-bool large_tile(int64_t large, int64_t small)
-{
-    const double rl = double((large + 255) / 256), rs = double((small + 511) / 512);
-    return rl <= 0.57 * rs;
-}
-
-template <class G>
+template <class G, class H>
 hipError_t fwd_tiles(const XentArgs& a, hipStream_t s)
 {
-    const uint32_t ntm = up(a.n, G::BM), ntn = up(a.v, G::BN);
-    xent_fwd_kernel<G><<<dim3(ntm * ntn), dim3(G::NT), 0, s>>>(a, ntm, ntn);
+    const TilePlan plan = plan_tiles(up(a.n, G::BM), up(a.v, G::BN), H::BM < G::BM);
+    xent_fwd_kernel<G, H><<<dim3(plan.blocks()), dim3(G::NT), 0, s>>>(a, plan);
     return hipGetLastError();
+}
+
+template <int DT>
+hipError_t fwd_tiles_dt(const XentArgs& a, hipStream_t s)
+{
+    using T = Tiles<DT>;
+    if constexpr (DT == 1) {
+        if (large_tile(int64_t(up(a.n, 256)) * up(a.v, 256), int64_t(up(a.n, 128)) * up(a.v, 128)))
+            return fwd_tiles<typename T::template Large<false, false>, typename T::template Half<false, false>>(a, s);
+    }
+    using S = typename T::template Small<false, false>;
+    return fwd_tiles<S, S>(a, s);
 }
 
 template <int DT>
 hipError_t fwd_dt(const XentArgs& a, hipStream_t s)
 {
-    using T = Tiles<DT>;
-    hipError_t e;
-    if (DT == 1 && large_tile(int64_t(up(a.n, 256)) * up(a.v, 256), int64_t(up(a.n, 128)) * up(a.v, 128)))
-        e = fwd_tiles<typename T::template Large<false, false>>(a, s);
-    else
-        e = fwd_tiles<typename T::template Small<false, false>>(a, s);
+    const hipError_t e = fwd_tiles_dt<DT>(a, s);
     if (e != hipSuccess) return e;
     xent_join_kernel<<<dim3(up(a.n, kJoinRows)), dim3(kJoinRows * kJoinLanes), 0, s>>>(a, int64_t(up(a.v, kXentCols)));
     return hipGetLastError();
 }
 
-template <class G>
+template <class G, class H>
 hipError_t dl_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
-    const uint32_t ntm = up(a.n, G::BM), ntn = up(pad, G::BN);
-    xent_dl_kernel<G><<<dim3(ntm * ntn), dim3(G::NT), 0, s>>>(a, v0, cols, pad, ntm, ntn);
+    const TilePlan plan = plan_tiles(up(a.n, G::BM), up(pad, G::BN), H::BM < G::BM);
+    xent_dl_kernel<G, H><<<dim3(plan.blocks()), dim3(G::NT), 0, s>>>(a, v0, cols, pad, plan);
     return hipGetLastError();
 }
 
-template <class GX, class GW>
+template <int DT>
+hipError_t dl_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
+{
+    using T = Tiles<DT>;
+    if constexpr (DT == 1) {
+        if (large_tile(int64_t(up(a.n, 256)) * up(pad, 256), int64_t(up(a.n, 128)) * up(pad, 128)))
+            return dl_tiles<typename T::template Large<false, false>, typename T::template Half<false, false>>(
+                a, v0, cols, pad, s);
+    }
+    using S = typename T::template Small<false, false>;
+    return dl_tiles<S, S>(a, v0, cols, pad, s);
+}
+
+template <class GX, class HX, class GW, class HW>
 hipError_t grad_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
-    const uint32_t xm = up(a.n, GX::BM), xn = up(a.d, GX::BN), wm = up(cols, GW::BM), wn = up(a.d, GW::BN);
-    const uint32_t n_dx = a.dx ? xm * xn : 0, n_dw = a.dw ? wm * wn : 0;
+    const bool can = HX::BM < GX::BM;
+    TilePlan px{0, 0, 0, 0}, pw{0, 0, 0, 0};
+    if (a.dx) px = plan_tiles(up(a.n, GX::BM), up(a.d, GX::BN), can && !a.dw);  // only the last tiles are halved
+    if (a.dw) pw = plan_tiles(up(cols, GW::BM), up(a.d, GW::BN), can, px.whole);
     const bool vec = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dw) % (GX::DT == 0 ? 16 : 8) == 0;
-    xent_grad_kernel<GX, GW><<<dim3(n_dx + n_dw), dim3(GX::NT), 0, s>>>(a, v0, cols, pad, n_dx, xm, xn, wm, wn, v0 == 0,
-                                                                       v0 + cols == a.v, vec);
+    xent_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() + pw.blocks()), dim3(GX::NT), 0, s>>>(
+        a, v0, cols, pad, px, pw, v0 == 0, v0 + cols == a.v, vec);
     return hipGetLastError();
+}
+
+template <int DT>
+hipError_t grad_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
+{
+    using T = Tiles<DT>;
+    const int64_t large = (a.dx ? int64_t(up(a.n, 256)) * up(a.d, 256) : 0) +
+                          (a.dw ? int64_t(up(cols, 256)) * up(a.d, 256) : 0);
+    const int64_t small = (a.dx ? int64_t(up(a.n, 128)) * up(a.d, 128) : 0) +
+                          (a.dw ? int64_t(up(cols, 128)) * up(a.d, 128) : 0);
+    if constexpr (DT == 1) {
+        if (large_tile(large, small))
+            return grad_tiles<typename T::template Large<false, true>, typename T::template Half<false, true>,
+                              typename T::template Large<true, true>, typename T::template Half<true, true>>(a, v0, cols,
+                                                                                                         pad, s);
+    }
+    using SX = typename T::template Small<false, true>;
+    using SW = typename T::template Small<true, true>;
+    return grad_tiles<SX, SX, SW, SW>(a, v0, cols, pad, s);
 }
 
 template <int DT>
 hipError_t bwd_dt(const XentArgs& a, hipStream_t s)
 {
-    using T = Tiles<DT>;
     if (DT == 1 && a.dw) {
         xent_list_kernel<<<dim3(up(a.v, kXentCols)), dim3(256), 0, s>>>(a);
         const hipError_t e = hipGetLastError();
@@ -492,22 +517,8 @@ hipError_t bwd_dt(const XentArgs& a, hipStream_t s)
     for (int64_t v0 = 0; v0 < a.v; v0 += a.piece) {
         const int64_t cols = a.v - v0 < a.piece ? a.v - v0 : a.piece;
         const int64_t pad = (cols + 15) / 16 * 16;
-        hipError_t e;
-        if (DT == 1 && large_tile(int64_t(up(a.n, 256)) * up(pad, 256), int64_t(up(a.n, 128)) * up(pad, 128)))
-            e = dl_tiles<typename T::template Large<false, false>>(a, v0, cols, pad, s);
-        else
-            e = dl_tiles<typename T::template Small<false, false>>(a, v0, cols, pad, s);
-        if (e != hipSuccess) return e;
-        const int64_t large = (a.dx ? int64_t(up(a.n, 256)) * up(a.d, 256) : 0) +
-                              (a.dw ? int64_t(up(cols, 256)) * up(a.d, 256) : 0);
-        const int64_t small = (a.dx ? int64_t(up(a.n, 128)) * up(a.d, 128) : 0) +
-                              (a.dw ? int64_t(up(cols, 128)) * up(a.d, 128) : 0);
-        if (DT == 1 && large_tile(large, small))
-            e = grad_tiles<typename T::template Large<false, true>, typename T::template Large<true, true>>(a, v0, cols,
-                                                                                                         pad, s);
-        else
-            e = grad_tiles<typename T::template Small<false, true>, typename T::template Small<true, true>>(a, v0, cols,
-                                                                                                         pad, s);
+        hipError_t e = dl_tiles_dt<DT>(a, v0, cols, pad, s);
+        if (e == hipSuccess) e = grad_tiles_dt<DT>(a, v0, cols, pad, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
