@@ -43,9 +43,10 @@ extern "C" {
  *   reset   : (batch, seqlen) bytes, or NULL (no resets)
  *   y       : (batch, seqlen, dim) dtype output
  *   h_last  : (batch, dim) fp32 output, the state after the last row, or NULL
- *   ckpt    : (ceil(seqlen/64), batch, dim) fp32 output, the state entering
- *             every 64th row, for ss_glr_bwd; or NULL
- * h_last may be exactly h0.  c must be finite and positive.
+ *   ckpt    : (ceil(seqlen/32), batch, dim) fp32 output, the state entering
+ *             every 32nd row, for ss_glr_bwd; or NULL
+ * h_last may be exactly h0.  c must be finite and positive.  Row strides (and
+ * dim) above 2^22 elements are SS_ERR_UNSUPPORTED.
  */
 size_t ss_glr_ckpt_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 size_t ss_glr_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim); /* 0: none needed */

@@ -4,10 +4,10 @@
 // its backward pass and its single-token form.
 //
 // The update is an affine map h -> a h + b, and maps compose: (a1, b1) then (a2, b2) is
-// (a2 a1, a2 b1 + b2).  A workgroup of 8 waves takes 32 VC channels (VC neighbouring ones per
-// lane) and walks its rows in tiles of 16 R: each half wave holds a run of R rows, forms their
+// (a2 a1, a2 b1 + b2).  A workgroup of 4 waves takes 32 VC channels (VC neighbouring ones per
+// lane) and walks its rows in tiles of 8 R: each half wave holds a run of R rows, forms their
 // a and b in registers, and its run's composed map; the two halves of a wave are joined by a
-// lane exchange, the 8 waves through LDS, and every run then replays its rows from the state
+// lane exchange, the 4 waves through LDS, and every run then replays its rows from the state
 // that enters it.  So the operands are read once and y is written once: the kernel is bound
 // by HBM traffic (bf16: 8 bytes per element), with the next tile's loads in flight while a
 // tile is worked on.
@@ -17,7 +17,7 @@
 //
 // Backward.  g_t = dL/dh_t = dy_t + a_{t+1} g_{t+1}: the same maps from the end.  Run q_t = a_t g_t
 // backward: q -> a (q + dy), so a run's product of a serves both directions.  The states
-// h_{t-1} are rebuilt from those kept every 64 rows.
+// h_{t-1} are rebuilt from those kept every 32 rows.
 //
 // 1 - a^2 = -expm1(-2 k s) is formed without cancellation: as a gate closes a tends to 1 and
 // the plain difference would lose every digit.
@@ -28,12 +28,12 @@ namespace ssk {
 namespace {
 
 constexpr int kRunLanes = 32;               // lanes per run: half a wave
-constexpr int kGlrWaves = 8;
+constexpr int kGlrWaves = 4;
 constexpr int kRuns = 2 * kGlrWaves;        // runs per tile
 constexpr int kGlrThreads = 64 * kGlrWaves;
 constexpr int kFwdRows = 8, kBwdRows = 4;   // rows per run
 static_assert(kRuns * kFwdRows == kGlrChunkUnit && kRuns * kBwdRows == kGlrRows, "tiles and kept states");
-static_assert(kGlrRows % kFwdRows == 0, "a kept state falls on a run's start");
+static_assert(kGlrRows % kFwdRows == 0 && kGlrChunkUnit % kGlrRows == 0, "a kept state falls on a run's start");
 
 // VC neighbouring elements of a row as loaded
 template <int DT, int VC>
@@ -49,40 +49,98 @@ struct Row<1, 2> {
     {
         return uint32_t(f32_to_bf16_bits(v[0])) | (uint32_t(f32_to_bf16_bits(v[1])) << 16);
     }
+    static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff)
+    {
+        return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+    }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, Raw v)
+    {
+        __builtin_amdgcn_raw_buffer_store_b32(v, r, voff, soff, 0);
+    }
 };
 template <>
 struct Row<1, 1> {
     using Raw = uint16_t;
     static __device__ __forceinline__ float get(Raw v, int) { return bf16_bits_to_f32(v); }
     static __device__ __forceinline__ Raw make(const float (&v)[1]) { return f32_to_bf16_bits(v[0]); }
+    static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff)
+    {
+        return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+    }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, Raw v)
+    {
+        __builtin_amdgcn_raw_buffer_store_b16(v, r, voff, soff, 0);
+    }
 };
+typedef uint32_t Words2 __attribute__((ext_vector_type(2)));
 template <>
 struct Row<0, 2> {
-    using Raw = float2;
-    static __device__ __forceinline__ float get(Raw v, int e) { return e == 0 ? v.x : v.y; }
-    static __device__ __forceinline__ Raw make(const float (&v)[2]) { return make_float2(v[0], v[1]); }
+    using Raw = Words2;
+    static __device__ __forceinline__ float get(Raw v, int e) { return __uint_as_float(e == 0 ? v.x : v.y); }
+    static __device__ __forceinline__ Raw make(const float (&v)[2])
+    {
+        return Raw{__float_as_uint(v[0]), __float_as_uint(v[1])};
+    }
+    static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff)
+    {
+        return __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0);
+    }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, Raw v)
+    {
+        __builtin_amdgcn_raw_buffer_store_b64(v, r, voff, soff, 0);
+    }
 };
 template <>
 struct Row<0, 1> {
-    using Raw = float;
-    static __device__ __forceinline__ float get(Raw v, int) { return v; }
-    static __device__ __forceinline__ Raw make(const float (&v)[1]) { return v[0]; }
+    using Raw = uint32_t;
+    static __device__ __forceinline__ float get(Raw v, int) { return __uint_as_float(v); }
+    static __device__ __forceinline__ Raw make(const float (&v)[1]) { return __float_as_uint(v[0]); }
+    static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff)
+    {
+        return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+    }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, Raw v)
+    {
+        __builtin_amdgcn_raw_buffer_store_b32(v, r, voff, soff, 0);
+    }
 };
 
 template <int DT>
-constexpr int64_t elem_bytes = DT == 0 ? 4 : 2;
+constexpr uint32_t elem_bytes = DT == 0 ? 4 : 2;
 
+// The rows of one tile of an operand: row q of this lane's run is a scalar offset away from the
+// lane's own.  Rows past the chunk's end and lanes past the last channel fall to the range
+// check: their loads read 0 and their stores are dropped.  The host keeps a tile below 2^31 bytes.
 template <int DT, int VC>
-__device__ __forceinline__ typename Row<DT, VC>::Raw load_row(const void* base, int64_t elem)
+struct Rows {
+    using RW = Row<DT, VC>;
+    uint32_t lane, step;  // this lane's offset in a tile, bytes per row
+    __device__ Rows(int64_t ld, int64_t d, bool live, int first)
+        : lane(live ? uint32_t(first * ld + d) * elem_bytes<DT> : kIdleOffset), step(uint32_t(ld) * elem_bytes<DT>)
+    {
+    }
+    // base: the operand's first element of the batch row; `rows` from `row` on exist
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile(const void* base, int64_t row, int rows) const
+    {
+        return make_rsrc(static_cast<const char*>(base) + row * int64_t(step), uint32_t(rows) * step);
+    }
+    __device__ __forceinline__ typename RW::Raw load(__amdgpu_buffer_rsrc_t r, int q) const
+    {
+        return RW::load(r, lane, uint32_t(q) * step);
+    }
+    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int q, const float (&v)[VC]) const
+    {
+        RW::store(r, lane, uint32_t(q) * step, RW::make(v));
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ const void* offset(const void* p, int64_t elems)
 {
-    return *reinterpret_cast<const typename Row<DT, VC>::Raw*>(static_cast<const char*>(base) + elem * elem_bytes<DT>);
+    return static_cast<const char*>(p) + elems * elem_bytes<DT>;
 }
-template <int DT, int VC>
-__device__ __forceinline__ void store_row(void* base, int64_t elem, const float (&v)[VC])
-{
-    *reinterpret_cast<typename Row<DT, VC>::Raw*>(static_cast<char*>(base) + elem * elem_bytes<DT>) =
-        Row<DT, VC>::make(v);
-}
+
+__device__ __forceinline__ float sigmoid1(float v) { return __builtin_amdgcn_rcpf(1.0f + exp2_hw(-v * kLog2e)); }
 
 // sigmoid(v) and 1 - sigmoid(v), both to full relative precision.  The exponent is held below
 // 2^126 so that e stays finite and e s tends to 1.
@@ -94,20 +152,18 @@ __device__ __forceinline__ float sigmoid2(float v, float* rest)
     return s;
 }
 
-// a = exp(-k s) and m = sqrt(1 - a^2).  Below t = 2 k s = 1/2 the series of 1 - e^-t to t^7
-// (truncation t^7/8! < 2e-7 relative), above it 1 - a^2 itself (a^2 < 0.61: no cancellation).
-__device__ __forceinline__ void decay_of(float k, float s, float* a, float* m)
+// a = exp(-k s) and w = 1 - a^2 = 1 - e^-t, t = 2 k s.  Below t = 1/2 a polynomial of
+// (1 - e^-t) / t (degree 4, a weighted least-squares fit of relative error below 1e-7 once
+// rounded), above it 1 - a^2 itself (a^2 < 0.61: no cancellation).
+__device__ __forceinline__ void decay_of(float k, float s, float* a, float* w)
 {
-    const float ks = k * s;
-    *a = exp2_hw(-ks * kLog2e);
-    const float t = ks + ks;
-    float p = fmaf(t, 1.0f / 5040.0f, -1.0f / 720.0f);
-    p = fmaf(t, p, 1.0f / 120.0f);
-    p = fmaf(t, p, -1.0f / 24.0f);
-    p = fmaf(t, p, 1.0f / 6.0f);
-    p = fmaf(t, p, -0.5f);
-    const float small = fmaf(t * t, p, t);
-    *m = __builtin_amdgcn_sqrtf(t < 0.5f ? small : fmaf(-*a, *a, 1.0f));
+    *a = exp2_hw((-kLog2e * k) * s);
+    const float t = (k + k) * s;
+    float p = fmaf(t, 0.00677103829f, -0.0410012789f);
+    p = fmaf(t, p, 0.166548148f);
+    p = fmaf(t, p, -0.49999249f);
+    p = fmaf(t, p, 0.99999994f);
+    *w = t < 0.5f ? t * p : fmaf(-*a, *a, 1.0f);
 }
 
 __device__ __forceinline__ float channel_rate(float decay, float c)
@@ -132,16 +188,15 @@ template <int VC>
 struct Place {
     int64_t b, c, d;   // batch row, chunk, first channel of this lane
     int64_t t0, t1;    // the chunk's rows
-    int64_t dc;        // d clamped to a channel that exists: loads stay inside
+    int64_t dc;        // d, or a channel that exists where d does not
     bool live;
     __device__ Place(const GlrArgs& a)
     {
-        const int64_t cols = (a.dim + kRunLanes * VC - 1) / (kRunLanes * VC);
-        const int64_t id = blockIdx.x;
-        const int64_t rest = id / cols;
-        d = (id % cols) * (kRunLanes * VC) + (threadIdx.x & 31) * VC;
-        b = rest % a.batch;
-        c = rest / a.batch;
+        const uint32_t cols = uint32_t((a.dim + kRunLanes * VC - 1) / (kRunLanes * VC));
+        const uint32_t id = blockIdx.x, rest = id / cols;
+        d = int64_t(id % cols) * (kRunLanes * VC) + (threadIdx.x & 31) * VC;
+        b = rest % uint32_t(a.batch);
+        c = rest / uint32_t(a.batch);
         live = d < a.dim;
         dc = live ? d : 0;
         t0 = c * a.chunk_len;
@@ -159,7 +214,8 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
     using RW = Row<DT, VC>;
     using Raw = typename RW::Raw;
     const Place<VC> w(a);
-    const int wave = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, run = wave * 2 + half;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = (threadIdx.x >> 5) & 1, run = wave * 2 + half, l32 = threadIdx.x & 31;
     const int64_t bd = w.b * a.dim + w.dc;
 
     float k[VC], h[VC], prod[VC];
@@ -179,52 +235,65 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
     }
 
     __shared__ float maps[2][kGlrWaves][2 * VC][kRunLanes];
+    const Rows<DT, VC> px(a.x_ld, w.d, w.live, run * R), pr(a.r_ld, w.d, w.live, run * R),
+        pi(a.i_ld, w.d, w.live, run * R), py(a.dim, w.d, w.live, run * R);
+    const int64_t row0 = w.b * a.seqlen;
     Raw rx[R], rr[R], ri[R];
     uint8_t rs[R];
     auto load = [&](int64_t tile) {
-        const int64_t first = tile + run * R;
+        const int rows = int(w.t1 - tile < T ? w.t1 - tile : T);
+        const auto br = pr.tile(a.r, row0 + tile, rows), bi = pi.tile(a.i, row0 + tile, rows),
+                   bx = px.tile(a.x, row0 + tile, rows);
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const int64_t t = first + q < a.seqlen ? first + q : a.seqlen - 1;
-            const int64_t row = w.b * a.seqlen + t;
-            rr[q] = load_row<DT, VC>(a.r, row * a.r_ld + w.dc);
-            ri[q] = load_row<DT, VC>(a.i, row * a.i_ld + w.dc);
-            rx[q] = load_row<DT, VC>(a.x, row * a.x_ld + w.dc);
-            if (RESET) rs[q] = a.reset[row];
+            rr[q] = pr.load(br, q);
+            ri[q] = pi.load(bi, q);
+            rx[q] = px.load(bx, q);
+            if (RESET) {
+                const int64_t t = tile + run * R + q;
+                rs[q] = a.reset[row0 + (t < a.seqlen ? t : a.seqlen - 1)];
+            }
         }
     };
     load(w.t0);
     int buf = 0;
     for (int64_t tile = w.t0; tile < w.t1; tile += T, buf ^= 1) {
-        const int64_t first = tile + run * R;
+        const int rows = int(w.t1 - tile < T ? w.t1 - tile : T);
         float av[R][VC], bv[R][VC], P[VC], E[VC];
 #pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            P[e] = 1.0f;
-            E[e] = 0.0f;
-        }
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const bool in = first + q < w.t1;
+        for (int q = 0; q < R; ++q)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
-                float rest, m;
-                const float sr = sigmoid2(RW::get(rr[q], e), &rest);
-                const float si = sigmoid2(RW::get(ri[q], e), &rest);
-                decay_of(k[e], sr, &av[q][e], &m);
+                float ww;
+                decay_of(k[e], sigmoid1(RW::get(rr[q], e)), &av[q][e], &ww);
+                float m = __builtin_amdgcn_sqrtf(ww);
                 if (RESET && rs[q]) {
                     av[q][e] = 0.0f;
                     m = 1.0f;
                 }
-                bv[q][e] = m * si * RW::get(rx[q], e);
-                // rows past the end leave the state as it is
-                av[q][e] = in ? av[q][e] : 1.0f;
-                bv[q][e] = in ? bv[q][e] : 0.0f;
+                bv[q][e] = m * sigmoid1(RW::get(ri[q], e)) * RW::get(rx[q], e);
+            }
+        if (rows < T) {
+            // rows past the end leave the state as it is
+#pragma unroll
+            for (int q = 0; q < R; ++q)
+#pragma unroll
+                for (int e = 0; e < VC; ++e) {
+                    av[q][e] = run * R + q < rows ? av[q][e] : 1.0f;
+                    bv[q][e] = run * R + q < rows ? bv[q][e] : 0.0f;
+                }
+        }
+        if (tile + T < w.t1) load(tile + T);
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+            P[e] = av[0][e];
+            E[e] = bv[0][e];
+#pragma unroll
+            for (int q = 1; q < R; ++q) {
                 P[e] *= av[q][e];
                 E[e] = carry<RESET>(av[q][e], E[e], bv[q][e]);
             }
         }
-        if (tile + T < w.t1) load(tile + T);
         // join the halves of the wave; the earlier half publishes the wave's map
         float P0[VC], E0[VC];
 #pragma unroll
@@ -232,8 +301,8 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
             P0[e] = other_half(P[e]);
             E0[e] = other_half(E[e]);
             if (half == 0) {
-                maps[buf][wave][2 * e][threadIdx.x & 31] = P0[e] * P[e];
-                maps[buf][wave][2 * e + 1][threadIdx.x & 31] = carry<RESET>(P0[e], E[e], E0[e]);
+                maps[buf][wave][2 * e][l32] = P0[e] * P[e];
+                maps[buf][wave][2 * e + 1][l32] = carry<RESET>(P0[e], E[e], E0[e]);
             }
         }
         __syncthreads();
@@ -242,9 +311,9 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
         for (int v = 0; v < kGlrWaves; ++v) {
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
-                if (v == wave) in[e] = h[e];
-                const float p = maps[buf][v][2 * e][threadIdx.x & 31];
-                h[e] = carry<RESET>(p, h[e], maps[buf][v][2 * e + 1][threadIdx.x & 31]);
+                if (!AGG && v == wave) in[e] = h[e];
+                const float p = maps[buf][v][2 * e][l32];
+                h[e] = carry<RESET>(p, h[e], maps[buf][v][2 * e + 1][l32]);
                 if (AGG) prod[e] *= p;
             }
         }
@@ -252,17 +321,18 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
 #pragma unroll
             for (int e = 0; e < VC; ++e)
                 if (half == 1) in[e] = carry<RESET>(P0[e], in[e], E0[e]);
-            if (a.ckpt && w.live && first % kGlrRows == 0 && first < w.t1) {
-                const int64_t at = (first / kGlrRows) * a.batch * a.dim + bd;
+            if (a.ckpt && (run * R) % kGlrRows == 0 && run * R < rows && w.live) {
+                const int64_t at = ((tile + run * R) / kGlrRows) * a.batch * a.dim + bd;
 #pragma unroll
                 for (int e = 0; e < VC; ++e) a.ckpt[at + e] = in[e];
             }
-            if (a.y && w.live) {
+            if (a.y) {
+                const auto by = py.tile(a.y, row0 + tile, rows);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
 #pragma unroll
                     for (int e = 0; e < VC; ++e) in[e] = carry<RESET>(av[q][e], in[e], bv[q][e]);
-                    if (first + q < w.t1) store_row<DT, VC>(a.y, (w.b * a.seqlen + first + q) * a.dim + w.d, in);
+                    py.store(by, q, in);
                 }
             }
         }
@@ -284,14 +354,14 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
 
 // AGG: only each chunk's composed map of q, from r and dy (ws_prod, ws_end)
 template <int DT, int VC, bool RESET, bool AGG>
-__global__ __launch_bounds__(kGlrThreads, 4) void glr_bwd_kernel(GlrArgs a)
+__global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrArgs a)
 {
     constexpr int R = kBwdRows, T = kRuns * R;
     using RW = Row<DT, VC>;
     using Raw = typename RW::Raw;
     const Place<VC> w(a);
-    const int wave = threadIdx.x >> 6, half = (threadIdx.x >> 5) & 1, run = wave * 2 + half;
-    const int l32 = threadIdx.x & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = (threadIdx.x >> 5) & 1, run = wave * 2 + half, l32 = threadIdx.x & 31;
     const int64_t bd = w.b * a.dim + w.dc;
 
     float k[VC], q[VC], prod[VC], dk[VC];
@@ -312,22 +382,28 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_bwd_kernel(GlrArgs a)
     }
 
     __shared__ float maps[2][kGlrWaves][3 * VC][kRunLanes];
+    const Rows<DT, VC> px(a.x_ld, w.d, w.live, run * R), pr(a.r_ld, w.d, w.live, run * R),
+        pi(a.i_ld, w.d, w.live, run * R), pd(a.dim, w.d, w.live, run * R), pg(a.g_ld, w.d, w.live, run * R);
+    const int64_t row0 = w.b * a.seqlen;
     Raw rx[R], rr[R], ri[R], rd[R];
     uint8_t rs[R];
     float kept[VC];
     auto load = [&](int64_t tile) {
-        const int64_t first = tile + run * R;
+        const int rows = int(w.t1 - tile < T ? w.t1 - tile : T);
+        const auto br = pr.tile(a.r, row0 + tile, rows), bi = pi.tile(a.i, row0 + tile, rows),
+                   bx = px.tile(a.x, row0 + tile, rows), bd_ = pd.tile(a.dy, row0 + tile, rows);
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            const int64_t t = first + j < a.seqlen ? first + j : a.seqlen - 1;
-            const int64_t row = w.b * a.seqlen + t;
-            rr[j] = load_row<DT, VC>(a.r, row * a.r_ld + w.dc);
-            rd[j] = load_row<DT, VC>(a.dy, row * a.dim + w.dc);
+            rr[j] = pr.load(br, j);
+            rd[j] = pd.load(bd_, j);
             if (!AGG) {
-                ri[j] = load_row<DT, VC>(a.i, row * a.i_ld + w.dc);
-                rx[j] = load_row<DT, VC>(a.x, row * a.x_ld + w.dc);
+                ri[j] = pi.load(bi, j);
+                rx[j] = px.load(bx, j);
             }
-            if (RESET) rs[j] = a.reset[row];
+            if (RESET) {
+                const int64_t t = tile + run * R + j;
+                rs[j] = a.reset[row0 + (t < a.seqlen ? t : a.seqlen - 1)];
+            }
         }
         if (!AGG) {
             const int64_t at = (tile / kGlrRows) * a.batch * a.dim + bd;
@@ -339,41 +415,55 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_bwd_kernel(GlrArgs a)
     load(last);
     int buf = 0;
     for (int64_t tile = last; tile >= w.t0; tile -= T, buf ^= 1) {
-        const int64_t first = tile + run * R;
-        float av[R][VC], m[R][VC], sr[R][VC], nr[R][VC], si[R][VC], ni[R][VC], x[R][VC], dy[R][VC], h[VC];
+        const int rows = int(w.t1 - tile < T ? w.t1 - tile : T);
+        // c1 = m si: dx = g c1.  bv = c1 x, the update's input.  slope: d log a takes
+        // g a (h_{t-1} - (a / w) bv), from dm/dlog a = -a^2 / m and w = m^2.
+        float av[R][VC], bv[R][VC], c1[R][VC], slope[R][VC], sr[R][VC], nr[R][VC], ni[R][VC], dy[R][VC], h[VC];
         float P[VC], E[VC], Q[VC];
 #pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            P[e] = 1.0f;
-            E[e] = Q[e] = 0.0f;
-            h[e] = kept[e];
-        }
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const bool in = first + j < w.t1;
+        for (int j = 0; j < R; ++j)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
+                float ww;
                 sr[j][e] = sigmoid2(RW::get(rr[j], e), &nr[j][e]);
-                decay_of(k[e], sr[j][e], &av[j][e], &m[j][e]);
+                decay_of(k[e], sr[j][e], &av[j][e], &ww);
                 if (RESET && rs[j]) {
                     av[j][e] = 0.0f;
-                    m[j][e] = 1.0f;
+                    ww = 1.0f;
                 }
-                dy[j][e] = in ? RW::get(rd[j], e) : 0.0f;
-                av[j][e] = in ? av[j][e] : 1.0f;
+                dy[j][e] = RW::get(rd[j], e);
                 if (!AGG) {
-                    si[j][e] = sigmoid2(RW::get(ri[j], e), &ni[j][e]);
-                    x[j][e] = in ? RW::get(rx[j], e) : 0.0f;
-                    E[e] = carry<RESET>(av[j][e], E[e], m[j][e] * si[j][e] * x[j][e]);
+                    c1[j][e] = __builtin_amdgcn_sqrtf(ww) * sigmoid2(RW::get(ri[j], e), &ni[j][e]);
+                    bv[j][e] = c1[j][e] * RW::get(rx[j], e);
+                    // where w underflows (the gate shut), bv is 0 and so is the slope's part
+                    slope[j][e] = av[j][e] * bv[j][e] * __builtin_amdgcn_rcpf(fmaxf(ww, 1.1754944e-38f));
                 }
-                P[e] *= av[j][e];
             }
+        if (rows < T) {
+            // rows past the end pass q on as it is; their dy, and x, read as 0
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+#pragma unroll
+                for (int e = 0; e < VC; ++e) av[j][e] = run * R + j < rows ? av[j][e] : 1.0f;
         }
+        if (!AGG) {
 #pragma unroll
-        for (int j = R - 1; j >= 0; --j)
-#pragma unroll
-            for (int e = 0; e < VC; ++e) Q[e] = carry<RESET>(av[j][e], Q[e] + dy[j][e], 0.0f);
+            for (int e = 0; e < VC; ++e) h[e] = kept[e];
+        }
         if (tile > w.t0) load(tile - T);
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+            P[e] = av[0][e];
+            if (!AGG) E[e] = bv[0][e];
+#pragma unroll
+            for (int j = 1; j < R; ++j) {
+                P[e] *= av[j][e];
+                if (!AGG) E[e] = carry<RESET>(av[j][e], E[e], bv[j][e]);
+            }
+            Q[e] = carry<RESET>(av[R - 1][e], dy[R - 1][e], 0.0f);
+#pragma unroll
+            for (int j = R - 2; j >= 0; --j) Q[e] = carry<RESET>(av[j][e], Q[e] + dy[j][e], 0.0f);
+        }
 
         float Po[VC], Eo[VC], Qo[VC];  // the other half's
 #pragma unroll
@@ -392,9 +482,11 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_bwd_kernel(GlrArgs a)
         if (!AGG) {
 #pragma unroll
             for (int v = 0; v < kGlrWaves - 1; ++v)
+                if (v < wave) {
 #pragma unroll
-                for (int e = 0; e < VC; ++e)
-                    if (v < wave) h[e] = carry<RESET>(maps[buf][v][3 * e][l32], h[e], maps[buf][v][3 * e + 2][l32]);
+                    for (int e = 0; e < VC; ++e)
+                        h[e] = carry<RESET>(maps[buf][v][3 * e][l32], h[e], maps[buf][v][3 * e + 2][l32]);
+                }
 #pragma unroll
             for (int e = 0; e < VC; ++e) hin[e] = half == 1 ? carry<RESET>(Po[e], h[e], Eo[e]) : h[e];
         }
@@ -402,7 +494,7 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_bwd_kernel(GlrArgs a)
         for (int v = kGlrWaves - 1; v >= 0; --v)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
-                if (v == wave) qin[e] = q[e];
+                if (!AGG && v == wave) qin[e] = q[e];
                 const float p = maps[buf][v][3 * e][l32];
                 q[e] = carry<RESET>(p, q[e], maps[buf][v][3 * e + 1][l32]);
                 if (AGG) prod[e] *= p;
@@ -414,37 +506,31 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_bwd_kernel(GlrArgs a)
 #pragma unroll
                 for (int e = 0; e < VC; ++e) {
                     before[j][e] = hin[e];
-                    hin[e] = carry<RESET>(av[j][e], hin[e], m[j][e] * si[j][e] * x[j][e]);
+                    hin[e] = carry<RESET>(av[j][e], hin[e], bv[j][e]);
                 }
 #pragma unroll
             for (int e = 0; e < VC; ++e)
                 if (half == 0) qin[e] = carry<RESET>(Po[e], qin[e], Qo[e]);
+            const auto bx = pg.tile(a.dx, row0 + tile, rows), br = pg.tile(a.dr, row0 + tile, rows),
+                       bi = pg.tile(a.di, row0 + tile, rows);
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
                 float dx[VC], dr[VC], di[VC];
 #pragma unroll
                 for (int e = 0; e < VC; ++e) {
                     const float g = qin[e] + dy[j][e];
-                    const float gm = g * m[j][e], gms = gm * si[j][e];
-                    dx[e] = gms;
-                    di[e] = gms * x[j][e] * ni[j][e];
-                    // d m / d log a = -a^2 / m; where a rounds to 1 (s so small that m is 0)
-                    // its product with ds/dr vanishes
-                    const float im = m[j][e] > 0.0f ? __builtin_amdgcn_rcpf(m[j][e]) : 0.0f;
-                    const float ga = carry<RESET>(av[j][e], g, 0.0f);
-                    const float dm = ga * av[j][e] * im * si[j][e] * x[j][e];
-                    const float dla = carry<RESET>(av[j][e], g * before[j][e], 0.0f) - (RESET && av[j][e] == 0.0f ? 0.0f : dm);
-                    const float dls = dla * sr[j][e];
+                    dx[e] = g * c1[j][e];
+                    di[e] = g * bv[j][e] * ni[j][e];
+                    qin[e] = carry<RESET>(av[j][e], g, 0.0f);
+                    // at a reset nothing of log a's gradient is left, whatever lies before it
+                    const float through = before[j][e] - slope[j][e];
+                    const float dls = carry<RESET>(av[j][e], g * through, 0.0f) * sr[j][e];
                     dr[e] = -k[e] * dls * nr[j][e];
-                    if (first + j < w.t1) dk[e] += dls;
-                    qin[e] = ga;
+                    dk[e] += rows < T && run * R + j >= rows ? 0.0f : dls;
                 }
-                if (w.live && first + j < w.t1) {
-                    const int64_t at = (w.b * a.seqlen + first + j) * a.g_ld + w.d;
-                    store_row<DT, VC>(a.dx, at, dx);
-                    store_row<DT, VC>(a.dr, at, dr);
-                    store_row<DT, VC>(a.di, at, di);
-                }
+                pg.store(bx, j, dx);
+                pg.store(br, j, dr);
+                pg.store(bi, j, di);
             }
         }
     }
@@ -492,26 +578,26 @@ template <int DT, int VC>
 __global__ __launch_bounds__(256) void glr_step_kernel(GlrStepArgs a)
 {
     using RW = Row<DT, VC>;
+    using Raw = typename RW::Raw;
     const int64_t d = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VC;
     if (d >= a.dim) return;
     float k[VC];
 #pragma unroll
     for (int e = 0; e < VC; ++e) k[e] = channel_rate(a.decay[d + e], a.c);
     for (int64_t b = blockIdx.y; b < a.batch; b += gridDim.y) {
-        const auto rr = load_row<DT, VC>(a.r, b * a.r_ld + d);
-        const auto ri = load_row<DT, VC>(a.i, b * a.i_ld + d);
-        const auto rx = load_row<DT, VC>(a.x, b * a.x_ld + d);
+        const auto rr = *static_cast<const Raw*>(offset<DT>(a.r, b * a.r_ld + d));
+        const auto ri = *static_cast<const Raw*>(offset<DT>(a.i, b * a.i_ld + d));
+        const auto rx = *static_cast<const Raw*>(offset<DT>(a.x, b * a.x_ld + d));
         float h[VC];
 #pragma unroll
         for (int e = 0; e < VC; ++e) {
-            float rest, av, m;
-            const float sr = sigmoid2(RW::get(rr, e), &rest);
-            const float si = sigmoid2(RW::get(ri, e), &rest);
-            decay_of(k[e], sr, &av, &m);
-            h[e] = fmaf(av, a.h[b * a.dim + d + e], m * si * RW::get(rx, e));
+            float av, w;
+            decay_of(k[e], sigmoid1(RW::get(rr, e)), &av, &w);
+            const float in = __builtin_amdgcn_sqrtf(w) * sigmoid1(RW::get(ri, e)) * RW::get(rx, e);
+            h[e] = fmaf(av, a.h[b * a.dim + d + e], in);
             a.h[b * a.dim + d + e] = h[e];
         }
-        store_row<DT, VC>(a.y, b * a.dim + d, h);
+        *const_cast<Raw*>(static_cast<const Raw*>(offset<DT>(a.y, b * a.dim + d))) = RW::make(h);
     }
 }
 

@@ -84,7 +84,7 @@ constexpr int64_t kGlrCols = 64;          // channels per workgroup
 // Fewer one-chunk workgroups than kGlrWhole leave CUs idle: the rows are then cut until there
 // are kGlrTarget workgroups, in chunks of at least kGlrMinChunk rows (the cut costs a pass over
 // the operands) and at most kGlrMaxChunks of them (a chunk joins its predecessors' maps itself).
-constexpr int64_t kGlrWhole = 256, kGlrTarget = 512, kGlrMinChunk = 512, kGlrMaxChunks = 64;
+constexpr int64_t kGlrWhole = 256, kGlrTarget = 1024, kGlrMinChunk = 512, kGlrMaxChunks = 64;
 
 void glr_plan(int64_t batch, int64_t seqlen, int64_t dim, int64_t* len, int64_t* chunks)
 {
@@ -132,6 +132,11 @@ bool glr_grid_ok(int64_t batch, int64_t dim, int64_t chunks)
     return mul(batch, ceil_div(dim, kGlrCols / 2), &n) && mul(n, chunks, &n) && n <= INT32_MAX;
 }
 
+bool glr_too_wide(int64_t a, int64_t b, int64_t c, int64_t d)
+{
+    return a > ssk::kGlrMaxStride || b > ssk::kGlrMaxStride || c > ssk::kGlrMaxStride || d > ssk::kGlrMaxStride;
+}
+
 }  // namespace
 
 extern "C" {
@@ -167,7 +172,8 @@ ss_status ss_glr_fwd(const void* x, int64_t x_row_stride, const void* r, int64_t
     if (x_row_stride < dim || r_row_stride < dim || i_row_stride < dim) return SS_ERR_INVALID_ARG;
     if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
     if (!known(dtype)) return SS_ERR_UNSUPPORTED;
-    if (!glr_grid_ok(batch, dim, w.chunks)) return SS_ERR_UNSUPPORTED;
+    if (!glr_grid_ok(batch, dim, w.chunks) || glr_too_wide(x_row_stride, r_row_stride, i_row_stride, dim))
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {x, r, i, y};
     for (const void* p : elems)
@@ -228,7 +234,8 @@ ss_status ss_glr_bwd(const void* x, int64_t x_row_stride, const void* r, int64_t
         return SS_ERR_INVALID_ARG;
     if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
     if (!known(dtype)) return SS_ERR_UNSUPPORTED;
-    if (!glr_grid_ok(batch, dim, w.chunks)) return SS_ERR_UNSUPPORTED;
+    if (!glr_grid_ok(batch, dim, w.chunks) || glr_too_wide(x_row_stride, r_row_stride, i_row_stride, grad_row_stride))
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {x, r, i, dy, dx, dr, di};
     for (const void* p : elems)

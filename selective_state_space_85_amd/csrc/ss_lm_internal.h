@@ -78,9 +78,11 @@ hipError_t launch_xent_bwd(const XentArgs& a, int dtype, hipStream_t stream);
 
 // Rows between two kept states, which is also the backward's tile: it rebuilds a
 // tile's states from the one that enters it.
-constexpr int64_t kGlrRows = 64;
+constexpr int64_t kGlrRows = 32;
 // Chunks are whole forward tiles.
-constexpr int64_t kGlrChunkUnit = 128;
+constexpr int64_t kGlrChunkUnit = 64;
+// Longest row stride, in elements: a tile stays below 2^31 bytes.
+constexpr int64_t kGlrMaxStride = int64_t(1) << 22;
 
 struct GlrArgs {
     const void* x;  // (batch, seqlen, dim), rows *_ld elements apart

@@ -98,9 +98,9 @@ def _call(name: str, status: int) -> None:
 # ---------------------------------------------------------------- gated linear recurrence
 
 def glr_ckpt_shape(batch: int, seqlen: int, dim: int) -> Tuple[int, int, int]:
-    """Shape of the float32 kept states (``ss_glr_ckpt_bytes``): one every 64 rows."""
+    """Shape of the float32 kept states (``ss_glr_ckpt_bytes``): one every 32 rows."""
     _size(_lm.load().ss_glr_ckpt_bytes(batch, seqlen, dim))
-    return (-(-seqlen // 64), batch, dim)
+    return (-(-seqlen // 32), batch, dim)
 
 
 def glr_workspace_bytes(batch: int, seqlen: int, dim: int) -> int:
