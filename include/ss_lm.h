@@ -46,7 +46,7 @@ extern "C" {
  *   ckpt    : (ceil(seqlen/32), batch, dim) fp32 output, the state entering
  *             every 32nd row, for ss_glr_bwd; or NULL
  * h_last may be exactly h0.  c must be finite and positive.  Row strides (and
- * dim) above 2^22 elements are SS_ERR_UNSUPPORTED.
+ * dim) above 2^20 elements are SS_ERR_UNSUPPORTED.
  */
 size_t ss_glr_ckpt_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 size_t ss_glr_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim); /* 0: none needed */

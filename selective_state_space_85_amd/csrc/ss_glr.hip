@@ -4,20 +4,21 @@
 // its backward pass and its single-token form.
 //
 // The update is an affine map h -> a h + b, and maps compose: (a1, b1) then (a2, b2) is
-// (a2 a1, a2 b1 + b2).  A workgroup of 4 waves takes 32 VC channels (VC neighbouring ones per
-// lane) and walks its rows in tiles of 8 R: each half wave holds a run of R rows, forms their
-// a and b in registers, and its run's composed map; the two halves of a wave are joined by a
-// lane exchange, the 4 waves through LDS, and every run then replays its rows from the state
-// that enters it.  So the operands are read once and y is written once: the kernel is bound
-// by HBM traffic (bf16: 8 bytes per element), with the next tile's loads in flight while a
-// tile is worked on.
+// (a2 a1, a2 b1 + b2).
 //
-// With few (batch row, channel block) pairs the rows are split in chunks: a first pass forms
-// each chunk's composed map, and the second pass starts every chunk from the maps before it.
+// Forward: one pass.  A workgroup of 8 waves takes 32 VC channels (VC neighbouring ones per lane)
+// of kFwdTile rows: each half wave holds a run of 16 rows, forms their a and b in registers, and
+// its run's composed map; halves are joined by a lane exchange, waves through LDS.  The tile's map
+// is published, the state entering the tile is found from the tiles before it (see `look_back`), and
+// every run replays its rows from the state that enters it.  The operands are read once and y is
+// written once: HBM traffic bounds it (bf16: 8 bytes per element, 33 vector instructions).
 //
-// Backward.  g_t = dL/dh_t = dy_t + a_{t+1} g_{t+1}: the same maps from the end.  Run q_t = a_t g_t
-// backward: q -> a (q + dy), so a run's product of a serves both directions.  The states
-// h_{t-1} are rebuilt from those kept every 32 rows.
+// Backward.  g_t = dL/dh_t = dy_t + a_{t+1} g_{t+1}: the same maps from the end.  q_t = a_t g_t runs
+// backward as q -> a (q + dy), so a run's product of a serves both directions.  A workgroup of 4
+// waves walks a chunk of rows in tiles of 32 from its end, the states h_{t-1} rebuilt from those kept
+// every 32 rows, the next tile's loads in flight.  (Its values per row are too many for the forward's
+// way.)  With few (batch row, channel block) pairs the rows are split in chunks: a first pass over
+// r and dy forms each chunk's composed map of q.
 //
 // 1 - a^2 = -expm1(-2 k s) is formed without cancellation: as a gate closes a tends to 1 and
 // the plain difference would lose every digit.
@@ -27,13 +28,13 @@
 namespace ssk {
 namespace {
 
-constexpr int kRunLanes = 32;               // lanes per run: half a wave
-constexpr int kGlrWaves = 4;
-constexpr int kRuns = 2 * kGlrWaves;        // runs per tile
-constexpr int kGlrThreads = 64 * kGlrWaves;
-constexpr int kFwdRows = 8, kBwdRows = 4;   // rows per run
-static_assert(kRuns * kFwdRows == kGlrChunkUnit && kRuns * kBwdRows == kGlrRows, "tiles and kept states");
-static_assert(kGlrRows % kFwdRows == 0 && kGlrChunkUnit % kGlrRows == 0, "a kept state falls on a run's start");
+constexpr int kRunLanes = 32;  // lanes per run: half a wave
+// forward: 8 waves, 16 rows per run
+constexpr int kFwdWaves = 8, kFwdThreads = 64 * kFwdWaves, kFwdRows = 16, kFwdTile = 2 * kFwdWaves * kFwdRows;
+// backward: 4 waves, 4 rows per run
+constexpr int kBwdWaves = 4, kBwdRuns = 2 * kBwdWaves, kBwdThreads = 64 * kBwdWaves, kBwdRows = 4;
+static_assert(kFwdTile == kGlrTile && kBwdRuns * kBwdRows == kGlrRows, "tiles and kept states");
+static_assert(kGlrRows % kFwdRows == 0, "a kept state falls on a run's start");
 
 // VC neighbouring elements of a row as loaded
 template <int DT, int VC>
@@ -183,7 +184,7 @@ __device__ __forceinline__ float carry(float a, float h, float b)
 // The other half wave's value.
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
-// What a workgroup works on.
+// What a workgroup of the backward works on.
 template <int VC>
 struct Place {
     int64_t b, c, d;   // batch row, chunk, first channel of this lane
@@ -206,146 +207,210 @@ struct Place {
 
 // ---- forward -------------------------------------------------------------------------------
 
-// AGG: only each chunk's composed map (ws_prod, ws_end)
-template <int DT, int VC, bool RESET, bool AGG>
-__global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
+// A tile's word for one channel: the state's bits in the low half; above them the product of a
+// (0 <= a <= 1: its two top bits are clear) and two flags.  kMap: the halves are the tile's map.
+// kState: the low half is the state after the tile.  A word is read and written whole, so nothing
+// else has to be ordered with it.  Words start as 0, neither flag set.
+constexpr uint32_t kMap = 0x40000000u, kState = 0x80000000u, kMapBits = 0x3fffffffu;
+constexpr int kWindow = 16;  // tiles looked back over
+
+__device__ __forceinline__ uint64_t word_of(float a, float h, uint32_t flag)
 {
-    constexpr int R = kFwdRows, T = kRuns * R;
+    return (uint64_t((__float_as_uint(a) & kMapBits) | flag) << 32) | __float_as_uint(h);
+}
+__device__ __forceinline__ void put_word(uint64_t* p, uint64_t v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t get_word(const uint64_t* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state after tile `tile` - 1 of this lane's channel; `words`: the channel's word of tile 0,
+// tiles `step` words apart.  Waits until one of the last kWindow tiles has its state and all
+// those after it have their maps, then applies the maps in order: the value is the same whichever
+// tile's state was there first, since every tile forms its state by the same chain.
+// The wait ends: tiles are handed out in order (a tile's predecessors hold a running workgroup or
+// are done), maps are published without waiting for anything, and the earliest unfinished tile
+// finds its predecessor's state.
+template <bool RESET>
+__device__ __forceinline__ float look_back(const uint64_t* words, int64_t step, int64_t tile, bool lane_used)
+{
+    uint64_t w[kWindow];
+    int depth;
+    for (;;) {
+#pragma unroll
+        for (int j = 0; j < kWindow; ++j) w[j] = j < tile && lane_used ? get_word(words + (tile - 1 - j) * step) : 0;
+        depth = -1;
+        bool open = true;
+#pragma unroll
+        for (int j = 0; j < kWindow; ++j) {
+            const uint32_t top = uint32_t(w[j] >> 32);
+            if (open && (top & kState)) depth = j;
+            open = open && !(top & kState) && (top & kMap);
+        }
+        if (__all(depth >= 0 || !lane_used)) break;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    float h = 0.0f;
+#pragma unroll
+    for (int j = kWindow - 1; j >= 0; --j) {
+        const float a = __uint_as_float(uint32_t(w[j] >> 32) & kMapBits), b = __uint_as_float(uint32_t(w[j]));
+        if (j < depth) h = carry<RESET>(a, h, b);
+        if (j == depth) h = b;
+    }
+    return h;
+}
+
+// The words of a call and its ticket, cleared.
+__global__ __launch_bounds__(256) void glr_clear_kernel(uint64_t* words, int64_t count, uint32_t* ticket)
+{
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i < count) words[i] = 0;
+    if (i == 0) *ticket = 0;
+}
+
+template <int DT, int VC, bool RESET>
+__global__ __launch_bounds__(kFwdThreads, 4) void glr_fwd_kernel(GlrArgs a)
+{
+    constexpr int R = kFwdRows, W = kFwdWaves;
     using RW = Row<DT, VC>;
     using Raw = typename RW::Raw;
-    const Place<VC> w(a);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = (threadIdx.x >> 5) & 1, run = wave * 2 + half, l32 = threadIdx.x & 31;
-    const int64_t bd = w.b * a.dim + w.dc;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int half = lane >> 5, run = wave * 2 + half, l32 = lane & 31;
 
-    float k[VC], h[VC], prod[VC];
-#pragma unroll
-    for (int e = 0; e < VC; ++e) {
-        k[e] = channel_rate(a.decay[w.dc + e], a.c);
-        h[e] = AGG || !a.h0 ? 0.0f : a.h0[bd + e];
-        prod[e] = 1.0f;
+    __shared__ float maps[W][2][kRunLanes * VC];  // (product, end) of each wave's rows
+    __shared__ float enter[W][kRunLanes * VC];    // the state entering each wave's rows
+    __shared__ uint32_t turn;
+    uint32_t id = blockIdx.x;
+    if (a.n_tiles > 1) {
+        // tiles in the order in which workgroups start: a tile's predecessors have all started
+        if (threadIdx.x == 0) turn = atomicAdd(a.ws_ticket, 1u);
+        __syncthreads();
+        id = __builtin_amdgcn_readfirstlane(turn);
     }
-    if (!AGG) {
-        for (int64_t c = 0; c < w.c; ++c)
-#pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                const int64_t at = c * a.batch * a.dim + bd + e;
-                h[e] = carry<RESET>(a.ws_prod[at], h[e], a.ws_end[at]);
-            }
-    }
+    const uint32_t cols = uint32_t((a.dim + kRunLanes * VC - 1) / (kRunLanes * VC));
+    const uint32_t units = cols * uint32_t(a.batch);
+    const uint32_t tile = id / units, unit = id % units;
+    const int64_t b = unit / cols, d0 = int64_t(unit % cols) * (kRunLanes * VC);
+    const int64_t d = d0 + l32 * VC, t0 = int64_t(tile) * kFwdTile;
+    const bool live = d < a.dim;
+    const int64_t dc = live ? d : 0;
+    const int rows = int(a.seqlen - t0 < kFwdTile ? a.seqlen - t0 : kFwdTile);
+    const int64_t row0 = b * a.seqlen + t0;
 
-    __shared__ float maps[2][kGlrWaves][2 * VC][kRunLanes];
-    const Rows<DT, VC> px(a.x_ld, w.d, w.live, run * R), pr(a.r_ld, w.d, w.live, run * R),
-        pi(a.i_ld, w.d, w.live, run * R), py(a.dim, w.d, w.live, run * R);
-    const int64_t row0 = w.b * a.seqlen;
+    float k[VC];
+#pragma unroll
+    for (int e = 0; e < VC; ++e) k[e] = channel_rate(a.decay[dc + e], a.c);
+    const Rows<DT, VC> px(a.x_ld, d, live, run * R), pr(a.r_ld, d, live, run * R), pi(a.i_ld, d, live, run * R);
+    const auto br = pr.tile(a.r, row0, rows), bi = pi.tile(a.i, row0, rows), bx = px.tile(a.x, row0, rows);
+
+    float av[R][VC], bv[R][VC];
     Raw rx[R], rr[R], ri[R];
-    uint8_t rs[R];
-    auto load = [&](int64_t tile) {
-        const int rows = int(w.t1 - tile < T ? w.t1 - tile : T);
-        const auto br = pr.tile(a.r, row0 + tile, rows), bi = pi.tile(a.i, row0 + tile, rows),
-                   bx = px.tile(a.x, row0 + tile, rows);
+    bool rs[R];
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            rr[q] = pr.load(br, q);
-            ri[q] = pi.load(bi, q);
-            rx[q] = px.load(bx, q);
-            if (RESET) {
-                const int64_t t = tile + run * R + q;
-                rs[q] = a.reset[row0 + (t < a.seqlen ? t : a.seqlen - 1)];
+    for (int q = 0; q < R; ++q) {
+        rr[q] = pr.load(br, q);
+        ri[q] = pi.load(bi, q);
+        rx[q] = px.load(bx, q);
+        if (RESET) rs[q] = a.reset[row0 + (run * R + q < rows ? run * R + q : 0)] != 0;
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+            float ww;
+            decay_of(k[e], sigmoid1(RW::get(rr[q], e)), &av[q][e], &ww);
+            float m = __builtin_amdgcn_sqrtf(ww);
+            if (RESET && rs[q]) {
+                av[q][e] = 0.0f;
+                m = 1.0f;
             }
+            bv[q][e] = m * sigmoid1(RW::get(ri[q], e)) * RW::get(rx[q], e);
         }
-    };
-    load(w.t0);
-    int buf = 0;
-    for (int64_t tile = w.t0; tile < w.t1; tile += T, buf ^= 1) {
-        const int rows = int(w.t1 - tile < T ? w.t1 - tile : T);
-        float av[R][VC], bv[R][VC], P[VC], E[VC];
+    if (rows < kFwdTile) {
+        // rows past the end leave the state as it is
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
-                float ww;
-                decay_of(k[e], sigmoid1(RW::get(rr[q], e)), &av[q][e], &ww);
-                float m = __builtin_amdgcn_sqrtf(ww);
-                if (RESET && rs[q]) {
-                    av[q][e] = 0.0f;
-                    m = 1.0f;
-                }
-                bv[q][e] = m * sigmoid1(RW::get(ri[q], e)) * RW::get(rx[q], e);
+                av[q][e] = run * R + q < rows ? av[q][e] : 1.0f;
+                bv[q][e] = run * R + q < rows ? bv[q][e] : 0.0f;
             }
-        if (rows < T) {
-            // rows past the end leave the state as it is
-#pragma unroll
-            for (int q = 0; q < R; ++q)
-#pragma unroll
-                for (int e = 0; e < VC; ++e) {
-                    av[q][e] = run * R + q < rows ? av[q][e] : 1.0f;
-                    bv[q][e] = run * R + q < rows ? bv[q][e] : 0.0f;
-                }
-        }
-        if (tile + T < w.t1) load(tile + T);
-#pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            P[e] = av[0][e];
-            E[e] = bv[0][e];
-#pragma unroll
-            for (int q = 1; q < R; ++q) {
-                P[e] *= av[q][e];
-                E[e] = carry<RESET>(av[q][e], E[e], bv[q][e]);
-            }
-        }
-        // join the halves of the wave; the earlier half publishes the wave's map
-        float P0[VC], E0[VC];
-#pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            P0[e] = other_half(P[e]);
-            E0[e] = other_half(E[e]);
-            if (half == 0) {
-                maps[buf][wave][2 * e][l32] = P0[e] * P[e];
-                maps[buf][wave][2 * e + 1][l32] = carry<RESET>(P0[e], E[e], E0[e]);
-            }
-        }
-        __syncthreads();
-        float in[VC];
-#pragma unroll
-        for (int v = 0; v < kGlrWaves; ++v) {
-#pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                if (!AGG && v == wave) in[e] = h[e];
-                const float p = maps[buf][v][2 * e][l32];
-                h[e] = carry<RESET>(p, h[e], maps[buf][v][2 * e + 1][l32]);
-                if (AGG) prod[e] *= p;
-            }
-        }
-        if (!AGG) {
-#pragma unroll
-            for (int e = 0; e < VC; ++e)
-                if (half == 1) in[e] = carry<RESET>(P0[e], in[e], E0[e]);
-            if (a.ckpt && (run * R) % kGlrRows == 0 && run * R < rows && w.live) {
-                const int64_t at = ((tile + run * R) / kGlrRows) * a.batch * a.dim + bd;
-#pragma unroll
-                for (int e = 0; e < VC; ++e) a.ckpt[at + e] = in[e];
-            }
-            if (a.y) {
-                const auto by = py.tile(a.y, row0 + tile, rows);
-#pragma unroll
-                for (int q = 0; q < R; ++q) {
-#pragma unroll
-                    for (int e = 0; e < VC; ++e) in[e] = carry<RESET>(av[q][e], in[e], bv[q][e]);
-                    py.store(by, q, in);
-                }
-            }
-        }
     }
-    if (run != 0 || !w.live) return;
+    // the run's map, then the wave's; the earlier half publishes it
+    float P[VC], E[VC], P0[VC], E0[VC];
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
-        if (AGG) {
-            const int64_t at = w.c * a.batch * a.dim + bd + e;
-            a.ws_prod[at] = prod[e];
-            a.ws_end[at] = h[e];
-        } else if (a.h_last && w.c == a.n_chunks - 1) {
-            a.h_last[bd + e] = h[e];
+        P[e] = av[0][e];
+        E[e] = bv[0][e];
+#pragma unroll
+        for (int q = 1; q < R; ++q) {
+            P[e] = carry<RESET>(av[q][e], P[e], 0.0f);
+            E[e] = carry<RESET>(av[q][e], E[e], bv[q][e]);
+        }
+        P0[e] = other_half(P[e]);
+        E0[e] = other_half(E[e]);
+        if (half == 0) {
+            maps[wave][0][l32 * VC + e] = carry<RESET>(P0[e], P[e], 0.0f);
+            maps[wave][1][l32 * VC + e] = carry<RESET>(P0[e], E[e], E0[e]);
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {
+        // one channel per lane from here on
+        const bool used = lane < kRunLanes * VC;
+        const int ch = used ? lane : 0;
+        const int64_t at = d0 + ch, state = b * a.dim + at;
+        const bool exists = used && at < a.dim;
+        float A = 1.0f, S = 0.0f, h;
+#pragma unroll
+        for (int v = 0; v < W; ++v) {
+            const float p = maps[v][0][ch];
+            A = carry<RESET>(p, A, 0.0f);
+            S = carry<RESET>(p, S, maps[v][1][ch]);
+        }
+        const int64_t step = int64_t(units) * (kRunLanes * VC);
+        uint64_t* const words = a.ws_words + int64_t(unit) * (kRunLanes * VC) + ch;
+        if (tile == 0) {
+            h = a.h0 && exists ? a.h0[state] : 0.0f;
+        } else {
+            if (used) put_word(words + tile * step, word_of(A, S, kMap));
+            h = look_back<RESET>(words, step, tile, used);
+        }
+        const float after = carry<RESET>(A, h, S);
+        if (tile + 1 < a.n_tiles) {
+            if (used) put_word(words + tile * step, word_of(0.0f, after, kState));
+        } else if (a.h_last && exists) {
+            a.h_last[state] = after;
+        }
+#pragma unroll
+        for (int v = 0; v < W; ++v) {
+            if (used) enter[v][ch] = h;
+            h = carry<RESET>(maps[v][0][ch], h, maps[v][1][ch]);
+        }
+    }
+    __syncthreads();
+    float in[VC];
+#pragma unroll
+    for (int e = 0; e < VC; ++e) {
+        in[e] = enter[wave][l32 * VC + e];
+        if (half == 1) in[e] = carry<RESET>(P0[e], in[e], E0[e]);
+    }
+    if (a.ckpt && (run * R) % kGlrRows == 0 && run * R < rows && live) {
+        const int64_t at = ((t0 + run * R) / kGlrRows * a.batch + b) * a.dim + d;
+#pragma unroll
+        for (int e = 0; e < VC; ++e) a.ckpt[at + e] = in[e];
+    }
+    if (a.y) {
+        const Rows<DT, VC> py(a.dim, d, live, run * R);
+        const auto by = py.tile(a.y, row0, rows);
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+#pragma unroll
+            for (int e = 0; e < VC; ++e) in[e] = carry<RESET>(av[q][e], in[e], bv[q][e]);
+            py.store(by, q, in);
         }
     }
 }
@@ -354,9 +419,9 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(GlrArgs a)
 
 // AGG: only each chunk's composed map of q, from r and dy (ws_prod, ws_end)
 template <int DT, int VC, bool RESET, bool AGG>
-__global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrArgs a)
+__global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrArgs a)
 {
-    constexpr int R = kBwdRows, T = kRuns * R;
+    constexpr int R = kBwdRows, T = kBwdRuns * R;
     using RW = Row<DT, VC>;
     using Raw = typename RW::Raw;
     const Place<VC> w(a);
@@ -381,7 +446,7 @@ __global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
             }
     }
 
-    __shared__ float maps[2][kGlrWaves][3 * VC][kRunLanes];
+    __shared__ float maps[2][kBwdWaves][3 * VC][kRunLanes];
     const Rows<DT, VC> px(a.x_ld, w.d, w.live, run * R), pr(a.r_ld, w.d, w.live, run * R),
         pi(a.i_ld, w.d, w.live, run * R), pd(a.dim, w.d, w.live, run * R), pg(a.g_ld, w.d, w.live, run * R);
     const int64_t row0 = w.b * a.seqlen;
@@ -457,7 +522,7 @@ __global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
             if (!AGG) E[e] = bv[0][e];
 #pragma unroll
             for (int j = 1; j < R; ++j) {
-                P[e] *= av[j][e];
+                P[e] = carry<RESET>(av[j][e], P[e], 0.0f);
                 if (!AGG) E[e] = carry<RESET>(av[j][e], E[e], bv[j][e]);
             }
             Q[e] = carry<RESET>(av[R - 1][e], dy[R - 1][e], 0.0f);
@@ -472,7 +537,7 @@ __global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
             Qo[e] = other_half(Q[e]);
             if (!AGG) Eo[e] = other_half(E[e]);
             if (half == 0) {
-                maps[buf][wave][3 * e][l32] = Po[e] * P[e];
+                maps[buf][wave][3 * e][l32] = carry<RESET>(Po[e], P[e], 0.0f);
                 maps[buf][wave][3 * e + 1][l32] = carry<RESET>(P[e], Qo[e], Q[e]);
                 if (!AGG) maps[buf][wave][3 * e + 2][l32] = carry<RESET>(Po[e], E[e], Eo[e]);
             }
@@ -481,7 +546,7 @@ __global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
         float hin[VC], qin[VC];
         if (!AGG) {
 #pragma unroll
-            for (int v = 0; v < kGlrWaves - 1; ++v)
+            for (int v = 0; v < kBwdWaves - 1; ++v)
                 if (v < wave) {
 #pragma unroll
                     for (int e = 0; e < VC; ++e)
@@ -491,13 +556,13 @@ __global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
             for (int e = 0; e < VC; ++e) hin[e] = half == 1 ? carry<RESET>(Po[e], h[e], Eo[e]) : h[e];
         }
 #pragma unroll
-        for (int v = kGlrWaves - 1; v >= 0; --v)
+        for (int v = kBwdWaves - 1; v >= 0; --v)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
                 if (!AGG && v == wave) qin[e] = q[e];
                 const float p = maps[buf][v][3 * e][l32];
                 q[e] = carry<RESET>(p, q[e], maps[buf][v][3 * e + 1][l32]);
-                if (AGG) prod[e] *= p;
+                if (AGG) prod[e] = carry<RESET>(p, prod[e], 0.0f);
             }
         if (!AGG) {
             float before[R][VC];  // h_{t-1}
@@ -547,7 +612,7 @@ __global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
     // the runs' sums over their rows, joined in a fixed order
     __syncthreads();
     float* const sums = &maps[0][0][0][0];
-    static_assert(kRuns * VC <= 2 * kGlrWaves * 3 * VC, "fits the maps' space");
+    static_assert(kBwdRuns * VC <= 2 * kBwdWaves * 3 * VC, "fits the maps' space");
 #pragma unroll
     for (int e = 0; e < VC; ++e) sums[(run * VC + e) * kRunLanes + l32] = dk[e];
     __syncthreads();
@@ -555,7 +620,7 @@ __global__ __launch_bounds__(kGlrThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
         float s = 0.0f;
-        for (int v = 0; v < kRuns; ++v) s += sums[(v * VC + e) * kRunLanes + l32];
+        for (int v = 0; v < kBwdRuns; ++v) s += sums[(v * VC + e) * kRunLanes + l32];
         a.part_decay[w.c * a.batch * a.dim + bd + e] = s;
         if (a.dh0 && w.c == 0) a.dh0[bd + e] = q[e];
     }
@@ -613,14 +678,14 @@ template <int DT, int VC, bool RESET>
 hipError_t fwd_variant(const GlrArgs& a, hipStream_t s)
 {
     const int64_t cols = (a.dim + kRunLanes * VC - 1) / (kRunLanes * VC);
-    const int64_t blocks = cols * a.batch * a.n_chunks;
-    if (a.n_chunks > 1) {
-        // the last chunk's map leads nowhere
-        glr_fwd_kernel<DT, VC, RESET, true><<<dim3(unsigned(blocks - cols * a.batch)), dim3(kGlrThreads), 0, s>>>(a);
+    const int64_t blocks = cols * a.batch * a.n_tiles;
+    if (a.n_tiles > 1) {
+        const int64_t words = blocks * (kRunLanes * VC);
+        glr_clear_kernel<<<dim3(unsigned((words + 255) / 256)), dim3(256), 0, s>>>(a.ws_words, words, a.ws_ticket);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    glr_fwd_kernel<DT, VC, RESET, false><<<dim3(unsigned(blocks)), dim3(kGlrThreads), 0, s>>>(a);
+    glr_fwd_kernel<DT, VC, RESET><<<dim3(unsigned(blocks)), dim3(kFwdThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -630,11 +695,11 @@ hipError_t bwd_variant(const GlrArgs& a, hipStream_t s)
     const int64_t cols = (a.dim + kRunLanes * VC - 1) / (kRunLanes * VC);
     const int64_t blocks = cols * a.batch * a.n_chunks;
     if (a.n_chunks > 1) {
-        glr_bwd_kernel<DT, VC, RESET, true><<<dim3(unsigned(blocks)), dim3(kGlrThreads), 0, s>>>(a);
+        glr_bwd_kernel<DT, VC, RESET, true><<<dim3(unsigned(blocks)), dim3(kBwdThreads), 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    glr_bwd_kernel<DT, VC, RESET, false><<<dim3(unsigned(blocks)), dim3(kGlrThreads), 0, s>>>(a);
+    glr_bwd_kernel<DT, VC, RESET, false><<<dim3(unsigned(blocks)), dim3(kBwdThreads), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     glr_decay_kernel<<<dim3(unsigned((a.dim + 63) / 64)), dim3(64), 0, s>>>(a);

@@ -80,15 +80,16 @@ bool any_overlap(const Range* outputs, size_t n_out, const Range* inputs, size_t
 
 // ---- gated linear recurrence ------------------------------------------------------------
 
-constexpr int64_t kGlrCols = 64;          // channels per workgroup
-// Fewer one-chunk workgroups than kGlrWhole leave CUs idle: the rows are then cut until there
-// are kGlrTarget workgroups, in chunks of at least kGlrMinChunk rows (the cut costs a pass over
-// the operands) and at most kGlrMaxChunks of them (a chunk joins its predecessors' maps itself).
-constexpr int64_t kGlrWhole = 256, kGlrTarget = 1024, kGlrMinChunk = 512, kGlrMaxChunks = 64;
+constexpr int64_t kGlrCols = 64;  // channels per workgroup
+// The backward with fewer one-chunk workgroups than kGlrWhole leaves CUs idle: the rows are then
+// cut until there are kGlrTarget workgroups, in chunks of at least kGlrMinChunk rows (the cut
+// costs a pass over r and dy) and at most kGlrMaxChunks of them (a chunk joins the maps of those
+// after it itself).
+constexpr int64_t kGlrWhole = 256, kGlrTarget = 768, kGlrMinChunk = 128, kGlrMaxChunks = 64;
 
 void glr_plan(int64_t batch, int64_t seqlen, int64_t dim, int64_t* len, int64_t* chunks)
 {
-    const int64_t unit = ssk::kGlrChunkUnit;
+    const int64_t unit = ssk::kGlrRows;
     const int64_t blocks = batch * ceil_div(dim, kGlrCols);
     int64_t k = 1;
     if (blocks < kGlrWhole) {
@@ -103,7 +104,8 @@ void glr_plan(int64_t batch, int64_t seqlen, int64_t dim, int64_t* len, int64_t*
 }
 
 struct GlrLayout {
-    int64_t len, chunks, prod, end, part, ckpt, total;
+    int64_t len, chunks, tiles;
+    int64_t ticket, words, prod, end, part, ckpt, total;
 };
 
 bool glr_sizes(int64_t batch, int64_t seqlen, int64_t dim)
@@ -112,12 +114,20 @@ bool glr_sizes(int64_t batch, int64_t seqlen, int64_t dim)
     return batch > 0 && seqlen > 0 && dim > 0 && mul(batch, seqlen, &n) && mul(n, dim, &n) && mul(n, 4, &n);
 }
 
+// The forward's part is there for the forward, and for a backward without kept states.
 bool glr_layout(int64_t batch, int64_t seqlen, int64_t dim, bool back, bool with_ckpt, GlrLayout* w)
 {
     if (!glr_sizes(batch, seqlen, dim)) return false;
     glr_plan(batch, seqlen, dim, &w->len, &w->chunks);
+    w->tiles = ceil_div(seqlen, ssk::kGlrTile);
     Regions r;
-    const int64_t maps = w->chunks > 1 ? w->chunks * batch * dim : 0;
+    int64_t words = 0;
+    if ((!back || !with_ckpt) && w->tiles > 1 &&
+        (!mul(w->tiles * batch, ceil_div(dim, kGlrCols), &words) || !mul(words, kGlrCols, &words)))
+        return false;
+    w->ticket = r.add(words ? 1 : 0, 4);
+    w->words = r.add(words, 8);
+    const int64_t maps = back && w->chunks > 1 ? w->chunks * batch * dim : 0;
     w->prod = r.add(maps, 4);
     w->end = r.add(maps, 4);
     w->part = r.add(back ? w->chunks * batch * dim : 0, 4);
@@ -126,10 +136,11 @@ bool glr_layout(int64_t batch, int64_t seqlen, int64_t dim, bool back, bool with
     return r.ok;
 }
 
-bool glr_grid_ok(int64_t batch, int64_t dim, int64_t chunks)
+bool glr_grid_ok(int64_t batch, int64_t dim, const GlrLayout& w)
 {
-    int64_t n;
-    return mul(batch, ceil_div(dim, kGlrCols / 2), &n) && mul(n, chunks, &n) && n <= INT32_MAX;
+    int64_t n, m;
+    return mul(batch, ceil_div(dim, kGlrCols / 2), &n) && mul(n, w.chunks, &m) && m <= INT32_MAX && mul(n, w.tiles, &m) &&
+           m <= INT32_MAX;
 }
 
 bool glr_too_wide(int64_t a, int64_t b, int64_t c, int64_t d)
@@ -172,7 +183,7 @@ ss_status ss_glr_fwd(const void* x, int64_t x_row_stride, const void* r, int64_t
     if (x_row_stride < dim || r_row_stride < dim || i_row_stride < dim) return SS_ERR_INVALID_ARG;
     if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
     if (!known(dtype)) return SS_ERR_UNSUPPORTED;
-    if (!glr_grid_ok(batch, dim, w.chunks) || glr_too_wide(x_row_stride, r_row_stride, i_row_stride, dim))
+    if (!glr_grid_ok(batch, dim, w) || glr_too_wide(x_row_stride, r_row_stride, i_row_stride, dim))
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {x, r, i, y};
@@ -209,15 +220,14 @@ ss_status ss_glr_fwd(const void* x, int64_t x_row_stride, const void* r, int64_t
     a.y = y;
     a.h_last = h_last;
     a.ckpt = ckpt;
-    if (w.chunks > 1) {
-        a.ws_prod = reinterpret_cast<float*>(ws + w.prod);
-        a.ws_end = reinterpret_cast<float*>(ws + w.end);
+    if (w.tiles > 1) {
+        a.ws_words = reinterpret_cast<uint64_t*>(ws + w.words);
+        a.ws_ticket = reinterpret_cast<uint32_t*>(ws + w.ticket);
     }
     a.batch = batch;
     a.seqlen = seqlen;
     a.dim = dim;
-    a.chunk_len = w.len;
-    a.n_chunks = w.chunks;
+    a.n_tiles = w.tiles;
     return done(ssk::launch_glr_fwd(a, dtype == SS_F32 ? 0 : 1, stream));
 }
 
@@ -234,7 +244,7 @@ ss_status ss_glr_bwd(const void* x, int64_t x_row_stride, const void* r, int64_t
         return SS_ERR_INVALID_ARG;
     if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
     if (!known(dtype)) return SS_ERR_UNSUPPORTED;
-    if (!glr_grid_ok(batch, dim, w.chunks) || glr_too_wide(x_row_stride, r_row_stride, i_row_stride, grad_row_stride))
+    if (!glr_grid_ok(batch, dim, w) || glr_too_wide(x_row_stride, r_row_stride, i_row_stride, grad_row_stride))
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {x, r, i, dy, dx, dr, di};
@@ -280,9 +290,14 @@ ss_status ss_glr_bwd(const void* x, int64_t x_row_stride, const void* r, int64_t
         a.ws_prod = reinterpret_cast<float*>(ws + w.prod);
         a.ws_end = reinterpret_cast<float*>(ws + w.end);
     }
+    if (!ckpt && w.tiles > 1) {
+        a.ws_words = reinterpret_cast<uint64_t*>(ws + w.words);
+        a.ws_ticket = reinterpret_cast<uint32_t*>(ws + w.ticket);
+    }
     a.batch = batch;
     a.seqlen = seqlen;
     a.dim = dim;
+    a.n_tiles = w.tiles;
     a.chunk_len = w.len;
     a.n_chunks = w.chunks;
     // the kept states: only read from here on when they are the caller's

@@ -76,13 +76,13 @@ hipError_t launch_xent_bwd(const XentArgs& a, int dtype, hipStream_t stream);
 
 // ---- gated linear recurrence ------------------------------------------------------------
 
-// Rows between two kept states, which is also the backward's tile: it rebuilds a
-// tile's states from the one that enters it.
+// Rows between two kept states, which is also the backward's tile: it rebuilds a tile's states
+// from the one that enters it.  The backward's chunks are whole tiles.
 constexpr int64_t kGlrRows = 32;
-// Chunks are whole forward tiles.
-constexpr int64_t kGlrChunkUnit = 64;
+// Rows of a forward tile.
+constexpr int64_t kGlrTile = 256;
 // Longest row stride, in elements: a tile stays below 2^31 bytes.
-constexpr int64_t kGlrMaxStride = int64_t(1) << 22;
+constexpr int64_t kGlrMaxStride = int64_t(1) << 20;
 
 struct GlrArgs {
     const void* x;  // (batch, seqlen, dim), rows *_ld elements apart
@@ -95,13 +95,17 @@ struct GlrArgs {
     const uint8_t* reset;  // (batch, seqlen), nullable
     void* y;               // (batch, seqlen, dim); null: only the states are wanted
     float* h_last;         // (batch, dim), nullable
-    float* ckpt;           // (ceil(seqlen / kGlrRows), batch, dim) states entering each tile, nullable
-    // the split plan (n_chunks > 1): per chunk and channel the affine map of the chunk
+    float* ckpt;           // (ceil(seqlen / kGlrRows), batch, dim) states entering every kGlrRows-th row, nullable
+    // forward with more than one tile: a word per tile and channel (channels rounded up to
+    // whole workgroups), and the next tile to be taken
+    uint64_t* ws_words;
+    uint32_t* ws_ticket;
+    int64_t batch, seqlen, dim;
+    int64_t n_tiles;       // ceil(seqlen / kGlrTile)
+    // backward; n_chunks > 1: per chunk and channel the affine map of the chunk
     float* ws_prod;        // (n_chunks, batch, dim)
     float* ws_end;         // (n_chunks, batch, dim)
-    int64_t batch, seqlen, dim;
-    int64_t chunk_len, n_chunks;  // chunk_len a multiple of kGlrChunkUnit
-    // backward
+    int64_t chunk_len, n_chunks;  // chunk_len a multiple of kGlrRows
     const void* dy;        // (batch, seqlen, dim)
     const float* dh_last;  // (batch, dim), nullable
     void* dx;              // (batch, seqlen, dim), rows g_ld elements apart

@@ -211,13 +211,16 @@ def test_nonfinite_rows_stay_in_their_sequence():
     rng = np.random.default_rng(4)
     v = [rng.standard_normal((b, l, d)).astype(np.float32) for _ in range(3)]
     v[0][1, 50, 7] = np.nan
+    v[1][0, 30, 9] = np.nan  # a gate: the row's decay is NaN too
     reset = np.zeros((b, l), np.uint8)
     reset[1, 120] = 1
+    reset[0, 41] = 1
     say("glr nan")
     y = host64(ss().glr_fwd(*[dev(a) for a in v], dev(decays(rng, d)), reset=tdev(reset)))
     bad = np.isnan(y)
     want = np.zeros_like(bad)
     want[1, 50:120, 7] = True
+    want[0, 30:41, 9] = True
     assert np.array_equal(bad, want)
 
 

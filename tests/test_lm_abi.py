@@ -130,8 +130,8 @@ REFUSED = [
     *[(f, {n: 63}, INVALID) for f in (glr_fwd, glr_bwd, glr_step) for n in ("xs", "rs", "is_")],
     (glr_bwd, dict(gs=63), INVALID),
     (glr_fwd, dict(xs=1 << 62), UNSUPPORTED),
-    (glr_fwd, dict(rs=(1 << 22) + 1), UNSUPPORTED),
-    (glr_bwd, dict(gs=(1 << 22) + 1), UNSUPPORTED),
+    (glr_fwd, dict(rs=(1 << 20) + 1), UNSUPPORTED),
+    (glr_bwd, dict(gs=(1 << 20) + 1), UNSUPPORTED),
     (glu_fwd, dict(xs=63), INVALID),
     (glu_fwd, dict(xs=68), INVALID),   # rows off a 16-byte boundary
     (xent_fwd, dict(xs=68), INVALID),
@@ -199,7 +199,7 @@ def test_refused_on_the_host(lib, case):
 def test_sizes(lib):
     assert lib.ss_glr_ckpt_bytes(2, 65, 10) == 3 * 2 * 10 * 4
     assert lib.ss_glr_ckpt_bytes(0, 1, 1) == BAD
-    assert lib.ss_glr_workspace_bytes(8, 2048, 5120) == 0, "enough workgroups: one chunk"
+    assert lib.ss_glr_workspace_bytes(8, 256, 5120) == 0, "one tile of rows"
     assert lib.ss_glr_workspace_bytes(1, 1, 1) == 0
     assert lib.ss_glr_workspace_bytes(1, 131072, 2048) > 0
     for q in (0, 1):
