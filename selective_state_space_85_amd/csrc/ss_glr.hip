@@ -48,7 +48,8 @@ struct Row<1, 2> {
     }
     static __device__ __forceinline__ Raw make(const float (&v)[2])
     {
-        return uint32_t(f32_to_bf16_bits(v[0])) | (uint32_t(f32_to_bf16_bits(v[1])) << 16);
+        typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(Raw, Pair{__bf16(v[0]), __bf16(v[1])});  // one instruction
     }
     static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff)
     {
@@ -500,16 +501,22 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
                 if (!AGG) {
                     c1[j][e] = __builtin_amdgcn_sqrtf(ww) * sigmoid2(RW::get(ri[j], e), &ni[j][e]);
                     bv[j][e] = c1[j][e] * RW::get(rx[j], e);
-                    // where w underflows (the gate shut), bv is 0 and so is the slope's part
-                    slope[j][e] = av[j][e] * bv[j][e] * __builtin_amdgcn_rcpf(fmaxf(ww, 1.1754944e-38f));
+                    // where w underflows (the gate shut), bv is 0 and so is the slope's part: the
+                    // least normal number beside w changes nothing else
+                    slope[j][e] = av[j][e] * bv[j][e] * __builtin_amdgcn_rcpf(ww + 1.1754944e-38f);
                 }
             }
         if (rows < T) {
-            // rows past the end pass q on as it is; their dy, and x, read as 0
+            // rows past the end pass q on as it is and add nothing to the decay's gradient; their dy,
+            // and x, read as 0
 #pragma unroll
             for (int j = 0; j < R; ++j)
 #pragma unroll
-                for (int e = 0; e < VC; ++e) av[j][e] = run * R + j < rows ? av[j][e] : 1.0f;
+                for (int e = 0; e < VC; ++e) {
+                    const bool in = run * R + j < rows;
+                    av[j][e] = in ? av[j][e] : 1.0f;
+                    sr[j][e] = in ? sr[j][e] : 0.0f;
+                }
         }
         if (!AGG) {
 #pragma unroll
@@ -591,7 +598,7 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
                     const float through = before[j][e] - slope[j][e];
                     const float dls = carry<RESET>(av[j][e], g * through, 0.0f) * sr[j][e];
                     dr[e] = -k[e] * dls * nr[j][e];
-                    dk[e] += rows < T && run * R + j >= rows ? 0.0f : dls;
+                    dk[e] += dls;
                 }
                 pg.store(bx, j, dx);
                 pg.store(br, j, dr);
@@ -626,13 +633,23 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
     }
 }
 
-// ddecay = -c sigmoid(decay) sum of the parts: one channel per thread, in a fixed order
-__global__ __launch_bounds__(64) void glr_decay_kernel(GlrArgs a)
+// ddecay = -c sigmoid(decay) sum of the parts, in a fixed order: 16 channels per workgroup, 16
+// threads each, every 16th part per thread.
+constexpr int kSumCols = 16, kSumParts = 16;
+__global__ __launch_bounds__(kSumCols * kSumParts) void glr_decay_kernel(GlrArgs a)
 {
-    const int64_t d = int64_t(blockIdx.x) * 64 + threadIdx.x;
-    if (d >= a.dim) return;
+    __shared__ float sums[kSumParts][kSumCols];
+    const int c = threadIdx.x % kSumCols, p = threadIdx.x / kSumCols;
+    const int64_t d = int64_t(blockIdx.x) * kSumCols + c, parts = a.n_chunks * a.batch;
     float s = 0.0f;
-    for (int64_t j = 0; j < a.n_chunks * a.batch; ++j) s += a.part_decay[j * a.dim + d];
+    if (d < a.dim)
+        for (int64_t j = p; j < parts; j += kSumParts) s += a.part_decay[j * a.dim + d];
+    sums[p][c] = s;
+    __syncthreads();
+    if (p != 0 || d >= a.dim) return;
+    s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kSumParts; ++v) s += sums[v][c];
     float rest;
     a.ddecay[d] = -a.c * sigmoid2(a.decay[d], &rest) * s;
 }
@@ -702,7 +719,7 @@ hipError_t bwd_variant(const GlrArgs& a, hipStream_t s)
     glr_bwd_kernel<DT, VC, RESET, false><<<dim3(unsigned(blocks)), dim3(kBwdThreads), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    glr_decay_kernel<<<dim3(unsigned((a.dim + 63) / 64)), dim3(64), 0, s>>>(a);
+    glr_decay_kernel<<<dim3(unsigned((a.dim + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumParts), 0, s>>>(a);
     return hipGetLastError();
 }
 
