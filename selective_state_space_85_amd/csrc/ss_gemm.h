@@ -8,6 +8,7 @@
 // operand is stored with k contiguous (KC: rows of A or B) or with m/n contiguous (MC:
 // the transpose), so products with a transposed operand need no transposing pass: the MC
 // fragments are read from LDS with the transposing read (bf16) or element by element (fp32).
+// All products are bf16 ones; fp32 operands are split into three bf16 parts (see MM<0>).
 //
 // LDS swizzle.  The direct load writes lane i's 16 bytes at base + 16 i, so a permutation of
 // a row's 16-byte chunks has to be applied to the source address instead:
@@ -49,11 +50,8 @@ template <>
 struct MM<1> {  // bf16 operands
     using T = __bf16;
     using Frag = bf16x8;
-    static constexpr int kEpc = 8;  // elements per 16-byte chunk
-    static __device__ __forceinline__ f32x4 mul(Frag b, Frag a, f32x4 c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
-    }
+    static constexpr int kEpc = 8;    // elements per 16-byte chunk
+    static constexpr int kSteps = 2;  // fragments' depths per k tile
     // fragment of rows [r0, r0 + 16) and chunks [4 kk, 4 kk + 4) of a KC tile
     static __device__ __forceinline__ Frag read_kc(const char* tile, int r0, int kk, int lane)
     {
@@ -82,39 +80,72 @@ struct MM<1> {  // bf16 operands
     static __device__ __forceinline__ T narrow(float v) { return __bf16(v); }
 };
 
+// fp32 operands.  An operand is the sum of three bf16 parts, each the rounding of what the ones
+// before it leave: 24 bits and more.  A product is formed from the six products of parts that
+// matter, smallest first (those left out are below 2^-26 of it), accumulated in fp32: as exact as
+// fp32 arithmetic, at a sixth of bf16's rate where the fp32 matrix instruction has a sixteenth.
+// An infinite operand gives NaN (its later parts are inf - inf).
 template <>
-struct MM<0> {  // fp32 operands
+struct MM<0> {
     using T = float;
-    using Frag = f32x4;
+    struct Frag {
+        f32x4 lo, hi;  // 8 k of one row
+    };
+    struct Parts {
+        bf16x8 p[3];
+    };
     static constexpr int kEpc = 4;
-    // k is taken in the order (k % 4) * 4 + k / 4 within a fragment's 16, on both sides alike
-    static __device__ __forceinline__ f32x4 mul(Frag b, Frag a, f32x4 c)
+    static constexpr int kSteps = 1;
+    static __device__ __forceinline__ Frag read_kc(const char* tile, int r0, int, int lane)
     {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j], a[j], c, 0, 0, 0);
-        return c;
+        const int row = r0 + (lane & 15), c = (lane >> 4) * 2;
+        const char* p = tile + row * 128;
+        return {*reinterpret_cast<const f32x4*>(p + (c ^ (row & 7)) * 16),
+                *reinterpret_cast<const f32x4*>(p + ((c + 1) ^ (row & 7)) * 16)};
     }
-    static __device__ __forceinline__ Frag read_kc(const char* tile, int r0, int kk, int lane)
-    {
-        const int row = r0 + (lane & 15);
-        const int c = (kk * 4 + (lane >> 4)) ^ (row & 7);
-        return *reinterpret_cast<const Frag*>(tile + row * 128 + c * 16);
-    }
-    static __device__ __forceinline__ int mc_idx(int k) { return (k >> 2) & 3; }
+    static __device__ __forceinline__ int mc_idx(int k) { return (k >> 3) & 3; }
     template <int COLS>
-    static __device__ __forceinline__ Frag read_mc(const char* tile, int r0, int kk, int lane)
+    static __device__ __forceinline__ Frag read_mc(const char* tile, int r0, int, int lane)
     {
-        const int k = kk * 16 + (lane >> 4) * 4;
+        const int k = (lane >> 4) * 8;
         const int gran = (r0 >> 4) ^ (mc_idx(k) & (COLS / 16 - 1));
         const float* p = reinterpret_cast<const float*>(tile) + k * COLS + gran * 16 + (lane & 15);
         Frag v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = p[j * COLS];
+        for (int j = 0; j < 4; ++j) {
+            v.lo[j] = p[j * COLS];
+            v.hi[j] = p[(j + 4) * COLS];
+        }
         return v;
+    }
+    static __device__ __forceinline__ Parts split(const Frag& f)
+    {
+        typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+        typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+        U4 out[3];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // two elements at a time: they are rounded, and packed, by one instruction
+            float v0 = j < 2 ? f.lo[2 * j] : f.hi[2 * j - 4], v1 = j < 2 ? f.lo[2 * j + 1] : f.hi[2 * j - 3];
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                const uint32_t u = __builtin_bit_cast(uint32_t, Pair{__bf16(v0), __bf16(v1)});
+                out[q][j] = u;
+                v0 -= __uint_as_float(u << 16);
+                v1 -= __uint_as_float(u & 0xffff0000u);
+            }
+        }
+        return {{__builtin_bit_cast(bf16x8, out[0]), __builtin_bit_cast(bf16x8, out[1]),
+                 __builtin_bit_cast(bf16x8, out[2])}};
     }
     static __device__ __forceinline__ float widen(T v) { return v; }
     static __device__ __forceinline__ T narrow(float v) { return v; }
 };
+
+__device__ __forceinline__ f32x4 mfma_bf16(bf16x8 b, bf16x8 a, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
 
 // The order of the tiles.  Workgroups go to the 8 XCDs in turn, each with an L2 of its own:
 // run_of gives each XCD one contiguous run of the order, and the order walks columns of kGroupM
@@ -140,7 +171,7 @@ __device__ __forceinline__ void tile_at(uint32_t at, uint32_t ntm, uint32_t ntn,
 // idle; when at most half of them are left with work, halves of its tiles take half the time.
 struct TilePlan {
     uint32_t ntm, ntn, whole, split;
-    uint32_t blocks() const { return whole + 2 * split; }
+    __host__ __device__ uint32_t blocks() const { return whole + 2 * split; }
 };
 // Workgroup id's tile, and which half of it (-1: all of it).
 __device__ __forceinline__ int tile_of(uint32_t id, const TilePlan& t, uint32_t* tm, uint32_t* tn)
@@ -256,11 +287,36 @@ __device__ __forceinline__ void mm_mul(const typename MM<G::DT>::Frag (&a)[G::FM
                                        const typename MM<G::DT>::Frag (&b)[G::FN], f32x4 (&acc)[G::FM][G::FN],
                                        Beside beside = Beside())
 {
+    if constexpr (G::DT == 1) {
 #pragma unroll
-    for (int i = 0; i < G::FM; ++i) {
+        for (int i = 0; i < G::FM; ++i) {
 #pragma unroll
-        for (int j = 0; j < G::FN; ++j) acc[i][j] = MM<G::DT>::mul(b[j], a[i], acc[i][j]);
-        beside(i);
+            for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(b[j], a[i], acc[i][j]);
+            beside(i);
+        }
+    } else {
+        typename MM<0>::Parts bp[G::FN], ap[2];
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) bp[j] = MM<0>::split(b[j]);
+        ap[0] = MM<0>::split(a[0]);
+        constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};  // smallest first
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            // the next row is split among this row's products: 44 vector instructions, two after
+            // each of the 24 matrix ones, which leave that many issue slots free
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + 1 < G::FM) ap[(i + 1) & 1] = MM<0>::split(a[i + 1]);
+#pragma unroll
+            for (int q = 0; q < 6; ++q)
+#pragma unroll
+                for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(bp[j].p[kB[q]], ap[i & 1].p[kA[q]], acc[i][j]);
+#pragma unroll
+            for (int q = 0; q < 6 * G::FN; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+            }
+            beside(i);
+        }
     }
 }
 
@@ -269,7 +325,7 @@ template <class G>
 __device__ __forceinline__ void mm_step(const char* a_tile, const char* b_tile, int wm, int wn, int lane, f32x4 (&acc)[G::FM][G::FN])
 {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
+    for (int kk = 0; kk < MM<G::DT>::kSteps; ++kk) {
         typename MM<G::DT>::Frag a[G::FM], b[G::FN];
         mm_read<G>(a_tile, b_tile, kk, wm, wn, lane, a, b);
         mm_mul<G>(a, b, acc);
@@ -409,8 +465,10 @@ __device__ __forceinline__ void mm_loop(const Prob& p, const char* const (&a_lan
         if (!late) phase_end();
         return;
     }
-    issue_a(0, 0);
-    issue_b(0, 0);
+    if (tiles > 0) {
+        issue_a(0, 0);
+        issue_b(0, 0);
+    }
     for (int t = 0; t < tiles; ++t) {
         // tile t has arrived for every wave, and every wave has finished reading tile t-1
         __syncthreads();
@@ -459,8 +517,8 @@ __device__ __forceinline__ void mm_tile(const Prob& p, char* lds)
 
 // The tiles of each element type: bf16 has a large one (one workgroup of 8 waves per CU, LDS
 // full) and its half, and a small one (4 waves, two workgroups per CU) for launches with too
-// little work for the large ones.  fp32's products are a sixteenth as fast, so that the small
-// one feeds them at any size.
+// little work for the large ones.  fp32 takes six products per pair of fragments, so that the
+// small one feeds them at any size.
 template <int DT>
 struct Tiles;
 template <>

@@ -185,6 +185,8 @@ struct GluDxProb {
     int64_t m0, n0;
     int half;   // k tiles per half
     int tiles;
+    int first;  // this part's first k tile
+    float* part;  // where this part's sums go; null: dx itself
     bool vec;
 
     __device__ const char* a_chunk(int row, int k) const
@@ -201,15 +203,21 @@ struct GluDxProb {
     }
     __device__ int64_t a_off(int t) const
     {
+        t += first;
         return t < half ? int64_t(t) * 128 : int64_t(t - half) * 128 + a.f_pad * int64_t(sizeof(T));
     }
     __device__ int64_t b_off(int t) const
     {
+        t += first;
         const int64_t second = reinterpret_cast<intptr_t>(a.wu) - reinterpret_cast<intptr_t>(a.wg);
         const int64_t row = int64_t(BK) * a.w_ld * int64_t(sizeof(T));
         return t < half ? t * row : (t - half) * row + second;
     }
-    __device__ int valid(int t) const { return k_left<DT>(a.f, t < half ? t : t - half); }
+    __device__ int valid(int t) const
+    {
+        t += first;
+        return k_left<DT>(a.f, t < half ? t : t - half);
+    }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -222,7 +230,11 @@ struct GluDxProb {
             for (int j = 0; j < G::FN; ++j) {
                 const int64_t n = n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
                 const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if (n < a.k) store4<DT>(static_cast<T*>(a.dx) + m * a.k + n, a.k - n, vec, v);
+                if (n >= a.k) continue;
+                if (part)
+                    store4<0>(part + m * a.k + n, a.k - n, a.k % 4 == 0, v);
+                else
+                    store4<DT>(static_cast<T*>(a.dx) + m * a.k + n, a.k - n, vec, v);
             }
         }
     }
@@ -275,17 +287,22 @@ struct GluDwProb {
     }
 };
 
-// Both sets of tiles: dw's after dx's.  HX, HW: their halves.
+// Both sets of tiles: dw's after dx's, of which there are dx_splits times px.  HX, HW: their halves.
 template <class GX, class HX, class GW, class HW>
 __global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, TilePlan px, TilePlan pw, bool vec_x, bool vec_w)
 {
     static_assert(GX::NT == GW::NT && GX::LDS == GW::LDS, "one launch");
     __shared__ __attribute__((aligned(1024))) char lds[GX::LDS];
     uint32_t tm, tn;
-    if (blockIdx.x < px.whole + 2 * px.split) {
-        const int h = tile_of(blockIdx.x, px, &tm, &tn);
+    const uint32_t per = px.blocks(), n_dx = per * uint32_t(a.dx_splits);
+    if (blockIdx.x < n_dx) {
+        const uint32_t part = blockIdx.x / per;
+        const int h = tile_of(blockIdx.x % per, px, &tm, &tn);
         const int half = int((a.f + GX::BK - 1) / GX::BK);
-        GluDxProb<GX::DT> p{a, int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, half, 2 * half, vec_x};
+        const int depth = int((2 * half + a.dx_splits - 1) / a.dx_splits), first = int(part) * depth;
+        const int left = 2 * half > first ? 2 * half - first : 0;  // rounding may leave the last parts nothing
+        GluDxProb<GX::DT> p{a, int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, half, left < depth ? left : depth, first,
+                            a.dx_part ? a.dx_part + int64_t(part) * a.m * a.k : nullptr, vec_x};
         if (h < 0) {
             mm_tile<GX>(p, lds);
             return;
@@ -293,7 +310,7 @@ __global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, TilePlan px
         p.m0 += h * HX::BM;
         if (p.m0 < a.m) mm_tile<HX>(p, lds);
     } else {
-        const int h = tile_of(blockIdx.x - (px.whole + 2 * px.split), pw, &tm, &tn);
+        const int h = tile_of(blockIdx.x - n_dx, pw, &tm, &tn);
         GluDwProb<GW::DT> p{a, int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, int((a.m + GW::BK - 1) / GW::BK), vec_w};
         if (h < 0) {
             mm_tile<GW>(p, lds);
@@ -301,6 +318,18 @@ __global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, TilePlan px
         }
         p.m0 += h * HW::BM;
         if (p.m0 < 2 * a.f_pad) mm_tile<HW>(p, lds);
+    }
+}
+
+// dx from its parts, in order.
+template <int DT>
+__global__ __launch_bounds__(256) void glu_dx_sum_kernel(GluArgs a)
+{
+    const int64_t n = a.m * a.k;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        float s = 0.0f;
+        for (int64_t p = 0; p < a.dx_splits; ++p) s += a.dx_part[p * n + i];
+        static_cast<typename MM<DT>::T*>(a.dx)[i] = MM<DT>::narrow(s);
     }
 }
 
@@ -313,12 +342,32 @@ __global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, TilePlan px
 constexpr int kStreamWaves = 4;
 constexpr int kStreamUnroll = 4;  // steps whose loads are in flight together
 
+template <int DT>
+struct Stream;
+template <>
+struct Stream<1> {
+    using Frag = bf16x8;
+    static __device__ __forceinline__ f32x4 mul(Frag w, Frag x, f32x4 c) { return mfma_bf16(w, x, c); }
+};
+template <>
+struct Stream<0> {  // the fp32 instruction: its rate does not matter here
+    using Frag = f32x4;
+    static __device__ __forceinline__ f32x4 mul(Frag w, Frag x, f32x4 c)
+    {
+        // k is taken in the order (k % 4) * 4 + k / 4 within a step's 16, on both sides alike
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], x[j], c, 0, 0, 0);
+        return c;
+    }
+};
+
 template <int DT, int MT, int ACT>
 __global__ __launch_bounds__(64 * kStreamWaves) void glu_stream_kernel(GluArgs a, bool vec)
 {
     using M = MM<DT>;
     using T = typename M::T;
-    using Frag = typename M::Frag;
+    using S = Stream<DT>;
+    using Frag = typename S::Frag;
     constexpr int KS = 4 * M::kEpc;  // k per step
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t f0 = int64_t(blockIdx.x) * 16;
@@ -354,8 +403,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void glu_stream_kernel(GluArgs a
         for (int q = 0; q < kStreamUnroll; ++q)
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                g[i] = M::mul(wg[q], xf[q][i], g[i]);
-                u[i] = M::mul(wu[q], xf[q][i], u[i]);
+                g[i] = S::mul(wg[q], xf[q][i], g[i]);
+                u[i] = S::mul(wu[q], xf[q][i], u[i]);
             }
     }
     for (; s < (a.k_pad + KS - 1) / KS; s += kStreamWaves) {
@@ -367,8 +416,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void glu_stream_kernel(GluArgs a
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const Frag xf = in ? *reinterpret_cast<const Frag*>(px[i] + k) : zero;
-            g[i] = M::mul(wg, xf, g[i]);
-            u[i] = M::mul(wu, xf, u[i]);
+            g[i] = S::mul(wg, xf, g[i]);
+            u[i] = S::mul(wu, xf, u[i]);
         }
     }
     __shared__ f32x4 part[kStreamWaves][2 * MT][64];
@@ -462,11 +511,17 @@ template <class GX, class HX, class GW, class HW>
 hipError_t launch_glu_grad(const GluArgs& a, hipStream_t s)
 {
     const bool can = HX::BM < GX::BM;
+    const uint32_t splits = uint32_t(a.dx_splits);
     TilePlan px{0, 0, 0, 0}, pw{0, 0, 0, 0};
-    if (a.dx) px = plan_tiles(up(a.m, GX::BM), up(a.k, GX::BN), can && !a.dwg);  // only the last tiles are halved
-    if (a.dwg) pw = plan_tiles(up(2 * a.f_pad, GW::BM), up(a.k, GW::BN), can, px.whole);
+    // only the last tiles of a launch are halved
+    if (a.dx) px = plan_tiles(up(a.m, GX::BM), up(a.k, GX::BN), can && !a.dwg && splits == 1);
+    if (a.dwg) pw = plan_tiles(up(2 * a.f_pad, GW::BM), up(a.k, GW::BN), can, px.whole * splits);
     const bool vx = vec_rows(a.dx, a.k, GX::DT), vw = vec_rows(a.dwg, a.k, GX::DT) && vec_rows(a.dwu, a.k, GX::DT);
-    glu_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() + pw.blocks()), dim3(GX::NT), 0, s>>>(a, px, pw, vx, vw);
+    glu_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() * splits + pw.blocks()), dim3(GX::NT), 0, s>>>(a, px, pw, vx, vw);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.dx || splits == 1) return e;
+    const int64_t blocks = (a.m * a.k + 255) / 256;
+    glu_dx_sum_kernel<GX::DT><<<dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -478,9 +533,9 @@ hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
                                            : launch_glu_gu<DT, kActGelu, true>(a, vec, s);
     if (e != hipSuccess) return e;
     using T = Tiles<DT>;
-    const int64_t large = (a.dx ? int64_t(up(a.m, 256)) * up(a.k, 256) : 0) +
+    const int64_t large = (a.dx ? int64_t(up(a.m, 256)) * up(a.k, 256) * a.dx_splits : 0) +
                           (a.dwg ? int64_t(up(2 * a.f_pad, 256)) * up(a.k, 256) : 0);
-    const int64_t small = (a.dx ? int64_t(up(a.m, 128)) * up(a.k, 128) : 0) +
+    const int64_t small = (a.dx ? int64_t(up(a.m, 128)) * up(a.k, 128) * a.dx_splits : 0) +
                           (a.dwg ? int64_t(up(2 * a.f_pad, 128)) * up(a.k, 128) : 0);
     if constexpr (DT == 1) {
         if (large_tile(large, small))

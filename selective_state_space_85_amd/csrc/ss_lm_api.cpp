@@ -383,10 +383,25 @@ ss_status mat_operand(const void* p, int64_t ld, int64_t dim, ss_dtype dtype, bo
     return SS_OK;
 }
 
+// Parts into which the sums of dx (rows x dim, over `depth` terms) are cut.  dx and the weights'
+// gradients (sums over the rows) are formed by one launch: with few rows dx has few tiles, each
+// with a far longer sum than the weights' tiles, and would end long after them.  Its sums are cut
+// to the weights' length, but not below 16 k tiles, nor into more than fill the chip twice over.
+int64_t dx_parts(int64_t rows, int64_t dim, int64_t depth, ss_dtype dtype)
+{
+    const int64_t bk = 8 * chunk_elems(dtype);
+    const int64_t own = ceil_div(depth, bk), others = ceil_div(rows, bk);
+    const int64_t tiles = ceil_div(rows, 128) * ceil_div(dim, 128);
+    int64_t s = own / (others > 16 ? others : 16);
+    const int64_t most = 1024 / tiles;
+    s = s < most ? s : most;
+    return s > 1 ? s : 1;
+}
+
 struct GluLayout {
-    int64_t k_pad, f_pad;
+    int64_t k_pad, f_pad, splits;
     bool pack;
-    int64_t x, wg, wu, dgu, total;
+    int64_t x, wg, wu, dgu, part, total;
 };
 
 bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluLayout* w)
@@ -401,12 +416,16 @@ bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluL
     w->wg = r.add(w->pack ? f * w->k_pad : 0, es);
     w->wu = r.add(w->pack ? f * w->k_pad : 0, es);
     w->dgu = r.add(back ? m * 2 * w->f_pad : 0, es);
+    w->splits = dx_parts(m, k, 2 * f, dtype);
+    int64_t part;
+    if (!mul(w->splits, m, &part) || !mul(part, k, &part)) return false;
+    w->part = r.add(back && w->splits > 1 ? part : 0, 4);
     w->total = r.at;
     return r.ok;
 }
 
 struct XentLayout {
-    int64_t d_pad, piece;
+    int64_t d_pad, piece, splits;
     bool pack;
     int64_t x, w, pmax, psum, tl, dl, lo, tokens, counts, acc, total;
 };
@@ -446,7 +465,10 @@ bool xent_layout(int64_t n, int64_t d, int64_t v, ss_dtype dtype, bool back, Xen
     w->lo = r.add(listed ? n : 0, 4);
     w->tokens = r.add(listed ? groups * n : 0, 4);
     w->counts = r.add(listed ? groups : 0, 4);
-    w->acc = r.add(back && w->piece < v ? n * d : 0, 4);
+    w->splits = dx_parts(n, d, w->piece, dtype);
+    int64_t sums;
+    if (!mul(w->splits, n, &sums) || !mul(sums, d, &sums)) return false;
+    w->acc = r.add(back && (w->piece < v || w->splits > 1) ? sums : 0, 4);
     w->total = r.at;
     return r.ok;
 }
@@ -522,6 +544,8 @@ ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, 
     a.f = f;
     a.f_pad = w.f_pad;
     a.k_pad = w.k_pad;
+    a.dx_splits = w.splits;
+    a.dx_part = back && w.splits > 1 ? reinterpret_cast<float*>(ws + w.part) : nullptr;
     a.act = act == SS_ACT_SILU ? ssk::kActSilu : ssk::kActGelu;
     if (w.pack) {
         hipError_t e = ssk::launch_pad_rows(x, x_ld, ws + w.x, m, k, w.k_pad, dt, stream);
@@ -592,7 +616,8 @@ ss_status xent_impl(const void* x, int64_t x_ld, const void* weight, const int64
     a.lo = reinterpret_cast<float*>(ws + w.lo);
     a.tokens = reinterpret_cast<int32_t*>(ws + w.tokens);
     a.counts = reinterpret_cast<int32_t*>(ws + w.counts);
-    a.dx_acc = w.piece < v ? reinterpret_cast<float*>(ws + w.acc) : nullptr;
+    a.dx_splits = w.splits;
+    a.dx_acc = w.piece < v || w.splits > 1 ? reinterpret_cast<float*>(ws + w.acc) : nullptr;
     if (w.pack) {
         hipError_t e = ssk::launch_pad_rows(x, x_ld, ws + w.x, n, d, w.d_pad, dt, stream);
         if (e == hipSuccess) e = ssk::launch_pad_rows(weight, d, ws + w.w, v, d, w.d_pad, dt, stream);

@@ -30,6 +30,9 @@ struct GluArgs {
     int64_t m, k, f, f_pad;
     int64_t k_pad;   // k rounded up to whole 16-byte chunks; x and w rows hold zeros there
     int act;
+    // the backward's sums of dx over 2 f are cut in dx_splits parts when tokens are few
+    float* dx_part;  // (dx_splits, m, k) fp32, null with one part
+    int64_t dx_splits;
 };
 
 // Copy of `rows` rows of `cols` elements (ld apart) into rows of cols_pad elements, the pad zeroed.
@@ -63,7 +66,10 @@ struct XentArgs {
     float* lo;            // (n,)
     int32_t* tokens;      // (ceil(v / kXentCols), n)
     int32_t* counts;      // (ceil(v / kXentCols),)
-    float* dx_acc;        // backward workspace: (n, d) fp32 sums over the pieces, null with one piece
+    // backward workspace: sums of dx over the pieces, each piece's sum in dx_splits parts, (dx_splits,
+    // n, d) fp32; null with one piece and one part
+    float* dx_acc;
+    int64_t dx_splits;
     void* dx;             // (n, d), nullable
     void* dw;             // (v, d), nullable
     int64_t n, d, v;

@@ -250,7 +250,9 @@ struct XentDxProb {
     const XentArgs& a;
     int64_t m0, n0, v0, cols, pad;
     int tiles;
-    bool first, last;
+    int from;       // this part's first k tile
+    float* acc_to;  // this part's sums over the pieces so far; null with one piece and one part
+    bool first, last;  // of the pieces; last: and the only part
 
     __device__ const char* a_chunk(int row, int k) const
     {
@@ -264,9 +266,9 @@ struct XentDxProb {
         c = c < a.d_pad ? c : a.d_pad - MM<DT>::kEpc;
         return reinterpret_cast<const char*>(static_cast<const T*>(a.w) + (v0 + k) * a.w_ld + c);
     }
-    __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
-    __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.w_ld * int64_t(sizeof(T)); }
-    __device__ int valid(int t) const { return k_left<DT>(cols, t); }
+    __device__ int64_t a_off(int t) const { return int64_t(t + from) * 128; }
+    __device__ int64_t b_off(int t) const { return int64_t(t + from) * BK * a.w_ld * int64_t(sizeof(T)); }
+    __device__ int valid(int t) const { return k_left<DT>(cols, t + from); }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -286,12 +288,12 @@ struct XentDxProb {
                 for (int e = 0; e < 4; ++e) {
                     if (c + e >= a.d) continue;
                     float v = acc[i][j][e];
-                    if (!first) v += a.dx_acc[m * a.d + c + e];
+                    if (!first) v += acc_to[m * a.d + c + e];
                     if (add) v = fmaf(lo, MM<DT>::widen(wt[c + e]), v);
                     if (last)
                         static_cast<T*>(a.dx)[m * a.d + c + e] = MM<DT>::narrow(v);
                     else
-                        a.dx_acc[m * a.d + c + e] = v;
+                        acc_to[m * a.d + c + e] = v;
                 }
             }
         }
@@ -391,7 +393,7 @@ struct XentDwProb {
     }
 };
 
-// Both sets of tiles: dw's after dx's.  HX, HW: their halves.
+// Both sets of tiles: dw's after dx's, of which there are dx_splits times px.  HX, HW: their halves.
 template <class GX, class HX, class GW, class HW>
 __global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad, TilePlan px,
                                                            TilePlan pw, bool first, bool last, bool vec_w)
@@ -399,10 +401,16 @@ __global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v
     static_assert(GX::NT == GW::NT && GX::LDS == GW::LDS, "one launch");
     __shared__ __attribute__((aligned(1024))) char lds[GX::LDS];
     uint32_t tm, tn;
-    if (blockIdx.x < px.whole + 2 * px.split) {
-        const int h = tile_of(blockIdx.x, px, &tm, &tn);
-        XentDxProb<GX::DT> p{a,   int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, v0,   cols,
-                             pad, int((cols + GX::BK - 1) / GX::BK), first, last};
+    const uint32_t per = px.blocks(), n_dx = per * uint32_t(a.dx_splits);
+    if (blockIdx.x < n_dx) {
+        const uint32_t part = blockIdx.x / per;
+        const int h = tile_of(blockIdx.x % per, px, &tm, &tn);
+        const int all = int((cols + GX::BK - 1) / GX::BK);
+        const int depth = int((all + a.dx_splits - 1) / a.dx_splits), from = int(part) * depth;
+        const int left = all - from > 0 ? all - from : 0;  // a short last piece may leave a part nothing
+        XentDxProb<GX::DT> p{a,    int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, v0, cols, pad, left < depth ? left : depth,
+                             from, a.dx_acc ? a.dx_acc + int64_t(part) * a.n * a.d : nullptr, first,
+                             last && a.dx_splits == 1};
         if (h < 0) {
             mm_tile<GX>(p, lds);
             return;
@@ -410,7 +418,7 @@ __global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v
         p.m0 += h * HX::BM;
         if (p.m0 < a.n) mm_tile<HX>(p, lds);
     } else {
-        const int h = tile_of(blockIdx.x - (px.whole + 2 * px.split), pw, &tm, &tn);
+        const int h = tile_of(blockIdx.x - n_dx, pw, &tm, &tn);
         XentDwProb<GW::DT> p{a,   int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, v0, cols,
                              pad, int((a.n + GW::BK - 1) / GW::BK), vec_w};
         if (h < 0) {
@@ -419,6 +427,22 @@ __global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v
         }
         p.m0 += h * HW::BM;
         if (p.m0 < cols) mm_tile<HW>(p, lds);
+    }
+}
+
+// dx from its parts, in order, and (bf16) its rows' target remainders.
+template <int DT>
+__global__ __launch_bounds__(256) void xent_dx_sum_kernel(XentArgs a)
+{
+    using T = typename MM<DT>::T;
+    const int64_t n = a.n * a.d;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        float s = 0.0f;
+        for (int64_t p = 0; p < a.dx_splits; ++p) s += a.dx_acc[p * n + i];
+        const int64_t row = i / a.d, t = a.target[row];
+        if (DT == 1 && live_target(t, a))
+            s = fmaf(a.lo[row], MM<DT>::widen(static_cast<const T*>(a.w)[t * a.w_ld + i % a.d]), s);
+        static_cast<T*>(a.dx)[i] = MM<DT>::narrow(s);
     }
 }
 
@@ -478,11 +502,13 @@ template <class GX, class HX, class GW, class HW>
 hipError_t grad_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
     const bool can = HX::BM < GX::BM;
+    const uint32_t splits = uint32_t(a.dx_splits);
     TilePlan px{0, 0, 0, 0}, pw{0, 0, 0, 0};
-    if (a.dx) px = plan_tiles(up(a.n, GX::BM), up(a.d, GX::BN), can && !a.dw);  // only the last tiles are halved
-    if (a.dw) pw = plan_tiles(up(cols, GW::BM), up(a.d, GW::BN), can, px.whole);
+    // only the last tiles of a launch are halved
+    if (a.dx) px = plan_tiles(up(a.n, GX::BM), up(a.d, GX::BN), can && !a.dw && splits == 1);
+    if (a.dw) pw = plan_tiles(up(cols, GW::BM), up(a.d, GW::BN), can, px.whole * splits);
     const bool vec = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dw) % (GX::DT == 0 ? 16 : 8) == 0;
-    xent_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() + pw.blocks()), dim3(GX::NT), 0, s>>>(
+    xent_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() * splits + pw.blocks()), dim3(GX::NT), 0, s>>>(
         a, v0, cols, pad, px, pw, v0 == 0, v0 + cols == a.v, vec);
     return hipGetLastError();
 }
@@ -491,9 +517,9 @@ template <int DT>
 hipError_t grad_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
     using T = Tiles<DT>;
-    const int64_t large = (a.dx ? int64_t(up(a.n, 256)) * up(a.d, 256) : 0) +
+    const int64_t large = (a.dx ? int64_t(up(a.n, 256)) * up(a.d, 256) * a.dx_splits : 0) +
                           (a.dw ? int64_t(up(cols, 256)) * up(a.d, 256) : 0);
-    const int64_t small = (a.dx ? int64_t(up(a.n, 128)) * up(a.d, 128) : 0) +
+    const int64_t small = (a.dx ? int64_t(up(a.n, 128)) * up(a.d, 128) * a.dx_splits : 0) +
                           (a.dw ? int64_t(up(cols, 128)) * up(a.d, 128) : 0);
     if constexpr (DT == 1) {
         if (large_tile(large, small))
@@ -521,7 +547,10 @@ hipError_t bwd_dt(const XentArgs& a, hipStream_t s)
         if (e == hipSuccess) e = grad_tiles_dt<DT>(a, v0, cols, pad, s);
         if (e != hipSuccess) return e;
     }
-    return hipSuccess;
+    if (!a.dx || a.dx_splits == 1) return hipSuccess;
+    const int64_t blocks = (a.n * a.d + 255) / 256;
+    xent_dx_sum_kernel<DT><<<dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -43,6 +43,10 @@ CASES = [
     (200, 333, 65, wl.F32, "silu", 3),
     (300, 136, 515, wl.BF16, "gelu", 24),
     (257, 320, 1000, wl.BF16, "silu", 0),
+    # few tokens and many features: dx's sums are cut in parts (2, 62, and more than there are k tiles for)
+    (40, 64, 1030, wl.BF16, "silu", 0),
+    (3, 40, 16000, wl.F32, "silu", 0),
+    (1, 16, 20510, wl.BF16, "gelu", 0),
 ]
 IDS = ["M%dK%dF%d-%s-%s%s" % (c[0], c[1], c[2], c[3], c[4], "-str" * (c[5] > 0)) for c in CASES]
 

@@ -51,6 +51,9 @@ CASES = [
     (200, 513, 300, wl.BF16, 1),
     (333, 96, 3001, wl.F32, 0),
     (70, 264, 5003, wl.BF16, 0),
+    # few tokens and a large vocabulary: dx's sums are cut in parts
+    (20, 72, 20000, wl.BF16, 0),
+    (9, 33, 9000, wl.F32, 0),
 ]
 IDS = ["N%dD%dV%d-%s%s" % (c[0], c[1], c[2], c[3], "-str" * (c[4] > 0)) for c in CASES]
 
@@ -70,10 +73,11 @@ def test_loss_and_gradients(case):
         check(k, host64(g[k]), ref[k], TOL[dt])
 
 
-@pytest.mark.parametrize("n,d,v", [(2304, 264, 20000), (40000, 32, 9001)], ids=["large-tiles", "pieces"])
+@pytest.mark.parametrize("n,d,v", [(2304, 264, 20000), (40000, 32, 9001), (5000, 16, 60000)],
+                         ids=["large-tiles", "pieces", "pieces-and-parts"])
 def test_large(n, d, v):
-    """256 x 256 tiles; and more tokens than one piece of the vocabulary holds, so that dx is
-    summed over pieces."""
+    """256 x 256 tiles; more tokens than one piece of the vocabulary holds, so that dx is summed
+    over pieces; and both pieces and sums of dx cut in parts."""
     x, w, t, dloss = make(n, d, v, wl.BF16, 2)
     say("xent large", n, d, v)
     loss, lse, g = run(x, w, t, dloss)
