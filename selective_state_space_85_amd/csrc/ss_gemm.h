@@ -515,26 +515,21 @@ __device__ __forceinline__ void mm_tile(const Prob& p, char* lds)
 
 // ---- choosing tiles (host) ---------------------------------------------------------------------
 
-// The tiles of each element type: bf16 has a large one (one workgroup of 8 waves per CU, LDS
-// full) and its half, and a small one (4 waves, two workgroups per CU) for launches with too
-// little work for the large ones.  fp32 takes six products per pair of fragments, so that the
-// small one feeds them at any size.
+// The tiles: a large one (one workgroup of 8 waves per CU, LDS full) and its half, for bf16 alone;
+// a small one and a mini one (4 waves; two and three workgroups per CU), which fill the chip with
+// less work and, since fp32 takes six products per pair of fragments, feed it at any size.
 template <int DT>
-struct Tiles;
-template <>
-struct Tiles<1> {
+struct Tiles {
     template <bool AM, bool BM_>
-    using Large = Geo<1, 256, 256, 2, 4, AM, BM_>;
+    using Small = Geo<DT, 128, 128, 2, 2, AM, BM_>;
     template <bool AM, bool BM_>
-    using Half = Geo<1, 128, 256, 2, 4, AM, BM_>;
-    template <bool AM, bool BM_>
-    using Small = Geo<1, 128, 128, 2, 2, AM, BM_>;
+    using Mini = Geo<DT, 64, 128, 2, 2, AM, BM_>;
 };
-template <>
-struct Tiles<0> {
-    template <bool AM, bool BM_>
-    using Small = Geo<0, 128, 128, 2, 2, AM, BM_>;
-};
+template <bool AM, bool BM_>
+using LargeTile = Geo<1, 256, 256, 2, 4, AM, BM_>;
+template <bool AM, bool BM_>
+using HalfTile = Geo<1, 128, 256, 2, 4, AM, BM_>;
+enum class Tile { Large, Small, Mini };
 
 constexpr uint32_t kCUs = 256;
 
@@ -548,16 +543,27 @@ inline TilePlan plan_tiles(uint32_t ntm, uint32_t ntn, bool can_split, uint32_t 
     return {ntm, ntn, total - split, split};
 }
 
-// Whether the large tile is the faster: a round of the chip is 256 large tiles or 512 small ones;
-// a small tile is a quarter of the work at 0.78 of the large one's rate (8192 x 8192 x 4096: 1006
-// against 1288 TFLOP/s), so a round of them takes 0.64 of a round of large ones.  A last round of
-// at most half the large tiles is taken in halves (see TilePlan).
-inline bool large_tile(int64_t large, int64_t small)
+// The fastest tile for launches of that many tiles of each kind, by what they take at k = 2048 on
+// 256 CUs, in units of a round of large tiles (57 us; bf16) or of small ones (106 us; fp32):
+// 1024 x 1024, 2048 x 2048 and 4096 x 4096 outputs, bf16: halves 28, 31, 69 us, small 24, 27, 79, mini
+// 17, 24, 92; fp32: small 110, 137, 426, mini 84, 158, 502.  n: tiles on the busiest CU.
+template <int DT>
+inline Tile best_tile(int64_t large, int64_t small, int64_t mini)
 {
-    const int64_t rest = large % kCUs;
-    const double rl = double(large / kCUs) + (rest == 0 ? 0.0 : rest <= kCUs / 2 ? 0.55 : 1.0);
-    return rl <= 0.64 * double((small + 511) / 512);
+    const double ns = double((small + kCUs - 1) / kCUs), nm = double((mini + kCUs - 1) / kCUs);
+    if (DT == 0) {
+        const double cs = ns == 1 ? 1.28 : ns, cm = nm == 1 ? 0.85 : nm == 2 ? 1.48 : 0.59 * nm;
+        return cm < cs ? Tile::Mini : Tile::Small;
+    }
+    const int64_t rounds = large / kCUs, rest = large % kCUs;
+    const double cl = double(rounds) + (rest == 0 ? 0.0 : rest <= kCUs / 2 ? 0.55 : rounds ? 1.0 : 0.75);
+    const double cs = ns == 1 ? 0.46 : 0.35 * ns, cm = nm == 1 ? 0.30 : nm == 2 ? 0.42 : 0.20 * nm;
+    if (cl <= cs && cl <= cm) return Tile::Large;
+    return cm < cs ? Tile::Mini : Tile::Small;
 }
+
+// Number of bm x bn tiles of a rows x cols output.
+inline int64_t count(int64_t rows, int64_t cols, int bm, int bn) { return int64_t(up(rows, bm)) * up(cols, bn); }
 
 }  // namespace
 }  // namespace ssk

@@ -468,14 +468,15 @@ hipError_t launch_glu_tile(const GluArgs& a, bool vec, hipStream_t s)
 template <int DT, int ACT, bool BACK>
 hipError_t launch_glu_gu(const GluArgs& a, bool vec, hipStream_t s)
 {
-    using T = Tiles<DT>;
+    const int64_t f = 2 * a.f;  // tile columns: f of Wg and f of Wu
+    const Tile t = best_tile<DT>(count(a.m, f, 256, 256), count(a.m, f, 128, 128), count(a.m, f, 64, 128));
     if constexpr (DT == 1) {
-        if (large_tile(int64_t(up(a.m, 256)) * up(a.f, 128), int64_t(up(a.m, 128)) * up(a.f, 64)))
-            return launch_glu_tile<typename T::template Large<false, false>, typename T::template Half<false, false>, ACT,
-                                   BACK>(a, vec, s);
+        if (t == Tile::Large)
+            return launch_glu_tile<LargeTile<false, false>, HalfTile<false, false>, ACT, BACK>(a, vec, s);
     }
-    using S = typename T::template Small<false, false>;
-    return launch_glu_tile<S, S, ACT, BACK>(a, vec, s);
+    using S = typename Tiles<DT>::template Small<false, false>;
+    using M = typename Tiles<DT>::template Mini<false, false>;
+    return t == Tile::Mini ? launch_glu_tile<M, M, ACT, BACK>(a, vec, s) : launch_glu_tile<S, S, ACT, BACK>(a, vec, s);
 }
 
 template <int DT, int ACT>
@@ -532,19 +533,21 @@ hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
     const hipError_t e = a.act == kActSilu ? launch_glu_gu<DT, kActSilu, true>(a, vec, s)
                                            : launch_glu_gu<DT, kActGelu, true>(a, vec, s);
     if (e != hipSuccess) return e;
-    using T = Tiles<DT>;
-    const int64_t large = (a.dx ? int64_t(up(a.m, 256)) * up(a.k, 256) * a.dx_splits : 0) +
-                          (a.dwg ? int64_t(up(2 * a.f_pad, 256)) * up(a.k, 256) : 0);
-    const int64_t small = (a.dx ? int64_t(up(a.m, 128)) * up(a.k, 128) * a.dx_splits : 0) +
-                          (a.dwg ? int64_t(up(2 * a.f_pad, 128)) * up(a.k, 128) : 0);
+    auto tiles = [&](int bm, int bn) {
+        return (a.dx ? count(a.m, a.k, bm, bn) * a.dx_splits : 0) + (a.dwg ? count(2 * a.f_pad, a.k, bm, bn) : 0);
+    };
+    const Tile t = best_tile<DT>(tiles(256, 256), tiles(128, 128), tiles(64, 128));
     if constexpr (DT == 1) {
-        if (large_tile(large, small))
-            return launch_glu_grad<typename T::template Large<false, true>, typename T::template Half<false, true>,
-                                   typename T::template Large<true, true>, typename T::template Half<true, true>>(a, s);
+        if (t == Tile::Large)
+            return launch_glu_grad<LargeTile<false, true>, HalfTile<false, true>, LargeTile<true, true>,
+                                   HalfTile<true, true>>(a, s);
     }
+    using T = Tiles<DT>;
     using SX = typename T::template Small<false, true>;
     using SW = typename T::template Small<true, true>;
-    return launch_glu_grad<SX, SX, SW, SW>(a, s);
+    using MX = typename T::template Mini<false, true>;
+    using MW = typename T::template Mini<true, true>;
+    return t == Tile::Mini ? launch_glu_grad<MX, MX, MW, MW>(a, s) : launch_glu_grad<SX, SX, SW, SW>(a, s);
 }
 
 }  // namespace

@@ -332,12 +332,12 @@ struct XentDwProb {
     {
         using M = MM<DT>;
         const int tid = threadIdx.x;
+        // the groups of columns that the tile shares with (a mini tile is half of one)
+        const int64_t top = m0 + G::BM < cols ? m0 + G::BM : cols;
 #pragma unroll 1
-        for (int half = 0; half < G::BM / int(kXentCols); ++half) {
-            const int64_t from = v0 + m0 + half * kXentCols;
-            if (from >= v0 + cols) break;
-            const int32_t* const list = a.tokens + from / kXentCols * a.n;
-            const int count = a.counts[from / kXentCols];
+        for (int64_t g = (v0 + m0) / kXentCols; g * kXentCols < v0 + top; ++g) {
+            const int32_t* const list = a.tokens + g * a.n;
+            const int count = a.counts[g];
 #pragma unroll 1
             for (int at = 0; at < count; at += BK) {
                 __syncthreads();  // the stage's last readers are done
@@ -357,7 +357,7 @@ struct XentDwProb {
                 if (tid < BK && at + tid < count) {
                     const int tok = list[at + tid];
                     const int m = int(a.target[tok] - v0 - m0);
-                    *reinterpret_cast<T*>(lds + a_mc_offset<G>(m, tid)) = M::narrow(a.lo[tok]);
+                    if (m >= 0 && m < G::BM) *reinterpret_cast<T*>(lds + a_mc_offset<G>(m, tid)) = M::narrow(a.lo[tok]);
                 }
                 __syncthreads();
                 mm_step<G>(lds, lds + 2 * G::A_BYTES, wm, wn, lane, acc);
@@ -459,13 +459,13 @@ hipError_t fwd_tiles(const XentArgs& a, hipStream_t s)
 template <int DT>
 hipError_t fwd_tiles_dt(const XentArgs& a, hipStream_t s)
 {
-    using T = Tiles<DT>;
+    const Tile t = best_tile<DT>(count(a.n, a.v, 256, 256), count(a.n, a.v, 128, 128), count(a.n, a.v, 64, 128));
     if constexpr (DT == 1) {
-        if (large_tile(int64_t(up(a.n, 256)) * up(a.v, 256), int64_t(up(a.n, 128)) * up(a.v, 128)))
-            return fwd_tiles<typename T::template Large<false, false>, typename T::template Half<false, false>>(a, s);
+        if (t == Tile::Large) return fwd_tiles<LargeTile<false, false>, HalfTile<false, false>>(a, s);
     }
-    using S = typename T::template Small<false, false>;
-    return fwd_tiles<S, S>(a, s);
+    using S = typename Tiles<DT>::template Small<false, false>;
+    using M = typename Tiles<DT>::template Mini<false, false>;
+    return t == Tile::Mini ? fwd_tiles<M, M>(a, s) : fwd_tiles<S, S>(a, s);
 }
 
 template <int DT>
@@ -488,14 +488,14 @@ hipError_t dl_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hi
 template <int DT>
 hipError_t dl_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
-    using T = Tiles<DT>;
+    const Tile t = best_tile<DT>(count(a.n, pad, 256, 256), count(a.n, pad, 128, 128), count(a.n, pad, 64, 128));
     if constexpr (DT == 1) {
-        if (large_tile(int64_t(up(a.n, 256)) * up(pad, 256), int64_t(up(a.n, 128)) * up(pad, 128)))
-            return dl_tiles<typename T::template Large<false, false>, typename T::template Half<false, false>>(
-                a, v0, cols, pad, s);
+        if (t == Tile::Large)
+            return dl_tiles<LargeTile<false, false>, HalfTile<false, false>>(a, v0, cols, pad, s);
     }
-    using S = typename T::template Small<false, false>;
-    return dl_tiles<S, S>(a, v0, cols, pad, s);
+    using S = typename Tiles<DT>::template Small<false, false>;
+    using M = typename Tiles<DT>::template Mini<false, false>;
+    return t == Tile::Mini ? dl_tiles<M, M>(a, v0, cols, pad, s) : dl_tiles<S, S>(a, v0, cols, pad, s);
 }
 
 template <class GX, class HX, class GW, class HW>
@@ -516,20 +516,22 @@ hipError_t grad_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, 
 template <int DT>
 hipError_t grad_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
-    using T = Tiles<DT>;
-    const int64_t large = (a.dx ? int64_t(up(a.n, 256)) * up(a.d, 256) * a.dx_splits : 0) +
-                          (a.dw ? int64_t(up(cols, 256)) * up(a.d, 256) : 0);
-    const int64_t small = (a.dx ? int64_t(up(a.n, 128)) * up(a.d, 128) * a.dx_splits : 0) +
-                          (a.dw ? int64_t(up(cols, 128)) * up(a.d, 128) : 0);
+    auto tiles = [&](int bm, int bn) {
+        return (a.dx ? count(a.n, a.d, bm, bn) * a.dx_splits : 0) + (a.dw ? count(cols, a.d, bm, bn) : 0);
+    };
+    const Tile t = best_tile<DT>(tiles(256, 256), tiles(128, 128), tiles(64, 128));
     if constexpr (DT == 1) {
-        if (large_tile(large, small))
-            return grad_tiles<typename T::template Large<false, true>, typename T::template Half<false, true>,
-                              typename T::template Large<true, true>, typename T::template Half<true, true>>(a, v0, cols,
-                                                                                                         pad, s);
+        if (t == Tile::Large)
+            return grad_tiles<LargeTile<false, true>, HalfTile<false, true>, LargeTile<true, true>, HalfTile<true, true>>(
+                a, v0, cols, pad, s);
     }
+    using T = Tiles<DT>;
     using SX = typename T::template Small<false, true>;
     using SW = typename T::template Small<true, true>;
-    return grad_tiles<SX, SX, SW, SW>(a, v0, cols, pad, s);
+    using MX = typename T::template Mini<false, true>;
+    using MW = typename T::template Mini<true, true>;
+    return t == Tile::Mini ? grad_tiles<MX, MX, MW, MW>(a, v0, cols, pad, s)
+                           : grad_tiles<SX, SX, SW, SW>(a, v0, cols, pad, s);
 }
 
 template <int DT>
