@@ -656,30 +656,74 @@ __global__ __launch_bounds__(kSumCols * kSumParts) void glr_decay_kernel(GlrArgs
 
 // ---- one token ------------------------------------------------------------------------------
 
+// VC neighbouring channels per thread, loaded and stored together, and ROWS batch rows whose loads
+// are in flight together; the channels' rates are formed once for them.  Bound by HBM traffic
+// (bf16: 16 bytes per element), and at few rows by the launch.
 template <int DT, int VC>
-__global__ __launch_bounds__(256) void glr_step_kernel(GlrStepArgs a)
+struct Chunk;  // VC elements
+template <>
+struct Chunk<0, 4> {
+    float4 v;
+    __device__ __forceinline__ float get(int e) const { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; }
+    static __device__ __forceinline__ Chunk make(const float (&f)[4]) { return {make_float4(f[0], f[1], f[2], f[3])}; }
+};
+template <>
+struct Chunk<1, 4> {
+    uint2 v;
+    __device__ __forceinline__ float get(int e) const
+    {
+        const uint32_t u = e < 2 ? v.x : v.y;
+        return __uint_as_float(e & 1 ? u & 0xffff0000u : u << 16);
+    }
+    static __device__ __forceinline__ Chunk make(const float (&f)[4])
+    {
+        return {make_uint2(Row<1, 2>::make({f[0], f[1]}), Row<1, 2>::make({f[2], f[3]}))};
+    }
+};
+template <int DT>
+struct Chunk<DT, 1> {
+    typename Row<DT, 1>::Raw v;
+    __device__ __forceinline__ float get(int) const { return Row<DT, 1>::get(v, 0); }
+    static __device__ __forceinline__ Chunk make(const float (&f)[1]) { return {Row<DT, 1>::make(f)}; }
+};
+
+constexpr int kStepThreads = 256;
+template <int DT, int VC, int ROWS>
+__global__ __launch_bounds__(kStepThreads) void glr_step_kernel(GlrStepArgs a)
 {
-    using RW = Row<DT, VC>;
-    using Raw = typename RW::Raw;
-    const int64_t d = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VC;
+    using C = Chunk<DT, VC>;
+    using H = Chunk<0, VC>;
+    const int64_t d = (int64_t(blockIdx.x) * kStepThreads + threadIdx.x) * VC;
     if (d >= a.dim) return;
     float k[VC];
 #pragma unroll
     for (int e = 0; e < VC; ++e) k[e] = channel_rate(a.decay[d + e], a.c);
-    for (int64_t b = blockIdx.y; b < a.batch; b += gridDim.y) {
-        const auto rr = *static_cast<const Raw*>(offset<DT>(a.r, b * a.r_ld + d));
-        const auto ri = *static_cast<const Raw*>(offset<DT>(a.i, b * a.i_ld + d));
-        const auto rx = *static_cast<const Raw*>(offset<DT>(a.x, b * a.x_ld + d));
-        float h[VC];
+    for (int64_t b0 = int64_t(blockIdx.y) * ROWS; b0 < a.batch; b0 += int64_t(gridDim.y) * ROWS) {
+        C r[ROWS], i[ROWS], x[ROWS];
+        H h[ROWS];
 #pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            float av, w;
-            decay_of(k[e], sigmoid1(RW::get(rr, e)), &av, &w);
-            const float in = __builtin_amdgcn_sqrtf(w) * sigmoid1(RW::get(ri, e)) * RW::get(rx, e);
-            h[e] = fmaf(av, a.h[b * a.dim + d + e], in);
-            a.h[b * a.dim + d + e] = h[e];
+        for (int q = 0; q < ROWS; ++q) {
+            const int64_t b = b0 + q < a.batch ? b0 + q : a.batch - 1;
+            r[q] = *static_cast<const C*>(offset<DT>(a.r, b * a.r_ld + d));
+            i[q] = *static_cast<const C*>(offset<DT>(a.i, b * a.i_ld + d));
+            x[q] = *static_cast<const C*>(offset<DT>(a.x, b * a.x_ld + d));
+            h[q] = *reinterpret_cast<const H*>(a.h + b * a.dim + d);
         }
-        *const_cast<Raw*>(static_cast<const Raw*>(offset<DT>(a.y, b * a.dim + d))) = RW::make(h);
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+            float v[VC];
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                float av, w;
+                decay_of(k[e], sigmoid1(r[q].get(e)), &av, &w);
+                const float in = __builtin_amdgcn_sqrtf(w) * sigmoid1(i[q].get(e)) * x[q].get(e);
+                v[e] = fmaf(av, h[q].get(e), in);
+            }
+            if (b0 + q < a.batch) {
+                *reinterpret_cast<H*>(a.h + (b0 + q) * a.dim + d) = H::make(v);
+                *const_cast<C*>(static_cast<const C*>(offset<DT>(a.y, (b0 + q) * a.dim + d))) = C::make(v);
+            }
+        }
     }
 }
 
@@ -742,17 +786,34 @@ hipError_t bwd_dt(const GlrArgs& a, hipStream_t s)
     return two ? bwd_variant<DT, 2, false>(a, s) : bwd_variant<DT, 1, false>(a, s);
 }
 
+// Rows of `ld` elements from p on start whole chunks of 4 elements.
+bool fours(const void* p, int64_t ld, int dtype)
+{
+    return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (dtype == 0 ? 16 : 8) == 0;
+}
+
+template <int DT, int VC>
+hipError_t step_vec(const GlrStepArgs& a, hipStream_t s)
+{
+    const int64_t cols = (a.dim + kStepThreads * VC - 1) / (kStepThreads * VC);
+    // two rows per thread when that leaves two workgroups per CU
+    if (cols * a.batch >= 1024) {
+        const int64_t rows = (a.batch + 1) / 2;
+        glr_step_kernel<DT, VC, 2><<<dim3(unsigned(cols), unsigned(rows < 65535 ? rows : 65535)), dim3(kStepThreads), 0,
+                                     s>>>(a);
+    } else {
+        glr_step_kernel<DT, VC, 1><<<dim3(unsigned(cols), unsigned(a.batch < 65535 ? a.batch : 65535)),
+                                     dim3(kStepThreads), 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
 template <int DT>
 hipError_t step_dt(const GlrStepArgs& a, hipStream_t s)
 {
-    const bool two = a.dim % 2 == 0 && even(a.x, a.x_ld, DT) && even(a.r, a.r_ld, DT) && even(a.i, a.i_ld, DT) &&
-                     even(a.y, a.dim, DT);
-    const unsigned rows = unsigned(a.batch < 65535 ? a.batch : 65535);
-    if (two)
-        glr_step_kernel<DT, 2><<<dim3(unsigned((a.dim + 511) / 512), rows), dim3(256), 0, s>>>(a);
-    else
-        glr_step_kernel<DT, 1><<<dim3(unsigned((a.dim + 255) / 256), rows), dim3(256), 0, s>>>(a);
-    return hipGetLastError();
+    const bool four = a.dim % 4 == 0 && fours(a.x, a.x_ld, DT) && fours(a.r, a.r_ld, DT) && fours(a.i, a.i_ld, DT) &&
+                      fours(a.y, a.dim, DT) && fours(a.h, a.dim, 0);
+    return four ? step_vec<DT, 4>(a, s) : step_vec<DT, 1>(a, s);
 }
 
 }  // namespace

@@ -11,7 +11,8 @@ from typing import Dict, Optional, Tuple, Union
 import torch
 
 from . import _lib, _lm
-from .ops import _DTYPES, _need
+from .ops import _DTYPES
+from .ops import _need as _refuse
 
 _ACTS = {"silu": _lm.SS_ACT_SILU, "gelu": _lm.SS_ACT_GELU}
 _BAD = ctypes.c_size_t(-1).value
@@ -26,6 +27,12 @@ def _dtype(t: torch.Tensor) -> int:
     if dt is None:
         raise TypeError("unsupported dtype %s" % t.dtype)
     return dt
+
+
+def _need(t: torch.Tensor, name: str, shape, dtype, device) -> None:
+    """The checks of ``ops._need``, which words the refusal: these calls last a few microseconds."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, device)
 
 
 def _gpu(t: torch.Tensor, fn: str) -> torch.device:
@@ -58,6 +65,8 @@ def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     n = shape[-1]
+    if t.is_contiguous():
+        return n
     st = t.stride()
     if len(shape) == 3:
         nb, nl = shape[0], shape[1]
@@ -71,6 +80,11 @@ def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     return ld
 
 
+# the current stream's handle: torch's own accessor of it, where there is one, takes a
+# twentieth of the time of making a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _on:
     """The tensor's device as the current one, and torch's current stream on it."""
 
@@ -78,7 +92,8 @@ class _on:
 
     def __init__(self, device: torch.device):
         self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device).cuda_stream
+        self.stream = (_raw_stream(device.index) if _raw_stream is not None
+                       else torch.cuda.current_stream(device).cuda_stream)
 
     def __enter__(self):
         if self.ctx is not None:
@@ -145,7 +160,7 @@ def glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, decay: torch.Tens
     if h0 is not None:
         _need(h0, "h0", (nb, nd), torch.float32, dev)
     reset = _reset(reset, nb, nl, dev)
-    y = out if out is not None else torch.empty(shape, dtype=x.dtype, device=dev)
+    y = out if out is not None else x.new_empty(shape)
     _need(y, "out", shape, x.dtype, dev)
     if h_last is None and return_last_state:
         h_last = torch.empty((nb, nd), dtype=torch.float32, device=dev)
@@ -191,7 +206,7 @@ def glr_bwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, decay: torch.Tens
         g = {"dx": out[..., :nd], "dr": out[..., nd:2 * nd], "di": out[..., 2 * nd:]}
         ld = 3 * nd
     else:
-        g = {n: torch.empty(shape, dtype=x.dtype, device=dev) for n in ("dx", "dr", "di")}
+        g = {n: x.new_empty(shape) for n in ("dx", "dr", "di")}
         ld = nd
     g["ddecay"] = torch.empty((nd,), dtype=torch.float32, device=dev)
     if want_dh0:
@@ -219,7 +234,7 @@ def glr_step(h: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: torch.Tensor,
     _need(h, "h", shape, torch.float32, dev)
     _need(decay, "decay", (nd,), torch.float32, dev)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(shape)
     else:
         _need(out, "out", shape, x.dtype, dev)
     with _on(dev) as stream:
@@ -270,7 +285,7 @@ def glu_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, act: s
     _need(w_up, "w_up", (f, k), x.dtype, dev)
     shape = x.shape[:-1] + (f,)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(shape)
     else:
         _need(out, "out", shape, x.dtype, dev)
     lib = _lm.load()
@@ -294,10 +309,10 @@ def glu_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dh: torch
     _need(dh, "dh", x.shape[:-1] + (f,), x.dtype, dev)
     g = {}
     if want_dx:
-        g["dx"] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        g["dx"] = x.new_empty(x.shape)
     if want_dw:
-        g["dw_gate"] = torch.empty((f, k), dtype=x.dtype, device=dev)
-        g["dw_up"] = torch.empty((f, k), dtype=x.dtype, device=dev)
+        g["dw_gate"] = x.new_empty((f, k))
+        g["dw_up"] = x.new_empty((f, k))
     lib = _lm.load()
     ws, ws_bytes = _space(_size(lib.ss_glu_bwd_workspace_bytes(m, k, f, dt)), workspace, dev)
     with _on(dev) as stream:
@@ -357,9 +372,9 @@ def xent_bwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, lse: torch.
     _need(dloss, "dloss", target.shape, torch.float32, dev)
     g = {}
     if want_dx:
-        g["dx"] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        g["dx"] = x.new_empty(x.shape)
     if want_dw:
-        g["dw"] = torch.empty((v, k), dtype=x.dtype, device=dev)
+        g["dw"] = x.new_empty((v, k))
     lib = _lm.load()
     ws, ws_bytes = _space(_size(lib.ss_xent_bwd_workspace_bytes(n, k, v, dt)), workspace, dev)
     with _on(dev) as stream:
