@@ -513,6 +513,129 @@ __device__ __forceinline__ void mm_tile(const Prob& p, char* lds)
     p.template finish<G>(acc, lds, wave / G::WN, wave % G::WN, lane);
 }
 
+// ---- few rows: the weights stream past them ------------------------------------------------------
+
+// Products of up to kStreamRows rows of x with 2 x 16 rows of weights per workgroup, whose waves
+// split k.  A wave reads its part of the 32 rows straight into MFMA operands (lane: row l % 16, 16
+// bytes of k per step), the rows of x likewise (every workgroup shares them: they stay in the
+// caches), and the waves' sums are joined in LDS.  Bound by reading the weights.
+// ALIGNED: every row starts on 16 bytes and k is whole 16-byte chunks; otherwise rows are read as
+// they lie, and the last chunk element by element.
+constexpr int kStreamWaves = 4;
+constexpr int kStreamUnroll = 4;  // steps whose loads are in flight together
+
+template <int DT>
+struct Stream;
+template <>
+struct Stream<1> {
+    using Frag = bf16x8;
+    static __device__ __forceinline__ f32x4 mul(Frag w, Frag x, f32x4 c) { return mfma_bf16(w, x, c); }
+};
+template <>
+struct Stream<0> {  // the fp32 instruction: its rate does not matter here
+    using Frag = f32x4;
+    static __device__ __forceinline__ f32x4 mul(Frag w, Frag x, f32x4 c)
+    {
+        // k is taken in the order (k % 4) * 4 + k / 4 within a step's 16, on both sides alike
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], x[j], c, 0, 0, 0);
+        return c;
+    }
+};
+
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ typename Stream<DT>::Frag stream_load(const typename MM<DT>::T* p)
+{
+    typename Stream<DT>::Frag f;
+    if constexpr (ALIGNED)
+        f = *reinterpret_cast<const typename Stream<DT>::Frag*>(p);
+    else
+        __builtin_memcpy(&f, p, sizeof(f));
+    return f;
+}
+// the chunk of which `left` elements exist (none: nothing is read)
+template <int DT>
+__device__ __forceinline__ typename Stream<DT>::Frag stream_tail(const typename MM<DT>::T* p, int64_t left)
+{
+    typename Stream<DT>::Frag f{};
+#pragma unroll
+    for (int e = 0; e < MM<DT>::kEpc; ++e)
+        if (e < left) f[e] = p[e];
+    return f;
+}
+
+// c0, c1: this wave's part of the products of w0's and w1's 16 rows (rows of C) with px's MT x 16
+// rows.  w0, w1, px: this lane's rows (row l % 16 of each).
+template <int DT, int MT, bool ALIGNED>
+__device__ __forceinline__ void stream_rows(const typename MM<DT>::T* w0, const typename MM<DT>::T* w1,
+                                            const typename MM<DT>::T* const (&px)[MT], int64_t k, f32x4 (&c0)[MT],
+                                            f32x4 (&c1)[MT])
+{
+    using S = Stream<DT>;
+    using Frag = typename S::Frag;
+    constexpr int KS = 4 * MM<DT>::kEpc;  // k per step
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kq = int((threadIdx.x & 63) >> 4) * MM<DT>::kEpc;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) c0[i] = c1[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t whole = k / KS, steps = (k + KS - 1) / KS;
+    int64_t s = wave;
+    for (; s + (kStreamUnroll - 1) * kStreamWaves < whole; s += kStreamUnroll * kStreamWaves) {
+        Frag a[kStreamUnroll], b[kStreamUnroll], x[kStreamUnroll][MT];
+#pragma unroll
+        for (int q = 0; q < kStreamUnroll; ++q) {
+            const int64_t at = (s + q * kStreamWaves) * KS + kq;
+            a[q] = stream_load<DT, ALIGNED>(w0 + at);
+            b[q] = stream_load<DT, ALIGNED>(w1 + at);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) x[q][i] = stream_load<DT, ALIGNED>(px[i] + at);
+        }
+#pragma unroll
+        for (int q = 0; q < kStreamUnroll; ++q)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                c0[i] = S::mul(a[q], x[q][i], c0[i]);
+                c1[i] = S::mul(b[q], x[q][i], c1[i]);
+            }
+    }
+    for (; s < steps; s += kStreamWaves) {
+        const int64_t at = s * KS + kq, left = k - at;
+        const bool all = left >= MM<DT>::kEpc;
+        const Frag a = all ? stream_load<DT, ALIGNED>(w0 + at) : stream_tail<DT>(w0 + at, left);
+        const Frag b = all ? stream_load<DT, ALIGNED>(w1 + at) : stream_tail<DT>(w1 + at, left);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const Frag x = all ? stream_load<DT, ALIGNED>(px[i] + at) : stream_tail<DT>(px[i] + at, left);
+            c0[i] = S::mul(a, x, c0[i]);
+            c1[i] = S::mul(b, x, c1[i]);
+        }
+    }
+}
+
+// The waves' parts joined; finish(i, s0, s1) has, for rows 16 i .. 16 i + 15 of x, the sums whose
+// element e is weight row (l / 16) 4 + e, x row 16 i + l % 16.
+template <int MT, class Finish>
+__device__ __forceinline__ void stream_join(const f32x4 (&c0)[MT], const f32x4 (&c1)[MT], Finish finish)
+{
+    __shared__ f32x4 part[kStreamWaves][2 * MT][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        part[wave][2 * i][lane] = c0[i];
+        part[wave][2 * i + 1][lane] = c1[i];
+    }
+    __syncthreads();
+    for (int i = wave; i < MT; i += kStreamWaves) {
+        f32x4 s0 = part[0][2 * i][lane], s1 = part[0][2 * i + 1][lane];
+#pragma unroll
+        for (int w = 1; w < kStreamWaves; ++w) {
+            s0 += part[w][2 * i][lane];
+            s1 += part[w][2 * i + 1][lane];
+        }
+        finish(i, s0, s1);
+    }
+}
+
 // ---- choosing tiles (host) ---------------------------------------------------------------------
 
 // The tiles: a large one (one workgroup of 8 waves per CU, LDS full) and its half, for bf16 alone;

@@ -90,16 +90,46 @@ __device__ __forceinline__ void store4(typename MM<DT>::T* p, int64_t left, bool
     }
 }
 
-// ---- g and u of a tile, and what is made of them ------------------------------------------
+// ---- g and u, and what is made of them ----------------------------------------------------
 
-// BACK: dg and du into the workspace instead of h
+// Four neighbouring features f.. of token m.  BACK: dg and du into the workspace instead of h.
+// vec: rows of h (dh) are aligned for 4-element accesses.
+template <int DT, int ACT, bool BACK>
+__device__ __forceinline__ void glu_emit(const GluArgs& a, int64_t m, int64_t f, f32x4 g, f32x4 u, bool vec)
+{
+    using T = typename MM<DT>::T;
+    if constexpr (!BACK) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_of<ACT>(g[e]) * u[e];
+        if (f < a.f) store4<DT>(static_cast<T*>(a.h) + m * a.f + f, a.f - f, vec, v);
+    } else {
+        if (f >= a.f_pad) return;
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dg[4], du[4];
+        if (f < a.f) load4<DT>(static_cast<const T*>(a.dh) + m * a.f + f, a.f - f, vec, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float act, slope;
+            act_grad<ACT>(g[e], &act, &slope);
+            // the pad columns f..f_pad hold zeros: later products read them
+            const bool in = f + e < a.f;
+            dg[e] = in ? d[e] * u[e] * slope : 0.0f;
+            du[e] = in ? d[e] * act : 0.0f;
+        }
+        // f_pad is a multiple of 4: whole groups, aligned
+        T* const row = static_cast<T*>(a.dgu) + m * 2 * a.f_pad + f;
+        store4<DT>(row, 4, true, dg);
+        store4<DT>(row + a.f_pad, 4, true, du);
+    }
+}
+
 template <int DT, int ACT, bool BACK>
 struct GluProb {
     using T = typename MM<DT>::T;
     const GluArgs& a;
     int64_t m0, f0;  // the tile's first token and first feature
     int tiles;
-    bool vec;        // rows of h (dh) are aligned for 4-element accesses
+    bool vec;
 
     __device__ const char* a_chunk(int row, int k) const
     {
@@ -127,33 +157,8 @@ struct GluProb {
             const int64_t m = m0 + (wm * G::FM + i) * 16 + (lane & 15);
             if (m >= a.m) continue;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int64_t f = f0 + wn * 32 + j * 16 + (lane >> 4) * 4;
-                const f32x4 g = acc[i][j], u = acc[i][j + 2];
-                if constexpr (!BACK) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = act_of<ACT>(g[e]) * u[e];
-                    if (f < a.f) store4<DT>(static_cast<T*>(a.h) + m * a.f + f, a.f - f, vec, v);
-                } else {
-                    if (f >= a.f_pad) continue;
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dg[4], du[4];
-                    if (f < a.f) load4<DT>(static_cast<const T*>(a.dh) + m * a.f + f, a.f - f, vec, d);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float act, slope;
-                        act_grad<ACT>(g[e], &act, &slope);
-                        // the pad columns f..f_pad hold zeros: later products read them
-                        const bool in = f + e < a.f;
-                        dg[e] = in ? d[e] * u[e] * slope : 0.0f;
-                        du[e] = in ? d[e] * act : 0.0f;
-                    }
-                    // f_pad is a multiple of 4: whole groups, aligned
-                    T* const row = static_cast<T*>(a.dgu) + m * 2 * a.f_pad + f;
-                    store4<DT>(row, 4, true, dg);
-                    store4<DT>(row + a.f_pad, 4, true, du);
-                }
-            }
+            for (int j = 0; j < 2; ++j)
+                glu_emit<DT, ACT, BACK>(a, m, f0 + wn * 32 + j * 16 + (lane >> 4) * 4, acc[i][j], acc[i][j + 2], vec);
         }
     }
 };
@@ -328,130 +333,53 @@ __global__ __launch_bounds__(256) void glu_dx_sum_kernel(GluArgs a)
     const int64_t n = a.m * a.k;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
         float s = 0.0f;
+#pragma unroll 8
         for (int64_t p = 0; p < a.dx_splits; ++p) s += a.dx_part[p * n + i];
         static_cast<typename MM<DT>::T*>(a.dx)[i] = MM<DT>::narrow(s);
     }
 }
 
-// ---- few tokens: the weights stream past them -------------------------------------------------
+// ---- few tokens ---------------------------------------------------------------------------------
 
-// A workgroup forms the outputs of 16 features for all tokens (MT x 16 of them).  Its waves
-// split k; a wave reads its part of the 16 rows of Wg and of Wu straight into MFMA operands
-// (lane: row l % 16, 16 bytes of k per step), the tokens' rows likewise (they are shared by
-// every workgroup and stay in the caches), and the waves' sums are joined in LDS.
-constexpr int kStreamWaves = 4;
-constexpr int kStreamUnroll = 4;  // steps whose loads are in flight together
-
-template <int DT>
-struct Stream;
-template <>
-struct Stream<1> {
-    using Frag = bf16x8;
-    static __device__ __forceinline__ f32x4 mul(Frag w, Frag x, f32x4 c) { return mfma_bf16(w, x, c); }
-};
-template <>
-struct Stream<0> {  // the fp32 instruction: its rate does not matter here
-    using Frag = f32x4;
-    static __device__ __forceinline__ f32x4 mul(Frag w, Frag x, f32x4 c)
-    {
-        // k is taken in the order (k % 4) * 4 + k / 4 within a step's 16, on both sides alike
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], x[j], c, 0, 0, 0);
-        return c;
-    }
-};
-
-template <int DT, int MT, int ACT>
+// 16 features per workgroup: their rows of Wg and of Wu.
+template <int DT, int MT, bool ALIGNED, int ACT, bool BACK>
 __global__ __launch_bounds__(64 * kStreamWaves) void glu_stream_kernel(GluArgs a, bool vec)
 {
-    using M = MM<DT>;
-    using T = typename M::T;
-    using S = Stream<DT>;
-    using Frag = typename S::Frag;
-    constexpr int KS = 4 * M::kEpc;  // k per step
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    using T = typename MM<DT>::T;
+    const int lane = threadIdx.x & 63;
     const int64_t f0 = int64_t(blockIdx.x) * 16;
     int64_t fr = f0 + (lane & 15);
     fr = fr < a.f ? fr : a.f - 1;
-    const int kq = (lane >> 4) * M::kEpc;
-    const T* const pg = static_cast<const T*>(a.wg) + fr * a.w_ld + kq;
-    const T* const pu = static_cast<const T*>(a.wu) + fr * a.w_ld + kq;
     const T* px[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         int64_t m = i * 16 + (lane & 15);
         m = m < a.m ? m : a.m - 1;
-        px[i] = static_cast<const T*>(a.x) + m * a.x_ld + kq;
+        px[i] = static_cast<const T*>(a.x_raw) + m * a.x_raw_ld;
     }
     f32x4 g[MT], u[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) g[i] = u[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const int64_t steps = a.k_pad / KS;  // whole steps
-    int64_t s = wave;
-    for (; s + (kStreamUnroll - 1) * kStreamWaves < steps; s += kStreamUnroll * kStreamWaves) {
-        Frag wg[kStreamUnroll], wu[kStreamUnroll], xf[kStreamUnroll][MT];
-#pragma unroll
-        for (int q = 0; q < kStreamUnroll; ++q) {
-            const int64_t k = (s + q * kStreamWaves) * KS;
-            wg[q] = *reinterpret_cast<const Frag*>(pg + k);
-            wu[q] = *reinterpret_cast<const Frag*>(pu + k);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) xf[q][i] = *reinterpret_cast<const Frag*>(px[i] + k);
-        }
-#pragma unroll
-        for (int q = 0; q < kStreamUnroll; ++q)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                g[i] = S::mul(wg[q], xf[q][i], g[i]);
-                u[i] = S::mul(wu[q], xf[q][i], u[i]);
-            }
-    }
-    for (; s < (a.k_pad + KS - 1) / KS; s += kStreamWaves) {
-        const int64_t k = s * KS;
-        const bool in = k + kq < a.k_pad;  // the last step may be partial: whole chunks
-        Frag zero{};
-        const Frag wg = in ? *reinterpret_cast<const Frag*>(pg + k) : zero;
-        const Frag wu = in ? *reinterpret_cast<const Frag*>(pu + k) : zero;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const Frag xf = in ? *reinterpret_cast<const Frag*>(px[i] + k) : zero;
-            g[i] = S::mul(wg, xf, g[i]);
-            u[i] = S::mul(wu, xf, u[i]);
-        }
-    }
-    __shared__ f32x4 part[kStreamWaves][2 * MT][64];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        part[wave][2 * i][lane] = g[i];
-        part[wave][2 * i + 1][lane] = u[i];
-    }
-    __syncthreads();
-    for (int i = wave; i < MT; i += kStreamWaves) {
-        f32x4 gs = part[0][2 * i][lane], us = part[0][2 * i + 1][lane];
-#pragma unroll
-        for (int w = 1; w < kStreamWaves; ++w) {
-            gs += part[w][2 * i][lane];
-            us += part[w][2 * i + 1][lane];
-        }
-        const int64_t m = i * 16 + (lane & 15), f = f0 + (lane >> 4) * 4;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = act_of<ACT>(gs[e]) * us[e];
-        if (m < a.m && f < a.f) store4<DT>(static_cast<T*>(a.h) + m * a.f + f, a.f - f, vec, v);
-    }
+    stream_rows<DT, MT, ALIGNED>(static_cast<const T*>(a.wg_raw) + fr * a.k, static_cast<const T*>(a.wu_raw) + fr * a.k,
+                                 px, a.k, g, u);
+    stream_join<MT>(g, u, [&](int i, f32x4 gs, f32x4 us) {
+        const int64_t m = i * 16 + (lane & 15);
+        if (m < a.m) glu_emit<DT, ACT, BACK>(a, m, f0 + (lane >> 4) * 4, gs, us, vec);
+    });
 }
 
 // ---- padded copy ------------------------------------------------------------------------------
 
+// One 16-byte chunk of a padded row per thread.
 template <int DT>
 __global__ __launch_bounds__(256) void pad_rows_kernel(const typename MM<DT>::T* src, int64_t ld,
                                                        typename MM<DT>::T* dst, int64_t rows, int64_t cols,
-                                                       int64_t cols_pad)
+                                                       int64_t chunks)
 {
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-        const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-        if (c < cols_pad) dst[r * cols_pad + c] = c < cols ? src[r * ld + c] : MM<DT>::narrow(0.0f);
+    constexpr int E = MM<DT>::kEpc;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * chunks; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / chunks, c = (i - r * chunks) * E;
+        const typename MM<DT>::T* p = src + r * ld + c;
+        *reinterpret_cast<typename Stream<DT>::Frag*>(dst + i * E) =
+            c + E <= cols ? stream_load<DT, false>(p) : stream_tail<DT>(p, cols - c);
     }
 }
 
@@ -479,17 +407,30 @@ hipError_t launch_glu_gu(const GluArgs& a, bool vec, hipStream_t s)
     return t == Tile::Mini ? launch_glu_tile<M, M, ACT, BACK>(a, vec, s) : launch_glu_tile<S, S, ACT, BACK>(a, vec, s);
 }
 
-template <int DT, int ACT>
+template <int DT, int MT, bool BACK>
+hipError_t launch_glu_stream_mt(const GluArgs& a, bool vec, hipStream_t s)
+{
+    const dim3 grid(up(BACK ? a.f_pad : a.f, 16)), block(64 * kStreamWaves);
+    if (a.act == kActSilu) {
+        if (a.aligned)
+            glu_stream_kernel<DT, MT, true, kActSilu, BACK><<<grid, block, 0, s>>>(a, vec);
+        else
+            glu_stream_kernel<DT, MT, false, kActSilu, BACK><<<grid, block, 0, s>>>(a, vec);
+    } else {
+        if (a.aligned)
+            glu_stream_kernel<DT, MT, true, kActGelu, BACK><<<grid, block, 0, s>>>(a, vec);
+        else
+            glu_stream_kernel<DT, MT, false, kActGelu, BACK><<<grid, block, 0, s>>>(a, vec);
+    }
+    return hipGetLastError();
+}
+
+template <int DT, bool BACK>
 hipError_t launch_glu_stream(const GluArgs& a, bool vec, hipStream_t s)
 {
-    const dim3 grid(up(a.f, 16)), block(64 * kStreamWaves);
-    if (a.m <= 16)
-        glu_stream_kernel<DT, 1, ACT><<<grid, block, 0, s>>>(a, vec);
-    else if (a.m <= 32)
-        glu_stream_kernel<DT, 2, ACT><<<grid, block, 0, s>>>(a, vec);
-    else
-        glu_stream_kernel<DT, 4, ACT><<<grid, block, 0, s>>>(a, vec);
-    return hipGetLastError();
+    if (a.m <= 16) return launch_glu_stream_mt<DT, 1, BACK>(a, vec, s);
+    if (a.m <= 32) return launch_glu_stream_mt<DT, 2, BACK>(a, vec, s);
+    return launch_glu_stream_mt<DT, 4, BACK>(a, vec, s);
 }
 
 bool vec_rows(const void* p, int64_t row, int dtype)
@@ -501,9 +442,7 @@ template <int DT>
 hipError_t glu_fwd_dt(const GluArgs& a, hipStream_t s)
 {
     const bool vec = vec_rows(a.h, a.f, DT);
-    if (a.m <= kGluStreamRows)
-        return a.act == kActSilu ? launch_glu_stream<DT, kActSilu>(a, vec, s)
-                                 : launch_glu_stream<DT, kActGelu>(a, vec, s);
+    if (a.m <= kStreamRows) return launch_glu_stream<DT, false>(a, vec, s);
     return a.act == kActSilu ? launch_glu_gu<DT, kActSilu, false>(a, vec, s)
                              : launch_glu_gu<DT, kActGelu, false>(a, vec, s);
 }
@@ -530,8 +469,9 @@ template <int DT>
 hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
 {
     const bool vec = vec_rows(a.dh, a.f, DT);
-    const hipError_t e = a.act == kActSilu ? launch_glu_gu<DT, kActSilu, true>(a, vec, s)
-                                           : launch_glu_gu<DT, kActGelu, true>(a, vec, s);
+    const hipError_t e = a.m <= kStreamRows ? launch_glu_stream<DT, true>(a, vec, s)
+                         : a.act == kActSilu ? launch_glu_gu<DT, kActSilu, true>(a, vec, s)
+                                             : launch_glu_gu<DT, kActGelu, true>(a, vec, s);
     if (e != hipSuccess) return e;
     auto tiles = [&](int bm, int bn) {
         return (a.dx ? count(a.m, a.k, bm, bn) * a.dx_splits : 0) + (a.dwg ? count(2 * a.f_pad, a.k, bm, bn) : 0);
@@ -556,13 +496,15 @@ hipError_t launch_pad_rows(const void* src, int64_t ld, void* dst, int64_t rows,
                            int dtype, hipStream_t stream)
 {
     (void)hipGetLastError();
-    const dim3 grid(up(cols_pad, 256), unsigned(rows < 65535 ? rows : 65535));
+    const int64_t chunks = cols_pad / (dtype == 0 ? MM<0>::kEpc : MM<1>::kEpc);
+    const int64_t blocks = (rows * chunks + 255) / 256;
+    const dim3 grid(unsigned(blocks < 16384 ? blocks : 16384));
     if (dtype == 0)
         pad_rows_kernel<0><<<grid, dim3(256), 0, stream>>>(static_cast<const float*>(src), ld, static_cast<float*>(dst),
-                                                          rows, cols, cols_pad);
+                                                          rows, cols, chunks);
     else
         pad_rows_kernel<1><<<grid, dim3(256), 0, stream>>>(static_cast<const __bf16*>(src), ld,
-                                                          static_cast<__bf16*>(dst), rows, cols, cols_pad);
+                                                          static_cast<__bf16*>(dst), rows, cols, chunks);
     return hipGetLastError();
 }
 

@@ -410,7 +410,8 @@ bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluL
     const int64_t es = elem_size(dtype);
     w->k_pad = padded(k, dtype);
     w->f_pad = padded(f, dtype);
-    w->pack = w->k_pad != k;
+    // padded copies for the tiles; the forward of few tokens has none
+    w->pack = w->k_pad != k && (back || m > ssk::kStreamRows);
     Regions r;
     w->x = r.add(w->pack ? m * w->k_pad : 0, es);
     w->wg = r.add(w->pack ? f * w->k_pad : 0, es);
@@ -450,12 +451,12 @@ bool xent_layout(int64_t n, int64_t d, int64_t v, ss_dtype dtype, bool back, Xen
     if (!mat_sizes(n, d, v) || !known(dtype)) return false;
     const int64_t es = elem_size(dtype);
     w->d_pad = padded(d, dtype);
-    w->pack = w->d_pad != d;
+    w->pack = w->d_pad != d && (back || n > ssk::kStreamRows);
     w->piece = xent_piece(n, v, es);
     Regions r;
     w->x = r.add(w->pack ? n * w->d_pad : 0, es);
     w->w = r.add(w->pack ? v * w->d_pad : 0, es);
-    const int64_t parts = back ? 0 : ceil_div(v, ssk::kXentCols) * n;
+    const int64_t parts = back ? 0 : ceil_div(v, n <= ssk::kStreamRows ? ssk::kXentStreamCols : ssk::kXentCols) * n;
     w->pmax = r.add(parts, 4);
     w->psum = r.add(parts, 4);
     w->tl = r.add(back ? 0 : n, 4);
@@ -547,10 +548,18 @@ ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, 
     a.dx_splits = w.splits;
     a.dx_part = back && w.splits > 1 ? reinterpret_cast<float*>(ws + w.part) : nullptr;
     a.act = act == SS_ACT_SILU ? ssk::kActSilu : ssk::kActGelu;
+    a.x_raw = x;
+    a.x_raw_ld = x_ld;
+    a.wg_raw = wg;
+    a.wu_raw = wu;
+    a.aligned = w.k_pad == k;
     if (w.pack) {
-        hipError_t e = ssk::launch_pad_rows(x, x_ld, ws + w.x, m, k, w.k_pad, dt, stream);
-        if (e == hipSuccess) e = ssk::launch_pad_rows(wg, k, ws + w.wg, f, k, w.k_pad, dt, stream);
-        if (e == hipSuccess) e = ssk::launch_pad_rows(wu, k, ws + w.wu, f, k, w.k_pad, dt, stream);
+        // of few tokens, the tiles read x for the weights' gradients and the weights for dx
+        const bool few = m <= ssk::kStreamRows;
+        hipError_t e = hipSuccess;
+        if (!few || dwg) e = ssk::launch_pad_rows(x, x_ld, ws + w.x, m, k, w.k_pad, dt, stream);
+        if (e == hipSuccess && (!few || dx)) e = ssk::launch_pad_rows(wg, k, ws + w.wg, f, k, w.k_pad, dt, stream);
+        if (e == hipSuccess && (!few || dx)) e = ssk::launch_pad_rows(wu, k, ws + w.wu, f, k, w.k_pad, dt, stream);
         if (e != hipSuccess) return done(e);
         a.x = ws + w.x;
         a.wg = ws + w.wg;
@@ -618,9 +627,16 @@ ss_status xent_impl(const void* x, int64_t x_ld, const void* weight, const int64
     a.counts = reinterpret_cast<int32_t*>(ws + w.counts);
     a.dx_splits = w.splits;
     a.dx_acc = w.piece < v || w.splits > 1 ? reinterpret_cast<float*>(ws + w.acc) : nullptr;
+    a.x_raw = x;
+    a.x_raw_ld = x_ld;
+    a.w_raw = weight;
+    a.aligned = w.d_pad == d;
     if (w.pack) {
-        hipError_t e = ssk::launch_pad_rows(x, x_ld, ws + w.x, n, d, w.d_pad, dt, stream);
-        if (e == hipSuccess) e = ssk::launch_pad_rows(weight, d, ws + w.w, v, d, w.d_pad, dt, stream);
+        // of few rows, the tiles read x for dw and w for dx
+        const bool few = n <= ssk::kStreamRows;
+        hipError_t e = hipSuccess;
+        if (!few || dw) e = ssk::launch_pad_rows(x, x_ld, ws + w.x, n, d, w.d_pad, dt, stream);
+        if (e == hipSuccess && (!few || dx)) e = ssk::launch_pad_rows(weight, d, ws + w.w, v, d, w.d_pad, dt, stream);
         if (e != hipSuccess) return done(e);
         a.x = ws + w.x;
         a.w = ws + w.w;

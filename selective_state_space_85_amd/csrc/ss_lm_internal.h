@@ -8,12 +8,14 @@
 
 namespace ssk {
 
+// Rows of x up to which products with weights stream the weights past them (ss_gemm.h) instead
+// of working in tiles.
+constexpr int64_t kStreamRows = 64;
+
 // ---- gated feed-forward projection -----------------------------------------------------
 
 constexpr int kActSilu = 0, kActGelu = 1;
 
-// Tokens up to which the weight-streaming kernel is used instead of the tiled one.
-constexpr int64_t kGluStreamRows = 64;
 
 struct GluArgs {
     const void* x;   // (m, k), rows x_ld elements apart
@@ -28,7 +30,14 @@ struct GluArgs {
     void* dwg;       // (f, k), nullable (both or neither)
     void* dwu;
     int64_t m, k, f, f_pad;
-    int64_t k_pad;   // k rounded up to whole 16-byte chunks; x and w rows hold zeros there
+    int64_t k_pad;   // k rounded up to whole 16-byte chunks; rows of x and w in tiles hold zeros there
+    // the operands as the caller gave them: the streaming kernels take any alignment.  Equal to x
+    // and the weights unless those are padded copies.
+    const void* x_raw;
+    int64_t x_raw_ld;
+    const void* wg_raw;
+    const void* wu_raw;
+    bool aligned;    // x_raw and the weights start every row on 16 bytes
     int act;
     // the backward's sums of dx over 2 f are cut in dx_splits parts when tokens are few
     float* dx_part;  // (dx_splits, m, k) fp32, null with one part
@@ -44,8 +53,9 @@ hipError_t launch_glu_bwd(const GluArgs& a, int dtype, hipStream_t stream);
 
 // ---- softmax cross entropy of a vocabulary projection -----------------------------------
 
-// Columns of the vocabulary behind one partial (maximum, sum) pair of a row.
-constexpr int64_t kXentCols = 128;
+// Columns of the vocabulary behind one partial (maximum, sum) pair of a row, in tiles and in the
+// streaming kernel.
+constexpr int64_t kXentCols = 128, kXentStreamCols = 32;
 
 struct XentArgs {
     const void* x;  // (n, d), rows x_ld elements apart
@@ -56,7 +66,7 @@ struct XentArgs {
     int64_t ignore_index;
     float* loss;        // forward output (n,)
     float* lse;         // forward output, backward input (n,)
-    float* part_max;    // forward workspace: (ceil(v / kXentCols), n)
+    float* part_max;    // forward workspace: (ceil(v / columns per pair), n)
     float* part_sum;
     float* target_logit;  // forward workspace (n,)
     const float* dloss;   // backward (n,)
@@ -74,6 +84,11 @@ struct XentArgs {
     void* dw;             // (v, d), nullable
     int64_t n, d, v;
     int64_t d_pad;        // d rounded up to whole 16-byte chunks
+    // as for GluArgs
+    const void* x_raw;
+    int64_t x_raw_ld;
+    const void* w_raw;
+    bool aligned;
     int64_t piece;        // columns of the vocabulary per piece (the backward)
 };
 

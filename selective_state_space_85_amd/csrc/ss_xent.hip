@@ -140,34 +140,137 @@ __global__ __launch_bounds__(G::NT) void xent_fwd_kernel(XentArgs a, TilePlan pl
     if (p.m0 < a.n) mm_tile<H>(p, lds);
 }
 
-// The pairs of a row, joined: 16 rows per workgroup, 16 threads a row.
-constexpr int kJoinRows = 16, kJoinLanes = 16;
-__global__ __launch_bounds__(kJoinRows * kJoinLanes) void xent_join_kernel(XentArgs a, int64_t groups)
+// The pairs of a row, joined: ROWS rows per workgroup, 256 / ROWS threads a row.
+template <int ROWS>
+__global__ __launch_bounds__(256) void xent_join_kernel(XentArgs a, int64_t groups)
 {
-    __shared__ float sm[kJoinLanes][kJoinRows], ss[kJoinLanes][kJoinRows];
-    const int r = threadIdx.x % kJoinRows, q = threadIdx.x / kJoinRows;
-    const int64_t row = int64_t(blockIdx.x) * kJoinRows + r;
+    constexpr int LANES = 256 / ROWS;
+    __shared__ float sm[LANES][ROWS], ss[LANES][ROWS];
+    const int r = threadIdx.x % ROWS, q = threadIdx.x / ROWS;
+    const int64_t row = int64_t(blockIdx.x) * ROWS + r;
     float m = -__builtin_inff(), s = 0.0f;
-    if (row < a.n)
-        for (int64_t g = q; g < groups; g += kJoinLanes) join(m, s, a.part_max[g * a.n + row], a.part_sum[g * a.n + row]);
+    if (row < a.n) {
+#pragma unroll 4
+        for (int64_t g = q; g < groups; g += LANES) join(m, s, a.part_max[g * a.n + row], a.part_sum[g * a.n + row]);
+    }
     sm[q][r] = m;
     ss[q][r] = s;
-    __syncthreads();
+    for (int half = LANES / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (q < half) {
+            join(m, s, sm[q + half][r], ss[q + half][r]);
+            sm[q][r] = m;
+            ss[q][r] = s;
+        }
+    }
     if (q != 0 || row >= a.n) return;
-    for (int w = 1; w < kJoinLanes; ++w) join(m, s, sm[w][r], ss[w][r]);
     const float lse = m + __builtin_amdgcn_logf(s) * kLn2;
     const int64_t t = a.target[row];
     a.lse[row] = lse;
     a.loss[row] = live_target(t, a) ? lse - a.target_logit[row] : 0.0f;
 }
 
+// Few rows: 32 columns of the vocabulary per workgroup.
+template <int DT, int MT, bool ALIGNED>
+struct XentStream {
+    using T = typename MM<DT>::T;
+    const XentArgs& a;
+    int64_t c0;  // first column
+    f32x4 s0[MT], s1[MT];
+
+    __device__ __forceinline__ void run()
+    {
+        const int lane = threadIdx.x & 63;
+        const T* px[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            int64_t m = i * 16 + (lane & 15);
+            m = m < a.n ? m : a.n - 1;
+            px[i] = static_cast<const T*>(a.x_raw) + m * a.x_raw_ld;
+        }
+        int64_t r0 = c0 + (lane & 15), r1 = r0 + 16;
+        r0 = r0 < a.v ? r0 : a.v - 1;
+        r1 = r1 < a.v ? r1 : a.v - 1;
+        const T* const w = static_cast<const T*>(a.w_raw);
+        stream_rows<DT, MT, ALIGNED>(w + r0 * a.d, w + r1 * a.d, px, a.d, s0, s1);
+    }
+};
+
+template <int DT, int MT, bool ALIGNED>
+__global__ __launch_bounds__(64 * kStreamWaves) void xent_fwd_stream_kernel(XentArgs a)
+{
+    XentStream<DT, MT, ALIGNED> x{a, int64_t(blockIdx.x) * kXentStreamCols, {}, {}};
+    x.run();
+    const int lane = threadIdx.x & 63;
+    stream_join<MT>(x.s0, x.s1, [&](int i, f32x4 l0, f32x4 l1) {
+        const int64_t m = i * 16 + (lane & 15), c = x.c0 + (lane >> 4) * 4;
+        const int64_t t = m < a.n ? a.target[m] : -1;
+        float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t col = c + (e & 3) + (e & 4) * 4;
+            const float v = e < 4 ? l0[e & 3] : l1[e & 3];
+            if (col == t && t < a.v) a.target_logit[m] = v;
+            if (col < a.v) top = fmaxf(top, v);
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float base = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t col = c + (e & 3) + (e & 4) * 4;
+            const float v = e < 4 ? l0[e & 3] : l1[e & 3];
+            if (col < a.v) sum += exp2_hw((v - base) * kLog2e);
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (lane < 16 && m < a.n) {
+            a.part_max[blockIdx.x * a.n + m] = top;
+            a.part_sum[blockIdx.x * a.n + m] = sum;
+        }
+    });
+}
+
 // ---- backward ------------------------------------------------------------------------------
 
-// dl of one piece: columns [v0, v0 + cols) of the vocabulary, rows of `pad` elements
+// dl of one piece: columns [v0, v0 + cols) of the vocabulary, rows of `pad` elements.
+struct Piece {
+    int64_t v0, cols, pad;
+};
+
+// What of row m's dl is the same for every column.
+struct RowOfDl {
+    int64_t target;
+    bool live;
+    float lse, scale;
+    __device__ RowOfDl(const XentArgs& a, int64_t m)
+        : target(a.target[m]), live(live_target(target, a)), lse(a.lse[m]), scale(a.dloss[m])
+    {
+    }
+};
+
+// Four neighbouring columns c.. of row m from their logits.
+template <int DT>
+__device__ __forceinline__ void dl_emit(const XentArgs& a, const Piece& p, const RowOfDl& row, int64_t m, int64_t c, f32x4 l)
+{
+    using T = typename MM<DT>::T;
+    if (c - p.v0 >= p.pad) return;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    T4 q;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float v = exp2_hw((l[e] - row.lse) * kLog2e) - (c + e == row.target ? 1.0f : 0.0f);
+        // the columns past the piece's end hold zeros: the products read them
+        const float full = row.live && c + e - p.v0 < p.cols ? v * row.scale : 0.0f;
+        q[e] = MM<DT>::narrow(full);
+        if (DT == 1 && row.live && c + e == row.target && c + e - p.v0 < p.cols) a.lo[m] = full - MM<DT>::widen(q[e]);
+    }
+    *reinterpret_cast<T4*>(static_cast<T*>(a.dl) + m * p.pad + (c - p.v0)) = q;
+}
+
 template <int DT>
 struct XentDlProb : XentLogits<DT> {
-    using T = typename MM<DT>::T;
-    int64_t v0, cols, pad;
+    Piece piece;
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -177,29 +280,29 @@ struct XentDlProb : XentLogits<DT> {
         for (int i = 0; i < G::FM; ++i) {
             const int64_t m = this->m0 + (wm * G::FM + i) * 16 + (lane & 15);
             if (m >= a.n) continue;
-            const int64_t t = a.target[m];
-            const bool live = live_target(t, a);
-            const float lse = a.lse[m], scale = a.dloss[m];
-            T* const row = static_cast<T*>(a.dl) + m * pad;
+            const RowOfDl row(a, m);
 #pragma unroll
-            for (int j = 0; j < G::FN; ++j) {
-                const int64_t c = this->n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
-                if (c - v0 >= pad) continue;
-                typedef T T4 __attribute__((ext_vector_type(4)));
-                T4 q;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = exp2_hw((acc[i][j][e] - lse) * kLog2e) - (c + e == t ? 1.0f : 0.0f);
-                    // the columns past the piece's end hold zeros: the products read them
-                    const float full = live && c + e - v0 < cols ? p * scale : 0.0f;
-                    q[e] = MM<DT>::narrow(full);
-                    if (DT == 1 && live && c + e == t && c + e - v0 < cols) a.lo[m] = full - MM<DT>::widen(q[e]);
-                }
-                *reinterpret_cast<T4*>(row + (c - v0)) = q;
-            }
+            for (int j = 0; j < G::FN; ++j)
+                dl_emit<DT>(a, piece, row, m, this->n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4, acc[i][j]);
         }
     }
 };
+
+// Few rows: 32 columns of the piece per workgroup.
+template <int DT, int MT, bool ALIGNED>
+__global__ __launch_bounds__(64 * kStreamWaves) void xent_dl_stream_kernel(XentArgs a, Piece piece)
+{
+    XentStream<DT, MT, ALIGNED> x{a, piece.v0 + int64_t(blockIdx.x) * kXentStreamCols, {}, {}};
+    x.run();
+    const int lane = threadIdx.x & 63;
+    stream_join<MT>(x.s0, x.s1, [&](int i, f32x4 l0, f32x4 l1) {
+        const int64_t m = i * 16 + (lane & 15), c = x.c0 + (lane >> 4) * 4;
+        if (m >= a.n) return;
+        const RowOfDl row(a, m);
+        dl_emit<DT>(a, piece, row, m, c, l0);
+        dl_emit<DT>(a, piece, row, m, c + 16, l1);
+    });
+}
 
 template <class G, class H>
 __global__ __launch_bounds__(G::NT) void xent_dl_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad, TilePlan plan)
@@ -208,7 +311,7 @@ __global__ __launch_bounds__(G::NT) void xent_dl_kernel(XentArgs a, int64_t v0, 
     uint32_t tm, tn;
     const int half = tile_of(blockIdx.x, plan, &tm, &tn);
     XentDlProb<G::DT> p{
-        {a, int64_t(tm) * G::BM, v0 + int64_t(tn) * G::BN, int((a.d_pad + G::BK - 1) / G::BK)}, v0, cols, pad};
+        {a, int64_t(tm) * G::BM, v0 + int64_t(tn) * G::BN, int((a.d_pad + G::BK - 1) / G::BK)}, {v0, cols, pad}};
     if (half < 0) {
         mm_tile<G>(p, lds);
         return;
@@ -438,6 +541,7 @@ __global__ __launch_bounds__(256) void xent_dx_sum_kernel(XentArgs a)
     const int64_t n = a.n * a.d;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
         float s = 0.0f;
+#pragma unroll 8
         for (int64_t p = 0; p < a.dx_splits; ++p) s += a.dx_acc[p * n + i];
         const int64_t row = i / a.d, t = a.target[row];
         if (DT == 1 && live_target(t, a))
@@ -468,12 +572,43 @@ hipError_t fwd_tiles_dt(const XentArgs& a, hipStream_t s)
     return t == Tile::Mini ? fwd_tiles<M, M>(a, s) : fwd_tiles<S, S>(a, s);
 }
 
+template <int DT, int MT>
+hipError_t fwd_stream(const XentArgs& a, hipStream_t s)
+{
+    const dim3 grid(up(a.v, kXentStreamCols)), block(64 * kStreamWaves);
+    if (a.aligned)
+        xent_fwd_stream_kernel<DT, MT, true><<<grid, block, 0, s>>>(a);
+    else
+        xent_fwd_stream_kernel<DT, MT, false><<<grid, block, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <int DT>
 hipError_t fwd_dt(const XentArgs& a, hipStream_t s)
 {
-    const hipError_t e = fwd_tiles_dt<DT>(a, s);
+    const bool stream = a.n <= kStreamRows;
+    const hipError_t e = !stream     ? fwd_tiles_dt<DT>(a, s)
+                         : a.n <= 16 ? fwd_stream<DT, 1>(a, s)
+                         : a.n <= 32 ? fwd_stream<DT, 2>(a, s)
+                                     : fwd_stream<DT, 4>(a, s);
     if (e != hipSuccess) return e;
-    xent_join_kernel<<<dim3(up(a.n, kJoinRows)), dim3(kJoinRows * kJoinLanes), 0, s>>>(a, int64_t(up(a.v, kXentCols)));
+    const int64_t groups = up(a.v, stream ? kXentStreamCols : kXentCols);
+    // few rows: more threads on each
+    if (a.n >= 4096)
+        xent_join_kernel<16><<<dim3(up(a.n, 16)), dim3(256), 0, s>>>(a, groups);
+    else
+        xent_join_kernel<2><<<dim3(up(a.n, 2)), dim3(256), 0, s>>>(a, groups);
+    return hipGetLastError();
+}
+
+template <int DT, int MT>
+hipError_t dl_stream(const XentArgs& a, const Piece& p, hipStream_t s)
+{
+    const dim3 grid(up(p.pad, kXentStreamCols)), block(64 * kStreamWaves);
+    if (a.aligned)
+        xent_dl_stream_kernel<DT, MT, true><<<grid, block, 0, s>>>(a, p);
+    else
+        xent_dl_stream_kernel<DT, MT, false><<<grid, block, 0, s>>>(a, p);
     return hipGetLastError();
 }
 
@@ -488,6 +623,9 @@ hipError_t dl_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hi
 template <int DT>
 hipError_t dl_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
+    if (a.n <= 16) return dl_stream<DT, 1>(a, {v0, cols, pad}, s);
+    if (a.n <= 32) return dl_stream<DT, 2>(a, {v0, cols, pad}, s);
+    if (a.n <= kStreamRows) return dl_stream<DT, 4>(a, {v0, cols, pad}, s);
     const Tile t = best_tile<DT>(count(a.n, pad, 256, 256), count(a.n, pad, 128, 128), count(a.n, pad, 64, 128));
     if constexpr (DT == 1) {
         if (t == Tile::Large)

@@ -179,7 +179,7 @@ REFUSED = [
     (glr_bwd, dict(ws=None), WORKSPACE),
     (glr_bwd, dict(wsb=255), WORKSPACE),
     (glr_bwd, dict(ws=addr(6)), INVALID),
-    (glu_fwd, dict(k=63), WORKSPACE),
+    (glu_fwd, dict(k=63), WORKSPACE),  # 100 tokens: in tiles, from padded copies
     (glu_bwd, dict(ws=None), WORKSPACE),
     (glu_bwd, dict(wsb=1000), WORKSPACE),
     (glu_bwd, dict(ws=addr(4)), INVALID),
@@ -208,6 +208,7 @@ def test_sizes(lib):
             >= lib.ss_glr_ckpt_bytes(2, 1000, 96))
     assert lib.ss_glu_workspace_bytes(100, 64, 96, BF16) == 0
     assert lib.ss_glu_workspace_bytes(100, 63, 96, BF16) >= (100 + 2 * 96) * 64 * 2
+    assert lib.ss_glu_workspace_bytes(64, 63, 96, BF16) == 0, "few tokens: the rows are read as they lie"
     assert lib.ss_glu_workspace_bytes(100, 63, 96, 9) == BAD
     assert lib.ss_glu_bwd_workspace_bytes(100, 64, 97, BF16) == 100 * 2 * 104 * 2
     assert lib.ss_xent_workspace_bytes(10, 64, 129, F32) >= 2 * 2 * 10 * 4 + 10 * 4
