@@ -117,6 +117,12 @@ __device__ __forceinline__ void glu_emit(const GluArgs& a, int64_t m, int64_t f,
             du[e] = in ? d[e] * act : 0.0f;
         }
         // f_pad is a multiple of 4: whole groups, aligned
+        if (a.few) {
+            float* const row = static_cast<float*>(a.dgu) + m * 2 * a.f_pad + f;
+            store4<0>(row, 4, true, dg);
+            store4<0>(row + a.f_pad, 4, true, du);
+            return;
+        }
         T* const row = static_cast<T*>(a.dgu) + m * 2 * a.f_pad + f;
         store4<DT>(row, 4, true, dg);
         store4<DT>(row + a.f_pad, 4, true, du);
@@ -442,7 +448,7 @@ template <int DT>
 hipError_t glu_fwd_dt(const GluArgs& a, hipStream_t s)
 {
     const bool vec = vec_rows(a.h, a.f, DT);
-    if (a.m <= kStreamRows) return launch_glu_stream<DT, false>(a, vec, s);
+    if (a.stream) return launch_glu_stream<DT, false>(a, vec, s);
     return a.act == kActSilu ? launch_glu_gu<DT, kActSilu, false>(a, vec, s)
                              : launch_glu_gu<DT, kActGelu, false>(a, vec, s);
 }
@@ -469,10 +475,14 @@ template <int DT>
 hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
 {
     const bool vec = vec_rows(a.dh, a.f, DT);
-    const hipError_t e = a.m <= kStreamRows ? launch_glu_stream<DT, true>(a, vec, s)
+    const hipError_t e = a.stream ? launch_glu_stream<DT, true>(a, vec, s)
                          : a.act == kActSilu ? launch_glu_gu<DT, kActSilu, true>(a, vec, s)
                                              : launch_glu_gu<DT, kActGelu, true>(a, vec, s);
     if (e != hipSuccess) return e;
+    if (a.few)
+        return launch_few_grad({static_cast<const float*>(a.dgu), 2 * a.f_pad, a.f_pad, a.wg_raw, a.wu_raw, a.dwg, a.dwu,
+                                a.x_raw, a.x_raw_ld, a.dx_part, a.dx, a.f, 2 * a.f, a.m, a.k, a.dx_per, a.dx_splits},
+                               DT, s);
     auto tiles = [&](int bm, int bn) {
         return (a.dx ? count(a.m, a.k, bm, bn) * a.dx_splits : 0) + (a.dwg ? count(2 * a.f_pad, a.k, bm, bn) : 0);
     };

@@ -398,8 +398,48 @@ int64_t dx_parts(int64_t rows, int64_t dim, int64_t depth, ss_dtype dtype)
     return s > 1 ? s : 1;
 }
 
+// How the products of `rows` rows of x with `cols` weight rows are formed (both directions), and
+// their gradients.
+struct RowsPlan {
+    bool aligned;  // rows are whole 16-byte chunks
+    bool stream;   // the weights stream past x; else tiles
+    bool few;      // the gradients in one pass over the weights
+    bool pad;      // padded copies are needed: tiles read them (in the forward, or the backward)
+};
+// Streaming reads x again for every 32 weight rows, from the caches: up to 16 rows that is little,
+// up to 64 it pays while tiles of 128 weight rows would leave CUs idle (46 563 weight rows of 3264 bf16,
+// 25 rows: tiles 74 us, streamed 94; 4 292 of 4632, 33 rows: 64 against 35), or where tiles would
+// need padded copies of the weights.
+RowsPlan rows_plan(int64_t rows, int64_t dim, int64_t cols, ss_dtype dtype, bool back)
+{
+    RowsPlan p;
+    p.aligned = dim % chunk_elems(dtype) == 0;
+    p.stream = rows <= 16 || (rows <= ssk::kStreamRows && (!p.aligned || ceil_div(cols, 128) < 256));
+    p.few = rows <= ssk::kFewRows;
+    p.pad = !p.aligned && (back ? !p.few : !p.stream);
+    return p;
+}
+
+// Parts of dx when few: enough ranges of the weights' rows for eight workgroups (of 512 columns) per
+// CU, of at least 8 rows, and few enough that the parts stay a quarter of the weights' size, or small.
+void few_parts(int64_t m, int64_t k, int64_t rows, ss_dtype dtype, int64_t* per, int64_t* parts)
+{
+    constexpr int64_t kSmall = int64_t(8) << 20;
+    int64_t s = 2048 / ceil_div(k, 512);
+    const int64_t by_rows = rows / 8;
+    int64_t by_size = rows * elem_size(dtype) / (16 * m);
+    const int64_t small = kSmall / (4 * m * k);
+    by_size = by_size > small ? by_size : small;
+    s = s < by_rows ? s : by_rows;
+    s = s < by_size ? s : by_size;
+    s = s > 1 ? s : 1;
+    *per = ceil_div(rows, s);
+    *parts = ceil_div(rows, *per);
+}
+
 struct GluLayout {
-    int64_t k_pad, f_pad, splits;
+    int64_t k_pad, f_pad, splits, per;
+    RowsPlan plan;
     bool pack;
     int64_t x, wg, wu, dgu, part, total;
 };
@@ -410,23 +450,28 @@ bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluL
     const int64_t es = elem_size(dtype);
     w->k_pad = padded(k, dtype);
     w->f_pad = padded(f, dtype);
-    // padded copies for the tiles; the forward of few tokens has none
-    w->pack = w->k_pad != k && (back || m > ssk::kStreamRows);
+    w->plan = rows_plan(m, k, 2 * f, dtype, back);
+    w->pack = w->plan.pad;
     Regions r;
     w->x = r.add(w->pack ? m * w->k_pad : 0, es);
     w->wg = r.add(w->pack ? f * w->k_pad : 0, es);
     w->wu = r.add(w->pack ? f * w->k_pad : 0, es);
-    w->dgu = r.add(back ? m * 2 * w->f_pad : 0, es);
-    w->splits = dx_parts(m, k, 2 * f, dtype);
+    w->dgu = r.add(back ? m * 2 * w->f_pad : 0, w->plan.few ? 4 : es);
+    w->per = 0;
+    if (w->plan.few)
+        few_parts(m, k, 2 * f, dtype, &w->per, &w->splits);
+    else
+        w->splits = dx_parts(m, k, 2 * f, dtype);
     int64_t part;
     if (!mul(w->splits, m, &part) || !mul(part, k, &part)) return false;
-    w->part = r.add(back && w->splits > 1 ? part : 0, 4);
+    w->part = r.add(back && (w->splits > 1 || w->plan.few) ? part : 0, 4);
     w->total = r.at;
     return r.ok;
 }
 
 struct XentLayout {
-    int64_t d_pad, piece, splits;
+    int64_t d_pad, piece, splits, per;
+    RowsPlan plan;
     bool pack;
     int64_t x, w, pmax, psum, tl, dl, lo, tokens, counts, acc, total;
 };
@@ -451,25 +496,30 @@ bool xent_layout(int64_t n, int64_t d, int64_t v, ss_dtype dtype, bool back, Xen
     if (!mat_sizes(n, d, v) || !known(dtype)) return false;
     const int64_t es = elem_size(dtype);
     w->d_pad = padded(d, dtype);
-    w->pack = w->d_pad != d && (back || n > ssk::kStreamRows);
-    w->piece = xent_piece(n, v, es);
+    w->plan = rows_plan(n, d, v, dtype, back);
+    w->pack = w->plan.pad;
+    w->piece = w->plan.few ? v : xent_piece(n, v, es);
     Regions r;
     w->x = r.add(w->pack ? n * w->d_pad : 0, es);
     w->w = r.add(w->pack ? v * w->d_pad : 0, es);
-    const int64_t parts = back ? 0 : ceil_div(v, n <= ssk::kStreamRows ? ssk::kXentStreamCols : ssk::kXentCols) * n;
+    const int64_t parts = back ? 0 : ceil_div(v, w->plan.stream ? ssk::kXentStreamCols : ssk::kXentCols) * n;
     w->pmax = r.add(parts, 4);
     w->psum = r.add(parts, 4);
     w->tl = r.add(back ? 0 : n, 4);
-    w->dl = r.add(back ? n * (ceil_div(w->piece, 16) * 16) : 0, es);
-    const bool listed = back && dtype == SS_BF16;
+    w->dl = r.add(back ? n * (ceil_div(w->piece, 16) * 16) : 0, w->plan.few ? 4 : es);
+    const bool listed = back && dtype == SS_BF16 && !w->plan.few;
     const int64_t groups = ceil_div(v, ssk::kXentCols);
     w->lo = r.add(listed ? n : 0, 4);
     w->tokens = r.add(listed ? groups * n : 0, 4);
     w->counts = r.add(listed ? groups : 0, 4);
-    w->splits = dx_parts(n, d, w->piece, dtype);
+    w->per = 0;
+    if (w->plan.few)
+        few_parts(n, d, v, dtype, &w->per, &w->splits);
+    else
+        w->splits = dx_parts(n, d, w->piece, dtype);
     int64_t sums;
     if (!mul(w->splits, n, &sums) || !mul(sums, d, &sums)) return false;
-    w->acc = r.add(back && (w->piece < v || w->splits > 1) ? sums : 0, 4);
+    w->acc = r.add(back && (w->piece < v || w->splits > 1 || w->plan.few) ? sums : 0, 4);
     w->total = r.at;
     return r.ok;
 }
@@ -546,16 +596,19 @@ ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, 
     a.f_pad = w.f_pad;
     a.k_pad = w.k_pad;
     a.dx_splits = w.splits;
-    a.dx_part = back && w.splits > 1 ? reinterpret_cast<float*>(ws + w.part) : nullptr;
+    a.dx_per = w.per;
+    a.dx_part = back && dx && (w.splits > 1 || w.plan.few) ? reinterpret_cast<float*>(ws + w.part) : nullptr;
     a.act = act == SS_ACT_SILU ? ssk::kActSilu : ssk::kActGelu;
     a.x_raw = x;
     a.x_raw_ld = x_ld;
     a.wg_raw = wg;
     a.wu_raw = wu;
-    a.aligned = w.k_pad == k;
+    a.aligned = w.plan.aligned;
+    a.stream = w.plan.stream;
+    a.few = w.plan.few;
     if (w.pack) {
-        // of few tokens, the tiles read x for the weights' gradients and the weights for dx
-        const bool few = m <= ssk::kStreamRows;
+        // after a streamed product, tiles read x for the weights' gradients and the weights for dx
+        const bool few = w.plan.stream;
         hipError_t e = hipSuccess;
         if (!few || dwg) e = ssk::launch_pad_rows(x, x_ld, ws + w.x, m, k, w.k_pad, dt, stream);
         if (e == hipSuccess && (!few || dx)) e = ssk::launch_pad_rows(wg, k, ws + w.wg, f, k, w.k_pad, dt, stream);
@@ -626,14 +679,17 @@ ss_status xent_impl(const void* x, int64_t x_ld, const void* weight, const int64
     a.tokens = reinterpret_cast<int32_t*>(ws + w.tokens);
     a.counts = reinterpret_cast<int32_t*>(ws + w.counts);
     a.dx_splits = w.splits;
-    a.dx_acc = w.piece < v || w.splits > 1 ? reinterpret_cast<float*>(ws + w.acc) : nullptr;
+    a.dx_per = w.per;
+    a.dx_acc = w.piece < v || w.splits > 1 || w.plan.few ? reinterpret_cast<float*>(ws + w.acc) : nullptr;
     a.x_raw = x;
     a.x_raw_ld = x_ld;
     a.w_raw = weight;
-    a.aligned = w.d_pad == d;
+    a.aligned = w.plan.aligned;
+    a.stream = w.plan.stream;
+    a.few = w.plan.few;
     if (w.pack) {
-        // of few rows, the tiles read x for dw and w for dx
-        const bool few = n <= ssk::kStreamRows;
+        // after a streamed product, tiles read x for dw and w for dx
+        const bool few = w.plan.stream;
         hipError_t e = hipSuccess;
         if (!few || dw) e = ssk::launch_pad_rows(x, x_ld, ws + w.x, n, d, w.d_pad, dt, stream);
         if (e == hipSuccess && (!few || dx)) e = ssk::launch_pad_rows(weight, d, ws + w.w, v, d, w.d_pad, dt, stream);

@@ -8,9 +8,30 @@
 
 namespace ssk {
 
-// Rows of x up to which products with weights stream the weights past them (ss_gemm.h) instead
-// of working in tiles.
+// Rows of x up to which products with weights may stream the weights past them (ss_gemm.h)
+// instead of working in tiles.
 constexpr int64_t kStreamRows = 64;
+// Rows of x up to which the gradients of such products are formed in one pass over the weights
+// (ss_few.hip).
+constexpr int64_t kFewRows = 16;
+
+// With s (m, rows), x (m, k) and weights W (rows, k): dx = s W in parts, dW = s^T x.  W may lie in
+// two matrices, the first `first` rows in w0 and the others in w1.
+struct FewGradArgs {
+    const float* s;   // rows of s_ld elements; its columns for w1 start at s_second
+    int64_t s_ld, s_second;
+    const void* w0;
+    const void* w1;
+    void* dw0;        // null: not wanted
+    void* dw1;
+    const void* x;
+    int64_t x_ld;
+    float* part;      // (parts, m, k); null: dx is not wanted
+    void* dx;         // (m, k)
+    int64_t first, rows, m, k;
+    int64_t per, parts;  // rows per part of the sums of dx
+};
+hipError_t launch_few_grad(const FewGradArgs& a, int dtype, hipStream_t stream);
 
 // ---- gated feed-forward projection -----------------------------------------------------
 
@@ -38,10 +59,13 @@ struct GluArgs {
     const void* wg_raw;
     const void* wu_raw;
     bool aligned;    // x_raw and the weights start every row on 16 bytes
+    bool stream;     // the products of x and the weights stream the weights
+    bool few;        // the backward in one pass over the weights: dgu is fp32
     int act;
     // the backward's sums of dx over 2 f are cut in dx_splits parts when tokens are few
-    float* dx_part;  // (dx_splits, m, k) fp32, null with one part
+    float* dx_part;  // (dx_splits, m, k) fp32, null with one part in tiles
     int64_t dx_splits;
+    int64_t dx_per;  // few: rows of the weights per part
 };
 
 // Copy of `rows` rows of `cols` elements (ld apart) into rows of cols_pad elements, the pad zeroed.
@@ -80,6 +104,7 @@ struct XentArgs {
     // n, d) fp32; null with one piece and one part
     float* dx_acc;
     int64_t dx_splits;
+    int64_t dx_per;  // few: rows of w per part
     void* dx;             // (n, d), nullable
     void* dw;             // (v, d), nullable
     int64_t n, d, v;
@@ -88,7 +113,7 @@ struct XentArgs {
     const void* x_raw;
     int64_t x_raw_ld;
     const void* w_raw;
-    bool aligned;
+    bool aligned, stream, few;
     int64_t piece;        // columns of the vocabulary per piece (the backward)
 };
 

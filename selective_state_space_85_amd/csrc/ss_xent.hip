@@ -255,6 +255,16 @@ __device__ __forceinline__ void dl_emit(const XentArgs& a, const Piece& p, const
 {
     using T = typename MM<DT>::T;
     if (c - p.v0 >= p.pad) return;
+    if (a.few) {  // fp32: nothing is rounded, nothing kept aside
+        f32x4 q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float v = exp2_hw((l[e] - row.lse) * kLog2e) - (c + e == row.target ? 1.0f : 0.0f);
+            q[e] = row.live && c + e - p.v0 < p.cols ? v * row.scale : 0.0f;
+        }
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dl) + m * p.pad + (c - p.v0)) = q;
+        return;
+    }
     typedef T T4 __attribute__((ext_vector_type(4)));
     T4 q;
 #pragma unroll
@@ -586,13 +596,12 @@ hipError_t fwd_stream(const XentArgs& a, hipStream_t s)
 template <int DT>
 hipError_t fwd_dt(const XentArgs& a, hipStream_t s)
 {
-    const bool stream = a.n <= kStreamRows;
-    const hipError_t e = !stream     ? fwd_tiles_dt<DT>(a, s)
+    const hipError_t e = !a.stream   ? fwd_tiles_dt<DT>(a, s)
                          : a.n <= 16 ? fwd_stream<DT, 1>(a, s)
                          : a.n <= 32 ? fwd_stream<DT, 2>(a, s)
                                      : fwd_stream<DT, 4>(a, s);
     if (e != hipSuccess) return e;
-    const int64_t groups = up(a.v, stream ? kXentStreamCols : kXentCols);
+    const int64_t groups = up(a.v, a.stream ? kXentStreamCols : kXentCols);
     // few rows: more threads on each
     if (a.n >= 4096)
         xent_join_kernel<16><<<dim3(up(a.n, 16)), dim3(256), 0, s>>>(a, groups);
@@ -623,9 +632,10 @@ hipError_t dl_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hi
 template <int DT>
 hipError_t dl_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
-    if (a.n <= 16) return dl_stream<DT, 1>(a, {v0, cols, pad}, s);
-    if (a.n <= 32) return dl_stream<DT, 2>(a, {v0, cols, pad}, s);
-    if (a.n <= kStreamRows) return dl_stream<DT, 4>(a, {v0, cols, pad}, s);
+    if (a.stream)
+        return a.n <= 16   ? dl_stream<DT, 1>(a, {v0, cols, pad}, s)
+               : a.n <= 32 ? dl_stream<DT, 2>(a, {v0, cols, pad}, s)
+                           : dl_stream<DT, 4>(a, {v0, cols, pad}, s);
     const Tile t = best_tile<DT>(count(a.n, pad, 256, 256), count(a.n, pad, 128, 128), count(a.n, pad, 64, 128));
     if constexpr (DT == 1) {
         if (t == Tile::Large)
@@ -675,6 +685,14 @@ hipError_t grad_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pa
 template <int DT>
 hipError_t bwd_dt(const XentArgs& a, hipStream_t s)
 {
+    if (a.few) {
+        const int64_t pad = (a.v + 15) / 16 * 16;
+        const hipError_t e = dl_tiles_dt<DT>(a, 0, a.v, pad, s);
+        if (e != hipSuccess) return e;
+        return launch_few_grad({static_cast<const float*>(a.dl), pad, 0, a.w_raw, nullptr, a.dw, nullptr, a.x_raw,
+                                a.x_raw_ld, a.dx ? a.dx_acc : nullptr, a.dx, a.v, a.v, a.n, a.d, a.dx_per, a.dx_splits},
+                               DT, s);
+    }
     if (DT == 1 && a.dw) {
         xent_list_kernel<<<dim3(up(a.v, kXentCols)), dim3(256), 0, s>>>(a);
         const hipError_t e = hipGetLastError();

@@ -14,6 +14,7 @@ hipError_t stub_status()
 
 namespace ssk {
 hipError_t launch_pad_rows(const void*, int64_t, void*, int64_t, int64_t, int64_t, int, hipStream_t) { return stub_status(); }
+hipError_t launch_few_grad(const FewGradArgs&, int, hipStream_t) { return stub_status(); }
 hipError_t launch_glu_fwd(const GluArgs&, int, hipStream_t) { return stub_status(); }
 hipError_t launch_glu_bwd(const GluArgs&, int, hipStream_t) { return stub_status(); }
 hipError_t launch_xent_fwd(const XentArgs&, int, hipStream_t) { return stub_status(); }
