@@ -97,10 +97,13 @@ ss_status ss_glr_step(float* h, const void* x, int64_t x_row_stride, const void*
  *   x        : (tokens, dim) dtype, rows x_row_stride elements apart
  *   w_gate, w_up : (features, dim) dtype
  *   h        : (tokens, features) dtype output
- * With dim a multiple of 16 bytes (8 bf16, 4 fp32), x, w_gate and w_up must be
- * 16-byte aligned and x_row_stride a multiple of 16 bytes
- * (SS_ERR_INVALID_ARG otherwise).  For other dims any element-aligned operands
- * are taken; they are first copied to padded rows in the workspace.
+ * bf16 with dim a multiple of 8: x, w_gate and w_up must be 16-byte aligned and
+ * x_row_stride a multiple of 8 (SS_ERR_INVALID_ARG otherwise).  Other dims, and
+ * fp32, take any element-aligned operands; bf16 ones may first be copied to
+ * padded rows in the workspace.
+ * fp32 products are formed from three bf16 parts of each operand, six products
+ * of parts accumulated in fp32: as exact as fp32 arithmetic, except that an
+ * infinite operand gives NaN.
  */
 typedef enum { SS_ACT_SILU = 0, SS_ACT_GELU = 1 } ss_activation;
 

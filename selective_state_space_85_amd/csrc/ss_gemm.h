@@ -8,7 +8,8 @@
 // operand is stored with k contiguous (KC: rows of A or B) or with m/n contiguous (MC:
 // the transpose), so products with a transposed operand need no transposing pass: the MC
 // fragments are read from LDS with the transposing read (bf16) or element by element (fp32).
-// All products are bf16 ones; fp32 operands are split into three bf16 parts (see MM<0>).
+// All products are bf16 ones; fp32 operands are split into three bf16 parts (see MM<0>) on their
+// way to LDS, which takes them at any alignment.
 //
 // LDS swizzle.  The direct load writes lane i's 16 bytes at base + 16 i, so a permutation of
 // a row's 16-byte chunks has to be applied to the source address instead:
@@ -88,59 +89,28 @@ struct MM<1> {  // bf16 operands
 template <>
 struct MM<0> {
     using T = float;
-    struct Frag {
-        f32x4 lo, hi;  // 8 k of one row
-    };
-    struct Parts {
-        bf16x8 p[3];
-    };
     static constexpr int kEpc = 4;
-    static constexpr int kSteps = 1;
-    static __device__ __forceinline__ Frag read_kc(const char* tile, int r0, int, int lane)
-    {
-        const int row = r0 + (lane & 15), c = (lane >> 4) * 2;
-        const char* p = tile + row * 128;
-        return {*reinterpret_cast<const f32x4*>(p + (c ^ (row & 7)) * 16),
-                *reinterpret_cast<const f32x4*>(p + ((c + 1) ^ (row & 7)) * 16)};
-    }
-    static __device__ __forceinline__ int mc_idx(int k) { return (k >> 3) & 3; }
-    template <int COLS>
-    static __device__ __forceinline__ Frag read_mc(const char* tile, int r0, int, int lane)
-    {
-        const int k = (lane >> 4) * 8;
-        const int gran = (r0 >> 4) ^ (mc_idx(k) & (COLS / 16 - 1));
-        const float* p = reinterpret_cast<const float*>(tile) + k * COLS + gran * 16 + (lane & 15);
-        Frag v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v.lo[j] = p[j * COLS];
-            v.hi[j] = p[(j + 4) * COLS];
-        }
-        return v;
-    }
-    static __device__ __forceinline__ Parts split(const Frag& f)
-    {
-        typedef __bf16 Pair __attribute__((ext_vector_type(2)));
-        typedef uint32_t U4 __attribute__((ext_vector_type(4)));
-        U4 out[3];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // two elements at a time: they are rounded, and packed, by one instruction
-            float v0 = j < 2 ? f.lo[2 * j] : f.hi[2 * j - 4], v1 = j < 2 ? f.lo[2 * j + 1] : f.hi[2 * j - 3];
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                const uint32_t u = __builtin_bit_cast(uint32_t, Pair{__bf16(v0), __bf16(v1)});
-                out[q][j] = u;
-                v0 -= __uint_as_float(u << 16);
-                v1 -= __uint_as_float(u & 0xffff0000u);
-            }
-        }
-        return {{__builtin_bit_cast(bf16x8, out[0]), __builtin_bit_cast(bf16x8, out[1]),
-                 __builtin_bit_cast(bf16x8, out[2])}};
-    }
     static __device__ __forceinline__ float widen(T v) { return v; }
     static __device__ __forceinline__ T narrow(float v) { return v; }
 };
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 8 neighbouring k of one row: their parts, packed
+__device__ __forceinline__ void split8(const float (&v)[8], u32x4 (&part)[3])
+{
+    typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // two elements at a time: they are rounded, and packed, by one instruction
+        float v0 = v[2 * j], v1 = v[2 * j + 1];
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const uint32_t u = __builtin_bit_cast(uint32_t, Pair{__bf16(v0), __bf16(v1)});
+            part[q][j] = u;
+            v0 -= __uint_as_float(u << 16);
+            v1 -= __uint_as_float(u & 0xffff0000u);
+        }
+    }
+}
 
 __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 b, bf16x8 a, f32x4 c)
 {
@@ -199,7 +169,8 @@ struct Geo {
     static constexpr int A_PARTS = GROUPS ? 2 : 1, A_PART = BM / A_PARTS, A_NT = NT / A_PARTS;
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
     static constexpr int B_STAGES = GROUPS ? 3 : 2;
-    static constexpr int LDS = 2 * A_BYTES + B_STAGES * B_BYTES;  // the A buffers, then the B buffers
+    // bf16: the A buffers, then the B buffers; fp32: one tile of each, in three parts of 64 bytes a row
+    static constexpr int LDS = DT == 1 ? 2 * A_BYTES + B_STAGES * B_BYTES : (BM + BN) * 192;
     static constexpr int NA = A_BYTES / 16 / NT, NB = B_BYTES / 16 / NT;  // chunks per thread
     static_assert(A_BYTES % (16 * NT) == 0 && B_BYTES % (16 * NT) == 0, "whole loads per thread");
 };
@@ -287,36 +258,11 @@ __device__ __forceinline__ void mm_mul(const typename MM<G::DT>::Frag (&a)[G::FM
                                        const typename MM<G::DT>::Frag (&b)[G::FN], f32x4 (&acc)[G::FM][G::FN],
                                        Beside beside = Beside())
 {
-    if constexpr (G::DT == 1) {
 #pragma unroll
-        for (int i = 0; i < G::FM; ++i) {
+    for (int i = 0; i < G::FM; ++i) {
 #pragma unroll
-            for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(b[j], a[i], acc[i][j]);
-            beside(i);
-        }
-    } else {
-        typename MM<0>::Parts bp[G::FN], ap[2];
-#pragma unroll
-        for (int j = 0; j < G::FN; ++j) bp[j] = MM<0>::split(b[j]);
-        ap[0] = MM<0>::split(a[0]);
-        constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};  // smallest first
-#pragma unroll
-        for (int i = 0; i < G::FM; ++i) {
-            // the next row is split among this row's products: 44 vector instructions, two after
-            // each of the 24 matrix ones, which leave that many issue slots free
-            __builtin_amdgcn_sched_barrier(0);
-            if (i + 1 < G::FM) ap[(i + 1) & 1] = MM<0>::split(a[i + 1]);
-#pragma unroll
-            for (int q = 0; q < 6; ++q)
-#pragma unroll
-                for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(bp[j].p[kB[q]], ap[i & 1].p[kA[q]], acc[i][j]);
-#pragma unroll
-            for (int q = 0; q < 6 * G::FN; ++q) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-            }
-            beside(i);
-        }
+        for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(b[j], a[i], acc[i][j]);
+        beside(i);
     }
 }
 
@@ -480,6 +426,162 @@ __device__ __forceinline__ void mm_loop(const Prob& p, const char* const (&a_lan
     }
 }
 
+// ---- fp32 --------------------------------------------------------------------------------------
+
+// A thread's items of one operand's k tile (ROWS rows or columns of it, 32 k), as loaded.
+//   KC: an item is 8 k of one row;
+//   MC: an item is 8 k of two neighbouring columns.
+// Either way the tile lies in LDS with k contiguous, each part a row of 64 bytes whose 16-byte chunk
+// c sits at position c ^ (row / 4 % 4).  Elements past the ends of k are zeros, and no element past
+// the ends of a row is read, whatever its alignment.
+template <bool MC, int ROWS, int NT>
+struct Staged {
+    static constexpr int ITEMS = MC ? ROWS / 2 * 4 : ROWS * 4, N = (ITEMS + NT - 1) / NT, LEN = MC ? 16 : 8;
+    float v[N][LEN];
+
+    static __device__ __forceinline__ bool has(int i, int tid) { return ITEMS % NT == 0 || i * NT + tid < ITEMS; }
+    // first row (column) and chunk of k of item i
+    static __device__ __forceinline__ void place(int i, int tid, int* row, int* chunk)
+    {
+        const int q = i * NT + tid;
+        if (MC) {
+            *row = q % (ROWS / 2) * 2;
+            *chunk = q / (ROWS / 2);
+        } else {
+            *row = q >> 2;
+            *chunk = q & 3;
+        }
+    }
+    // p[i]: item i's first element at k tile 0, clamped to a row (column) that exists; two: its second
+    // column exists; ld: elements per k (MC); valid: k of this tile that exist
+    __device__ __forceinline__ void load(const float* const (&p)[N], const bool (&two)[N], int64_t off, int64_t ld, int valid,
+                                         int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            int row, chunk;
+            place(i, tid, &row, &chunk);
+            const int left = has(i, tid) ? valid - chunk * 8 : 0;
+            const float* q = p[i] + off;
+            if (!MC) {
+                if (left >= 8) {
+                    __builtin_memcpy(v[i], q, 32);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[i][e] = e < left ? q[e] : 0.0f;
+                }
+            } else {
+                if (left >= 8 && two[i]) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) __builtin_memcpy(&v[i][2 * e], q + e * ld, 8);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[i][2 * e] = e < left ? q[e * ld] : 0.0f;
+                        v[i][2 * e + 1] = e < left && two[i] ? q[e * ld + 1] : 0.0f;
+                    }
+                }
+            }
+        }
+    }
+    // tile: three parts of ROWS rows
+    __device__ __forceinline__ void store(char* tile, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!has(i, tid)) continue;
+            int row, chunk;
+            place(i, tid, &row, &chunk);
+#pragma unroll
+            for (int c = 0; c < (MC ? 2 : 1); ++c) {
+                float one[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) one[e] = MC ? v[i][2 * e + c] : v[i][e];
+                u32x4 part[3];
+                split8(one, part);
+                const int r = row + c;
+                char* const to = tile + r * 64 + (chunk ^ (r >> 2 & 3)) * 16;
+#pragma unroll
+                for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4*>(to + q * (ROWS * 64)) = part[q];
+            }
+        }
+    }
+};
+__device__ __forceinline__ bf16x8 staged_frag(const char* part, int r0, int lane)
+{
+    const int row = r0 + (lane & 15);
+    return *reinterpret_cast<const bf16x8*>(part + row * 64 + ((lane >> 4) ^ (row >> 2 & 3)) * 16);
+}
+
+// One workgroup's tile of an fp32 product.  Elements pass through registers, where each is split
+// once per workgroup; the next k tile's loads are in flight while this one's products are formed.
+// Prob: a_at(row, k) / b_at(row, k), the address of an element, rows past the end clamped to the last;
+// a_cols() / b_cols(), for MC operands the columns that exist from the tile's first on; a_ld() / b_ld(),
+// their elements per k; a_off, b_off (in bytes), valid, tiles, finish as for mm_tile.
+template <class G, class Prob>
+__device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
+{
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / G::WN, wn = wave % G::WN;
+    using SA = Staged<G::A_MC, G::BM, G::NT>;
+    using SB = Staged<G::B_MC, G::BN, G::NT>;
+    SA sa;
+    SB sb;
+    const float* pa[SA::N];
+    const float* pb[SB::N];
+    bool ta[SA::N], tb[SB::N];
+    int row, chunk;
+#pragma unroll
+    for (int i = 0; i < SA::N; ++i) {
+        SA::place(i, tid, &row, &chunk);
+        ta[i] = !G::A_MC || row + 1 < p.a_cols();
+        pa[i] = p.a_at(row, SA::has(i, tid) ? chunk * 8 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < SB::N; ++i) {
+        SB::place(i, tid, &row, &chunk);
+        tb[i] = !G::B_MC || row + 1 < p.b_cols();
+        pb[i] = p.b_at(row, SB::has(i, tid) ? chunk * 8 : 0);
+    }
+    auto load = [&](int t) {
+        sa.load(pa, ta, p.a_off(t) / 4, p.a_ld(), p.valid(t), tid);
+        sb.load(pb, tb, p.b_off(t) / 4, p.b_ld(), p.valid(t), tid);
+    };
+    f32x4 acc[G::FM][G::FN];
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    char* const at = lds;
+    char* const bt = lds + G::BM * 192;
+    if (p.tiles > 0) load(0);
+    for (int t = 0; t < p.tiles; ++t) {
+        __syncthreads();  // the last tile's readers are done
+        sa.store(at, tid);
+        sb.store(bt, tid);
+        __syncthreads();
+        if (t + 1 < p.tiles) load(t + 1);
+        bf16x8 b[3][G::FN];
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) b[q][j] = staged_frag(bt + q * (G::BN * 64), (wn * G::FN + j) * 16, lane);
+        constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};  // smallest first
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            bf16x8 a[3];
+#pragma unroll
+            for (int q = 0; q < 3; ++q) a[q] = staged_frag(at + q * (G::BM * 64), (wm * G::FM + i) * 16, lane);
+#pragma unroll
+            for (int q = 0; q < 6; ++q)
+#pragma unroll
+                for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(b[kB[q]][j], a[kA[q]], acc[i][j]);
+        }
+    }
+    p.template finish<G>(acc, lds, wm, wn, lane);
+}
+
 // One workgroup's tile.  Prob supplies
 //   a_chunk(row, k) / b_chunk(row, k): address of the chunk of A (B) whose first element is
 //       (tile row `row`, k) at k tile 0, rows past the end clamped to the last;
@@ -489,6 +591,10 @@ __device__ __forceinline__ void mm_loop(const Prob& p, const char* const (&a_lan
 template <class G, class Prob>
 __device__ __forceinline__ void mm_tile(const Prob& p, char* lds)
 {
+    if constexpr (G::DT == 0) {
+        mm_tile_f32<G>(p, lds);
+        return;
+    } else {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform, and known to be
     const char* a_lane[G::NA];
@@ -511,6 +617,7 @@ __device__ __forceinline__ void mm_tile(const Prob& p, char* lds)
         for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     mm_loop<G>(p, a_lane, b_lane, p.tiles, lds, acc);
     p.template finish<G>(acc, lds, wave / G::WN, wave % G::WN, lane);
+    }
 }
 
 // ---- few rows: the weights stream past them ------------------------------------------------------

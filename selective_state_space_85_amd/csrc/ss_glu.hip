@@ -152,7 +152,13 @@ struct GluProb {
     }
     __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
     __device__ int64_t b_off(int t) const { return int64_t(t) * 128; }
-    __device__ int valid(int t) const { return k_left<DT>(a.k_pad, t); }
+    __device__ int valid(int t) const { return k_left<DT>(DT == 0 ? a.k : a.k_pad, t); }
+    __device__ const float* a_at(int row, int k) const { return reinterpret_cast<const float*>(a_chunk(row, k)); }
+    __device__ const float* b_at(int row, int k) const { return reinterpret_cast<const float*>(b_chunk(row, k)); }
+    __device__ int64_t a_cols() const { return 0; }
+    __device__ int64_t b_cols() const { return 0; }
+    __device__ int64_t a_ld() const { return 0; }
+    __device__ int64_t b_ld() const { return 0; }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -230,6 +236,17 @@ struct GluDxProb {
         return k_left<DT>(a.f, t < half ? t : t - half);
     }
 
+    __device__ const float* a_at(int row, int k) const { return reinterpret_cast<const float*>(a_chunk(row, k)); }
+    __device__ const float* b_at(int col, int k) const
+    {
+        const int64_t c = n0 + col < a.k ? n0 + col : a.k - 1;
+        return static_cast<const float*>(a.wg) + int64_t(k) * a.w_ld + c;
+    }
+    __device__ int64_t a_cols() const { return 0; }
+    __device__ int64_t b_cols() const { return a.k - n0; }
+    __device__ int64_t a_ld() const { return 0; }
+    __device__ int64_t b_ld() const { return a.w_ld; }
+
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
     {
@@ -277,6 +294,21 @@ struct GluDwProb {
     __device__ int64_t a_off(int t) const { return int64_t(t) * BK * 2 * a.f_pad * int64_t(sizeof(T)); }
     __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
     __device__ int valid(int t) const { return k_left<DT>(a.m, t); }
+
+    __device__ const float* a_at(int col, int k) const
+    {
+        const int64_t c = m0 + col < 2 * a.f_pad ? m0 + col : 2 * a.f_pad - 1;
+        return static_cast<const float*>(a.dgu) + int64_t(k) * 2 * a.f_pad + c;
+    }
+    __device__ const float* b_at(int col, int k) const
+    {
+        const int64_t c = n0 + col < a.k ? n0 + col : a.k - 1;
+        return static_cast<const float*>(a.x) + int64_t(k) * a.x_ld + c;
+    }
+    __device__ int64_t a_cols() const { return 2 * a.f_pad - m0; }
+    __device__ int64_t b_cols() const { return a.k - n0; }
+    __device__ int64_t a_ld() const { return 2 * a.f_pad; }
+    __device__ int64_t b_ld() const { return a.x_ld; }
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const

@@ -352,8 +352,12 @@ namespace {
 // ---- the two matrix operators: x (rows, dim) against weights (cols, dim) ------------------
 
 // Elements per 16 bytes: rows are read in whole 16-byte chunks.
+// (fp32 tiles take any alignment.)
 int64_t chunk_elems(ss_dtype dtype) { return 16 / elem_size(dtype); }
 int64_t padded(int64_t n, ss_dtype dtype) { return ceil_div(n, chunk_elems(dtype)) * chunk_elems(dtype); }
+
+// Every row starts on 16 bytes.
+bool whole_rows(const void* p, int64_t ld, ss_dtype dtype) { return aligned(p, 16) && ld % chunk_elems(dtype) == 0; }
 
 // Sizes whose products are formed unchecked below.
 bool mat_sizes(int64_t rows, int64_t dim, int64_t cols)
@@ -377,8 +381,8 @@ bool mat_grid_ok(int64_t rows, int64_t cols)
 ss_status mat_operand(const void* p, int64_t ld, int64_t dim, ss_dtype dtype, bool* pack)
 {
     if (ld < dim) return SS_ERR_INVALID_ARG;
-    *pack = dim % chunk_elems(dtype) != 0;
-    if (*pack) return aligned(p, uintptr_t(elem_size(dtype))) ? SS_OK : SS_ERR_INVALID_ARG;
+    *pack = dtype == SS_BF16 && dim % chunk_elems(dtype) != 0;
+    if (*pack || dtype == SS_F32) return aligned(p, uintptr_t(elem_size(dtype))) ? SS_OK : SS_ERR_INVALID_ARG;
     if (!aligned(p, 16) || ld % chunk_elems(dtype) != 0) return SS_ERR_INVALID_ARG;
     return SS_OK;
 }
@@ -401,10 +405,10 @@ int64_t dx_parts(int64_t rows, int64_t dim, int64_t depth, ss_dtype dtype)
 // How the products of `rows` rows of x with `cols` weight rows are formed (both directions), and
 // their gradients.
 struct RowsPlan {
-    bool aligned;  // rows are whole 16-byte chunks
+    bool aligned;  // rows are of whole 16-byte chunks
     bool stream;   // the weights stream past x; else tiles
     bool few;      // the gradients in one pass over the weights
-    bool pad;      // padded copies are needed: tiles read them (in the forward, or the backward)
+    bool pad;      // padded copies are needed: bf16 tiles read them (in the forward, or the backward)
 };
 // Streaming reads x again for every 32 weight rows, from the caches: up to 16 rows that is little,
 // up to 64 it pays while tiles of 128 weight rows would leave CUs idle (46 563 weight rows of 3264 bf16,
@@ -414,9 +418,9 @@ RowsPlan rows_plan(int64_t rows, int64_t dim, int64_t cols, ss_dtype dtype, bool
 {
     RowsPlan p;
     p.aligned = dim % chunk_elems(dtype) == 0;
-    p.stream = rows <= 16 || (rows <= ssk::kStreamRows && (!p.aligned || ceil_div(cols, 128) < 256));
+    p.stream = rows <= 16 || (rows <= ssk::kStreamRows && ((dtype == SS_BF16 && !p.aligned) || ceil_div(cols, 128) < 256));
     p.few = rows <= ssk::kFewRows;
-    p.pad = !p.aligned && (back ? !p.few : !p.stream);
+    p.pad = dtype == SS_BF16 && !p.aligned && (back ? !p.few : !p.stream);
     return p;
 }
 
@@ -603,7 +607,7 @@ ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, 
     a.x_raw_ld = x_ld;
     a.wg_raw = wg;
     a.wu_raw = wu;
-    a.aligned = w.plan.aligned;
+    a.aligned = w.plan.aligned && whole_rows(x, x_ld, dtype) && whole_rows(wg, k, dtype) && whole_rows(wu, k, dtype);
     a.stream = w.plan.stream;
     a.few = w.plan.few;
     if (w.pack) {
@@ -684,7 +688,7 @@ ss_status xent_impl(const void* x, int64_t x_ld, const void* weight, const int64
     a.x_raw = x;
     a.x_raw_ld = x_ld;
     a.w_raw = weight;
-    a.aligned = w.plan.aligned;
+    a.aligned = w.plan.aligned && whole_rows(x, x_ld, dtype) && whole_rows(weight, d, dtype);
     a.stream = w.plan.stream;
     a.few = w.plan.few;
     if (w.pack) {

@@ -50,7 +50,13 @@ struct XentLogits {
     }
     __device__ int64_t a_off(int t) const { return int64_t(t) * 128; }
     __device__ int64_t b_off(int t) const { return int64_t(t) * 128; }
-    __device__ int valid(int t) const { return k_left<DT>(a.d_pad, t); }
+    __device__ int valid(int t) const { return k_left<DT>(DT == 0 ? a.d : a.d_pad, t); }
+    __device__ const float* a_at(int row, int k) const { return reinterpret_cast<const float*>(a_chunk(row, k)); }
+    __device__ const float* b_at(int row, int k) const { return reinterpret_cast<const float*>(b_chunk(row, k)); }
+    __device__ int64_t a_cols() const { return 0; }
+    __device__ int64_t b_cols() const { return 0; }
+    __device__ int64_t a_ld() const { return 0; }
+    __device__ int64_t b_ld() const { return 0; }
 };
 
 // ---- forward -------------------------------------------------------------------------------
@@ -383,6 +389,17 @@ struct XentDxProb {
     __device__ int64_t b_off(int t) const { return int64_t(t + from) * BK * a.w_ld * int64_t(sizeof(T)); }
     __device__ int valid(int t) const { return k_left<DT>(cols, t + from); }
 
+    __device__ const float* a_at(int row, int k) const { return reinterpret_cast<const float*>(a_chunk(row, k)); }
+    __device__ const float* b_at(int col, int k) const
+    {
+        const int64_t c = n0 + col < a.d ? n0 + col : a.d - 1;
+        return static_cast<const float*>(a.w) + (v0 + k) * a.w_ld + c;
+    }
+    __device__ int64_t a_cols() const { return 0; }
+    __device__ int64_t b_cols() const { return a.d - n0; }
+    __device__ int64_t a_ld() const { return 0; }
+    __device__ int64_t b_ld() const { return a.w_ld; }
+
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
     {
@@ -438,6 +455,21 @@ struct XentDwProb {
     __device__ int64_t a_off(int t) const { return int64_t(t) * BK * pad * int64_t(sizeof(T)); }
     __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
     __device__ int valid(int t) const { return k_left<DT>(a.n, t); }
+
+    __device__ const float* a_at(int col, int k) const
+    {
+        const int64_t c = m0 + col < pad ? m0 + col : pad - 1;
+        return static_cast<const float*>(a.dl) + int64_t(k) * pad + c;
+    }
+    __device__ const float* b_at(int col, int k) const
+    {
+        const int64_t c = n0 + col < a.d ? n0 + col : a.d - 1;
+        return static_cast<const float*>(a.x) + int64_t(k) * a.x_ld + c;
+    }
+    __device__ int64_t a_cols() const { return pad - m0; }
+    __device__ int64_t b_cols() const { return a.d - n0; }
+    __device__ int64_t a_ld() const { return pad; }
+    __device__ int64_t b_ld() const { return a.x_ld; }
 
     // the target entries' remainders
     template <class G>

@@ -88,6 +88,25 @@ def test_large_tiles(m, k, f):
         check(n, host64(g[n]), ref[n], TOL["bf16"])
 
 
+@pytest.mark.parametrize("m", [3, 40, 150])
+def test_fp32_rows_off_any_boundary(m):
+    """fp32 takes operands that start off a 16-byte boundary with an odd row stride."""
+    k, f = 64, 70
+    x, wg, wu, dh = make(m, k, f, wl.F32, 9, 5)
+    xt = dev(np.concatenate([np.zeros((m, 2), np.float32), x[:, :k + 1]], 1))[:, 3:3 + k]
+    flat = dev(np.concatenate([[0.0], wg.reshape(-1)]).astype(np.float32))
+    g_ = flat[1:].view(f, k)
+    say("glu fp32 unaligned", m)
+    h = ss().glu_fwd(xt, g_, dev(wu))
+    g = ss().glu_bwd(xt, g_, dev(wu), dev(dh))
+    torch.cuda.synchronize()
+    x64 = wide(x)[:, 1:1 + k]
+    check("h", host64(h), lm_ref.glu(x64, wide(wg), wide(wu), "silu"), TOL["f32"])
+    ref = lm_ref.glu_bwd(x64, wide(wg), wide(wu), wide(dh), "silu")
+    for n in ref:
+        check(n, host64(g[n]), ref[n], TOL["f32"])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_activation_extremes(act):
     """Pre-activations from -1e4 to 1e4: the activation and its slope neither overflow nor
@@ -158,8 +177,8 @@ def test_refusals():
         m.glu_fwd(x, w.bfloat16(), w.bfloat16())
     with pytest.raises(ValueError):
         m.glu_fwd(x.t().contiguous().t(), w, w)
-    with pytest.raises(m.SSError):  # rows that start off a 16-byte boundary
-        m.glu_fwd(torch.zeros((4, 67), device="cuda")[:, 3:], w, w)
+    with pytest.raises(m.SSError):  # bf16 rows that start off a 16-byte boundary
+        m.glu_fwd(torch.zeros((4, 67), device="cuda").bfloat16()[:, 3:], w.bfloat16(), w.bfloat16())
     with pytest.raises(m.SSError):
         m.glu_bwd(x, w, w, torch.zeros((4, 32), device="cuda"), want_dx=False, want_dw=False)
     with pytest.raises(m.SSError):
