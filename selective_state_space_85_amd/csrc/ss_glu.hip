@@ -277,6 +277,8 @@ struct GluDwProb {
     const GluArgs& a;
     int64_t m0, n0;  // m0: first column of dgu (of its 2 f_pad), n0: first column of x
     int tiles;
+    int first;    // this part's first k tile
+    float* part;  // where this part's sums go; null: the gradients themselves
     bool vec;
 
     __device__ const char* a_chunk(int col, int k) const
@@ -291,9 +293,9 @@ struct GluDwProb {
         c = c < a.k_pad ? c : a.k_pad - MM<DT>::kEpc;
         return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + int64_t(k) * a.x_ld + c);
     }
-    __device__ int64_t a_off(int t) const { return int64_t(t) * BK * 2 * a.f_pad * int64_t(sizeof(T)); }
-    __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
-    __device__ int valid(int t) const { return k_left<DT>(a.m, t); }
+    __device__ int64_t a_off(int t) const { return int64_t(t + first) * BK * 2 * a.f_pad * int64_t(sizeof(T)); }
+    __device__ int64_t b_off(int t) const { return int64_t(t + first) * BK * a.x_ld * int64_t(sizeof(T)); }
+    __device__ int valid(int t) const { return k_left<DT>(a.m, t + first); }
 
     __device__ const float* a_at(int col, int k) const
     {
@@ -324,28 +326,40 @@ struct GluDwProb {
             for (int j = 0; j < G::FN; ++j) {
                 const int64_t n = n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
                 const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if (n < a.k) store4<DT>(row + n, a.k - n, vec, v);
+                if (n >= a.k) continue;
+                if (part)
+                    store4<0>(part + c * a.k + n, a.k - n, a.k % 4 == 0, v);
+                else
+                    store4<DT>(row + n, a.k - n, vec, v);
             }
         }
     }
 };
 
-// Both sets of tiles: dw's after dx's, of which there are dx_splits times px.  HX, HW: their halves.
+// A part's share of `all` k tiles: the first, and how many (rounding may leave the last parts nothing).
+__device__ __forceinline__ void share(int64_t all, int64_t parts, uint32_t part, int* first, int* tiles)
+{
+    const int64_t depth = (all + parts - 1) / parts, from = part * depth, left = all > from ? all - from : 0;
+    *first = int(from);
+    *tiles = int(left < depth ? left : depth);
+}
+
+// Both sets of tiles: dx's, dx_splits times px, and then dw's, dw_splits times pw.  HX, HW: their halves.
 template <class GX, class HX, class GW, class HW>
 __global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, TilePlan px, TilePlan pw, bool vec_x, bool vec_w)
 {
     static_assert(GX::NT == GW::NT && GX::LDS == GW::LDS, "one launch");
     __shared__ __attribute__((aligned(1024))) char lds[GX::LDS];
     uint32_t tm, tn;
-    const uint32_t per = px.blocks(), n_dx = per * uint32_t(a.dx_splits);
+    const uint32_t per_x = px.blocks(), n_dx = per_x * uint32_t(a.dx_splits);
+    int first, tiles;
     if (blockIdx.x < n_dx) {
-        const uint32_t part = blockIdx.x / per;
-        const int h = tile_of(blockIdx.x % per, px, &tm, &tn);
+        const uint32_t part = blockIdx.x / per_x;
+        const int h = tile_of(blockIdx.x % per_x, px, &tm, &tn);
         const int half = int((a.f + GX::BK - 1) / GX::BK);
-        const int depth = int((2 * half + a.dx_splits - 1) / a.dx_splits), first = int(part) * depth;
-        const int left = 2 * half > first ? 2 * half - first : 0;  // rounding may leave the last parts nothing
-        GluDxProb<GX::DT> p{a, int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, half, left < depth ? left : depth, first,
-                            a.dx_part ? a.dx_part + int64_t(part) * a.m * a.k : nullptr, vec_x};
+        share(2 * half, a.dx_splits, part, &first, &tiles);
+        GluDxProb<GX::DT> p{a,     int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, half, tiles,
+                            first, a.dx_part ? a.dx_part + int64_t(part) * a.m * a.k : nullptr, vec_x};
         if (h < 0) {
             mm_tile<GX>(p, lds);
             return;
@@ -353,14 +367,33 @@ __global__ __launch_bounds__(GX::NT) void glu_grad_kernel(GluArgs a, TilePlan px
         p.m0 += h * HX::BM;
         if (p.m0 < a.m) mm_tile<HX>(p, lds);
     } else {
-        const int h = tile_of(blockIdx.x - n_dx, pw, &tm, &tn);
-        GluDwProb<GW::DT> p{a, int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, int((a.m + GW::BK - 1) / GW::BK), vec_w};
+        const uint32_t id = blockIdx.x - n_dx, per_w = pw.blocks(), part = id / per_w;
+        const int h = tile_of(id % per_w, pw, &tm, &tn);
+        share((a.m + GW::BK - 1) / GW::BK, a.dw_splits, part, &first, &tiles);
+        GluDwProb<GW::DT> p{a,     int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, tiles,
+                            first, a.dw_part ? a.dw_part + int64_t(part) * 2 * a.f_pad * a.k : nullptr, vec_w};
         if (h < 0) {
             mm_tile<GW>(p, lds);
             return;
         }
         p.m0 += h * HW::BM;
         if (p.m0 < 2 * a.f_pad) mm_tile<HW>(p, lds);
+    }
+}
+
+// The weights' gradients from their parts, in order.
+template <int DT>
+__global__ __launch_bounds__(256) void glu_dw_sum_kernel(GluArgs a)
+{
+    using T = typename MM<DT>::T;
+    const int64_t n = a.f * a.k, all = 2 * a.f_pad * a.k;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < 2 * n; i += int64_t(gridDim.x) * 256) {
+        const bool up_half = i >= n;
+        const int64_t at = up_half ? i - n + a.f_pad * a.k : i;
+        float s = 0.0f;
+#pragma unroll 8
+        for (int64_t p = 0; p < a.dw_splits; ++p) s += a.dw_part[p * all + at];
+        static_cast<T*>(up_half ? a.dwu : a.dwg)[up_half ? i - n : i] = MM<DT>::narrow(s);
     }
 }
 
@@ -489,18 +522,24 @@ template <class GX, class HX, class GW, class HW>
 hipError_t launch_glu_grad(const GluArgs& a, hipStream_t s)
 {
     const bool can = HX::BM < GX::BM;
-    const uint32_t splits = uint32_t(a.dx_splits);
+    const uint32_t sx = uint32_t(a.dx_splits), sw = uint32_t(a.dw_splits);
     TilePlan px{0, 0, 0, 0}, pw{0, 0, 0, 0};
     // only the last tiles of a launch are halved
-    if (a.dx) px = plan_tiles(up(a.m, GX::BM), up(a.k, GX::BN), can && !a.dwg && splits == 1);
-    if (a.dwg) pw = plan_tiles(up(2 * a.f_pad, GW::BM), up(a.k, GW::BN), can, px.whole * splits);
+    if (a.dx) px = plan_tiles(up(a.m, GX::BM), up(a.k, GX::BN), can && !a.dwg && sx == 1);
+    if (a.dwg) pw = plan_tiles(up(2 * a.f_pad, GW::BM), up(a.k, GW::BN), can && sw == 1, px.whole * sx);
     const bool vx = vec_rows(a.dx, a.k, GX::DT), vw = vec_rows(a.dwg, a.k, GX::DT) && vec_rows(a.dwu, a.k, GX::DT);
-    glu_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() * splits + pw.blocks()), dim3(GX::NT), 0, s>>>(a, px, pw, vx, vw);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.dx || splits == 1) return e;
-    const int64_t blocks = (a.m * a.k + 255) / 256;
-    glu_dx_sum_kernel<GX::DT><<<dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s>>>(a);
-    return hipGetLastError();
+    glu_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() * sx + pw.blocks() * sw), dim3(GX::NT), 0, s>>>(a, px, pw, vx, vw);
+    hipError_t e = hipGetLastError();
+    auto blocks = [](int64_t n) { return dim3(unsigned(n / 256 + 1 < 4096 ? n / 256 + 1 : 4096)); };
+    if (e == hipSuccess && a.dx && sx > 1) {
+        glu_dx_sum_kernel<GX::DT><<<blocks(a.m * a.k), dim3(256), 0, s>>>(a);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && a.dwg && sw > 1) {
+        glu_dw_sum_kernel<GX::DT><<<blocks(2 * a.f * a.k), dim3(256), 0, s>>>(a);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 template <int DT>
@@ -516,7 +555,7 @@ hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
                                 a.x_raw, a.x_raw_ld, a.dx_part, a.dx, a.f, 2 * a.f, a.m, a.k, a.dx_per, a.dx_splits},
                                DT, s);
     auto tiles = [&](int bm, int bn) {
-        return (a.dx ? count(a.m, a.k, bm, bn) * a.dx_splits : 0) + (a.dwg ? count(2 * a.f_pad, a.k, bm, bn) : 0);
+        return (a.dx ? count(a.m, a.k, bm, bn) * a.dx_splits : 0) + (a.dwg ? count(2 * a.f_pad, a.k, bm, bn) * a.dw_splits : 0);
     };
     const Tile t = best_tile<DT>(tiles(256, 256), tiles(128, 128), tiles(64, 128));
     if constexpr (DT == 1) {

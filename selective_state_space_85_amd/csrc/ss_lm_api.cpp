@@ -387,11 +387,12 @@ ss_status mat_operand(const void* p, int64_t ld, int64_t dim, ss_dtype dtype, bo
     return SS_OK;
 }
 
-// Parts into which the sums of dx (rows x dim, over `depth` terms) are cut.  dx and the weights'
-// gradients (sums over the rows) are formed by one launch: with few rows dx has few tiles, each
-// with a far longer sum than the weights' tiles, and would end long after them.  Its sums are cut
-// to the weights' length, but not below 16 k tiles, nor into more than fill the chip twice over.
-int64_t dx_parts(int64_t rows, int64_t dim, int64_t depth, ss_dtype dtype)
+// Parts into which the sums of a rows x dim gradient over `depth` terms are cut.  dx (sums over the
+// weights' rows) and the weights' gradients (sums over x's rows) are formed by one launch: where one
+// of them has few tiles, each with a far longer sum than the other's, those would end long after
+// the rest.  Its sums are cut to the others' length, but not below 16 k tiles, nor into more than fill
+// the chip twice over.
+int64_t grad_parts(int64_t rows, int64_t dim, int64_t depth, ss_dtype dtype)
 {
     const int64_t bk = 8 * chunk_elems(dtype);
     const int64_t own = ceil_div(depth, bk), others = ceil_div(rows, bk);
@@ -442,10 +443,10 @@ void few_parts(int64_t m, int64_t k, int64_t rows, ss_dtype dtype, int64_t* per,
 }
 
 struct GluLayout {
-    int64_t k_pad, f_pad, splits, per;
+    int64_t k_pad, f_pad, splits, per, dw_splits;
     RowsPlan plan;
     bool pack;
-    int64_t x, wg, wu, dgu, part, total;
+    int64_t x, wg, wu, dgu, part, dw_part, total;
 };
 
 bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluLayout* w)
@@ -465,19 +466,22 @@ bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluL
     if (w->plan.few)
         few_parts(m, k, 2 * f, dtype, &w->per, &w->splits);
     else
-        w->splits = dx_parts(m, k, 2 * f, dtype);
+        w->splits = grad_parts(m, k, 2 * f, dtype);
     int64_t part;
     if (!mul(w->splits, m, &part) || !mul(part, k, &part)) return false;
     w->part = r.add(back && (w->splits > 1 || w->plan.few) ? part : 0, 4);
+    w->dw_splits = w->plan.few ? 1 : grad_parts(2 * w->f_pad, k, m, dtype);
+    if (!mul(w->dw_splits, 2 * w->f_pad, &part) || !mul(part, k, &part)) return false;
+    w->dw_part = r.add(back && w->dw_splits > 1 ? part : 0, 4);
     w->total = r.at;
     return r.ok;
 }
 
 struct XentLayout {
-    int64_t d_pad, piece, splits, per;
+    int64_t d_pad, piece, splits, per, dw_splits;
     RowsPlan plan;
     bool pack;
-    int64_t x, w, pmax, psum, tl, dl, lo, tokens, counts, acc, total;
+    int64_t x, w, pmax, psum, tl, dl, lo, tokens, counts, acc, dw_part, total;
 };
 
 // Columns per piece of the backward: as many as keep the piece's gradient of the logits within
@@ -520,10 +524,13 @@ bool xent_layout(int64_t n, int64_t d, int64_t v, ss_dtype dtype, bool back, Xen
     if (w->plan.few)
         few_parts(n, d, v, dtype, &w->per, &w->splits);
     else
-        w->splits = dx_parts(n, d, w->piece, dtype);
+        w->splits = grad_parts(n, d, w->piece, dtype);
     int64_t sums;
     if (!mul(w->splits, n, &sums) || !mul(sums, d, &sums)) return false;
     w->acc = r.add(back && (w->piece < v || w->splits > 1 || w->plan.few) ? sums : 0, 4);
+    w->dw_splits = w->plan.few ? 1 : grad_parts(w->piece, d, n, dtype);
+    if (!mul(w->dw_splits, w->piece, &sums) || !mul(sums, d, &sums)) return false;
+    w->dw_part = r.add(back && w->dw_splits > 1 ? sums : 0, 4);
     w->total = r.at;
     return r.ok;
 }
@@ -602,6 +609,8 @@ ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, 
     a.dx_splits = w.splits;
     a.dx_per = w.per;
     a.dx_part = back && dx && (w.splits > 1 || w.plan.few) ? reinterpret_cast<float*>(ws + w.part) : nullptr;
+    a.dw_splits = w.dw_splits;
+    a.dw_part = back && dwg && w.dw_splits > 1 ? reinterpret_cast<float*>(ws + w.dw_part) : nullptr;
     a.act = act == SS_ACT_SILU ? ssk::kActSilu : ssk::kActGelu;
     a.x_raw = x;
     a.x_raw_ld = x_ld;
@@ -683,6 +692,8 @@ ss_status xent_impl(const void* x, int64_t x_ld, const void* weight, const int64
     a.tokens = reinterpret_cast<int32_t*>(ws + w.tokens);
     a.counts = reinterpret_cast<int32_t*>(ws + w.counts);
     a.dx_splits = w.splits;
+    a.dw_splits = w.dw_splits;
+    a.dw_part = w.dw_splits > 1 ? reinterpret_cast<float*>(ws + w.dw_part) : nullptr;
     a.dx_per = w.per;
     a.dx_acc = w.piece < v || w.splits > 1 || w.plan.few ? reinterpret_cast<float*>(ws + w.acc) : nullptr;
     a.x_raw = x;

@@ -66,6 +66,9 @@ struct GluArgs {
     float* dx_part;  // (dx_splits, m, k) fp32, null with one part in tiles
     int64_t dx_splits;
     int64_t dx_per;  // few: rows of the weights per part
+    // and those of the weights' gradients over the tokens when features are few
+    float* dw_part;  // (dw_splits, 2 f_pad, k) fp32, null with one part
+    int64_t dw_splits;
 };
 
 // Copy of `rows` rows of `cols` elements (ld apart) into rows of cols_pad elements, the pad zeroed.
@@ -105,6 +108,10 @@ struct XentArgs {
     float* dx_acc;
     int64_t dx_splits;
     int64_t dx_per;  // few: rows of w per part
+    // sums of dw over the rows of x in dw_splits parts, (dw_splits, columns of the piece, d) fp32;
+    // null with one part
+    float* dw_part;
+    int64_t dw_splits;
     void* dx;             // (n, d), nullable
     void* dw;             // (v, d), nullable
     int64_t n, d, v;

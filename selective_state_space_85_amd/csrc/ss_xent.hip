@@ -438,6 +438,8 @@ struct XentDwProb {
     const XentArgs& a;
     int64_t m0, n0, v0, cols, pad;
     int tiles;
+    int first;    // this part's first k tile
+    float* part;  // where this part's sums go; null: dw itself
     bool vec;
 
     __device__ const char* a_chunk(int col, int k) const
@@ -452,9 +454,9 @@ struct XentDwProb {
         c = c < a.d_pad ? c : a.d_pad - MM<DT>::kEpc;
         return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + int64_t(k) * a.x_ld + c);
     }
-    __device__ int64_t a_off(int t) const { return int64_t(t) * BK * pad * int64_t(sizeof(T)); }
-    __device__ int64_t b_off(int t) const { return int64_t(t) * BK * a.x_ld * int64_t(sizeof(T)); }
-    __device__ int valid(int t) const { return k_left<DT>(a.n, t); }
+    __device__ int64_t a_off(int t) const { return int64_t(t + first) * BK * pad * int64_t(sizeof(T)); }
+    __device__ int64_t b_off(int t) const { return int64_t(t + first) * BK * a.x_ld * int64_t(sizeof(T)); }
+    __device__ int valid(int t) const { return k_left<DT>(a.n, t + first); }
 
     __device__ const float* a_at(int col, int k) const
     {
@@ -513,7 +515,9 @@ struct XentDwProb {
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char* lds, int wm, int wn, int lane) const
     {
-        if constexpr (DT == 1) remainders<G>(acc, lds, wm, wn, lane);
+        if constexpr (DT == 1) {
+            if (first == 0) remainders<G>(acc, lds, wm, wn, lane);  // by the first part
+        }
 #pragma unroll
         for (int i = 0; i < G::FM; ++i) {
             const int64_t r = m0 + (wm * G::FM + i) * 16 + (lane & 15);
@@ -522,7 +526,11 @@ struct XentDwProb {
 #pragma unroll
             for (int j = 0; j < G::FN; ++j) {
                 const int64_t c = n0 + (wn * G::FN + j) * 16 + (lane >> 4) * 4;
-                if (vec && c + 4 <= a.d) {
+                if (part) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < a.d) part[r * a.d + c + e] = acc[i][j][e];
+                } else if (vec && c + 4 <= a.d) {
                     typedef T T4 __attribute__((ext_vector_type(4)));
                     T4 q;
 #pragma unroll
@@ -538,7 +546,16 @@ struct XentDwProb {
     }
 };
 
-// Both sets of tiles: dw's after dx's, of which there are dx_splits times px.  HX, HW: their halves.
+// A part's share of `all` k tiles: the first, and how many (rounding, or a short last piece, may leave
+// parts nothing).
+__device__ __forceinline__ void share(int64_t all, int64_t parts, uint32_t part, int* first, int* tiles)
+{
+    const int64_t depth = (all + parts - 1) / parts, from = part * depth, left = all > from ? all - from : 0;
+    *first = int(from);
+    *tiles = int(left < depth ? left : depth);
+}
+
+// Both sets of tiles: dx's, dx_splits times px, and then dw's, dw_splits times pw.  HX, HW: their halves.
 template <class GX, class HX, class GW, class HW>
 __global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v0, int64_t cols, int64_t pad, TilePlan px,
                                                            TilePlan pw, bool first, bool last, bool vec_w)
@@ -546,14 +563,13 @@ __global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v
     static_assert(GX::NT == GW::NT && GX::LDS == GW::LDS, "one launch");
     __shared__ __attribute__((aligned(1024))) char lds[GX::LDS];
     uint32_t tm, tn;
-    const uint32_t per = px.blocks(), n_dx = per * uint32_t(a.dx_splits);
+    const uint32_t per_x = px.blocks(), n_dx = per_x * uint32_t(a.dx_splits);
+    int from, tiles;
     if (blockIdx.x < n_dx) {
-        const uint32_t part = blockIdx.x / per;
-        const int h = tile_of(blockIdx.x % per, px, &tm, &tn);
-        const int all = int((cols + GX::BK - 1) / GX::BK);
-        const int depth = int((all + a.dx_splits - 1) / a.dx_splits), from = int(part) * depth;
-        const int left = all - from > 0 ? all - from : 0;  // a short last piece may leave a part nothing
-        XentDxProb<GX::DT> p{a,    int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, v0, cols, pad, left < depth ? left : depth,
+        const uint32_t part = blockIdx.x / per_x;
+        const int h = tile_of(blockIdx.x % per_x, px, &tm, &tn);
+        share((cols + GX::BK - 1) / GX::BK, a.dx_splits, part, &from, &tiles);
+        XentDxProb<GX::DT> p{a,    int64_t(tm) * GX::BM, int64_t(tn) * GX::BN, v0, cols, pad, tiles,
                              from, a.dx_acc ? a.dx_acc + int64_t(part) * a.n * a.d : nullptr, first,
                              last && a.dx_splits == 1};
         if (h < 0) {
@@ -563,15 +579,30 @@ __global__ __launch_bounds__(GX::NT) void xent_grad_kernel(XentArgs a, int64_t v
         p.m0 += h * HX::BM;
         if (p.m0 < a.n) mm_tile<HX>(p, lds);
     } else {
-        const int h = tile_of(blockIdx.x - n_dx, pw, &tm, &tn);
-        XentDwProb<GW::DT> p{a,   int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, v0, cols,
-                             pad, int((a.n + GW::BK - 1) / GW::BK), vec_w};
+        const uint32_t id = blockIdx.x - n_dx, per_w = pw.blocks(), part = id / per_w;
+        const int h = tile_of(id % per_w, pw, &tm, &tn);
+        share((a.n + GW::BK - 1) / GW::BK, a.dw_splits, part, &from, &tiles);
+        XentDwProb<GW::DT> p{a,    int64_t(tm) * GW::BM, int64_t(tn) * GW::BN, v0, cols, pad, tiles,
+                             from, a.dw_part ? a.dw_part + int64_t(part) * cols * a.d : nullptr, vec_w};
         if (h < 0) {
             mm_tile<GW>(p, lds);
             return;
         }
         p.m0 += h * HW::BM;
         if (p.m0 < cols) mm_tile<HW>(p, lds);
+    }
+}
+
+// A piece's rows of dw from their parts, in order.
+template <int DT>
+__global__ __launch_bounds__(256) void xent_dw_sum_kernel(XentArgs a, int64_t v0, int64_t cols)
+{
+    const int64_t n = cols * a.d;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        float s = 0.0f;
+#pragma unroll 8
+        for (int64_t p = 0; p < a.dw_splits; ++p) s += a.dw_part[p * n + i];
+        static_cast<typename MM<DT>::T*>(a.dw)[v0 * a.d + i] = MM<DT>::narrow(s);
     }
 }
 
@@ -682,14 +713,18 @@ template <class GX, class HX, class GW, class HW>
 hipError_t grad_tiles(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
     const bool can = HX::BM < GX::BM;
-    const uint32_t splits = uint32_t(a.dx_splits);
+    const uint32_t sx = uint32_t(a.dx_splits), sw = uint32_t(a.dw_splits);
     TilePlan px{0, 0, 0, 0}, pw{0, 0, 0, 0};
     // only the last tiles of a launch are halved
-    if (a.dx) px = plan_tiles(up(a.n, GX::BM), up(a.d, GX::BN), can && !a.dw && splits == 1);
-    if (a.dw) pw = plan_tiles(up(cols, GW::BM), up(a.d, GW::BN), can, px.whole * splits);
+    if (a.dx) px = plan_tiles(up(a.n, GX::BM), up(a.d, GX::BN), can && !a.dw && sx == 1);
+    if (a.dw) pw = plan_tiles(up(cols, GW::BM), up(a.d, GW::BN), can && sw == 1, px.whole * sx);
     const bool vec = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.dw) % (GX::DT == 0 ? 16 : 8) == 0;
-    xent_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() * splits + pw.blocks()), dim3(GX::NT), 0, s>>>(
+    xent_grad_kernel<GX, HX, GW, HW><<<dim3(px.blocks() * sx + pw.blocks() * sw), dim3(GX::NT), 0, s>>>(
         a, v0, cols, pad, px, pw, v0 == 0, v0 + cols == a.v, vec);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.dw || sw == 1) return e;
+    const int64_t blocks = (cols * a.d + 255) / 256;
+    xent_dw_sum_kernel<GX::DT><<<dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s>>>(a, v0, cols);
     return hipGetLastError();
 }
 
@@ -697,7 +732,7 @@ template <int DT>
 hipError_t grad_tiles_dt(const XentArgs& a, int64_t v0, int64_t cols, int64_t pad, hipStream_t s)
 {
     auto tiles = [&](int bm, int bn) {
-        return (a.dx ? count(a.n, a.d, bm, bn) * a.dx_splits : 0) + (a.dw ? count(cols, a.d, bm, bn) : 0);
+        return (a.dx ? count(a.n, a.d, bm, bn) * a.dx_splits : 0) + (a.dw ? count(cols, a.d, bm, bn) * a.dw_splits : 0);
     };
     const Tile t = best_tile<DT>(tiles(256, 256), tiles(128, 128), tiles(64, 128));
     if constexpr (DT == 1) {

@@ -47,6 +47,9 @@ CASES = [
     (40, 64, 1030, wl.BF16, "silu", 0),
     (3, 40, 16000, wl.F32, "silu", 0),
     (1, 16, 20510, wl.BF16, "gelu", 0),
+    # many tokens and few features: the weights' sums are cut in parts
+    (5000, 40, 33, wl.BF16, "silu", 0),
+    (4100, 24, 20, wl.F32, "gelu", 0),
 ]
 IDS = ["M%dK%dF%d-%s-%s%s" % (c[0], c[1], c[2], c[3], c[4], "-str" * (c[5] > 0)) for c in CASES]
 

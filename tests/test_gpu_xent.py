@@ -54,6 +54,10 @@ CASES = [
     # few tokens and a large vocabulary: dx's sums are cut in parts
     (20, 72, 20000, wl.BF16, 0),
     (9, 33, 9000, wl.F32, 0),
+    (18, 33, 9000, wl.F32, 0),
+    # many tokens and a small vocabulary: dw's sums are cut in parts
+    (5000, 40, 130, wl.BF16, 0),
+    (3000, 24, 50, wl.F32, 0),
 ]
 IDS = ["N%dD%dV%d-%s%s" % (c[0], c[1], c[2], c[3], "-str" * (c[4] > 0)) for c in CASES]
 
