@@ -4,12 +4,17 @@
 //
 // One workgroup of WM x WN waves forms a BM x BN tile of C in its registers, fp32, from
 // 16x16 MFMA products; A and B tiles of 8 x 16 bytes per row of k pass through LDS, two
-// buffers in turn, loaded from global memory straight to LDS 16 bytes a lane.  Either
-// operand is stored with k contiguous (KC: rows of A or B) or with m/n contiguous (MC:
-// the transpose), so products with a transposed operand need no transposing pass: the MC
-// fragments are read from LDS with the transposing read (bf16) or element by element (fp32).
-// All products are bf16 ones; fp32 operands are split into three bf16 parts (see MM<0>) on their
-// way to LDS, which takes them at any alignment.
+// buffers (three of B under the two-group schedule, see mm_loop) in turn, loaded from global
+// memory straight to LDS 16 bytes a lane.  Either operand is stored with k contiguous (KC: rows
+// of A or B) or with m/n contiguous (MC: the transpose), so products with a transposed operand
+// need no transposing pass: bf16 MC fragments are read from LDS with the transposing read.
+// All products are bf16 ones; fp32 operands are split into three bf16 parts (see MM<0>) in
+// registers on their way to LDS, and transposed there where they are MC; that takes any alignment.
+//
+// What bounds it at large sizes is the power that the matrix cores may take.  8192 x 8192 outputs
+// over 4096, bf16, both operands KC: 434 us, 1266 TFLOP/s (B MC 1254, both MC 1201), the cores 71%
+// busy at 1.8 GHz; operands of zeros, which cost little power: 1700.  fp32, 4096 x 4096 over 2048:
+// 366 us, 188 TFLOP/s.
 //
 // LDS swizzle.  The direct load writes lane i's 16 bytes at base + 16 i, so a permutation of
 // a row's 16-byte chunks has to be applied to the source address instead:
@@ -261,7 +266,10 @@ __device__ __forceinline__ void mm_mul(const typename MM<G::DT>::Frag (&a)[G::FM
 #pragma unroll
     for (int i = 0; i < G::FM; ++i) {
 #pragma unroll
-        for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(b[j], a[i], acc[i][j]);
+        for (int q = 0; q < G::FN; ++q) {
+            const int j = i & 1 ? G::FN - 1 - q : q;  // there and back: every two neighbours share an operand
+            acc[i][j] = mfma_bf16(b[j], a[i], acc[i][j]);
+        }
         beside(i);
     }
 }
@@ -774,15 +782,15 @@ inline TilePlan plan_tiles(uint32_t ntm, uint32_t ntn, bool can_split, uint32_t 
 }
 
 // The fastest tile for launches of that many tiles of each kind, by what they take at k = 2048 on
-// 256 CUs, in units of a round of large tiles (57 us; bf16) or of small ones (106 us; fp32):
+// 256 CUs, in units of a round of large tiles (57 us; bf16) or of small ones (98 us; fp32):
 // 1024 x 1024, 2048 x 2048 and 4096 x 4096 outputs, bf16: halves 28, 31, 69 us, small 24, 27, 79, mini
-// 17, 24, 92; fp32: small 110, 137, 426, mini 84, 158, 502.  n: tiles on the busiest CU.
+// 17, 24, 92; fp32: small 115, 132, 390, mini 86, 139, 451.  n: tiles on the busiest CU.
 template <int DT>
 inline Tile best_tile(int64_t large, int64_t small, int64_t mini)
 {
     const double ns = double((small + kCUs - 1) / kCUs), nm = double((mini + kCUs - 1) / kCUs);
     if (DT == 0) {
-        const double cs = ns == 1 ? 1.28 : ns, cm = nm == 1 ? 0.85 : nm == 2 ? 1.48 : 0.59 * nm;
+        const double cs = ns == 1 ? 1.35 : ns, cm = nm == 1 ? 0.88 : nm == 2 ? 1.42 : 0.58 * nm;
         return cm < cs ? Tile::Mini : Tile::Small;
     }
     const int64_t rounds = large / kCUs, rest = large % kCUs;
