@@ -14,7 +14,7 @@
 // What bounds it at large sizes is the power that the matrix cores may take.  8192 x 8192 outputs
 // over 4096, bf16, both operands KC: 434 us, 1266 TFLOP/s (B MC 1254, both MC 1201), the cores 71%
 // busy at 1.8 GHz; operands of zeros, which cost little power: 1700.  fp32, 4096 x 4096 over 2048:
-// 366 us, 188 TFLOP/s.
+// 390 us, 176 TFLOP/s.
 //
 // LDS swizzle.  The direct load writes lane i's 16 bytes at base + 16 i, so a permutation of
 // a row's 16-byte chunks has to be applied to the source address instead:

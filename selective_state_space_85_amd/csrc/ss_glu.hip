@@ -12,7 +12,11 @@
 // workspace matrix; the second launch holds the tiles of dx (contraction over the 2 f columns
 // of that matrix against the rows of Wg, then of Wu) and those of dWg and dWu (its transpose
 // against x) together, so that one set's last tiles run beside the other's first.
-// All three are bound by the matrix cores at training sizes.
+// All three are bound by the matrix cores at training sizes (k = 2560, f = 6912, bf16, silu):
+// forward, 4096 tokens 228 us, 16384 tokens 935 us (1270 and 1240 TFLOP/s); backward, 16384 tokens
+// 1080 us for dg and du again and 2.12 ms for the gradients (1070 and 1090 TFLOP/s).  Keeping g and
+// u would spare the 1.08 ms and take 4 m f bytes for each layer (453 MB here).
+// Few tokens: the weights stream past them (see ss_gemm.h); one token 13.5 us, 5.2 TB/s.
 #include "ss_gemm.h"
 #include "ss_lm_internal.h"
 

@@ -33,6 +33,7 @@ struct Regions {
             ok = false;
             return 0;
         }
+        if (bytes == 0) return at;  // not there
         from &= ~int64_t(255);
         if (__builtin_add_overflow(from, bytes, &at)) ok = false;
         return from;
@@ -84,7 +85,8 @@ constexpr int64_t kGlrCols = 64;  // channels per workgroup
 // The backward with fewer one-chunk workgroups than kGlrWhole leaves CUs idle: the rows are then
 // cut until there are kGlrTarget workgroups, in chunks of at least kGlrMinChunk rows (the cut
 // costs a pass over r and dy) and at most kGlrMaxChunks of them (a chunk joins the maps of those
-// after it itself).
+// after it itself).  Both passes, whole and cut: (1, 16384, 2048) bf16 900 and 201 us, (4, 2048, 2560)
+// 160 and 134, (3, 1021, 1533) fp32 81 and 84; with twice as many chunks 214, 126 and 86.
 constexpr int64_t kGlrWhole = 256, kGlrTarget = 768, kGlrMinChunk = 128, kGlrMaxChunks = 64;
 
 void glr_plan(int64_t batch, int64_t seqlen, int64_t dim, int64_t* len, int64_t* chunks)
@@ -411,16 +413,35 @@ struct RowsPlan {
     bool few;      // the gradients in one pass over the weights
     bool pad;      // padded copies are needed: bf16 tiles read them (in the forward, or the backward)
 };
-// Streaming reads x again for every 32 weight rows, from the caches: up to 16 rows that is little,
-// up to 64 it pays while tiles of 128 weight rows would leave CUs idle (46 563 weight rows of 3264 bf16,
-// 25 rows: tiles 74 us, streamed 94; 4 292 of 4632, 33 rows: 64 against 35), or where tiles would
-// need padded copies of the weights.
+// Streaming reads x again for every 32 weight rows, from the caches, which costs more the more rows
+// there are; tiles of 128 weight rows cost the same up to 64 rows, but leave CUs idle while there
+// are fewer than 256 of them.  Times in us, streamed and in tiles, k = 2560:
+//   bf16,   43 tiles:  1 row 10 19, 64 rows 18 26;   108: 1 row 14 27, 32 rows 21 27, 64 rows 31 27;
+//          216 tiles:  8 rows 28 29, 16 rows 32 29;  313: 1 row 33 31;   432: 1 row 53 47, 16 rows 72 48;
+//   fp32, 108 tiles: 64 rows 73 103;  216: 32 rows 97 114, 64 rows 162 115;  432: 16 rows 160 170.
+// bf16 rows that are not whole 16-byte chunks would need padded copies of the weights for tiles, and
+// are always streamed.
+// The gradients in one pass save a second reading of the weights (and padded copies), at 2 m
+// multiply-adds per element on the vector units.  Times in us of both passes so and in tiles:
+//   bf16, 2560 -> 2 x 6912: 1 row 78 88, 4 rows 83 86, 8 rows 98 88;  768 -> 2 x 2048: 1 row 39 33;
+//   bf16, 2561 -> 2 x 6913: 1 row 121 188, 8 rows 160 204, 16 rows 237 216;
+//   fp32, 2560 -> 2 x 6912: 1 row 119 142, 8 rows 139 149, 16 rows 178 158.
+constexpr int64_t kFewAligned = 4, kFewWeights = int64_t(16) << 20;  // bf16: rows, elements of the weights
 RowsPlan rows_plan(int64_t rows, int64_t dim, int64_t cols, ss_dtype dtype, bool back)
 {
     RowsPlan p;
     p.aligned = dim % chunk_elems(dtype) == 0;
-    p.stream = rows <= 16 || (rows <= ssk::kStreamRows && ((dtype == SS_BF16 && !p.aligned) || ceil_div(cols, 128) < 256));
-    p.few = rows <= ssk::kFewRows;
+    const int64_t tiles = ceil_div(cols, 128), idle = tiles < 256 ? 256 - tiles : 0;
+    if (dtype == SS_F32) {
+        p.stream = rows <= 16 || (rows <= ssk::kStreamRows && rows <= idle);
+        p.few = rows <= ssk::kFewRows;
+    } else if (p.aligned) {
+        p.stream = rows <= ssk::kStreamRows && rows * 16 <= idle * 5;
+        p.few = rows <= kFewAligned && cols * dim >= kFewWeights;
+    } else {
+        p.stream = rows <= ssk::kStreamRows;
+        p.few = rows <= ssk::kFewRows;
+    }
     p.pad = dtype == SS_BF16 && !p.aligned && (back ? !p.few : !p.stream);
     return p;
 }
@@ -487,7 +508,8 @@ struct XentLayout {
 // Columns per piece of the backward: as many as keep the piece's gradient of the logits within
 // kXentPieceBytes (it is written once and read twice, so it had better stay in the last-level
 // cache), but no fewer than kXentMinPiece (each piece reads and writes the fp32 sums of dx).
-// Pieces are evened out, in whole tiles of 256 columns.
+// Pieces are evened out, in whole tiles of 256 columns.  Loss and gradients of 8192 tokens, 2560
+// wide, 50257 entries with 64 MB, 256 MB and 1 GB: 8.0, 7.5 and 7.5 ms.
 constexpr int64_t kXentPieceBytes = int64_t(256) << 20, kXentMinPiece = 4096;
 
 int64_t xent_piece(int64_t n, int64_t v, int64_t es)

@@ -13,7 +13,7 @@ namespace ssk {
 constexpr int64_t kStreamRows = 64;
 // Rows of x up to which the gradients of such products are formed in one pass over the weights
 // (ss_few.hip).
-constexpr int64_t kFewRows = 16;
+constexpr int64_t kFewRows = 8;
 
 // With s (m, rows), x (m, k) and weights W (rows, k): dx = s W in parts, dW = s^T x.  W may lie in
 // two matrices, the first `first` rows in w0 and the others in w1.
