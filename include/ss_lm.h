@@ -119,7 +119,8 @@ ss_status ss_glu_fwd(const void* x, int64_t x_row_stride, const void* w_gate, co
  *   dx      : (tokens, dim) dtype output, or NULL (not wanted)
  *   dw_gate, dw_up : (features, dim) dtype outputs, or both NULL
  * The gradients of x Wg^T and x Wu^T are rounded to dtype between the
- * products.  Alignment as for ss_glu_fwd.
+ * products (of up to 32 bf16 tokens dw_gate and dw_up take what the rounding
+ * leaves too).  Alignment as for ss_glu_fwd.
  */
 size_t ss_glu_bwd_workspace_bytes(int64_t tokens, int64_t dim, int64_t features, ss_dtype dtype);
 

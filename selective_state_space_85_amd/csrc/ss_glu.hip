@@ -8,10 +8,11 @@
 // each wave column, so that one wave holds g and u of the same elements in its accumulators
 // and the product never leaves the registers; g and u are not stored.
 // Backward: the same product again with dh in the epilogue gives dg and du (rounded once to
-// the operands' type, as the next product's operands must be), side by side in one (m, 2 f)
-// workspace matrix; the second launch holds the tiles of dx (contraction over the 2 f columns
-// of that matrix against the rows of Wg, then of Wu) and those of dWg and dWu (its transpose
-// against x) together, so that one set's last tiles run beside the other's first.
+// the operands' type, as the next product's operands must be; of a few bf16 tokens what the
+// rounding leaves is kept too, see kGluLoRows), side by side in one (m, 2 f) workspace matrix;
+// the second launch holds the tiles of dx (contraction over the 2 f columns of that matrix
+// against the rows of Wg, then of Wu) and those of dWg and dWu (its transpose against x)
+// together, so that one set's last tiles run beside the other's first.
 // All three are bound by the matrix cores at training sizes (k = 2560, f = 6912, bf16, silu):
 // forward, 4096 tokens 228 us, 16384 tokens 935 us (1270 and 1240 TFLOP/s); backward, 16384 tokens
 // 1080 us for dg and du again and 2.12 ms for the gradients (1070 and 1090 TFLOP/s).  Keeping g and
@@ -130,6 +131,16 @@ __device__ __forceinline__ void glu_emit(const GluArgs& a, int64_t m, int64_t f,
         T* const row = static_cast<T*>(a.dgu) + m * 2 * a.f_pad + f;
         store4<DT>(row, 4, true, dg);
         store4<DT>(row + a.f_pad, 4, true, du);
+        if (DT == 1 && a.lo) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dg[e] -= MM<DT>::widen(MM<DT>::narrow(dg[e]));
+                du[e] -= MM<DT>::widen(MM<DT>::narrow(du[e]));
+            }
+            T* const rest = row + a.m * 2 * a.f_pad;
+            store4<DT>(rest, 4, true, dg);
+            store4<DT>(rest + a.f_pad, 4, true, du);
+        }
     }
 }
 
@@ -280,6 +291,7 @@ struct GluDwProb {
     static constexpr int BK = 8 * MM<DT>::kEpc;
     const GluArgs& a;
     int64_t m0, n0;  // m0: first column of dgu (of its 2 f_pad), n0: first column of x
+    // rows of dgu: the tokens, and the same again for the remainders (all in one k tile)
     int tiles;
     int first;    // this part's first k tile
     float* part;  // where this part's sums go; null: the gradients themselves
@@ -295,11 +307,12 @@ struct GluDwProb {
     {
         int64_t c = n0 + col;
         c = c < a.k_pad ? c : a.k_pad - MM<DT>::kEpc;
-        return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + int64_t(k) * a.x_ld + c);
+        const int64_t token = a.lo && k >= a.m ? k - a.m : k;
+        return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + token * a.x_ld + c);
     }
     __device__ int64_t a_off(int t) const { return int64_t(t + first) * BK * 2 * a.f_pad * int64_t(sizeof(T)); }
     __device__ int64_t b_off(int t) const { return int64_t(t + first) * BK * a.x_ld * int64_t(sizeof(T)); }
-    __device__ int valid(int t) const { return k_left<DT>(a.m, t + first); }
+    __device__ int valid(int t) const { return k_left<DT>(a.lo ? 2 * a.m : a.m, t + first); }
 
     __device__ const float* a_at(int col, int k) const
     {

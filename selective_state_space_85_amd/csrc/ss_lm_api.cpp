@@ -466,7 +466,7 @@ void few_parts(int64_t m, int64_t k, int64_t rows, ss_dtype dtype, int64_t* per,
 struct GluLayout {
     int64_t k_pad, f_pad, splits, per, dw_splits;
     RowsPlan plan;
-    bool pack;
+    bool pack, lo;
     int64_t x, wg, wu, dgu, part, dw_part, total;
 };
 
@@ -482,7 +482,8 @@ bool glu_layout(int64_t m, int64_t k, int64_t f, ss_dtype dtype, bool back, GluL
     w->x = r.add(w->pack ? m * w->k_pad : 0, es);
     w->wg = r.add(w->pack ? f * w->k_pad : 0, es);
     w->wu = r.add(w->pack ? f * w->k_pad : 0, es);
-    w->dgu = r.add(back ? m * 2 * w->f_pad : 0, w->plan.few ? 4 : es);
+    w->lo = dtype == SS_BF16 && !w->plan.few && m <= ssk::kGluLoRows;
+    w->dgu = r.add(back ? (w->lo ? 2 * m : m) * 2 * w->f_pad : 0, w->plan.few ? 4 : es);
     w->per = 0;
     if (w->plan.few)
         few_parts(m, k, 2 * f, dtype, &w->per, &w->splits);
@@ -620,6 +621,7 @@ ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, 
     a.h = h;
     a.dh = dh;
     a.dgu = ws ? ws + w.dgu : nullptr;
+    a.lo = w.lo;
     a.dx = dx;
     a.dwg = dwg;
     a.dwu = dwu;

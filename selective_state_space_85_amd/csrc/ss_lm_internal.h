@@ -38,6 +38,11 @@ hipError_t launch_few_grad(const FewGradArgs& a, int dtype, hipStream_t stream);
 constexpr int kActSilu = 0, kActGelu = 1;
 
 
+// Tokens up to which the weights' gradients in tiles, bf16, use what the rounding of dg and du left
+// as well: their sums have few terms to even the roundings out, and a k tile (64 tokens) has
+// room for both without another product.
+constexpr int64_t kGluLoRows = 32;
+
 struct GluArgs {
     const void* x;   // (m, k), rows x_ld elements apart
     int64_t x_ld;
@@ -47,6 +52,7 @@ struct GluArgs {
     void* h;         // (m, f); the backward: unused
     const void* dh;  // backward: (m, f)
     void* dgu;       // backward workspace: (m, 2 f_pad), dg in the first half of a row, du in the second
+    bool lo;         // and behind them as many rows of what their rounding left (see kGluLoRows)
     void* dx;        // (m, k), nullable
     void* dwg;       // (f, k), nullable (both or neither)
     void* dwu;

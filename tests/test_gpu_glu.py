@@ -187,3 +187,20 @@ def test_refusals():
     with pytest.raises(m.SSError):
         m.glu_bwd(x, w, w, torch.zeros((4, 32), device="cuda"),
                   workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("m,k,f", [(3, 2048, 4200), (4, 1032, 16450), (9, 256, 16500), (64, 136, 2600)],
+                         ids=["one-pass", "one-pass-beside-tiles", "tiles", "streamed"])
+def test_few_tokens_of_large_weights(m, k, f):
+    """bf16, a few tokens: each way that the products and their gradients are formed."""
+    x, wg, wu, dh = make(m, k, f, wl.BF16, 11)
+    say("glu few", m, k, f)
+    t = [dev(v) for v in (x, wg, wu)]
+    h = ss().glu_fwd(*t)
+    g = ss().glu_bwd(*t, dev(dh))
+    torch.cuda.synchronize()
+    p = [wide(v) for v in (x, wg, wu)]
+    check("h", host64(h), lm_ref.glu(*p, "silu"), TOL["bf16"])
+    ref = lm_ref.glu_bwd(*p, wide(dh), "silu")
+    for n in ref:
+        check(n, host64(g[n]), ref[n], TOL["bf16"])

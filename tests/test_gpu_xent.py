@@ -210,3 +210,18 @@ def test_refusals():
     loss, lse = m.xent_fwd(x, w, t)
     with pytest.raises(m.SSError):
         m.xent_bwd(x, w, t, lse, loss, want_dx=False, want_dw=False)
+
+
+@pytest.mark.parametrize("n,d,v", [(3, 512, 33000), (9, 64, 33000), (12, 1024, 3000)],
+                         ids=["one-pass-beside-tiles", "tiles", "streamed"])
+def test_few_tokens_of_large_vocabularies(n, d, v):
+    """bf16, a few tokens: each way that the logits and the gradients are formed."""
+    x, w, t, dloss = make(n, d, v, wl.BF16, 12)
+    say("xent few", n, d, v)
+    loss, lse, g = run(x, w, t, dloss)
+    lr, zr, _, _ = lm_ref.xent(wide(x), wide(w), t)
+    check("loss", host64(loss), lr, TOL["f32"])
+    check("lse", host64(lse), zr, TOL["f32"])
+    ref = lm_ref.xent_bwd(wide(x), wide(w), t, dloss.astype(np.float64))
+    for k in ref:
+        check(k, host64(g[k]), ref[k], TOL[wl.BF16])
