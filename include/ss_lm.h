@@ -101,9 +101,11 @@ ss_status ss_glr_step(float* h, const void* x, int64_t x_row_stride, const void*
  * x_row_stride a multiple of 8 (SS_ERR_INVALID_ARG otherwise).  Other dims, and
  * fp32, take any element-aligned operands; bf16 ones may first be copied to
  * padded rows in the workspace.
- * fp32 products are formed from three bf16 parts of each operand, six products
- * of parts accumulated in fp32: as exact as fp32 arithmetic, except that an
- * infinite operand gives NaN.
+ * fp32 products of more than a few rows are formed from three bf16 parts of each
+ * operand, six products of parts accumulated in fp32: each product is within
+ * 2^-23 of itself (fp32 rounds one by up to 2^-24), and operands below 2^-110
+ * keep no bits below 2^-134.  Infinities, NaN and numbers up to the largest
+ * give what fp32 arithmetic gives.
  */
 typedef enum { SS_ACT_SILU = 0, SS_ACT_GELU = 1 } ss_activation;
 

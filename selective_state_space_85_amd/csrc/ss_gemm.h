@@ -87,10 +87,13 @@ struct MM<1> {  // bf16 operands
 };
 
 // fp32 operands.  An operand is the sum of three bf16 parts, each the rounding of what the ones
-// before it leave: 24 bits and more.  A product is formed from the six products of parts that
-// matter, smallest first (those left out are below 2^-26 of it), accumulated in fp32: as exact as
-// fp32 arithmetic, at a sixth of bf16's rate where the fp32 matrix instruction has a sixteenth.
-// An infinite operand gives NaN (its later parts are inf - inf).
+// before it leave: all of its 24 bits, down to 2^-134 (bf16's range ends there: operands below 2^-110
+// lose their last bits).  A product is formed from the six products of parts that matter, smallest
+// first, accumulated in fp32, at a sixth of bf16's rate where the fp32 matrix instruction has a
+// sixteenth.  The three left out are together up to 2^-24.0 of the product (the largest found; below
+// 2^-23 by their sizes), 2^-27.4 in the mean square of random pairs; fp32 rounds a product by as much.
+// An operand that bf16 rounds to infinity (from 3.3962e38 on) has inf - inf among its parts; such
+// tiles are formed again by the fp32 instruction (see mm_tile_f32).
 template <>
 struct MM<0> {
     using T = float;
@@ -514,6 +517,20 @@ struct Staged {
             }
         }
     }
+    // tile: ROWS rows of the elements as they are
+    __device__ __forceinline__ void store_whole(float* tile, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!has(i, tid)) continue;
+            int row, chunk;
+            place(i, tid, &row, &chunk);
+#pragma unroll
+            for (int c = 0; c < (MC ? 2 : 1); ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) tile[(row + c) * 32 + chunk * 8 + e] = MC ? v[i][2 * e + c] : v[i][e];
+        }
+    }
 };
 __device__ __forceinline__ bf16x8 staged_frag(const char* part, int r0, int lane)
 {
@@ -523,6 +540,10 @@ __device__ __forceinline__ bf16x8 staged_frag(const char* part, int r0, int lane
 
 // One workgroup's tile of an fp32 product.  Elements pass through registers, where each is split
 // once per workgroup; the next k tile's loads are in flight while this one's products are formed.
+// A tile whose sums are not all finite is formed again, by the fp32 instruction from the elements
+// themselves: an infinity, or a number that bf16 rounds to one, makes all that it takes part in NaN
+// above, where infinite or finite results may be due.  The check costs 0.5 to 2.5% of a pass (4096 tokens,
+// 2048 -> 2 x 2048: 1387 -> 1393 us; 777, 1001 -> 2 x 2731: 340 -> 347), the rest such tiles alone.
 // Prob: a_at(row, k) / b_at(row, k), the address of an element, rows past the end clamped to the last;
 // a_cols() / b_cols(), for MC operands the columns that exist from the tile's first on; a_ld() / b_ld(),
 // their elements per k; a_off, b_off (in bytes), valid, tiles, finish as for mm_tile.
@@ -539,23 +560,26 @@ __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
     const float* pa[SA::N];
     const float* pb[SB::N];
     bool ta[SA::N], tb[SB::N];
-    int row, chunk;
+    auto set = [&](int thread) {
+        int row, chunk;
 #pragma unroll
-    for (int i = 0; i < SA::N; ++i) {
-        SA::place(i, tid, &row, &chunk);
-        ta[i] = !G::A_MC || row + 1 < p.a_cols();
-        pa[i] = p.a_at(row, SA::has(i, tid) ? chunk * 8 : 0);
-    }
+        for (int i = 0; i < SA::N; ++i) {
+            SA::place(i, thread, &row, &chunk);
+            ta[i] = !G::A_MC || row + 1 < p.a_cols();
+            pa[i] = p.a_at(row, SA::has(i, thread) ? chunk * 8 : 0);
+        }
 #pragma unroll
-    for (int i = 0; i < SB::N; ++i) {
-        SB::place(i, tid, &row, &chunk);
-        tb[i] = !G::B_MC || row + 1 < p.b_cols();
-        pb[i] = p.b_at(row, SB::has(i, tid) ? chunk * 8 : 0);
-    }
+        for (int i = 0; i < SB::N; ++i) {
+            SB::place(i, thread, &row, &chunk);
+            tb[i] = !G::B_MC || row + 1 < p.b_cols();
+            pb[i] = p.b_at(row, SB::has(i, thread) ? chunk * 8 : 0);
+        }
+    };
     auto load = [&](int t) {
         sa.load(pa, ta, p.a_off(t) / 4, p.a_ld(), p.valid(t), tid);
         sb.load(pb, tb, p.b_off(t) / 4, p.b_ld(), p.valid(t), tid);
     };
+    set(tid);
     f32x4 acc[G::FM][G::FN];
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
@@ -563,6 +587,8 @@ __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
         for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     char* const at = lds;
     char* const bt = lds + G::BM * 192;
+    __shared__ int odd;  // some sum is not finite
+    if (tid == 0) odd = 0;
     if (p.tiles > 0) load(0);
     for (int t = 0; t < p.tiles; ++t) {
         __syncthreads();  // the last tile's readers are done
@@ -585,6 +611,47 @@ __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
             for (int q = 0; q < 6; ++q)
 #pragma unroll
                 for (int j = 0; j < G::FN; ++j) acc[i][j] = mfma_bf16(b[kB[q]][j], a[kA[q]], acc[i][j]);
+        }
+    }
+    if (p.tiles > 0) {
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) finite = finite && fabsf(acc[i][j][e]) < __builtin_inff();
+        if (!finite) odd = 1;
+        __syncthreads();
+        if (odd) {
+            // formed anew: kept through the loop above, the addresses would cost its registers
+            int thread = tid;
+            asm volatile("" : "+v"(thread));
+            set(thread);
+            float* const wa = reinterpret_cast<float*>(lds);
+            float* const wb = wa + G::BM * 32;
+#pragma unroll
+            for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int t = 0; t < p.tiles; ++t) {
+                load(t);
+                __syncthreads();
+                sa.store_whole(wa, tid);
+                sb.store_whole(wb, tid);
+                __syncthreads();
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e) {
+                    // element e of a lane's 8 is the same k on both sides
+                    const int from = (lane & 15) * 32 + (lane >> 4) * 8 + e;
+#pragma unroll
+                    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < G::FN; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wb[(wn * G::FN + j) * 512 + from],
+                                                                            wa[(wm * G::FM + i) * 512 + from], acc[i][j], 0, 0, 0);
+                }
+            }
         }
     }
     p.template finish<G>(acc, lds, wm, wn, lane);
