@@ -178,13 +178,23 @@ __device__ __forceinline__ float channel_rate(float decay, float c)
     return c * (fmaxf(decay, 0.0f) + log1pf(expf(-fabsf(decay))));
 }
 
-// a h + b, the update and the composition of maps.  With resets a product of 0 means that
-// nothing of h remains, not even a NaN or an infinity (0 times which would be NaN).
+// a h + b, the update and the composition of maps.  With resets a factor of 0 means that
+// nothing of h remains, not even a NaN or an infinity (0 times which would be NaN), so a row's a
+// and a product of them are 0 at resets alone: elsewhere they are at least the least positive number
+// (`factor`, `joined`), which takes nothing from a finite state and leaves the others what they are.
 template <bool RESET>
 __device__ __forceinline__ float carry(float a, float h, float b)
 {
     const float v = fmaf(a, h, b);
     return RESET && a == 0.0f ? b : v;
+}
+// A factor that is not a reset's; a NaN stays one.
+__device__ __forceinline__ float factor(float a) { return __uint_as_float(max(__float_as_uint(a), 1u)); }
+// The product of two maps' factors.
+template <bool RESET>
+__device__ __forceinline__ float joined(float a, float b)
+{
+    return RESET && (a == 0.0f || b == 0.0f) ? 0.0f : factor(a * b);
 }
 
 // The other half wave's value.
@@ -322,6 +332,7 @@ __global__ __launch_bounds__(kFwdThreads, 4) void glr_fwd_kernel(GlrArgs a)
         rx[q] = px.load(bx, q);
         if (RESET) rs[q] = a.reset[row0 + (run * R + q < rows ? run * R + q : 0)] != 0;
     }
+    bool cut = false;  // a reset among the run's rows
 #pragma unroll
     for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -329,9 +340,9 @@ __global__ __launch_bounds__(kFwdThreads, 4) void glr_fwd_kernel(GlrArgs a)
             float ww;
             decay_of(k[e], sigmoid1(RW::get(rr[q], e)), &av[q][e], &ww);
             float m = __builtin_amdgcn_sqrtf(ww);
-            if (RESET && rs[q]) {
-                av[q][e] = 0.0f;
-                m = 1.0f;
+            if (RESET) {
+                av[q][e] = rs[q] ? 0.0f : factor(av[q][e]);
+                m = rs[q] ? 1.0f : m;
             }
             bv[q][e] = m * sigmoid1(RW::get(ri[q], e)) * RW::get(rx[q], e);
         }
@@ -345,6 +356,10 @@ __global__ __launch_bounds__(kFwdThreads, 4) void glr_fwd_kernel(GlrArgs a)
                 bv[q][e] = run * R + q < rows ? bv[q][e] : 0.0f;
             }
     }
+    if (RESET) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) cut = cut || (rs[q] && run * R + q < rows);
+    }
     // the run's map, then the wave's; the earlier half publishes it
     float P[VC], E[VC], P0[VC], E0[VC];
 #pragma unroll
@@ -353,13 +368,14 @@ __global__ __launch_bounds__(kFwdThreads, 4) void glr_fwd_kernel(GlrArgs a)
         E[e] = bv[0][e];
 #pragma unroll
         for (int q = 1; q < R; ++q) {
-            P[e] = carry<RESET>(av[q][e], P[e], 0.0f);
+            P[e] *= av[q][e];
             E[e] = carry<RESET>(av[q][e], E[e], bv[q][e]);
         }
+        P[e] = cut ? 0.0f : factor(P[e]);
         P0[e] = other_half(P[e]);
         E0[e] = other_half(E[e]);
         if (half == 0) {
-            maps[wave][0][l32 * VC + e] = carry<RESET>(P0[e], P[e], 0.0f);
+            maps[wave][0][l32 * VC + e] = joined<RESET>(P0[e], P[e]);
             maps[wave][1][l32 * VC + e] = carry<RESET>(P0[e], E[e], E0[e]);
         }
     }
@@ -374,7 +390,7 @@ __global__ __launch_bounds__(kFwdThreads, 4) void glr_fwd_kernel(GlrArgs a)
 #pragma unroll
         for (int v = 0; v < W; ++v) {
             const float p = maps[v][0][ch];
-            A = carry<RESET>(p, A, 0.0f);
+            A = joined<RESET>(p, A);
             S = carry<RESET>(p, S, maps[v][1][ch]);
         }
         const int64_t step = int64_t(units) * (kRunLanes * VC);
@@ -473,7 +489,7 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
             }
             if (RESET) {
                 const int64_t t = tile + run * R + j;
-                rs[j] = a.reset[row0 + (t < a.seqlen ? t : a.seqlen - 1)];
+                rs[j] = t < a.seqlen ? a.reset[row0 + t] : 0;
             }
         }
         if (!AGG) {
@@ -491,6 +507,11 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
         // g a (h_{t-1} - (a / w) bv), from dm/dlog a = -a^2 / m and w = m^2.
         float av[R][VC], bv[R][VC], c1[R][VC], slope[R][VC], sr[R][VC], nr[R][VC], ni[R][VC], dy[R][VC], h[VC];
         float P[VC], E[VC], Q[VC];
+        bool cut = false;  // a reset among the run's rows
+        if (RESET) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) cut = cut || rs[j];
+        }
 #pragma unroll
         for (int j = 0; j < R; ++j)
 #pragma unroll
@@ -498,9 +519,9 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
                 float ww;
                 sr[j][e] = sigmoid2(RW::get(rr[j], e), &nr[j][e]);
                 decay_of(k[e], sr[j][e], &av[j][e], &ww);
-                if (RESET && rs[j]) {
-                    av[j][e] = 0.0f;
-                    ww = 1.0f;
+                if (RESET) {
+                    av[j][e] = rs[j] ? 0.0f : factor(av[j][e]);
+                    ww = rs[j] ? 1.0f : ww;
                 }
                 dy[j][e] = RW::get(rd[j], e);
                 if (!AGG) {
@@ -534,9 +555,10 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
             if (!AGG) E[e] = bv[0][e];
 #pragma unroll
             for (int j = 1; j < R; ++j) {
-                P[e] = carry<RESET>(av[j][e], P[e], 0.0f);
+                P[e] *= av[j][e];
                 if (!AGG) E[e] = carry<RESET>(av[j][e], E[e], bv[j][e]);
             }
+            P[e] = cut ? 0.0f : factor(P[e]);
             Q[e] = carry<RESET>(av[R - 1][e], dy[R - 1][e], 0.0f);
 #pragma unroll
             for (int j = R - 2; j >= 0; --j) Q[e] = carry<RESET>(av[j][e], Q[e] + dy[j][e], 0.0f);
@@ -549,7 +571,7 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
             Qo[e] = other_half(Q[e]);
             if (!AGG) Eo[e] = other_half(E[e]);
             if (half == 0) {
-                maps[buf][wave][3 * e][l32] = carry<RESET>(Po[e], P[e], 0.0f);
+                maps[buf][wave][3 * e][l32] = joined<RESET>(Po[e], P[e]);
                 maps[buf][wave][3 * e + 1][l32] = carry<RESET>(P[e], Qo[e], Q[e]);
                 if (!AGG) maps[buf][wave][3 * e + 2][l32] = carry<RESET>(Po[e], E[e], Eo[e]);
             }
@@ -574,7 +596,7 @@ __global__ __launch_bounds__(kBwdThreads, AGG ? 4 : 3) void glr_bwd_kernel(GlrAr
                 if (!AGG && v == wave) qin[e] = q[e];
                 const float p = maps[buf][v][3 * e][l32];
                 q[e] = carry<RESET>(p, q[e], maps[buf][v][3 * e + 1][l32]);
-                if (AGG) prod[e] = carry<RESET>(p, prod[e], 0.0f);
+                if (AGG) prod[e] = joined<RESET>(p, prod[e]);
             }
         if (!AGG) {
             float before[R][VC];  // h_{t-1}

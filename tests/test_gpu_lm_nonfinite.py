@@ -154,3 +154,82 @@ def test_projection_of_infinities(m, act):
         ref = lm_ref.glu_bwd(*p, dh.astype(np.float64), act)
         for n in ref:
             same(n, host64(g[n]), ref[n], TOL["f32"])
+
+
+# decays so fast that the product of a over a few rows lies below float32's range: nothing of a
+# NaN or an infinity is lost with it
+@pytest.mark.parametrize("dt", [wl.F32, wl.BF16])
+@pytest.mark.parametrize("l,d", [(40, 33), (700, 64)])
+@pytest.mark.parametrize("with_reset", [False, True], ids=["no-resets", "resets-elsewhere"])
+@pytest.mark.parametrize("what", [np.nan, np.inf], ids=["nan", "inf"])
+def test_fast_decays_keep_nonfinite_states(what, with_reset, l, d, dt):
+    rng = np.random.default_rng(l)
+    b = 2
+    v = [rand(rng, (b, l, d), dt) for _ in range(3)]
+    w = [wide(a).astype(np.float32) for a in v]
+    w[0][0, 5, 7] = what
+    t = [torch.from_numpy(a).cuda().to(torch.bfloat16 if dt == wl.BF16 else torch.float32) for a in w]
+    decay = np.full(d, 2.0, np.float32)  # k = 17, a about e^-8.5
+    reset = None
+    if with_reset:
+        reset = np.zeros((b, l), np.uint8)
+        reset[1, 17] = 1  # the other batch row's
+    say("glr fast", what, with_reset, l, d, dt)
+    y, hl = ss().glr_fwd(*t, dev(decay), reset=None if reset is None else torch.from_numpy(reset).cuda(),
+                         return_last_state=True)
+    torch.cuda.synchronize()
+    y, hl = host64(y), host64(hl)
+    bad = np.zeros((b, l, d), bool)
+    bad[0, 5:, 7] = True
+    assert np.array_equal(~np.isfinite(y), bad)
+    assert np.all(np.isnan(y[bad])) if np.isnan(what) else np.all(y[bad] == what)
+    assert np.array_equal(~np.isfinite(hl), bad[:, -1])
+    # backward: a NaN among dy reaches every row before it
+    dy = np.zeros((b, l, d), np.float32)
+    dy[0, l - 2, 9] = np.nan
+    w[0][0, 5, 7] = 0.0
+    t[0] = torch.from_numpy(w[0]).cuda().to(t[0].dtype)
+    g = ss().glr_bwd(*t, dev(decay), torch.from_numpy(dy).cuda().to(t[0].dtype),
+                     reset=None if reset is None else torch.from_numpy(reset).cuda())
+    torch.cuda.synchronize()
+    bad[:] = False
+    bad[0, :l - 1, 9] = True
+    for n in ("dx", "dr", "di"):
+        assert np.array_equal(np.isnan(host64(g[n])), bad), n
+    assert np.array_equal(np.isnan(host64(g["dh0"])), bad[:, 0])
+    assert np.array_equal(np.isnan(host64(g["ddecay"])), bad[0, 0])
+
+
+@pytest.mark.parametrize("dt", [wl.F32, wl.BF16])
+@pytest.mark.parametrize("l,d", [(40, 33), (700, 64)])
+def test_a_reset_ends_nonfinite_states_of_fast_decays(l, d, dt):
+    """A reset cuts a NaN off on both sides: from the states after it, and from the gradients of
+    the rows before it."""
+    rng = np.random.default_rng(l + 1)
+    b, at = 2, l // 2
+    w = [wide(rand(rng, (b, l, d), dt)).astype(np.float32) for _ in range(3)]
+    w[0][0, 5, 7] = np.nan
+    to = torch.bfloat16 if dt == wl.BF16 else torch.float32
+    t = [torch.from_numpy(a).cuda().to(to) for a in w]
+    decay = dev(np.full(d, 2.0, np.float32))
+    reset = np.zeros((b, l), np.uint8)
+    reset[0, at] = 1
+    r = torch.from_numpy(reset).cuda()
+    say("glr fast reset", l, d, dt)
+    y = host64(ss().glr_fwd(*t, decay, reset=r))
+    bad = np.zeros((b, l, d), bool)
+    bad[0, 5:at, 7] = True
+    assert np.array_equal(np.isnan(y), bad)
+    w[0][0, 5, 7] = 0.0
+    t[0] = torch.from_numpy(w[0]).cuda().to(to)
+    dy = np.zeros((b, l, d), np.float32)
+    dy[0, l - 2, 9] = np.nan
+    g = ss().glr_bwd(*t, decay, torch.from_numpy(dy).cuda().to(to), reset=r)
+    torch.cuda.synchronize()
+    bad[:] = False
+    bad[0, at:l - 1, 9] = True
+    for n in ("dx", "di"):
+        assert np.array_equal(np.isnan(host64(g[n])), bad), n
+    bad[0, at] = False  # the reset row's a is 0 whatever its gate
+    assert np.array_equal(np.isnan(host64(g["dr"])), bad)
+    assert not np.isnan(host64(g["dh0"])).any()
