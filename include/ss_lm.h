@@ -16,6 +16,8 @@
  *  - Workspace contents on entry are unused; sizes depend on the shape alone.
  *    Workspaces are 256-byte aligned and overlap nothing.
  *  - Outputs overlap neither the inputs nor each other.
+ *  - Sizes whose launch would take 2^32 threads or more along a grid's axis are
+ *    SS_ERR_UNSUPPORTED.
  *  - Every sum is taken in a fixed order: results are the same from run to run.
  */
 #ifndef SS_LM_H

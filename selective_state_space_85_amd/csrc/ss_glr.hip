@@ -38,6 +38,7 @@ constexpr int kRunLanes = 32;  // lanes per run: half a wave
 constexpr int kFwdWaves = 8, kFwdThreads = 64 * kFwdWaves, kFwdRows = 16, kFwdTile = 2 * kFwdWaves * kFwdRows;
 // backward: 4 waves, 4 rows per run
 constexpr int kBwdWaves = 4, kBwdRuns = 2 * kBwdWaves, kBwdThreads = 64 * kBwdWaves, kBwdRows = 4;
+static_assert(kFwdThreads == kGlrFwdThreads && kBwdThreads == kGlrBwdThreads && kRunLanes == 32, "launches");
 static_assert(kFwdTile == kGlrTile && kBwdRuns * kBwdRows == kGlrRows, "tiles and kept states");
 static_assert(kGlrRows % kFwdRows == 0, "a kept state falls on a run's start");
 
@@ -716,7 +717,7 @@ struct Chunk<DT, 1> {
     static __device__ __forceinline__ Chunk make(const float (&f)[1]) { return {Row<DT, 1>::make(f)}; }
 };
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = kGlrStepThreads;
 template <int DT, int VC, int ROWS>
 __global__ __launch_bounds__(kStepThreads) void glr_step_kernel(GlrStepArgs a)
 {
@@ -758,17 +759,10 @@ __global__ __launch_bounds__(kStepThreads) void glr_step_kernel(GlrStepArgs a)
 
 // ---- launches ---------------------------------------------------------------------------------
 
-// Two channels per lane need every row of every operand aligned to two elements.
-bool even(const void* p, int64_t ld, int dtype)
-{
-    return p == nullptr || (ld % 2 == 0 && reinterpret_cast<uintptr_t>(p) % (dtype == 0 ? 8 : 4) == 0);
-}
-
 template <int DT, int VC, bool RESET>
 hipError_t fwd_variant(const GlrArgs& a, hipStream_t s)
 {
-    const int64_t cols = (a.dim + kRunLanes * VC - 1) / (kRunLanes * VC);
-    const int64_t blocks = cols * a.batch * a.n_tiles;
+    const int64_t blocks = glr_blocks(a, VC, a.n_tiles);
     if (a.n_tiles > 1) {
         const int64_t words = blocks * (kRunLanes * VC);
         glr_clear_kernel<<<dim3(unsigned((words + 255) / 256)), dim3(256), 0, s>>>(a.ws_words, words, a.ws_ticket);
@@ -782,8 +776,7 @@ hipError_t fwd_variant(const GlrArgs& a, hipStream_t s)
 template <int DT, int VC, bool RESET>
 hipError_t bwd_variant(const GlrArgs& a, hipStream_t s)
 {
-    const int64_t cols = (a.dim + kRunLanes * VC - 1) / (kRunLanes * VC);
-    const int64_t blocks = cols * a.batch * a.n_chunks;
+    const int64_t blocks = glr_blocks(a, VC, a.n_chunks);
     if (a.n_chunks > 1) {
         glr_bwd_kernel<DT, VC, RESET, true><<<dim3(unsigned(blocks)), dim3(kBwdThreads), 0, s>>>(a);
         const hipError_t e = hipGetLastError();
@@ -799,8 +792,7 @@ hipError_t bwd_variant(const GlrArgs& a, hipStream_t s)
 template <int DT>
 hipError_t fwd_dt(const GlrArgs& a, hipStream_t s)
 {
-    const bool two = a.dim % 2 == 0 && even(a.x, a.x_ld, DT) && even(a.r, a.r_ld, DT) && even(a.i, a.i_ld, DT) &&
-                     even(a.y, a.dim, DT);
+    const bool two = glr_fwd_channels(a, DT) == 2;
     if (a.reset) return two ? fwd_variant<DT, 2, true>(a, s) : fwd_variant<DT, 1, true>(a, s);
     return two ? fwd_variant<DT, 2, false>(a, s) : fwd_variant<DT, 1, false>(a, s);
 }
@@ -808,17 +800,9 @@ hipError_t fwd_dt(const GlrArgs& a, hipStream_t s)
 template <int DT>
 hipError_t bwd_dt(const GlrArgs& a, hipStream_t s)
 {
-    const bool two = a.dim % 2 == 0 && even(a.x, a.x_ld, DT) && even(a.r, a.r_ld, DT) && even(a.i, a.i_ld, DT) &&
-                     even(a.dy, a.dim, DT) && even(a.dx, a.g_ld, DT) && even(a.dr, a.g_ld, DT) &&
-                     even(a.di, a.g_ld, DT);
+    const bool two = glr_bwd_channels(a, DT) == 2;
     if (a.reset) return two ? bwd_variant<DT, 2, true>(a, s) : bwd_variant<DT, 1, true>(a, s);
     return two ? bwd_variant<DT, 2, false>(a, s) : bwd_variant<DT, 1, false>(a, s);
-}
-
-// Rows of `ld` elements from p on start whole chunks of 4 elements.
-bool fours(const void* p, int64_t ld, int dtype)
-{
-    return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (dtype == 0 ? 16 : 8) == 0;
 }
 
 template <int DT, int VC>
@@ -840,9 +824,7 @@ hipError_t step_vec(const GlrStepArgs& a, hipStream_t s)
 template <int DT>
 hipError_t step_dt(const GlrStepArgs& a, hipStream_t s)
 {
-    const bool four = a.dim % 4 == 0 && fours(a.x, a.x_ld, DT) && fours(a.r, a.r_ld, DT) && fours(a.i, a.i_ld, DT) &&
-                      fours(a.y, a.dim, DT) && fours(a.h, a.dim, 0);
-    return four ? step_vec<DT, 4>(a, s) : step_vec<DT, 1>(a, s);
+    return glr_step_channels(a, DT) == 4 ? step_vec<DT, 4>(a, s) : step_vec<DT, 1>(a, s);
 }
 
 }  // namespace

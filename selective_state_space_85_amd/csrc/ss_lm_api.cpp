@@ -7,6 +7,7 @@
 #include "ss_internal.h"
 #include "ss_lm.h"
 #include "ss_lm_internal.h"
+#include "ss_tiles.h"
 
 namespace {
 
@@ -56,6 +57,9 @@ bool strided_overlap(const void* p, const void* q, int64_t bytes, int64_t row, i
     const int64_t off = static_cast<int64_t>((a < b ? b - a : a - b) % static_cast<uintptr_t>(stride));
     return off < row || off + row > stride;
 }
+
+// Whether a launch fits: HIP takes fewer than 2^32 threads along a grid's axis.
+bool launch_fits(int64_t blocks, int64_t threads) { return blocks <= int64_t(UINT32_MAX) / threads; }
 
 ss_status check_workspace(void* workspace, size_t given, int64_t need, const Range* others, size_t count)
 {
@@ -230,7 +234,10 @@ ss_status ss_glr_fwd(const void* x, int64_t x_row_stride, const void* r, int64_t
     a.seqlen = seqlen;
     a.dim = dim;
     a.n_tiles = w.tiles;
-    return done(ssk::launch_glr_fwd(a, dtype == SS_F32 ? 0 : 1, stream));
+    const int dt = dtype == SS_F32 ? 0 : 1;
+    if (!launch_fits(ssk::glr_blocks(a, ssk::glr_fwd_channels(a, dt), w.tiles), ssk::kGlrFwdThreads))
+        return SS_ERR_UNSUPPORTED;
+    return done(ssk::launch_glr_fwd(a, dt, stream));
 }
 
 ss_status ss_glr_bwd(const void* x, int64_t x_row_stride, const void* r, int64_t r_row_stride, const void* i,
@@ -305,10 +312,6 @@ ss_status ss_glr_bwd(const void* x, int64_t x_row_stride, const void* r, int64_t
     // the kept states: only read from here on when they are the caller's
     a.ckpt = ckpt ? const_cast<float*>(ckpt) : reinterpret_cast<float*>(ws + w.ckpt);
     const int dt = dtype == SS_F32 ? 0 : 1;
-    if (!ckpt) {
-        const hipError_t e = ssk::launch_glr_fwd(a, dt, stream);  // y is null: the states alone
-        if (e != hipSuccess) return done(e);
-    }
     a.dy = dy;
     a.dh_last = dh_last;
     a.dx = dx;
@@ -318,6 +321,13 @@ ss_status ss_glr_bwd(const void* x, int64_t x_row_stride, const void* r, int64_t
     a.dh0 = dh0;
     a.part_decay = reinterpret_cast<float*>(ws + w.part);
     a.ddecay = ddecay;
+    if (!launch_fits(ssk::glr_blocks(a, ssk::glr_bwd_channels(a, dt), w.chunks), ssk::kGlrBwdThreads) ||
+        (!ckpt && !launch_fits(ssk::glr_blocks(a, ssk::glr_fwd_channels(a, dt), w.tiles), ssk::kGlrFwdThreads)))
+        return SS_ERR_UNSUPPORTED;
+    if (!ckpt) {
+        const hipError_t e = ssk::launch_glr_fwd(a, dt, stream);  // y is null: the states alone
+        if (e != hipSuccess) return done(e);
+    }
     return done(ssk::launch_glr_bwd(a, dt, stream));
 }
 
@@ -330,7 +340,6 @@ ss_status ss_glr_step(float* h, const void* x, int64_t x_row_stride, const void*
     if (x_row_stride < dim || r_row_stride < dim || i_row_stride < dim) return SS_ERR_INVALID_ARG;
     if (!isfinite(c) || c <= 0.0f) return SS_ERR_INVALID_ARG;
     if (!known(dtype)) return SS_ERR_UNSUPPORTED;
-    if (ceil_div(dim, 256) > INT32_MAX) return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype);
     const void* elems[] = {x, r, i, y};
     for (const void* p : elems)
@@ -344,7 +353,10 @@ ss_status ss_glr_step(float* h, const void* x, int64_t x_row_stride, const void*
                          span(y, batch * dim * es)};
     if (any_overlap(all + 4, 2, all, 4)) return SS_ERR_INVALID_ARG;
     const ssk::GlrStepArgs a{h, x, r, i, x_row_stride, r_row_stride, i_row_stride, decay, c, y, batch, dim};
-    return done(ssk::launch_glr_step(a, dtype == SS_F32 ? 0 : 1, stream));
+    const int dt = dtype == SS_F32 ? 0 : 1;
+    if (!launch_fits(ceil_div(dim, ssk::kGlrStepThreads * ssk::glr_step_channels(a, dt)), ssk::kGlrStepThreads))
+        return SS_ERR_UNSUPPORTED;
+    return done(ssk::launch_glr_step(a, dt, stream));
 }
 
 }  // extern "C"
@@ -377,6 +389,31 @@ bool mat_grid_ok(int64_t rows, int64_t cols)
 {
     int64_t n;
     return mul(ceil_div(rows, 128), ceil_div(cols, 64), &n) && n <= INT32_MAX / 2;
+}
+
+// The threads of a launch of tiles stay below HIP's limit.  Sizes within mat_grid_ok.
+template <int DT>
+bool tiles_fit(int64_t large, int64_t small, int64_t mini)
+{
+    return ssk::tile_threads(ssk::best_tile<DT>(large, small, mini), large, small, mini) <= int64_t(UINT32_MAX);
+}
+// Two outputs of one launch, each in `parts` (0: not wanted).
+struct TiledOutput {
+    int64_t rows, cols, parts;
+};
+bool tiles_fit(TiledOutput a, TiledOutput b, ss_dtype dtype)
+{
+    auto tiles = [&](int bm, int bn) {
+        return (a.parts ? ssk::count(a.rows, a.cols, bm, bn) * a.parts : 0) +
+               (b.parts ? ssk::count(b.rows, b.cols, bm, bn) * b.parts : 0);
+    };
+    const int64_t large = tiles(256, 256), small = tiles(128, 128), mini = tiles(64, 128);
+    return dtype == SS_F32 ? tiles_fit<0>(large, small, mini) : tiles_fit<1>(large, small, mini);
+}
+// The one-pass gradients' launches.
+bool few_fits(int64_t rows, int64_t dim)
+{
+    return launch_fits(ceil_div(dim, 512), 128) && launch_fits(ceil_div(rows * dim, 256), 256);
 }
 
 // x's checks: its stride and alignment; *pack: it has to be copied to padded rows
@@ -590,6 +627,11 @@ ss_status glu_impl(const void* x, int64_t x_ld, const void* wg, const void* wu, 
     GluLayout w;
     if (!glu_layout(m, k, f, dtype, back, &w)) return SS_ERR_INVALID_ARG;
     if (!mat_grid_ok(m, f) || !mat_grid_ok(m, k) || !mat_grid_ok(2 * w.f_pad, k)) return SS_ERR_UNSUPPORTED;
+    if (w.plan.stream ? !launch_fits(ceil_div(w.f_pad, 16), 256) : !tiles_fit({m, 2 * w.f_pad, 1}, {0, 0, 0}, dtype))
+        return SS_ERR_UNSUPPORTED;
+    if (back && (w.plan.few ? !few_fits(m, k)
+                            : !tiles_fit({m, k, dx ? w.splits : 0}, {2 * w.f_pad, k, dwg ? w.dw_splits : 0}, dtype)))
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype);
     bool pack;
     ss_status st = mat_operand(x, x_ld, k, dtype, &pack);
@@ -671,6 +713,21 @@ ss_status xent_impl(const void* x, int64_t x_ld, const void* weight, const int64
     XentLayout w;
     if (!xent_layout(n, d, v, dtype, back, &w)) return SS_ERR_INVALID_ARG;
     if (!mat_grid_ok(n, v) || !mat_grid_ok(n, d) || !mat_grid_ok(v, d) || n > INT32_MAX) return SS_ERR_UNSUPPORTED;
+    // a piece (the forward's is the whole vocabulary), and the last one
+    const int64_t piece = back ? w.piece : v;
+    const int64_t pieces[] = {piece, v - (ceil_div(v, piece) - 1) * piece};
+    for (const int64_t cols : pieces) {
+        const int64_t width = back ? ceil_div(cols, 16) * 16 : cols;
+        if (w.plan.stream ? !launch_fits(ceil_div(width, ssk::kXentStreamCols), 256)
+                          : !tiles_fit({n, width, 1}, {0, 0, 0}, dtype))
+            return SS_ERR_UNSUPPORTED;
+        if (back && (w.plan.few ? !few_fits(n, d)
+                                : !tiles_fit({n, d, dx ? w.splits : 0}, {cols, d, dw ? w.dw_splits : 0}, dtype)))
+            return SS_ERR_UNSUPPORTED;
+    }
+    // the lists of targets; the forward's join
+    if (back ? dw && !launch_fits(ceil_div(v, ssk::kXentCols), 256) : !launch_fits(ceil_div(n, n >= 4096 ? 16 : 2), 256))
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype);
     bool pack;
     ss_status st = mat_operand(x, x_ld, d, dtype, &pack);

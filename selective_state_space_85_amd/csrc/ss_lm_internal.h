@@ -176,6 +176,36 @@ struct GlrArgs {
     float* ddecay;         // (dim,)
 };
 
+// Rows of `ld` elements from p on start whole groups of n (2 or 4) elements.
+inline bool whole_groups(const void* p, int64_t ld, int dtype, int n)
+{
+    return p == nullptr || (ld % n == 0 && reinterpret_cast<uintptr_t>(p) % uintptr_t((dtype == 0 ? 4 : 2) * n) == 0);
+}
+// Channels per lane, two where every row of every operand allows it: the forward's, the backward's.
+inline int glr_fwd_channels(const GlrArgs& a, int dtype)
+{
+    return a.dim % 2 == 0 && whole_groups(a.x, a.x_ld, dtype, 2) && whole_groups(a.r, a.r_ld, dtype, 2) &&
+                   whole_groups(a.i, a.i_ld, dtype, 2) && whole_groups(a.y, a.dim, dtype, 2)
+               ? 2
+               : 1;
+}
+inline int glr_bwd_channels(const GlrArgs& a, int dtype)
+{
+    return a.dim % 2 == 0 && whole_groups(a.x, a.x_ld, dtype, 2) && whole_groups(a.r, a.r_ld, dtype, 2) &&
+                   whole_groups(a.i, a.i_ld, dtype, 2) && whole_groups(a.dy, a.dim, dtype, 2) &&
+                   whole_groups(a.dx, a.g_ld, dtype, 2) && whole_groups(a.dr, a.g_ld, dtype, 2) &&
+                   whole_groups(a.di, a.g_ld, dtype, 2)
+               ? 2
+               : 1;
+}
+// Workgroups of a launch over `spans` tiles or chunks of rows, with that many channels per lane (32 lanes).
+inline int64_t glr_blocks(const GlrArgs& a, int channels, int64_t spans)
+{
+    return (a.dim + 32 * channels - 1) / (32 * channels) * a.batch * spans;
+}
+// Their threads.
+constexpr int kGlrFwdThreads = 512, kGlrBwdThreads = 256;
+
 hipError_t launch_glr_fwd(const GlrArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_glr_bwd(const GlrArgs& a, int dtype, hipStream_t stream);
 
@@ -190,6 +220,16 @@ struct GlrStepArgs {
     void* y;
     int64_t batch, dim;
 };
+// Channels per thread of the step, and its threads.
+inline int glr_step_channels(const GlrStepArgs& a, int dtype)
+{
+    return whole_groups(a.x, a.x_ld, dtype, 4) && whole_groups(a.r, a.r_ld, dtype, 4) &&
+                   whole_groups(a.i, a.i_ld, dtype, 4) && whole_groups(a.y, a.dim, dtype, 4) &&
+                   whole_groups(a.h, a.dim, 0, 4)
+               ? 4
+               : 1;
+}
+constexpr int kGlrStepThreads = 256;
 hipError_t launch_glr_step(const GlrStepArgs& a, int dtype, hipStream_t stream);
 
 }  // namespace ssk

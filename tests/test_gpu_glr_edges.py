@@ -95,3 +95,19 @@ def test_lengths(case):
     for n in ref:
         check(n, host64(g[n]), ref[n], TOL["f32"] if n in ("ddecay", "dh0") else TOL[dt])
         assert torch.equal(g2[n], g[n]), n
+
+
+def test_the_largest_launch():
+    """As many sequences as one launch takes (2^32 threads less one workgroup's), and one more refused."""
+    b, d = (1 << 23) - 1, 2
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    say("glr largest launch")
+    x, r, i = ((torch.randn((b + 1, 1, d), generator=gen, device="cuda")).bfloat16() for _ in range(3))
+    decay = torch.tensor([-2.0, 0.5], device="cuda")
+    y = ss().glr_fwd(x[:b], r[:b], i[:b], decay)
+    h = torch.zeros((b, d), device="cuda")
+    ys = ss().glr_step(h, x[:b, 0], r[:b, 0], i[:b, 0], decay)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, 0], ys)
+    with pytest.raises(ss().SSError, match="UNSUPPORTED"):
+        ss().glr_fwd(x, r, i, decay)
