@@ -206,8 +206,10 @@ ss_status ss_glr_fwd(const void* x, int64_t x_row_stride, const void* r, int64_t
     const Range all[] = {span(x, xb), span(r, rb), span(i, ib), span(decay, dim * 4), span(reset, rows),
                          span(h0, state), span(y, rows * dim * es),
                          span(ckpt, static_cast<int64_t>(ss_glr_ckpt_bytes(batch, seqlen, dim))),
-                         span(h_last == h0 ? nullptr : h_last, state)};
-    if (any_overlap(all + 6, 3, all, 6)) return SS_ERR_INVALID_ARG;
+                         span(h_last, state)};
+    if (any_overlap(all + 6, 3, all, 5)) return SS_ERR_INVALID_ARG;
+    for (int k = 6; k < 9; ++k)  // h_last may be h0 itself
+        if (overlap(all[k], all[5]) && !(k == 8 && h_last == h0)) return SS_ERR_INVALID_ARG;
     const ss_status st = check_workspace(workspace, workspace_bytes, w.total, all, 9);
     if (st != SS_OK) return st;
 
