@@ -161,8 +161,8 @@ __device__ __forceinline__ float sigmoid2(float v, float* rest)
 }
 
 // a = exp(-k s) and w = 1 - a^2 = 1 - e^-t, t = 2 k s.  Below t = 1/2 a polynomial of
-// (1 - e^-t) / t (degree 4, a weighted least-squares fit of relative error below 1e-7 once
-// rounded), above it 1 - a^2 itself (a^2 < 0.61: no cancellation).
+// (1 - e^-t) / t (degree 4, a weighted least-squares fit: 1.04e-7 off at most, 1.6e-7 with every
+// step rounded, and w within 2.0e-7), above it 1 - a^2 itself (a^2 < 0.61: no cancellation).
 __device__ __forceinline__ void decay_of(float k, float s, float* a, float* w)
 {
     *a = exp2_hw((-kLog2e * k) * s);
