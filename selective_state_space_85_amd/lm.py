@@ -22,11 +22,15 @@ def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _dtype(t: torch.Tensor) -> int:
-    dt = _DTYPES.get(t.dtype)
+def _code(dtype: torch.dtype) -> int:
+    dt = _DTYPES.get(dtype)
     if dt is None:
-        raise TypeError("unsupported dtype %s" % t.dtype)
+        raise TypeError("unsupported dtype %s" % dtype)
     return dt
+
+
+def _dtype(t: torch.Tensor) -> int:
+    return _code(t.dtype)
 
 
 def _need(t: torch.Tensor, name: str, shape, dtype, device) -> None:
@@ -247,12 +251,12 @@ def glr_step(h: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: torch.Tensor,
 
 def glu_workspace_bytes(tokens: int, dim: int, features: int, dtype: torch.dtype) -> int:
     """Workspace of ``ss_glu_fwd`` (0: none needed)."""
-    return _size(_lm.load().ss_glu_workspace_bytes(tokens, dim, features, _DTYPES[dtype]))
+    return _size(_lm.load().ss_glu_workspace_bytes(tokens, dim, features, _code(dtype)))
 
 
 def glu_bwd_workspace_bytes(tokens: int, dim: int, features: int, dtype: torch.dtype) -> int:
     """Workspace of ``ss_glu_bwd``."""
-    return _size(_lm.load().ss_glu_bwd_workspace_bytes(tokens, dim, features, _DTYPES[dtype]))
+    return _size(_lm.load().ss_glu_bwd_workspace_bytes(tokens, dim, features, _code(dtype)))
 
 
 def _tokens(x: torch.Tensor, fn: str) -> Tuple[int, int, int]:
@@ -326,12 +330,12 @@ def glu_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dh: torch
 
 def xent_workspace_bytes(tokens: int, dim: int, vocab: int, dtype: torch.dtype) -> int:
     """Workspace of ``ss_xent_fwd``."""
-    return _size(_lm.load().ss_xent_workspace_bytes(tokens, dim, vocab, _DTYPES[dtype]))
+    return _size(_lm.load().ss_xent_workspace_bytes(tokens, dim, vocab, _code(dtype)))
 
 
 def xent_bwd_workspace_bytes(tokens: int, dim: int, vocab: int, dtype: torch.dtype) -> int:
     """Workspace of ``ss_xent_bwd``."""
-    return _size(_lm.load().ss_xent_bwd_workspace_bytes(tokens, dim, vocab, _DTYPES[dtype]))
+    return _size(_lm.load().ss_xent_bwd_workspace_bytes(tokens, dim, vocab, _code(dtype)))
 
 
 def xent_fwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, *, ignore_index: int = -100,
