@@ -138,7 +138,8 @@ ss_status ss_glu_bwd(const void* x, int64_t x_row_stride, const void* w_gate, co
  *   lse[i]  = log(sum_j exp(l[i,j]))
  *   loss[i] = lse[i] - l[i, target[i]]
  * without storing the logits.  A row whose target equals ignore_index, or lies
- * outside [0, vocab), has loss 0 and no gradient.
+ * outside [0, vocab), has loss 0 and no gradient: dx is 0 there and nothing of
+ * its x or dloss, whatever they hold, enters dw.
  *
  *   x      : (tokens, dim) dtype, rows x_row_stride elements apart
  *   w      : (vocab, dim) dtype

@@ -57,6 +57,13 @@ __device__ __forceinline__ void put4(typename MM<DT>::T* p, int64_t left, const 
     }
 }
 
+__device__ __forceinline__ bool row_counts(const FewGradArgs& a, int64_t i)
+{
+    if (!a.target) return true;
+    const int64_t t = a.target[i];
+    return t != a.ignore_index && t >= 0 && t < a.rows;
+}
+
 template <int DT, int MR, bool DX, bool DW>
 __global__ __launch_bounds__(kFewThreads) void few_grad_kernel(FewGradArgs a)
 {
@@ -69,7 +76,7 @@ __global__ __launch_bounds__(kFewThreads) void few_grad_kernel(FewGradArgs a)
     for (int i = 0; i < MR; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[i][e] = sum[i][e] = 0.0f;
-        if (DW && i < a.m && left > 0) get4<DT>(static_cast<const T*>(a.x) + i * a.x_ld + c, left, x[i]);
+        if (DW && i < a.m && left > 0 && row_counts(a, i)) get4<DT>(static_cast<const T*>(a.x) + i * a.x_ld + c, left, x[i]);
     }
     for (int64_t rb = r0; rb < r1; rb += kFewTile) {
         __syncthreads();
@@ -128,7 +135,7 @@ __global__ __launch_bounds__(256) void few_sum_kernel(FewGradArgs a)
     float s = 0.0f;
 #pragma unroll 8
     for (int64_t p = 0; p < a.parts; ++p) s += a.part[p * n + i];
-    static_cast<typename MM<DT>::T*>(a.dx)[i] = MM<DT>::narrow(s);
+    static_cast<typename MM<DT>::T*>(a.dx)[i] = MM<DT>::narrow(row_counts(a, i / a.k) ? s : 0.0f);
 }
 
 template <int DT, int MR>

@@ -278,6 +278,20 @@ __device__ __forceinline__ void mm_mul(const typename MM<G::DT>::Frag (&a)[G::FM
     }
 }
 
+// Whether the thread's sums are neither infinite nor NaN.
+template <class G>
+__device__ __forceinline__ bool all_finite(const f32x4 (&acc)[G::FM][G::FN])
+{
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) finite = finite && fabsf(acc[i][j][e]) < __builtin_inff();
+    return finite;
+}
+
 // acc += A B^T over the k tile in a_tile and b_tile, for the wave at (wm, wn).
 template <class G>
 __device__ __forceinline__ void mm_step(const char* a_tile, const char* b_tile, int wm, int wn, int lane, f32x4 (&acc)[G::FM][G::FN])
@@ -547,7 +561,8 @@ __device__ __forceinline__ bf16x8 staged_frag(const char* part, int r0, int lane
 // 2048 -> 2 x 2048: 1387 -> 1393 us; 777, 1001 -> 2 x 2731: 340 -> 347), the rest such tiles alone.
 // Prob: a_at(row, k) / b_at(row, k), the address of an element, rows past the end clamped to the last;
 // a_cols() / b_cols(), for MC operands the columns that exist from the tile's first on; a_ld() / b_ld(),
-// their elements per k; a_off, b_off (in bytes), valid, tiles, finish as for mm_tile.
+// their elements per k; a_off, b_off (in bytes), valid, tiles, finish as for mm_tile; kSkips, and where
+// that is true skips(t, k): rows k of k tile t of B that tiles formed again leave out.
 template <class G, class Prob>
 __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
 {
@@ -615,14 +630,7 @@ __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
         }
     }
     if (p.tiles > 0) {
-        bool finite = true;
-#pragma unroll
-        for (int i = 0; i < G::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < G::FN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) finite = finite && fabsf(acc[i][j][e]) < __builtin_inff();
-        if (!finite) odd = 1;
+        if (!all_finite<G>(acc)) odd = 1;
         __syncthreads();
         if (odd) {
             // formed anew: kept through the loop above, the addresses would cost its registers
@@ -637,6 +645,19 @@ __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
                 for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             for (int t = 0; t < p.tiles; ++t) {
                 load(t);
+                if constexpr (Prob::kSkips) {
+                    static_assert(G::B_MC, "k of B are rows that may be left out");
+                    const int exist = p.valid(t);
+#pragma unroll
+                    for (int i = 0; i < SB::N; ++i) {
+                        int col, chunk;
+                        SB::place(i, tid, &col, &chunk);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (SB::has(i, tid) && chunk * 8 + e < exist && p.skips(t, chunk * 8 + e))
+                                sb.v[i][2 * e] = sb.v[i][2 * e + 1] = 0.0f;
+                    }
+                }
                 __syncthreads();
                 sa.store_whole(wa, tid);
                 sb.store_whole(wb, tid);

@@ -174,6 +174,7 @@ struct GluProb {
     __device__ int64_t b_cols() const { return 0; }
     __device__ int64_t a_ld() const { return 0; }
     __device__ int64_t b_ld() const { return 0; }
+    static constexpr bool kSkips = false;
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -261,6 +262,7 @@ struct GluDxProb {
     __device__ int64_t b_cols() const { return a.k - n0; }
     __device__ int64_t a_ld() const { return 0; }
     __device__ int64_t b_ld() const { return a.w_ld; }
+    static constexpr bool kSkips = false;
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -328,6 +330,7 @@ struct GluDwProb {
     __device__ int64_t b_cols() const { return a.k - n0; }
     __device__ int64_t a_ld() const { return 2 * a.f_pad; }
     __device__ int64_t b_ld() const { return a.x_ld; }
+    static constexpr bool kSkips = false;
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -569,7 +572,7 @@ hipError_t glu_bwd_dt(const GluArgs& a, hipStream_t s)
     if (e != hipSuccess) return e;
     if (a.few)
         return launch_few_grad({static_cast<const float*>(a.dgu), 2 * a.f_pad, a.f_pad, a.wg_raw, a.wu_raw, a.dwg, a.dwu,
-                                a.x_raw, a.x_raw_ld, a.dx_part, a.dx, a.f, 2 * a.f, a.m, a.k, a.dx_per, a.dx_splits},
+                                a.x_raw, a.x_raw_ld, a.dx_part, a.dx, a.f, 2 * a.f, a.m, a.k, a.dx_per, a.dx_splits, nullptr, 0},
                                DT, s);
     auto tiles = [&](int bm, int bn) {
         return (a.dx ? count(a.m, a.k, bm, bn) * a.dx_splits : 0) + (a.dwg ? count(2 * a.f_pad, a.k, bm, bn) * a.dw_splits : 0);

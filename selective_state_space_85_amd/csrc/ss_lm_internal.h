@@ -30,6 +30,10 @@ struct FewGradArgs {
     void* dx;         // (m, k)
     int64_t first, rows, m, k;
     int64_t per, parts;  // rows per part of the sums of dx
+    // null, or (m,): rows whose target is ignore_index or outside [0, rows) have s = 0, their dx is
+    // 0 and nothing of their x enters dW
+    const int64_t* target;
+    int64_t ignore_index;
 };
 hipError_t launch_few_grad(const FewGradArgs& a, int dtype, hipStream_t stream);
 

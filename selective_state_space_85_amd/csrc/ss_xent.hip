@@ -19,7 +19,9 @@
 // gets it times the target's row of w in the epilogue, and a dw tile takes one more k tile
 // (per BK tokens whose targets lie in it) of these remainders against those tokens' rows of x.
 //
-// A row whose target is ignore_index, or lies outside [0, v), has loss 0 and no gradient.
+// A row whose target is ignore_index, or lies outside [0, v), has loss 0 and no gradient, whatever
+// it holds: its dl is 0, its dx is set to 0 (0 times an infinite weight is NaN), and a dw tile whose
+// sums are not all finite is formed again without such rows (0 times a NaN of theirs).
 #include "ss_gemm.h"
 #include "ss_lm_internal.h"
 
@@ -60,6 +62,7 @@ struct XentLogits {
     __device__ int64_t b_cols() const { return 0; }
     __device__ int64_t a_ld() const { return 0; }
     __device__ int64_t b_ld() const { return 0; }
+    static constexpr bool kSkips = false;
 };
 
 // ---- forward -------------------------------------------------------------------------------
@@ -402,6 +405,7 @@ struct XentDxProb {
     __device__ int64_t b_cols() const { return a.d - n0; }
     __device__ int64_t a_ld() const { return 0; }
     __device__ int64_t b_ld() const { return a.w_ld; }
+    static constexpr bool kSkips = false;
 
     template <class G>
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char*, int wm, int wn, int lane) const
@@ -411,7 +415,7 @@ struct XentDxProb {
             const int64_t m = m0 + (wm * G::FM + i) * 16 + (lane & 15);
             if (m >= a.n) continue;
             const int64_t t = a.target[m];
-            const bool add = DT == 1 && last && live_target(t, a);
+            const bool live = live_target(t, a), add = DT == 1 && last && live;
             const float lo = add ? a.lo[m] : 0.0f;
             const T* const wt = static_cast<const T*>(a.w) + (add ? t : 0) * a.w_ld;
 #pragma unroll
@@ -424,7 +428,7 @@ struct XentDxProb {
                     if (!first) v += acc_to[m * a.d + c + e];
                     if (add) v = fmaf(lo, MM<DT>::widen(wt[c + e]), v);
                     if (last)
-                        static_cast<T*>(a.dx)[m * a.d + c + e] = MM<DT>::narrow(v);
+                        static_cast<T*>(a.dx)[m * a.d + c + e] = MM<DT>::narrow(live ? v : 0.0f);
                     else
                         acc_to[m * a.d + c + e] = v;
                 }
@@ -475,6 +479,49 @@ struct XentDwProb {
     __device__ int64_t b_cols() const { return a.d - n0; }
     __device__ int64_t a_ld() const { return pad; }
     __device__ int64_t b_ld() const { return a.x_ld; }
+    // tiles formed again leave out the rows of x without a target
+    static constexpr bool kSkips = true;
+    __device__ bool skips(int t, int k) const { return !live_target(a.target[int64_t(t + first) * BK + k], a); }
+
+    // bf16: a tile whose sums are not all finite, again
+    template <class G>
+    __device__ void again(f32x4 (&acc)[G::FM][G::FN], char* lds, int wm, int wn, int lane) const
+    {
+        const int tid = threadIdx.x;
+        int* const odd = reinterpret_cast<int*>(lds);
+        __syncthreads();  // every wave has read its last operands
+        if (tid == 0) *odd = 0;
+        __syncthreads();
+        if (!all_finite<G>(acc)) *odd = 1;
+        __syncthreads();
+        if (!*odd) return;
+        char* const a_dst = lds + (G::A_PARTS > 1 ? wm * (G::A_PART * 128) + wn * 1024 : (tid >> 6) * 1024);
+        char* const b_dst = lds + 2 * G::A_BYTES + (tid >> 6) * 1024;
+        const char* const zero = reinterpret_cast<const char*>(g_zero_chunk);
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            const int exist = valid(t);
+            __syncthreads();  // the last tile's readers are done
+            int col, k;
+#pragma unroll
+            for (int i = 0; i < G::NA; ++i) {
+                a_place<G>(i, tid, &col, &k);
+                load_to_lds(k < exist ? a_chunk(col, k) + a_off(t) : zero, a_dst + i * (G::A_NT * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < G::NB; ++i) {
+                b_place<G>(i, tid, &col, &k);
+                load_to_lds(k < exist && !skips(t, k) ? b_chunk(col, k) + b_off(t) : zero, b_dst + i * (G::NT * 16));
+            }
+            wait_loads<0>();
+            __syncthreads();
+            mm_step<G>(lds, lds + 2 * G::A_BYTES, wm, wn, lane, acc);
+        }
+    }
 
     // the target entries' remainders
     template <class G>
@@ -519,6 +566,7 @@ struct XentDwProb {
     __device__ void finish(f32x4 (&acc)[G::FM][G::FN], char* lds, int wm, int wn, int lane) const
     {
         if constexpr (DT == 1) {
+            again<G>(acc, lds, wm, wn, lane);
             if (first == 0) remainders<G>(acc, lds, wm, wn, lane);  // by the first part
         }
 #pragma unroll
@@ -620,7 +668,9 @@ __global__ __launch_bounds__(256) void xent_dx_sum_kernel(XentArgs a)
 #pragma unroll 8
         for (int64_t p = 0; p < a.dx_splits; ++p) s += a.dx_acc[p * n + i];
         const int64_t row = i / a.d, t = a.target[row];
-        if (DT == 1 && live_target(t, a))
+        if (!live_target(t, a))
+            s = 0.0f;
+        else if (DT == 1)
             s = fmaf(a.lo[row], MM<DT>::widen(static_cast<const T*>(a.w)[t * a.w_ld + i % a.d]), s);
         static_cast<T*>(a.dx)[i] = MM<DT>::narrow(s);
     }
@@ -760,7 +810,8 @@ hipError_t bwd_dt(const XentArgs& a, hipStream_t s)
         const hipError_t e = dl_tiles_dt<DT>(a, 0, a.v, pad, s);
         if (e != hipSuccess) return e;
         return launch_few_grad({static_cast<const float*>(a.dl), pad, 0, a.w_raw, nullptr, a.dw, nullptr, a.x_raw,
-                                a.x_raw_ld, a.dx ? a.dx_acc : nullptr, a.dx, a.v, a.v, a.n, a.d, a.dx_per, a.dx_splits},
+                                a.x_raw_ld, a.dx ? a.dx_acc : nullptr, a.dx, a.v, a.v, a.n, a.d, a.dx_per, a.dx_splits,
+                                a.target, a.ignore_index},
                                DT, s);
     }
     if (DT == 1 && a.dw) {
