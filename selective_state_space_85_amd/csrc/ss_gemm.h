@@ -278,18 +278,18 @@ __device__ __forceinline__ void mm_mul(const typename MM<G::DT>::Frag (&a)[G::FM
     }
 }
 
-// Whether the thread's sums are neither infinite nor NaN.
+// Whether the thread's sums are neither infinite nor NaN: 0 times each is 0.
 template <class G>
 __device__ __forceinline__ bool all_finite(const f32x4 (&acc)[G::FM][G::FN])
 {
-    bool finite = true;
+    float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
 #pragma unroll
         for (int j = 0; j < G::FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) finite = finite && fabsf(acc[i][j][e]) < __builtin_inff();
-    return finite;
+            for (int e = 0; e < 4; ++e) zero[e] = fmaf(acc[i][j][e], 0.0f, zero[e]);
+    return zero[0] + zero[1] + zero[2] + zero[3] == 0.0f;
 }
 
 // acc += A B^T over the k tile in a_tile and b_tile, for the wave at (wm, wn).
@@ -557,8 +557,8 @@ __device__ __forceinline__ bf16x8 staged_frag(const char* part, int r0, int lane
 // once per workgroup; the next k tile's loads are in flight while this one's products are formed.
 // A tile whose sums are not all finite is formed again, by the fp32 instruction from the elements
 // themselves: an infinity, or a number that bf16 rounds to one, makes all that it takes part in NaN
-// above, where infinite or finite results may be due.  The check costs 0.5 to 2.5% of a pass (4096 tokens,
-// 2048 -> 2 x 2048: 1387 -> 1393 us; 777, 1001 -> 2 x 2731: 340 -> 347), the rest such tiles alone.
+// above, where infinite or finite results may be due.  The check costs up to 1% of a pass (894 tokens,
+// 2560 -> 2 x 1600: 463 -> 465 us; 777, 1001 -> 2 x 2731: 339 -> 343), the rest such tiles alone.
 // Prob: a_at(row, k) / b_at(row, k), the address of an element, rows past the end clamped to the last;
 // a_cols() / b_cols(), for MC operands the columns that exist from the tile's first on; a_ld() / b_ld(),
 // their elements per k; a_off, b_off (in bytes), valid, tiles, finish as for mm_tile; kSkips, and where
@@ -632,7 +632,7 @@ __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
     if (p.tiles > 0) {
         if (!all_finite<G>(acc)) odd = 1;
         __syncthreads();
-        if (odd) {
+        if (__builtin_expect(odd, 0)) {
             // formed anew: kept through the loop above, the addresses would cost its registers
             int thread = tid;
             asm volatile("" : "+v"(thread));
