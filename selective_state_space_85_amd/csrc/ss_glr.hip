@@ -12,9 +12,10 @@
 // is published, the state entering the tile is found from the tiles before it (see `look_back`), and
 // every run replays its rows from the state that enters it.  The operands are read once and y is
 // written once: HBM traffic bounds it (bf16: 8 bytes per element, 33 vector instructions).
-// (1, 131072, 2048) bf16: 432 us, 4.96 TB/s, as much as a copy of 1 GiB reaches (4.8);
-// (8, 2048, 5120) with kept states: 144 us; (3, 1021, 1533) fp32 with resets: 26 us.  In two passes
-// over r and x (chunks' maps, then their states) the first took 840.
+// (1, 131072, 2048) bf16: 435 us, 4.94 TB/s, as much as a copy of 1 GiB reaches (4.8);
+// (8, 2048, 5120) with kept states: 144 us; (3, 1021, 1533) fp32 with resets, one channel per lane: 26 us
+// for 16 at a copy's rate, its 576 workgroups on 512 places.  In two passes over r and x (chunks' maps,
+// then their states) the first took 840.
 //
 // Backward.  g_t = dL/dh_t = dy_t + a_{t+1} g_{t+1}: the same maps from the end.  q_t = a_t g_t runs
 // backward as q -> a (q + dy), so a run's product of a serves both directions.  A workgroup of 4
@@ -23,7 +24,7 @@
 // way.)  With few (batch row, channel block) pairs the rows are split in chunks: a first pass over
 // r and dy forms each chunk's composed map of q.  (8, 2048, 5120) bf16, 14 bytes per element: 296 us,
 // 4.1 TB/s: every tile waits on the one before it, which three workgroups per CU do not hide
-// quite.  (3, 1021, 1533) fp32 with resets, cut in chunks of 128 rows: 14 + 38 us.
+// quite.  (3, 1021, 1533) fp32 with resets, cut in 7 chunks of 160 rows: 14 + 38 us.
 //
 // 1 - a^2 = -expm1(-2 k s) is formed without cancellation: as a gate closes a tends to 1 and
 // the plain difference would lose every digit.
@@ -118,7 +119,8 @@ constexpr uint32_t elem_bytes = DT == 0 ? 4 : 2;
 
 // The rows of one tile of an operand: row q of this lane's run is a scalar offset away from the
 // lane's own.  Rows past the chunk's end and lanes past the last channel fall to the range
-// check: their loads read 0 and their stores are dropped.  The host keeps a tile below 2^31 bytes.
+// check, which counts the scalar offset with the lane's (a raw buffer's does on gfx9): their loads
+// read 0 and their stores are dropped.  The host keeps a tile below 2^31 bytes.
 template <int DT, int VC>
 struct Rows {
     using RW = Row<DT, VC>;

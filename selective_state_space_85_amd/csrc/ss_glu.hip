@@ -8,14 +8,16 @@
 // each wave column, so that one wave holds g and u of the same elements in its accumulators
 // and the product never leaves the registers; g and u are not stored.
 // Backward: the same product again with dh in the epilogue gives dg and du (rounded once to
-// the operands' type, as the next product's operands must be; of a few bf16 tokens what the
-// rounding leaves is kept too, see kGluLoRows), side by side in one (m, 2 f) workspace matrix;
+// the operands' type, as the next product's operands must be: of bf16 gradients 0.00235 of their root
+// mean square is off for 0.00166 by their own rounding alone, where products of the remainders too
+// would double the gradients' time; of a few bf16 tokens what the rounding leaves is kept for the
+// weights' gradients, see kGluLoRows), side by side in one (m, 2 f) workspace matrix;
 // the second launch holds the tiles of dx (contraction over the 2 f columns of that matrix
 // against the rows of Wg, then of Wu) and those of dWg and dWu (its transpose against x)
 // together, so that one set's last tiles run beside the other's first.
 // All three are bound by the matrix cores at training sizes (k = 2560, f = 6912, bf16, silu):
 // forward, 4096 tokens 228 us, 16384 tokens 935 us (1270 and 1240 TFLOP/s); backward, 16384 tokens
-// 1080 us for dg and du again and 2.12 ms for the gradients (1070 and 1090 TFLOP/s).  Keeping g and
+// 1090 us for dg and du again and 2.12 ms for the gradients (1060 and 1090 TFLOP/s).  Keeping g and
 // u would spare the 1.08 ms and take 4 m f bytes for each layer (453 MB here).
 // Few tokens: the weights stream past them (see ss_gemm.h); one token 13.5 us, 5.2 TB/s.
 #include "ss_gemm.h"

@@ -90,7 +90,9 @@ constexpr int64_t kGlrCols = 64;  // channels per workgroup
 // cut until there are kGlrTarget workgroups, in chunks of at least kGlrMinChunk rows (the cut
 // costs a pass over r and dy) and at most kGlrMaxChunks of them (a chunk joins the maps of those
 // after it itself).  Both passes, whole and cut: (1, 16384, 2048) bf16 900 and 201 us, (4, 2048, 2560)
-// 160 and 134, (3, 1021, 1533) fp32 81 and 84; with twice as many chunks 214, 126 and 86.
+// 160 and 134, (3, 1021, 1533) fp32 81 and 84; with twice as many chunks 214, 126 and 86.  These have
+// 32, 160 and 72 workgroups; between 256 and 768, where whole rows leave some CUs a workgroup short
+// of three, nothing was measured.  Kernels of one channel per lane have twice the workgroups counted.
 constexpr int64_t kGlrWhole = 256, kGlrTarget = 768, kGlrMinChunk = 128, kGlrMaxChunks = 64;
 
 void glr_plan(int64_t batch, int64_t seqlen, int64_t dim, int64_t* len, int64_t* chunks)
@@ -458,6 +460,7 @@ struct RowsPlan {
 //   bf16,   43 tiles:  1 row 10 19, 64 rows 18 26;   108: 1 row 14 27, 32 rows 21 27, 64 rows 31 27;
 //          216 tiles:  8 rows 28 29, 16 rows 32 29;  313: 1 row 33 31;   432: 1 row 53 47, 16 rows 72 48;
 //   fp32, 108 tiles: 64 rows 73 103;  216: 32 rows 97 114, 64 rows 162 115;  432: 16 rows 160 170.
+// At other k the times' proportions may differ.
 // bf16 rows that are not whole 16-byte chunks would need padded copies of the weights for tiles, and
 // are always streamed.
 // The gradients in one pass save a second reading of the weights (and padded copies), at 2 m
@@ -487,6 +490,8 @@ RowsPlan rows_plan(int64_t rows, int64_t dim, int64_t cols, ss_dtype dtype, bool
 
 // Parts of dx when few: enough ranges of the weights' rows for eight workgroups (of 512 columns) per
 // CU, of at least 8 rows, and few enough that the parts stay a quarter of the weights' size, or small.
+// A narrow x has up to 2048 of them, which few_sum_kernel adds by one thread per element: 2 rows, 276
+// wide, against 65098 weight rows, loss and gradients, take 147 us for 15 at a copy's rate.
 void few_parts(int64_t m, int64_t k, int64_t rows, ss_dtype dtype, int64_t* per, int64_t* parts)
 {
     constexpr int64_t kSmall = int64_t(8) << 20;

@@ -17,7 +17,10 @@
 // bf16: a row's target entry of dl, (p - 1) dloss, is far larger than its others, and what
 // rounding takes from it would be the largest error of both gradients.  It is kept aside: dx
 // gets it times the target's row of w in the epilogue, and a dw tile takes one more k tile
-// (per BK tokens whose targets lie in it) of these remainders against those tokens' rows of x.
+// (per BK tokens whose targets lie in it) of these remainders against those tokens' rows of x.  The
+// other entries' rounding does not show beside the outputs' own: 0.00166 of their root mean square
+// either way.  Where most targets are the same few entries, their tiles of dw take that many more
+// k tiles, unpipelined, and end the launch later; times here are of targets spread evenly.
 //
 // A row whose target is ignore_index, or lies outside [0, v), has loss 0 and no gradient, whatever
 // it holds: its dl is 0, its dx is set to 0 (0 times an infinite weight is NaN), and a dw tile whose

@@ -1,7 +1,9 @@
 """torch-facing wrappers of the language-model operators (include/ss_lm.h): argument marshalling only.
 
 Names and argument order follow the C entry points (``ss_glr_fwd`` -> ``glr_fwd``).  Every
-operator runs in the HIP kernels of libssscan.so on torch's current stream.
+operator runs in the HIP kernels of libssscan.so on torch's current stream.  As with the scan, the
+results carry no autograd graph, also of tensors that require gradients: a forward and its backward
+are joined in a ``torch.autograd.Function``, as ``examples/recurrent_lm.py`` does.
 """
 from __future__ import annotations
 
