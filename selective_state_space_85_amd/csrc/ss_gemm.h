@@ -555,10 +555,12 @@ __device__ __forceinline__ bf16x8 staged_frag(const char* part, int r0, int lane
 
 // One workgroup's tile of an fp32 product.  Elements pass through registers, where each is split
 // once per workgroup; the next k tile's loads are in flight while this one's products are formed.
-// A tile whose sums are not all finite is formed again, by the fp32 instruction from the elements
+// Sums that are not finite are formed again, by the fp32 instruction from the elements
 // themselves: an infinity, or a number that bf16 rounds to one, makes all that it takes part in NaN
 // above, where infinite or finite results may be due.  The check costs up to 1% of a pass (894 tokens,
-// 2560 -> 2 x 1600: 463 -> 465 us; 777, 1001 -> 2 x 2731: 339 -> 343), the rest such tiles alone.
+// 2560 -> 2 x 1600: 461 -> 462 us; 777, 1001 -> 2 x 2731: 338 -> 341), the rest such tiles alone: the loss
+// of 333 tokens of 50257 entries takes 1.34 ms for 0.19 with every second entry at the type's lowest value,
+// and 0.19 with them at -1e30.
 // Prob: a_at(row, k) / b_at(row, k), the address of an element, rows past the end clamped to the last;
 // a_cols() / b_cols(), for MC operands the columns that exist from the tile's first on; a_ld() / b_ld(),
 // their elements per k; a_off, b_off (in bytes), valid, tiles, finish as for mm_tile; kSkips, and where
@@ -639,40 +641,48 @@ __device__ __forceinline__ void mm_tile_f32(const Prob& p, char* lds)
             set(thread);
             float* const wa = reinterpret_cast<float*>(lds);
             float* const wb = wa + G::BM * 32;
+            // a row of fragments at a time, and finite sums stay as they are: they do not depend on what
+            // shares their tile
 #pragma unroll
-            for (int i = 0; i < G::FM; ++i)
+            for (int i = 0; i < G::FM; ++i) {
+                f32x4 whole[G::FN];
 #pragma unroll
-                for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            for (int t = 0; t < p.tiles; ++t) {
-                load(t);
-                if constexpr (Prob::kSkips) {
-                    static_assert(G::B_MC, "k of B are rows that may be left out");
-                    const int exist = p.valid(t);
-#pragma unroll
-                    for (int i = 0; i < SB::N; ++i) {
-                        int col, chunk;
-                        SB::place(i, tid, &col, &chunk);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (SB::has(i, tid) && chunk * 8 + e < exist && p.skips(t, chunk * 8 + e))
-                                sb.v[i][2 * e] = sb.v[i][2 * e + 1] = 0.0f;
-                    }
-                }
-                __syncthreads();
-                sa.store_whole(wa, tid);
-                sb.store_whole(wb, tid);
-                __syncthreads();
+                for (int j = 0; j < G::FN; ++j) whole[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-                for (int e = 0; e < 8; ++e) {
-                    // element e of a lane's 8 is the same k on both sides
-                    const int from = (lane & 15) * 32 + (lane >> 4) * 8 + e;
+                for (int t = 0; t < p.tiles; ++t) {
+                    load(t);
+                    if constexpr (Prob::kSkips) {
+                        static_assert(G::B_MC, "k of B are rows that may be left out");
+                        const int exist = p.valid(t);
 #pragma unroll
-                    for (int i = 0; i < G::FM; ++i)
+                        for (int n = 0; n < SB::N; ++n) {
+                            int col, chunk;
+                            SB::place(n, tid, &col, &chunk);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (SB::has(n, tid) && chunk * 8 + e < exist && p.skips(t, chunk * 8 + e))
+                                    sb.v[n][2 * e] = sb.v[n][2 * e + 1] = 0.0f;
+                        }
+                    }
+                    __syncthreads();
+                    sa.store_whole(wa, tid);
+                    sb.store_whole(wb, tid);
+                    __syncthreads();
+#pragma unroll 1
+                    for (int e = 0; e < 8; ++e) {
+                        // element e of a lane's 8 is the same k on both sides
+                        const int from = (lane & 15) * 32 + (lane >> 4) * 8 + e;
+                        const float av = wa[(wm * G::FM + i) * 512 + from];
 #pragma unroll
                         for (int j = 0; j < G::FN; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wb[(wn * G::FN + j) * 512 + from],
-                                                                            wa[(wm * G::FM + i) * 512 + from], acc[i][j], 0, 0, 0);
+                            whole[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wb[(wn * G::FN + j) * 512 + from], av, whole[j], 0, 0, 0);
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!(fabsf(acc[i][j][e]) < __builtin_inff())) acc[i][j][e] = whole[j][e];
             }
         }
     }

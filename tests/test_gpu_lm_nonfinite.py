@@ -156,6 +156,32 @@ def test_projection_of_infinities(m, act):
             same(n, host64(g[n]), ref[n], TOL["f32"])
 
 
+@pytest.mark.parametrize("m,k,f", [(200, 40, 700), (1100, 48, 1000)])
+def test_neighbours_keep_their_bits(m, k, f):
+    """fp32 in tiles: a NaN and an infinite token change nothing of the others, to the bit."""
+    rng = np.random.default_rng(m)
+    x = rng.standard_normal((m, k)).astype(np.float32)
+    w, w2 = ((rng.standard_normal((f, k)) / np.sqrt(k)).astype(np.float32) for _ in range(2))
+    bad = x.copy()
+    bad[17, 3], bad[131, 5] = np.nan, np.inf
+    rows = np.ones(m, bool)
+    rows[[17, 131]] = False
+    at = torch.from_numpy(np.flatnonzero(rows)).cuda()
+    t = torch.from_numpy(rng.integers(0, f, m)).cuda()
+    dh, dloss = dev(rng.standard_normal((m, f)).astype(np.float32)), torch.ones(m, device="cuda")
+    say("neighbours", m, k, f)
+
+    def both(xs):
+        xt = dev(xs)
+        loss, lse = ss().xent_fwd(xt, dev(w), t)
+        return (ss().glu_fwd(xt, dev(w), dev(w2)), ss().glu_bwd(xt, dev(w), dev(w2), dh)["dx"], loss, lse,
+                ss().xent_bwd(xt, dev(w), t, lse, dloss)["dx"])
+
+    for got, want in zip(both(bad), both(x)):
+        assert torch.equal(got[at], want[at])
+        assert not bool(torch.isfinite(got[17]).any())
+
+
 # decays so fast that the product of a over a few rows lies below float32's range: nothing of a
 # NaN or an infinity is lost with it
 @pytest.mark.parametrize("dt", [wl.F32, wl.BF16])
