@@ -16,7 +16,13 @@ and the operators beside the scan in a recurrent language model (``include/ss_lm
     h = glu_fwd(x, w_gate, w_up)                             # act(x w_gate^T) * (x w_up^T); glu_bwd
     loss, lse = xent_fwd(x, w_vocab, target)                 # cross entropy without stored logits; xent_bwd
 
-The library itself is ``libssscan.so`` (``include/ss_scan.h``, ``include/ss_lm.h``), built by
+and those of a layer that mixes tokens by linear attention, and of the next token (``include/ss_attn.h``):
+
+    q, k = qknorm_fwd(q, k, w_q, w_k, pos, inv_freq)         # norms per head and position rotation; qknorm_bwd
+    o = lattn_fwd(q, k, v, log_decay)                        # linear attention with a decay per head; lattn_bwd, lattn_step
+    token = sample(logits, u, temperature=0.8, top_p=0.95)   # top_k=, min_p=
+
+The library itself is ``libssscan.so`` (``include/ss_scan.h``, ``include/ss_lm.h``, ``include/ss_attn.h``), built by
 ``selective_state_space_85_amd.build``.
 """
 from ._lib import LIB_PATH, SSError, load as load_library  # noqa: F401
@@ -25,10 +31,14 @@ from .ops import (conv1d_silu, scan_bwd, scan_bwd_workspace_bytes, scan_ckpt_sha
 from .lm import (glr_bwd, glr_bwd_workspace_bytes, glr_ckpt_shape, glr_fwd, glr_step, glr_workspace_bytes,  # noqa: F401
                  glu_bwd, glu_bwd_workspace_bytes, glu_fwd, glu_workspace_bytes, xent_bwd, xent_bwd_workspace_bytes,
                  xent_fwd, xent_workspace_bytes)
+from .attn import (lattn_bwd, lattn_bwd_workspace_bytes, lattn_fwd, lattn_step, lattn_workspace_bytes,  # noqa: F401
+                   qknorm_bwd, qknorm_bwd_workspace_bytes, qknorm_fwd, sample, sample_workspace_bytes)
 
 __all__ = ["scan_fwd", "scan_fwd_noalloc", "scan_bwd", "step", "conv1d_silu", "ssd_fwd", "scan_plan", "scan_workspace_bytes",
            "scan_bwd_workspace_bytes", "scan_ckpt_shape", "ssd_workspace_bytes",
            "glr_fwd", "glr_bwd", "glr_step", "glr_ckpt_shape", "glr_workspace_bytes", "glr_bwd_workspace_bytes",
            "glu_fwd", "glu_bwd", "glu_workspace_bytes", "glu_bwd_workspace_bytes",
            "xent_fwd", "xent_bwd", "xent_workspace_bytes", "xent_bwd_workspace_bytes",
+           "lattn_fwd", "lattn_bwd", "lattn_step", "lattn_workspace_bytes", "lattn_bwd_workspace_bytes",
+           "qknorm_fwd", "qknorm_bwd", "qknorm_bwd_workspace_bytes", "sample", "sample_workspace_bytes",
            "load_library", "LIB_PATH", "SSError"]

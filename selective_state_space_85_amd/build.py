@@ -16,7 +16,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libssscan.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("ss_kernels.hip", "ss_bwd.hip", "ss_conv.hip", "ss_ssd.hip", "ss_glr.hip",
-                                               "ss_glu.hip", "ss_xent.hip", "ss_few.hip", "ss_api.cpp", "ss_lm_api.cpp")]
+                                               "ss_glu.hip", "ss_xent.hip", "ss_few.hip", "ss_lattn_bf16.hip",
+                                               "ss_lattn_f32.hip", "ss_lattn.hip", "ss_qknorm.hip", "ss_sample.hip",
+                                               "ss_api.cpp", "ss_lm_api.cpp", "ss_attn_api.cpp")]
 # the measurement probes (stream and ALU-issue kernels), a library of their own
 PROBE_DIR = os.path.join(PKG, "probe")
 PROBE_SOURCES = [os.path.join(PROBE_DIR, "ss_probe.hip")]

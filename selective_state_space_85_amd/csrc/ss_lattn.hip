@@ -1,0 +1,132 @@
+// gfx950 kernels of linear attention beside its walks (ss_lattn.h): the states between segments, the
+// sums over heads that share queries and keys, and the single token.
+#include <hip/hip_runtime.h>
+
+#include "ss_attn_internal.h"
+#include "ss_device.h"
+
+namespace ssk {
+namespace {
+
+// ---- states between segments ------------------------------------------------------------
+// What segment i leaves, T_i, and the decay over it, f_i, give the state before each:
+// S_0 = h0, S_{i+1} = f_i S_i + T_i (T_i alone where the segment has a reset).  One thread per cell of
+// the state; S_i takes T_i's place.
+constexpr int kJoinThreads = 256;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(LattnArgs a)
+{
+    const LattnJob& j = a.job[blockIdx.z];
+    const int64_t cells = int64_t(j.dk) * j.dv, bh = blockIdx.x, n = a.batch * a.heads;
+    for (int64_t c = int64_t(blockIdx.y) * kJoinThreads + threadIdx.x; c < cells; c += int64_t(gridDim.y) * kJoinThreads) {
+        const int64_t i = c / j.dv, k = c % j.dv;
+        float s = j.h0 ? j.h0[bh * cells + i * j.si + k * j.sj] : 0.0f;
+        for (int64_t g = 0; g < a.segs; ++g) {
+            float* const p = j.seg + (g * n + bh) * cells + c;
+            const float left = *p, f = j.keep[g * n + bh];
+            *p = s;
+            s = f < 0.0f ? left : fmaf(f, s, left);
+        }
+    }
+}
+
+// ---- sums over the heads that share one ---------------------------------------------------
+constexpr int kShareThreads = 256;
+template <int DT>
+__global__ __launch_bounds__(kShareThreads) void share_kernel(const float* part, void* out, int64_t n, int64_t share,
+                                                              int64_t width)
+{
+    using T = typename Elem<DT>::T;
+    for (int64_t i = int64_t(blockIdx.x) * kShareThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kShareThreads) {
+        const float* p = part + i / width * share * width + i % width;
+        float s = p[0];
+        for (int64_t g = 1; g < share; ++g) s += p[g * width];
+        Elem<DT>::store(static_cast<T*>(out), i, s);
+    }
+}
+
+// ---- one token --------------------------------------------------------------------------
+// S <- a S + k v^T, o = scale S^T q.  A workgroup has one (batch row, head) and 64 columns of the
+// state; 16 threads side by side take 4 columns each, and the 16 groups of them every 16th row.
+constexpr int kStepThreads = 256, kStepCols = 64, kStepGroups = 16;
+template <int DT>
+__global__ __launch_bounds__(kStepThreads) void lattn_step_kernel(LattnStepArgs a)
+{
+    using T = typename Elem<DT>::T;
+    __shared__ float part[kStepGroups][kStepCols];
+    const int64_t tiles = (a.dv + kStepCols - 1) / kStepCols;
+    const int64_t c0 = blockIdx.x % tiles * kStepCols, bh = blockIdx.x / tiles;
+    const int64_t b = bh / a.heads, h = bh % a.heads, hk = h / (a.heads / a.qk_heads);
+    const int col = threadIdx.x % 16 * 4, group = threadIdx.x / 16;
+    const T* const q = static_cast<const T*>(a.q) + b * a.q_ld + hk * a.dk;
+    const T* const k = static_cast<const T*>(a.k) + b * a.k_ld + hk * a.dk;
+    const T* const v = static_cast<const T*>(a.v) + b * a.v_ld + h * a.dv;
+    const float decay = expf(a.log_decay[h]);
+    float vv[4], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int e = 0; e < 4; ++e) vv[e] = c0 + col + e < a.dv ? Elem<DT>::load(v, c0 + col + e) : 0.0f;
+    for (int64_t i = group; i < a.dk; i += kStepGroups) {
+        const float kk = Elem<DT>::load(k, i), qq = Elem<DT>::load(q, i);
+        float* const s = a.h + (bh * a.dk + i) * a.dv + c0 + col;
+        for (int e = 0; e < 4; ++e) {
+            if (c0 + col + e >= a.dv) continue;
+            const float x = fmaf(decay, s[e], kk * vv[e]);
+            s[e] = x;
+            sum[e] = fmaf(qq, x, sum[e]);
+        }
+    }
+    for (int e = 0; e < 4; ++e) part[group][col + e] = sum[e];
+    __syncthreads();
+    if (threadIdx.x < kStepCols && c0 + threadIdx.x < a.dv) {
+        float s = 0.0f;
+        for (int g = 0; g < kStepGroups; ++g) s += part[g][threadIdx.x];
+        Elem<DT>::store(static_cast<T*>(a.o), bh * a.dv + c0 + threadIdx.x, s * a.scale);
+    }
+}
+
+bool chunks16(const void* p, int64_t ld, int64_t width, int64_t es)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && width * es % 16 == 0;
+}
+
+}  // namespace
+
+hipError_t launch_lattn_join(const LattnArgs& a, hipStream_t stream)
+{
+    const dim3 grid(static_cast<uint32_t>(a.batch * a.heads),
+                    static_cast<uint32_t>((int64_t(a.job[0].dk) * a.job[0].dv + kJoinThreads - 1) / kJoinThreads),
+                    static_cast<uint32_t>(a.jobs));
+    join_kernel<<<grid, kJoinThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_lattn(const LattnArgs& a, int dtype, hipStream_t stream)
+{
+    const int64_t es = dtype == 0 ? 4 : 2;
+    bool vec = true;
+    for (int i = 0; i < a.jobs; ++i) {
+        const LattnJob& j = a.job[i];
+        vec = vec && chunks16(j.q, j.q_ld, j.dk, es) && chunks16(j.k, j.k_ld, j.dk, es) &&
+              chunks16(j.v, j.v_ld, j.dv, es) && reinterpret_cast<uintptr_t>(j.out) % 16 == 0;
+    }
+    return dtype == 0 ? launch_lattn_f32(a, vec, stream) : launch_lattn_bf16(a, vec, stream);
+}
+
+hipError_t launch_lattn_share(const float* part, void* out, int64_t rows, int64_t heads, int64_t share, int64_t width,
+                              int dtype, hipStream_t stream)
+{
+    const int64_t n = rows * (heads / share) * width;
+    const int64_t blocks = (n + kShareThreads - 1) / kShareThreads;
+    const uint32_t grid = static_cast<uint32_t>(blocks < 8192 ? blocks : 8192);
+    if (dtype == 0) share_kernel<0><<<grid, kShareThreads, 0, stream>>>(part, out, n, share, width);
+    else share_kernel<1><<<grid, kShareThreads, 0, stream>>>(part, out, n, share, width);
+    return hipGetLastError();
+}
+
+hipError_t launch_lattn_step(const LattnStepArgs& a, int dtype, hipStream_t stream)
+{
+    const uint32_t grid = static_cast<uint32_t>(a.batch * a.heads * ((a.dv + kStepCols - 1) / kStepCols));
+    if (dtype == 0) lattn_step_kernel<0><<<grid, kStepThreads, 0, stream>>>(a);
+    else lattn_step_kernel<1><<<grid, kStepThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace ssk

@@ -1,0 +1,336 @@
+"""Linear attention with a decay for each head on the GPU against its recurrence in 64 bits: the
+forward, every gradient, the single token, and their agreement."""
+import numpy as np
+import pytest
+import torch
+
+import attn_ref as ref
+from gpu_util import host64, rel_err, say
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def ss():
+    import selective_state_space_85_amd as ss
+
+    assert torch.cuda.is_available()
+    return ss
+
+
+def norm_err(got, want):
+    n = np.linalg.norm(want)
+    return float(np.linalg.norm(got - want) / n) if n else float(np.abs(got).max(initial=0.0))
+
+
+def tolerance(dtype, terms):
+    """Of an output's error relative to it, both in the 2-norm.  bf16: the output is rounded once, and
+    so is the state or the product q k^T that each of its terms has as a factor, half a step each.
+    fp32: every sum of n terms takes n roundings of half a step (2^-24), of which the errors add up as
+    their squares do; products, powers and weights are a few more.  The 4 covers sums whose terms
+    cancel to a few times less than they are."""
+    return 2 * 2.0 ** -8 if dtype is BF16 else 4 * 2.0 ** -24 * np.sqrt(terms)
+
+
+def check(name, got, want, dtype, terms, state=False):
+    """state: fp32 results of a bf16 call, whose weighted terms keep 24 bits."""
+    got = host64(got)
+    assert got.shape == want.shape, name
+    assert np.isfinite(got).all(), name
+    tol = tolerance(F32 if state else dtype, terms)
+    e = norm_err(got, want)
+    say("   %s: %.2e of %.2e" % (name, e, tol))
+    assert e <= tol, (name, e, tol)
+    # no element far off by itself: six standard deviations of what the roundings leave
+    far = rel_err(got, want)
+    assert far <= (8 * tol if dtype is BF16 and not state else 64 * tol), (name, far)
+
+
+def make(dtype, b, l, hk, h, dk, dv, seed=0, h0=False, reset=None, sliced=False, decays=None):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+
+    def normal(*shape, dtype=dtype):
+        return torch.randn(shape, generator=gen, device="cuda").to(dtype)
+
+    if sliced:  # one projection's output holds the operands side by side, with room between them
+        wide = normal(b, l, 2 * hk * dk + h * dv + sliced)
+        q = wide[..., :hk * dk].unflatten(-1, (hk, dk))
+        k = wide[..., hk * dk:2 * hk * dk].unflatten(-1, (hk, dk))
+        v = wide[..., 2 * hk * dk + sliced:].unflatten(-1, (h, dv))
+    else:
+        q, k, v = normal(b, l, hk, dk), normal(b, l, hk, dk), normal(b, l, h, dv)
+    if decays is None:
+        span = np.arange(h) / max(1, h - 1)
+        decays = np.log1p(-np.exp2(-3.0 - 6.0 * span))
+    args = dict(q=q, k=k, v=v, log_decay=torch.tensor(decays, dtype=F32, device="cuda"))
+    extra = dict(h0=normal(b, h, dk, dv, dtype=F32) * 2.0 if h0 else None, reset=None)
+    if reset is not None:
+        extra["reset"] = torch.rand((b, l), generator=gen, device="cuda") < reset
+    return args, extra, normal
+
+
+def numbers(args, extra):
+    a = {n: host64(t) for n, t in args.items()}
+    e = {n: None if t is None else host64(t) if t.dtype is F32 else t.cpu().numpy().astype(np.uint8)
+         for n, t in extra.items()}
+    return a, e
+
+
+#       type  b  l  hk h  dk  dv   h0     reset  sliced
+CASES = [
+    (F32, 1, 1, 1, 1, 16, 16, False, None, 0),
+    (BF16, 1, 1, 2, 2, 64, 64, True, None, 0),
+    (F32, 2, 2, 1, 3, 1, 1, True, None, 0),
+    (BF16, 2, 63, 2, 2, 64, 64, True, None, 0),
+    (BF16, 1, 64, 2, 2, 128, 128, False, None, 0),
+    (BF16, 2, 65, 1, 2, 128, 64, True, None, 0),
+    (F32, 2, 65, 2, 4, 64, 128, True, 0.1, 0),
+    (F32, 1, 33, 1, 1, 256, 256, True, 0.1, 0),
+    (BF16, 1, 200, 1, 1, 256, 256, True, 0.02, 0),
+    (BF16, 2, 130, 2, 6, 128, 128, True, 0.05, 16),
+    (F32, 2, 129, 2, 6, 72, 91, True, 0.05, 3),
+    (BF16, 3, 129, 2, 2, 33, 17, True, 0.05, 5),
+    (BF16, 1, 97, 1, 2, 129, 200, True, 0.3, 0),
+    (F32, 1, 100, 1, 2, 130, 66, True, 1.0, 0),
+    (BF16, 2, 320, 3, 3, 96, 40, False, 0.01, 8),
+    (F32, 1, 2100, 1, 2, 32, 48, True, None, 0),      # cut in segments
+    (BF16, 1, 2111, 2, 2, 64, 64, True, 0.001, 8),
+    (BF16, 1, 1600, 1, 2, 128, 128, True, 0.002, 0),
+    (F32, 2, 1090, 1, 1, 128, 256, False, 0.002, 0),
+]
+
+
+@pytest.mark.parametrize("dtype,b,l,hk,h,dk,dv,h0,reset,sliced", CASES)
+def test_forward(ss, dtype, b, l, hk, h, dk, dv, h0, reset, sliced):
+    say("lattn_fwd", dtype, b, l, hk, h, dk, dv, h0, reset, sliced)
+    args, extra, _ = make(dtype, b, l, hk, h, dk, dv, 1, h0, reset, sliced)
+    o, last = ss.lattn_fwd(**args, **extra, return_last_state=True)
+    torch.cuda.synchronize()
+    a, e = numbers(args, extra)
+    want_o, want_last = ref.lattn(**a, scale=dk ** -0.5, **e)
+    check("o", o, want_o, dtype, dk + l)
+    check("h_last", last, want_last, dtype, 3 * l, state=True)
+
+
+@pytest.mark.parametrize("dtype,b,l,hk,h,dk,dv,h0,reset,sliced", CASES)
+def test_gradients(ss, dtype, b, l, hk, h, dk, dv, h0, reset, sliced):
+    say("lattn_bwd", dtype, b, l, hk, h, dk, dv, h0, reset, sliced)
+    args, extra, normal = make(dtype, b, l, hk, h, dk, dv, 2, h0, reset, sliced)
+    do = normal(b, l, h, dv)
+    dh = normal(b, h, dk, dv, dtype=F32) if h0 else None
+    g = ss.lattn_bwd(**args, **extra, do=do, dh_last=dh, want_dh0=True, scale=0.3)
+    torch.cuda.synchronize()
+    a, e = numbers(args, extra)
+    want = ref.lattn_bwd(**a, **e, scale=0.3, do=host64(do), dh_last=None if dh is None else host64(dh))
+    assert set(g) == set(want)
+    for n in ("dq", "dk", "dv"):
+        check(n, g[n], want[n], dtype, max(dk, dv) + l + h // hk)
+    check("dh0", g["dh0"], want["dh0"], dtype, 3 * l, state=True)
+
+
+@pytest.mark.parametrize("dtype,b,hk,h,dk,dv", [
+    (F32, 1, 1, 1, 1, 1), (BF16, 1, 2, 2, 128, 128), (F32, 3, 2, 6, 72, 91), (BF16, 5, 1, 4, 64, 256),
+    (BF16, 2, 3, 3, 33, 17), (F32, 40, 4, 4, 256, 64), (BF16, 300, 2, 2, 64, 64)])
+def test_step(ss, dtype, b, hk, h, dk, dv):
+    say("lattn_step", dtype, b, hk, h, dk, dv)
+    args, extra, _ = make(dtype, b, 1, hk, h, dk, dv, 3, True)
+    state = extra["h0"].clone()
+    one = {n: t[:, 0] if n != "log_decay" else t for n, t in args.items()}
+    o = ss.lattn_step(state, **one)
+    torch.cuda.synchronize()
+    a, e = numbers(args, extra)
+    want_o, want_h = ref.lattn(**a, scale=dk ** -0.5, h0=e["h0"])
+    got = host64(o)
+    tol = (2.0 ** -8 if dtype is BF16 else 0.0) + 4 * 2.0 ** -24 * np.sqrt(dk + 4)  # one rounding of o, and the sum's
+    assert norm_err(got, want_o[:, 0]) <= tol
+    assert norm_err(host64(state), want_h) <= 4 * 2.0 ** -24
+
+
+def test_gradients_against_differences(ss):
+    """Central differences of the fp32 forward along random directions of every input."""
+    say("lattn_bwd against differences")
+    args, extra, normal = make(F32, 2, 90, 1, 2, 24, 20, 4, True, 0.05)
+    do, dh = normal(2, 90, 2, 20), normal(2, 2, 24, 20)
+    g = ss.lattn_bwd(**args, **extra, do=do, dh_last=dh, want_dh0=True)
+    a, e = numbers(args, extra)
+
+    def value(**other):
+        o, last = ref.lattn(**{**a, **{n: t for n, t in other.items() if n != "h0"}}, scale=24 ** -0.5, reset=e["reset"],
+                            h0=other.get("h0", e["h0"]))
+        return (o * host64(do)).sum() + (last * host64(dh)).sum()
+
+    rng = np.random.default_rng(5)
+    for n, d in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("h0", "dh0")):
+        x = e["h0"] if n == "h0" else a[n]
+        way = rng.standard_normal(x.shape)
+        step = 1e-4
+        slope = (value(**{n: x + step * way}) - value(**{n: x - step * way})) / (2 * step)
+        got = float((host64(g[d]) * way).sum())
+        # the sum of N fp32 gradients against a direction: each within 2^-20 of the gradients' scale
+        scale = float(np.linalg.norm(host64(g[d])))
+        assert abs(got - slope) <= 2.0 ** -18 * scale + 1e-6 * abs(slope), (n, got, slope)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step_by_step_as_in_parallel(ss, dtype):
+    """A prompt in parallel, then its continuation token by token, against the whole in parallel."""
+    say("lattn prompt and steps", dtype)
+    args, _, _ = make(dtype, 2, 150, 2, 4, 64, 72, 6)
+    whole, end = ss.lattn_fwd(**args, return_last_state=True)
+    cut = 131
+    part = {n: t if n == "log_decay" else t[:, :cut].contiguous() for n, t in args.items()}
+    o, state = ss.lattn_fwd(**part, return_last_state=True)
+    rows = [o]
+    for t in range(cut, 150):
+        rows.append(ss.lattn_step(state, **{n: x if n == "log_decay" else x[:, t] for n, x in args.items()})[:, None])
+    got, want = host64(torch.cat(rows, 1)), host64(whole)
+    # both are within the tolerance of the same numbers
+    assert norm_err(got, want) <= 2 * tolerance(dtype, 64 + 150)
+    assert norm_err(host64(state), host64(end)) <= 2 * tolerance(F32, 3 * 150)
+
+
+def test_continues_in_place(ss):
+    """h_last written over h0, a sequence in two parts."""
+    say("lattn in place")
+    args, extra, _ = make(BF16, 2, 140, 1, 2, 64, 64, 7, True)
+    whole, end = ss.lattn_fwd(**args, **extra, return_last_state=True)
+    state = extra["h0"].clone()
+    rows = []
+    for lo, hi in ((0, 64), (64, 140)):
+        part = {n: t if n == "log_decay" else t[:, lo:hi].contiguous() for n, t in args.items()}
+        rows.append(ss.lattn_fwd(**part, h0=state, h_last=state))
+    assert torch.equal(torch.cat(rows, 1), whole)  # cut at a chunk's end: the same operations
+    assert torch.equal(state, end)
+
+
+@pytest.mark.parametrize("decay", [0.0, -1e-30, -5.0, -200.0, -1e30, float("-inf")])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_extreme_decays(ss, dtype, decay):
+    say("lattn decay", decay, dtype)
+    args, extra, normal = make(dtype, 1, 150, 2, 2, 64, 64, 8, True, decays=np.array([decay, -0.1]))
+    o, last = ss.lattn_fwd(**args, **extra, return_last_state=True)
+    do = normal(1, 150, 2, 64)
+    dh = normal(1, 2, 64, 64, dtype=F32)
+    g = ss.lattn_bwd(**args, **extra, do=do, dh_last=dh, want_dh0=True)
+    a, e = numbers(args, extra)
+    with np.errstate(invalid="ignore"):
+        want_o, want_last = ref.lattn(**a, scale=0.125, **e)
+        want = ref.lattn_bwd(**a, **e, scale=0.125, do=host64(do), dh_last=host64(dh))
+    check("o", o, want_o, dtype, 64 + 150)
+    check("h_last", last, want_last, dtype, 450, state=True)
+    for n in ("dq", "dk", "dv"):
+        check(n, g[n], want[n], dtype, 64 + 150)
+    check("dh0", g["dh0"], want["dh0"], dtype, 450, state=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("l,at", [(150, 70), (150, 149), (64, 0), (1200, 700)])
+def test_what_a_row_does_not_see(ss, dtype, bad, l, at):
+    """A row that holds NaN or infinities changes no row before it, and none behind a reset."""
+    say("lattn rows unseen", dtype, bad, l, at)
+    args, extra, normal = make(dtype, 1, l, 1, 2, 64, 64, 9, True)
+    reset = torch.zeros((1, l), dtype=torch.bool, device="cuda")
+    if at + 1 < l:
+        reset[0, at + 1] = True
+    extra["reset"] = reset
+    do = normal(1, l, 2, 64)
+    want_o, want_last = ss.lattn_fwd(**args, **extra, return_last_state=True)
+    want = ss.lattn_bwd(**args, **extra, do=do)
+    for n in ("q", "k", "v"):
+        args[n] = args[n].clone()
+        args[n][0, at] = bad
+    o, last = ss.lattn_fwd(**args, **extra, return_last_state=True)
+    keep = [t for t in range(l) if t != at]
+    assert torch.equal(o[:, keep], want_o[:, keep])
+    assert not torch.isfinite(o[:, at].float()).any()
+    if at + 1 < l:
+        assert torch.equal(last, want_last)
+    do = do.clone()
+    do[0, at] = bad
+    g = ss.lattn_bwd(**args, **extra, do=do)
+    # the gradients of the rows behind the reset have nothing of it; those before it do
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(g[n][:, at + 1:], want[n][:, at + 1:]), n
+        if at:
+            assert torch.equal(g["dq"][:, :at], want["dq"][:, :at])
+
+
+def test_state_dropped_at_a_reset(ss):
+    """A state of NaN is dropped by a reset, in the forward and, from the other end, in the backward."""
+    say("lattn NaN state")
+    for dtype in (F32, BF16):
+        args, extra, normal = make(dtype, 2, 100, 1, 2, 64, 40, 10, True)
+        reset = torch.zeros((2, 100), dtype=torch.uint8, device="cuda")
+        reset[0, 0] = 1
+        reset[1, 37] = 7  # any byte but 0
+        extra["reset"] = reset
+        clean = dict(extra, h0=torch.zeros_like(extra["h0"]))
+        want_o, want_last = ss.lattn_fwd(**args, **clean, return_last_state=True)
+        extra["h0"][:] = float("nan")
+        o, last = ss.lattn_fwd(**args, **extra, return_last_state=True)
+        assert torch.equal(o[0], want_o[0]) and torch.equal(o[1, 37:], want_o[1, 37:])
+        assert torch.isnan(o[1, :37].float()).all()
+        assert torch.equal(last, want_last)
+        do = normal(2, 100, 2, 40)
+        dh = torch.full((2, 2, 64, 40), float("nan"), device="cuda")
+        g = ss.lattn_bwd(**args, **clean, do=do, dh_last=dh, want_dh0=True)
+        w = ss.lattn_bwd(**args, **clean, do=do, want_dh0=True)
+        for n in ("dk", "dv"):
+            assert torch.equal(g[n][1, :37], w[n][1, :37]) and torch.isnan(g[n][1, 37:].float()).all()
+        assert torch.equal(g["dh0"], w["dh0"]) and (g["dh0"][0] == 0).all()
+
+
+def test_memory_beside_the_outputs(ss):
+    """Nothing outside an output is written, and only what it spans."""
+    say("lattn memory beside the outputs")
+    for dtype, dk, dv in ((BF16, 72, 40), (F32, 33, 17), (BF16, 128, 136)):
+        args, extra, _ = make(dtype, 2, 70, 1, 2, dk, dv, 11, True)
+        wide = torch.full((3, 70, 2, dv), 7.0, dtype=dtype, device="cuda")
+        state = torch.full((3, 2, dk, dv), 7.0, device="cuda")
+        want, want_h = ss.lattn_fwd(**args, **extra, return_last_state=True)
+        ss.lattn_fwd(**args, **extra, out=wide[:2], h_last=state[:2])
+        assert torch.equal(wide[:2], want) and torch.equal(state[:2], want_h)
+        assert (wide[2] == 7).all() and (state[2] == 7).all()
+
+
+def test_same_results_from_run_to_run(ss):
+    say("lattn run to run")
+    args, extra, normal = make(BF16, 1, 2200, 2, 4, 128, 128, 12, True, 0.002)
+    do = normal(1, 2200, 4, 128)
+    first = ss.lattn_fwd(**args, **extra), ss.lattn_bwd(**args, **extra, do=do)
+    for _ in range(3):
+        o, g = ss.lattn_fwd(**args, **extra), ss.lattn_bwd(**args, **extra, do=do)
+        assert torch.equal(o, first[0])
+        assert all(torch.equal(g[n], first[1][n]) for n in g)
+
+
+def test_refusals(ss):
+    args, extra, normal = make(F32, 1, 8, 2, 4, 16, 16, 13)
+    with pytest.raises(ValueError):
+        ss.lattn_fwd(args["q"], args["k"], normal(1, 8, 3, 16), args["log_decay"][:3].contiguous())
+    with pytest.raises(ValueError):
+        ss.lattn_fwd(args["q"][:, :4], args["k"], args["v"], args["log_decay"])
+    with pytest.raises(TypeError):
+        ss.lattn_fwd(args["q"].half(), args["k"].half(), args["v"].half(), args["log_decay"])
+    with pytest.raises(TypeError):
+        ss.lattn_fwd(**{**args, "k": args["k"].bfloat16()})
+    with pytest.raises(ValueError):
+        ss.lattn_fwd(args["q"].transpose(1, 2), args["k"].transpose(1, 2), args["v"].transpose(1, 2), args["log_decay"])
+    with pytest.raises(ValueError):
+        ss.lattn_fwd(**{n: t.cpu() for n, t in args.items()})
+    with pytest.raises(TypeError):
+        ss.lattn_fwd(**args, reset=torch.zeros((1, 8), device="cuda"))
+    big = {n: t if n == "log_decay" else torch.zeros((1, 8, t.shape[2], 257), device="cuda") for n, t in args.items()}
+    with pytest.raises((ss.SSError, ValueError)):
+        ss.lattn_fwd(**big)
+    with pytest.raises(ss.SSError):
+        ss.lattn_fwd(**args, scale=float("nan"))
+    with pytest.raises(ss.SSError):
+        ss.lattn_fwd(**args, out=args["v"])
+    long = make(F32, 1, 2100, 1, 1, 16, 16, 14)[0]
+    with pytest.raises(ss.SSError):
+        ss.lattn_fwd(**long, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
