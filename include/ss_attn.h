@@ -39,7 +39,8 @@ extern "C" {
  *   o         : (batch, seqlen, heads, v_dim) dtype output
  *   h_last    : (batch, heads, k_dim, v_dim) fp32 output, the state after the last row, or NULL;
  *               may be exactly h0
- * k_dim and v_dim are at most 256 (SS_ERR_UNSUPPORTED above).  scale must be finite.
+ * scale must be finite.  k_dim and v_dim above 256, row strides (and heads * k_dim, heads * v_dim)
+ * above 2^20 elements and seqlen from 2^30 on are SS_ERR_UNSUPPORTED.
  * bf16: the state is fp32 throughout; it and the products q k^T are rounded to bf16 where they
  * enter a product with q or v.  A state that holds an infinity gives infinities or NaN.
  */

@@ -74,11 +74,18 @@ bool lattn_layout(const LattnDims& d, bool back, LattnLayout* w)
     return r.ok;
 }
 
-// Whether the walks' launches fit a grid.
+// Rows' strides that the kernels' 32-bit offsets over a chunk take, in elements.
+constexpr int64_t kLattnMaxStride = int64_t(1) << 20;
+bool lattn_too_wide(int64_t a, int64_t b, int64_t c, int64_t d)
+{
+    return a > kLattnMaxStride || b > kLattnMaxStride || c > kLattnMaxStride || d > kLattnMaxStride;
+}
+
+// Whether the walks' launches fit a grid, and a sequence's rows their counters.
 bool lattn_grid_ok(const LattnDims& d, const LattnLayout& w)
 {
     int64_t n;
-    return mul(d.batch * d.heads, w.segs, &n) && mul(n, 2, &n) && n <= INT32_MAX && launch_fits(n, 256);
+    return d.seqlen < (int64_t(1) << 30) && mul(d.batch * d.heads, w.segs, &n) && mul(n, 2, &n) && n <= INT32_MAX && launch_fits(n, 256);
 }
 
 size_t lattn_bytes(const LattnDims& d, ss_dtype dtype, bool back)
@@ -131,7 +138,8 @@ ss_status ss_lattn_fwd(const void* q, int64_t q_row_stride, const void* k, int64
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
     if (!lattn_layout(d, false, &w)) return SS_ERR_INVALID_ARG;
-    if (!lattn_grid_ok(d, w)) return SS_ERR_UNSUPPORTED;
+    if (!lattn_grid_ok(d, w) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, heads * v_dim))
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {q, k, v, o};
     for (const void* p : elems)
@@ -181,7 +189,9 @@ ss_status ss_lattn_bwd(const void* q, int64_t q_row_stride, const void* k, int64
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
     if (!lattn_layout(d, true, &w)) return SS_ERR_INVALID_ARG;
-    if (!lattn_grid_ok(d, w)) return SS_ERR_UNSUPPORTED;
+    if (!lattn_grid_ok(d, w) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, do_row_stride) ||
+        lattn_too_wide(heads * k_dim, heads * v_dim, 0, 0))
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {q, k, v, d_o, dq, dk, dv};
     for (const void* p : elems)

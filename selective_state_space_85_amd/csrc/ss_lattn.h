@@ -22,6 +22,7 @@
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "ss_attn_internal.h"
 
@@ -43,6 +44,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, bf16x2{__bf16(a), __bf16(b)});
+}
+
+__device__ __forceinline__ float masked(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
+// The same by the instruction's name, for values that no matrix instruction wrote: where a half of the
+// result is used by itself too, the compiler would convert it a second time.
+__device__ __forceinline__ uint32_t pack_named(float a, float b)
+{
+    uint32_t r;
+    asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
 
 // What a product of 32 x 32 blocks needs of an element type.  A fragment holds kDepth indices of the
@@ -91,55 +102,60 @@ struct Ops<1> {  // bf16
         }
         return __builtin_bit_cast(Frag, r);
     }
-    // acc += a (w . v): the weighted rows in three bf16 parts, each the rounding of what the ones
-    // before it leave, so that the state keeps fp32's 24 bits
-    static __device__ __forceinline__ void split(const Frag& v, const float (&w)[8], Frag (&part)[3])
+    // Rows of v times their weights, in three bf16 parts, each the rounding of what the ones before it
+    // leave, so that the state keeps fp32's 24 bits.  In kSteps steps of a few instructions, for the
+    // places between products; step i does part i % 3 of elements 2 (i / 3) and 2 (i / 3) + 1.
+    static constexpr int kSteps = 12;
+    struct Weighing {
+        float x, y;
+    };
+    template <int I>
+    static __device__ __forceinline__ void weigh(const Frag& v, const float* w, Frag (&part)[3], Weighing& s)
     {
-        const u32x4 u = __builtin_bit_cast(u32x4, v);
-        u32x4 p[3];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x = bf_lo(u[i]) * w[2 * i], y = bf_hi(u[i]) * w[2 * i + 1];
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                p[q][i] = pack_bf16(x, y);
-                x -= bf_lo(p[q][i]);
-                y -= bf_hi(p[q][i]);
-            }
+        constexpr int q = I % 3, i = I / 3;
+        const uint32_t u = __builtin_bit_cast(u32x4, v)[i];
+        if constexpr (q == 0) {
+            s.x = bf_lo(u) * w[2 * i];
+            s.y = bf_hi(u) * w[2 * i + 1];
         }
-#pragma unroll
-        for (int q = 0; q < 3; ++q) part[q] = __builtin_bit_cast(Frag, p[q]);
+        const uint32_t r = pack_named(s.x, s.y);
+        s.x -= bf_lo(r);
+        s.y -= bf_hi(r);
+        u32x4 p = __builtin_bit_cast(u32x4, part[q]);
+        p[i] = r;
+        part[q] = __builtin_bit_cast(Frag, p);
     }
     static constexpr int kParts = 3;
-    // bits set where one of the fragment's elements is infinite or NaN
-    static __device__ __forceinline__ uint32_t not_finite(const Frag& v)
+    // whether an element of column lane % 32 is infinite or NaN: times a matrix of zeros, they leave NaN
+    template <int N>
+    static __device__ __forceinline__ bool not_finite(const Frag (&v)[N])
     {
-        const u32x4 u = __builtin_bit_cast(u32x4, v);
-        uint32_t bad = 0;
+        const Frag zero = __builtin_bit_cast(Frag, u32x4{0, 0, 0, 0});
+        f32x16 c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bad |= (u[i] & 0x7f807f80u) + 0x00800080u;
-        return bad & 0x80008000u;
+        for (int r = 0; r < 16; ++r) c[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) c = mma(zero, v[i], c);
+        return !(c[0] == 0.0f);
     }
     // the fragment with those elements zeroed
-    static __device__ __forceinline__ Frag finite_part(const Frag& v)
+    static __device__ __forceinline__ Frag finite_part(const Frag& v, uint32_t ones)
     {
         u32x4 u = __builtin_bit_cast(u32x4, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t e = u[i] & 0x7f807f80u;
-            u[i] &= ((e & 0xffffu) == 0x7f80u ? 0u : 0xffffu) | (e >= 0x7f800000u ? 0u : 0xffff0000u);
+            u[i] &= ((e & 0xffffu) == 0x7f80u ? 0u : ones & 0xffffu) | (e >= 0x7f800000u ? 0u : ones & 0xffff0000u);
         }
         return __builtin_bit_cast(Frag, u);
     }
     // the fragment with the elements of the lane's indices below `from` zeroed
-    static __device__ __forceinline__ Frag drop_below(const Frag& v, int index, int from)
+    static __device__ __forceinline__ Frag drop_below(const Frag& v, int index, int from, uint32_t ones)
     {
         u32x4 u = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (index + 2 * i < from) u[i] &= 0xffff0000u;
-            if (index + 2 * i + 1 < from) u[i] &= 0x0000ffffu;
-        }
+        for (int i = 0; i < 4; ++i)
+            u[i] &= (index + 2 * i < from ? 0u : ones & 0xffffu) | (index + 2 * i + 1 < from ? 0u : ones & 0xffff0000u);
         return __builtin_bit_cast(Frag, u);
     }
     static __device__ __forceinline__ float widen(E v) { return __uint_as_float(uint32_t(v) << 16); }
@@ -147,7 +163,12 @@ struct Ops<1> {  // bf16
     {
         *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     }
-    static __device__ __forceinline__ void store1(E* p, float v) { *p = __builtin_bit_cast(uint16_t, __bf16(v)); }
+    // of values that no matrix instruction wrote, each under a mask
+    static __device__ __forceinline__ void store4_masked(E* p, const float (&v)[4], const uint32_t (&m)[4])
+    {
+        *reinterpret_cast<u32x2*>(p) = u32x2{pack_named(masked(v[0], m[0]), masked(v[1], m[1])),
+                                             pack_named(masked(v[2], m[2]), masked(v[3], m[3]))};
+    }
 };
 
 template <>
@@ -174,30 +195,37 @@ struct Ops<0> {  // fp32: the fp32 matrix instruction, four of them to a fragmen
         return Frag{c[4 * u], c[4 * u + 1], c[4 * u + 2], c[4 * u + 3]};
     }
     static constexpr int kParts = 1;
-    static __device__ __forceinline__ void split(const Frag& v, const float (&w)[4], Frag (&part)[1])
+    static constexpr int kSteps = 4;
+    struct Weighing {};
+    template <int I>
+    static __device__ __forceinline__ void weigh(const Frag& v, const float* w, Frag (&part)[1], Weighing&)
     {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[0][i] = v[i] * w[i];
+        part[0][I] = v[I] * w[I];
     }
-    static __device__ __forceinline__ uint32_t not_finite(const Frag& v)
+    template <int N>
+    static __device__ __forceinline__ bool not_finite(const Frag (&v)[N])
     {
-        uint32_t bad = 0;
+        float c = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bad |= (__float_as_uint(v[i]) & 0x7f800000u) + 0x00800000u;
-        return bad & 0x80000000u;
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c = fmaf(v[i][e], 0.0f, c);
+        }
+        return !(c == 0.0f);
     }
-    static __device__ __forceinline__ Frag finite_part(Frag v)
+    static __device__ __forceinline__ Frag finite_part(Frag v, uint32_t ones)
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if ((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u) v[i] = 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = __float_as_uint(v[i]);
+            v[i] = __uint_as_float(u & ((u & 0x7f800000u) == 0x7f800000u ? 0u : ones));
+        }
         return v;
     }
-    static __device__ __forceinline__ Frag drop_below(Frag v, int index, int from)
+    static __device__ __forceinline__ Frag drop_below(Frag v, int index, int from, uint32_t ones)
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (index + i < from) v[i] = 0.0f;
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) & (index + i < from ? 0u : ones));
         return v;
     }
     static __device__ __forceinline__ float widen(E v) { return v; }
@@ -205,32 +233,81 @@ struct Ops<0> {  // fp32: the fp32 matrix instruction, four of them to a fragmen
     {
         *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
     }
-    static __device__ __forceinline__ void store1(E* p, float v) { *p = v; }
+    static __device__ __forceinline__ void store4_masked(E* p, const float (&v)[4], const uint32_t (&m)[4])
+    {
+        *reinterpret_cast<f32x4*>(p) = f32x4{masked(v[0], m[0]), masked(v[1], m[1]), masked(v[2], m[2]), masked(v[3], m[3])};
+    }
 };
 
-// 16 bytes of a row: elements [c, c + kEpc) of `width`, zero past its end.  VEC: the host has checked
-// that rows are whole 16-byte chunks.
-template <int DT, bool VEC>
-__device__ __forceinline__ u32x4 load_piece(const typename Ops<DT>::E* row, int c, int width, bool live)
+// An operand's rows of one chunk as a range-checked buffer: loads past its rows give zeros, stores there
+// are dropped.  Offsets count bytes from the row that lies lowest in memory; a lane that has nothing to
+// load or store adds kNowhere, which no row's offset brings back into a buffer's range (the host keeps
+// 64 rows under 2^29 bytes).
+constexpr uint32_t kNowhere = 0x80000000u;
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes)
 {
-    constexpr int kEpc = Ops<DT>::kEpc;
-    if constexpr (VEC) {
-        // no branch: a lane without elements reads the row's first ones and drops them
-        const bool in = live && c < width;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(row + (in ? c : 0));
-        const uint32_t keep = in ? 0xffffffffu : 0u;
-        return u32x4{v[0] & keep, v[1] & keep, v[2] & keep, v[3] & keep};
-    } else {
-        union {
-            u32x4 v;
-            typename Ops<DT>::E e[kEpc];
-        } p;
-        p.v = u32x4{0, 0, 0, 0};
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), short(0), int(bytes), 0x00020000);
+}
+
+// 16 bytes of a row.  VEC: the host has checked that rows are whole 16-byte chunks, and `at` is kNowhere
+// past the width; otherwise element by element, `left` of them.
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 load_piece(Rsrc r, uint32_t at, int left)
+{
+    if constexpr (VEC) return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+    u32x4 v;
+    if constexpr (DT == 0) {
 #pragma unroll
-        for (int i = 0; i < kEpc; ++i)
-            if (live && c + i < width) p.e[i] = row[c + i];
-        return p.v;
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b32(r, i < left ? at + 4 * i : kNowhere, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(r, 2 * i < left ? at + 4 * i : kNowhere, 0, 0));
+            const uint32_t hi = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(r, 2 * i + 1 < left ? at + 4 * i + 2 : kNowhere, 0, 0));
+            v[i] = lo | hi << 16;
+        }
     }
+    return v;
+}
+
+// The same as a store.
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_piece(Rsrc r, uint32_t at, int left, const u32x4& v)
+{
+    if constexpr (VEC) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
+    } else if constexpr (DT == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b32(v[i], r, i < left ? at + 4 * i : kNowhere, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_raw_buffer_store_b16(uint16_t(v[i]), r, 2 * i < left ? at + 4 * i : kNowhere, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16(uint16_t(v[i] >> 16), r, 2 * i + 1 < left ? at + 4 * i + 2 : kNowhere, 0, 0);
+        }
+    }
+}
+
+// All bits set.  In a branch that is seldom taken, masks made from it keep the compiler from running
+// the branch's arithmetic always and selecting.
+__device__ __forceinline__ uint32_t cold()
+{
+    uint32_t ones = 0xffffffffu;
+    asm volatile("" : "+v"(ones));
+    return ones;
+}
+
+// f(0), f(1), ... f(N - 1), each with its index as a type.
+template <int N, typename F, int... I>
+__device__ __forceinline__ void unroll_each(F&& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unroll(F&& f)
+{
+    unroll_each<N>(f, std::make_integer_sequence<int, N>());
 }
 
 // The geometry of one instantiation.  Rows in LDS are padded by 16 bytes.
@@ -250,7 +327,7 @@ struct LattnShape {
 // grid (slices * heads * batch * segments, jobs), slices fastest.
 // STATE: forms what each segment leaves in the state, from zero, and nothing else.
 template <int DT, int DKP, int NW, bool VEC, bool STATE>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0 || DKP == 256 ? 1 : 2))) void lattn_kernel(LattnArgs a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0 || DKP == 256 || NW == 2 ? 1 : 2))) void lattn_kernel(LattnArgs a)
 {
     using O = Ops<DT>;
     using E = typename O::E;
@@ -263,11 +340,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
     __shared__ __align__(16) E sK[C][G::kKP];
     __shared__ __align__(16) E sV[C][G::kVP];
     __shared__ __align__(16) E sP[STATE ? 1 : C][G::kPP];
+    __shared__ float s_enter[C + 1];    // out_scale a^j
     __shared__ float s_pow[C + 1];      // a^j
-    __shared__ float s_leave[2 * C];    // in_scale a^(C - 1 - x), 0 past C
+    __shared__ float s_pair[2 * C];              // pair_scale a^(C - 1 - x), 0 past C
+    __shared__ float s_weight[C];                // in_scale a^(C - 1 - s)
+    __shared__ __align__(16) float s_leave[C];   // a chunk's weights: the same where it is whole
 
     const LattnJob& j = a.job[blockIdx.y];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l32 = lane & 31, hl = lane >> 5;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, l32 = lane & 31, hl = lane >> 5;
+    // Hides from the compiler that addresses derived from the lane stay the same from chunk to chunk:
+    // kept in registers they push others out to memory.
+    auto renew = [&] {
+        asm volatile("" : "+v"(lane));
+        l32 = lane & 31;
+        hl = lane >> 5;
+    };
     const int slices = (j.dv + kLattnSlice - 1) / kLattnSlice;
     uint32_t x = blockIdx.x;
     const int v0 = int(x % uint32_t(slices)) * kLattnSlice;
@@ -281,21 +369,45 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
 
     // powers of the decay, in 64 bits: they stand for the whole walk
     const double log_a = double(a.log_decay[h]);
-    for (int i = tid; i <= C; i += G::kThreads) s_pow[i] = i == 0 ? 1.0f : float(exp(log_a * i));
+    for (int i = tid; i <= C; i += G::kThreads) {
+        const double power = i == 0 ? 1.0 : exp(log_a * i);
+        s_pow[i] = float(power);
+        s_enter[i] = float(power * double(j.out_scale));
+    }
     for (int i = tid; i < 2 * C; i += G::kThreads)
-        s_leave[i] = i >= C ? 0.0f : i == C - 1 ? j.in_scale : float(exp(log_a * (C - 1 - i)) * double(j.in_scale));
+        s_pair[i] = i >= C ? 0.0f : i == C - 1 ? j.pair_scale : float(exp(log_a * (C - 1 - i)) * double(j.pair_scale));
+    for (int i = tid; i < C; i += G::kThreads)
+        s_weight[i] = s_leave[i] = i == C - 1 ? j.in_scale : float(exp(log_a * (C - 1 - i)) * double(j.in_scale));
 
-    const E* const pq = static_cast<const E*>(j.q) + b * L * j.q_ld + (h / j.q_share) * j.dk;
-    const E* const pk = static_cast<const E*>(j.k) + b * L * j.k_ld + (h / j.k_share) * j.dk;
-    const E* const pv = static_cast<const E*>(j.v) + b * L * j.v_ld + (h / j.v_share) * j.dv + v0;
+    constexpr uint32_t kEs = sizeof(E);
+    const char* const pq = static_cast<const char*>(j.q) + (b * L * j.q_ld + (h / j.q_share) * j.dk) * kEs;
+    const char* const pk = static_cast<const char*>(j.k) + (b * L * j.k_ld + (h / j.k_share) * j.dk) * kEs;
+    const char* const pv = static_cast<const char*>(j.v) + (b * L * j.v_ld + (h / j.v_share) * j.dv + v0) * kEs;
+    const uint32_t lq = uint32_t(j.q_ld) * kEs, lk = uint32_t(j.k_ld) * kEs, lv = uint32_t(j.v_ld) * kEs;
+    const uint32_t oes = j.out_f32 ? 4 : kEs, lo = uint32_t(H * j.dv) * oes;
+    char* const po = static_cast<char*>(j.out) + (b * L * H * j.dv + h * j.dv + v0) * oes;
     const int vw = j.dv - v0;  // columns from here on
+    const int ow = vw < kLattnSlice ? vw : kLattnSlice;  // columns of this workgroup
     const uint8_t* const pr = a.reset ? a.reset + b * L : nullptr;
     const bool rev = j.rev;
-    auto token = [&](int64_t r) { return rev ? L - 1 - r : r; };
+    // An operand at the walk's current chunk of C rows: `at` is the row that lies lowest in memory.
+    struct Side {
+        const char* at;
+        uint32_t ld, width;  // bytes
+    };
+    auto side = [&](const char* p, uint32_t ld, uint32_t width, int t0) {
+        return Side{p + (rev ? L - t0 - C : t0) * int64_t(ld), ld, width};
+    };
+    auto next = [&](Side& s) { s.at += (rev ? -int64_t(C) : int64_t(C)) * int64_t(s.ld); };
+    // n of its rows as a buffer, and what to add to the offset of row r in a whole chunk, which is
+    // (rev ? C - 1 - r : r) rows: a short chunk lacks its last rows, from the end the lowest in memory
+    auto rows = [&](const Side& s, int n) {
+        const uint32_t miss = uint32_t(C - n) * s.ld;
+        return buffer_of(s.at + (rev ? miss : 0u), n > 0 ? uint32_t(C - 1) * s.ld + s.width - miss : 0);
+    };
+    auto shift = [&](const Side& s, int n) { return rev ? 0u - uint32_t(C - n) * s.ld : 0u; };
 
-    // this wave's columns of v, and whether it has any
-    const int c0 = 32 * w;
-    const bool mine = c0 < vw;
+    const int c0 = 32 * w;  // this wave's columns of v; past the width they are zeros and nothing is stored
 
     // ---- the state before the first row ----
     f32x16 st[kDB];
@@ -312,222 +424,397 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
     }
 
     // ---- a chunk's operands, loaded one chunk ahead ----
+    constexpr int kQC = DKP / O::kEpc, kVC = 32 * NW / O::kEpc;  // 16-byte pieces of a row
+    constexpr int kQR = G::kThreads / kQC, kVR = G::kThreads / kVC;  // rows that the threads load at once
+    static_assert(G::kThreads % kQC == 0 && G::kThreads % kVC == 0, "a thread's pieces lie in one column");
+    const int qr = tid / kQC, qc = tid % kQC * O::kEpc, vr = tid / kVC, vc = tid % kVC * O::kEpc;
     u32x4 fq[STATE ? 1 : G::kQPieces], fk[G::kQPieces], fv[G::kVPieces];
     uint32_t flag = 0;
-    auto issue = [&](int64_t t0) {
-#pragma unroll
-        for (int i = 0; i < G::kQPieces; ++i) {
-            const int p = tid + G::kThreads * i, r = p / (DKP / O::kEpc), c = p % (DKP / O::kEpc) * O::kEpc;
-            const bool live = t0 + r < row1;
-            const int64_t t = live ? token(t0 + r) : 0;
-            if constexpr (!STATE) fq[i] = load_piece<DT, VEC>(pq + t * j.q_ld, c, j.dk, live);
-            fk[i] = load_piece<DT, VEC>(pk + t * j.k_ld, c, j.dk, live);
-        }
-#pragma unroll
-        for (int i = 0; i < G::kVPieces; ++i) {
-            const int p = tid + G::kThreads * i, r = p / (32 * NW / O::kEpc), c = p % (32 * NW / O::kEpc) * O::kEpc;
-            const bool live = t0 + r < row1;
-            const int64_t t = live ? token(t0 + r) : 0;
-            fv[i] = load_piece<DT, VEC>(pv + t * j.v_ld, c, vw, live);
-        }
+    const Rsrc rr = buffer_of(pr, pr ? uint32_t(L) : 0);
+    Side q = side(pq, lq, j.dk * kEs, int(row0)), k = side(pk, lk, j.dk * kEs, int(row0)), v = side(pv, lv, vw * kEs, int(row0));
+    // results go out a chunk later: the first time nothing does
+    Side out = side(po, lo, ow * oes, int(row0) - C);
+    u32x4 fo[STATE ? 1 : G::kVPieces];
+    int out_rows = 0;
+    // a thread's first piece of a whole chunk, and the bytes to the next
+    auto first = [&](const Side& s, int r, int c, int width) {
+        return (c < width ? uint32_t(c) * kEs : kNowhere) + uint32_t(rev ? C - 1 - r : r) * s.ld;
+    };
+    auto step = [&](const Side& s, int r) { return rev ? 0u - r * s.ld : r * s.ld; };
+    const uint32_t oq = first(q, qr, qc, j.dk), ok = first(k, qr, qc, j.dk), ov = first(v, vr, vc, vw);
+    const uint32_t oo = first(out, vr, vc, ow);
+    // The stores and loads of a chunk, one piece at a time, so that they go out between products.  Stores
+    // come first: a wait for loads then waits for no store that was issued behind them.
+    struct Moves {
+        Rsrc out, q, k, v;
+        uint32_t ao, aq, ak, av, so, sq, sk, sv;
+    } mv;
+    auto start_store = [&] {
+        mv.out = rows(out, out_rows);
+        mv.ao = oo + shift(out, out_rows);
+        mv.so = step(out, kVR);
+        next(out);
+    };
+    auto start_load = [&](int t0, int n) {
         // whether the state of the row before is dropped on the way to this row: from the end, the
         // reset is the one of the row that was walked before
-        flag = 0;
-        if (pr) {
-            const int64_t r = t0 + lane, t = rev ? L - r : r;
-            if (lane < C && r < row1 && t < L) flag = pr[t];
+        const int t = rev ? int(L) - t0 - lane : t0 + lane;
+        flag = uint8_t(__builtin_amdgcn_raw_buffer_load_b8(rr, lane < n && t < int(L) ? uint32_t(t) : kNowhere, 0, 0));
+        mv.q = rows(q, n);
+        mv.k = rows(k, n);
+        mv.v = rows(v, n);
+        mv.aq = oq + shift(q, n);
+        mv.ak = ok + shift(k, n);
+        mv.av = ov + shift(v, n);
+        mv.sq = step(q, kQR);
+        mv.sk = step(k, kQR);
+        mv.sv = step(v, kVR);
+        next(q);
+        next(k);
+        next(v);
+    };
+    constexpr int kStores = G::kVPieces, kLoads = (STATE ? 1 : 2) * G::kQPieces + G::kVPieces;
+    auto store_one = [&](auto i_v) {
+        constexpr int i = decltype(i_v)::value;
+        store_piece<DT, VEC>(mv.out, mv.ao + i * mv.so, ow - vc, fo[i]);
+    };
+    auto load_one = [&](auto i_v) {
+        constexpr int i = decltype(i_v)::value;
+        if constexpr (i < G::kVPieces) {
+            fv[i] = load_piece<DT, VEC>(mv.v, mv.av + i * mv.sv, vw - vc);
+        } else if constexpr (i < G::kVPieces + G::kQPieces) {
+            constexpr int p = i - G::kVPieces;
+            fk[p] = load_piece<DT, VEC>(mv.k, mv.ak + p * mv.sk, j.dk - qc);
+        } else {
+            constexpr int p = i - G::kVPieces - G::kQPieces;
+            fq[p] = load_piece<DT, VEC>(mv.q, mv.aq + p * mv.sq, j.dk - qc);
         }
     };
 
-    // decays between this lane's rows of P^T (s) and its column (t): the same in every chunk.  Blocks
-    // of P^T: 0 is (s 0-31, t 0-31), 1 is (s 0-31, t 32-63), 2 is (s 32-63, t 32-63).
-    constexpr int kBlocks = kTB == 2 ? 3 : 1;
-    const bool diag = w != 1 || kTB == 1;
-    float pair[16];
-    __syncthreads();
-    if constexpr (!STATE) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int gap = l32 - (8 * (r >> 2) + 4 * hl + (r & 3)) + (diag ? 0 : 32);
-            pair[r] = gap >= 0 ? s_pow[gap] * j.pair_scale : 0.0f;
-        }
-    }
+    // Blocks of P^T: 0 is (s 0-31, t 0-31), 1 is (s 0-31, t 32-63), 2 is (s 32-63, t 32-63).  A wave left
+    // without one forms the last one too and writes the same numbers: every wave runs the same code.
+    constexpr int kBlocks = kTB == 2 ? 3 : 1, kRounds = (kBlocks + NW - 1) / NW;
 
-    issue(row0);
+    // bit r: whether column t of a block on the diagonal sees the row s of register r
+    uint32_t diagonal = 0;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) diagonal |= (8 * (r >> 2) + 4 * hl + (r & 3) <= l32 ? 1u : 0u) << r;
+
+    const int left0 = int(row1 - row0);
+    start_load(int(row0), left0 < C ? left0 : C);
+    unroll<kLoads>(load_one);
     bool cut = false;  // STATE: whether a reset lies in the segment
-    for (int64_t t0 = row0; t0 < row1; t0 += C) {
-        const int n = int(row1 - t0 < C ? row1 - t0 : C);  // rows of this chunk
+    for (int t0 = int(row0), left = left0; left > 0; t0 += C, left -= C) {
+        const int n = left < C ? left : C;  // rows of this chunk
+        renew();
         // ---- the chunk into LDS, the next one's loads on their way ----
 #pragma unroll
         for (int i = 0; i < G::kQPieces; ++i) {
-            const int p = tid + G::kThreads * i, r = p / (DKP / O::kEpc), c = p % (DKP / O::kEpc) * O::kEpc;
-            if constexpr (!STATE) *reinterpret_cast<u32x4*>(&sQ[r][c]) = fq[i];
-            *reinterpret_cast<u32x4*>(&sK[r][c]) = fk[i];
+            if constexpr (!STATE) *reinterpret_cast<u32x4*>(&sQ[qr + i * kQR][qc]) = fq[i];
+            *reinterpret_cast<u32x4*>(&sK[qr + i * kQR][qc]) = fk[i];
         }
 #pragma unroll
-        for (int i = 0; i < G::kVPieces; ++i) {
-            const int p = tid + G::kThreads * i, r = p / (32 * NW / O::kEpc), c = p % (32 * NW / O::kEpc) * O::kEpc;
-            *reinterpret_cast<u32x4*>(&sV[r][c]) = fv[i];
-        }
+        for (int i = 0; i < G::kVPieces; ++i) *reinterpret_cast<u32x4*>(&sV[vr + i * kVR][vc]) = fv[i];
         const uint64_t resets = __ballot(flag != 0);
         const int last = resets ? 63 - __builtin_clzll(resets) : 0;  // the last reset's row: what is before leaves nothing
-        if (t0 + C < row1) issue(t0 + C);
+        if constexpr (!STATE) {
+            start_store();
+            unroll<kStores>(store_one);
+        }
+        start_load(t0 + C, left - C < 0 ? 0 : left - C < C ? left - C : C);
         __syncthreads();
+        if constexpr (STATE) unroll<kLoads>(load_one);
 
         // the state of the row before the chunk reaches its first row undecayed if it is the gradient
         // that the last row's state has from outside
         const int e0 = rev && t0 == 0 ? 0 : 1;
 
+        Frag vf[kKS];  // this wave's columns of v
+        auto columns = [&] {
+#pragma unroll
+            for (int ks = 0; ks < kKS; ++ks) vf[ks] = O::col(&sV[ks * kDepth][c0], G::kVP, lane);
+        };
+        columns();
         f32x16 o[kTB];
+        bool odd = false;  // whether one of them is infinite or NaN
         if constexpr (!STATE) {
-            // ---- P^T = K Q^T with its decays, into LDS as P (t, s) ----
+            // ---- P^T = K Q^T with its decays, into LDS as P (t, s); O^T = S^T Q^T ----
+            f32x16 p[kRounds];
+            uint32_t see[kRounds];
+            auto block = [&](int i, int& sb, int& tb) {
+                const int blk = w + i * NW < kBlocks ? w + i * NW : kBlocks - 1;
+                sb = blk == 2 ? 32 : 0;
+                tb = blk == 0 ? 0 : 32;
+            };
 #pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) {
-                if (blk % NW != w) continue;
-                const int sb = blk == 2 ? 32 : 0, tb = blk == 0 ? 0 : 32;
-                f32x16 p;
+            for (int i = 0; i < kRounds; ++i) {
+                int sb, tb;
+                block(i, sb, tb);
+                see[i] = sb == tb ? diagonal : 0xffffu;
+            }
+            if (resets) {
+                cold();
 #pragma unroll
-                for (int r = 0; r < 16; ++r) p[r] = 0.0f;
+                for (int i = 0; i < kRounds; ++i) {
+                    int sb, tb;
+                    block(i, sb, tb);
+                    // the first row that row t sees
+                    const uint64_t upto = resets & (~uint64_t(0) >> (63 - tb - l32));
+                    const int from = upto ? 63 - __builtin_clzll(upto) : 0;
 #pragma unroll
-                for (int d = 0; d < DKP / kDepth; ++d)
-                    p = O::mma(O::row(&sK[sb + l32][d * kDepth + kHalf * hl]), O::row(&sQ[tb + l32][d * kDepth + kHalf * hl]), p);
-                const int t = tb + l32;
-                // the first row that row t sees
-                const uint64_t upto = resets & (~uint64_t(0) >> (63 - t));
-                const int from = upto ? 63 - __builtin_clzll(upto) : 0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int s = sb + 8 * q + 4 * hl;
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = s + e <= t && s + e >= from ? p[4 * q + e] * pair[4 * q + e] : 0.0f;
-                    O::store4(&sP[t][s], v);
+                    for (int r = 0; r < 16; ++r)
+                        if (sb + 8 * (r >> 2) + 4 * hl + (r & 3) < from) see[i] &= ~(1u << r);
                 }
             }
-            // ---- O^T = S^T Q^T ----
-            if (mine) {
+            // four rows s of a block of P at a time
+            auto pairs = [&](auto i_v) {
+                constexpr int i = decltype(i_v)::value / 4, q4 = decltype(i_v)::value % 4;
+                int sb, tb;
+                block(i, sb, tb);
+                const int t = tb + l32, s = sb + 8 * q4 + 4 * hl;
+                const float* const f = &s_pair[C - 1 - t + s];
+                float x[4];
+                uint32_t m[4];
+                // every product masked afterwards: a choice would become a branch
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = p[i][4 * q4 + e] * f[e];
+                    m[e] = uint32_t(__builtin_amdgcn_sbfe(int(see[i]), 4 * q4 + e, 1));
+                }
+                O::store4_masked(&sP[t][s], x, m);
+            };
+#pragma unroll
+            for (int tb = 0; tb < kTB; ++tb) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[tb][r] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) p[i][r] = 0.0f;
+            }
+            // every fragment is read some steps before its product
+            constexpr int kSteps = DKP / kDepth, kAhead = 3, kPieces = 4 * kRounds;
+            unroll<kRounds>([&](auto x_v) {
+                constexpr int x = decltype(x_v)::value;
+                int sb, tb;
+                block(x, sb, tb);
+                Frag kq[kAhead + 1][2];
+                auto fetch = [&](int i) {
+                    kq[i % (kAhead + 1)][0] = O::row(&sK[sb + l32][kDepth * i + kHalf * hl]);
+                    kq[i % (kAhead + 1)][1] = O::row(&sQ[tb + l32][kDepth * i + kHalf * hl]);
+                };
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) fetch(i);
+                unroll<kSteps>([&](auto i_v) {
+                    constexpr int i = decltype(i_v)::value;
+                    if constexpr (i + kAhead < kSteps) fetch(i + kAhead);
+                    p[x] = O::mma(kq[i % (kAhead + 1)][0], kq[i % (kAhead + 1)][1], p[x]);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            });
+            Frag qf[3][kTB];
+            auto queries = [&](int i) {
+#pragma unroll
+                for (int tb = 0; tb < kTB; ++tb) qf[i % 3][tb] = O::row(&sQ[32 * tb + l32][kDepth * i + kHalf * hl]);
+            };
+            queries(0);
+            queries(1);
+            // the products of S with, between them, the next chunk's loads and the rest of P
+            unroll<kSteps>([&](auto i_v) {
+                constexpr int i = decltype(i_v)::value;
+                if constexpr (i + 2 < kSteps) queries(i + 2);
+                const Frag s = O::from_acc(st[i / kSub], i % kSub);
+#pragma unroll
+                for (int tb = 0; tb < kTB; ++tb) o[tb] = O::mma(s, qf[i % 3][tb], o[tb]);
+                constexpr int m0 = kLoads * i / kSteps, m1 = kLoads * (i + 1) / kSteps;
+                unroll<m1 - m0>([&](auto m_v) { load_one(std::integral_constant<int, m0 + decltype(m_v)::value>()); });
+                constexpr int p0 = i < 2 ? 0 : kPieces * (i - 2) / (kSteps - 2), p1 = i < 2 ? 0 : kPieces * (i - 1) / (kSteps - 2);
+                unroll<p1 - p0>([&](auto m_v) { pairs(std::integral_constant<int, p0 + decltype(m_v)::value>()); });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            odd = __ballot(O::not_finite(vf)) != 0;
+#pragma unroll
+            for (int tb = 0; tb < kTB; ++tb) {
+                const float f = s_enter[32 * tb + l32 + e0];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[tb][r] *= f;
+            }
+            if (resets) {
+                const uint32_t ones = cold();
 #pragma unroll
                 for (int tb = 0; tb < kTB; ++tb) {
+                    const bool sees = (resets & (~uint64_t(0) >> (63 - 32 * tb - l32))) == 0;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) o[tb][r] = 0.0f;
-                }
-#pragma unroll
-                for (int d = 0; d < kDB; ++d) {
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) {
-                        const Frag s = O::from_acc(st[d], u);
-#pragma unroll
-                        for (int tb = 0; tb < kTB; ++tb)
-                            o[tb] = O::mma(s, O::row(&sQ[32 * tb + l32][32 * d + kDepth * u + kHalf * hl]), o[tb]);
-                    }
-                }
-#pragma unroll
-                for (int tb = 0; tb < kTB; ++tb) {
-                    const int t = 32 * tb + l32;
-                    const bool sees = (resets & (~uint64_t(0) >> (63 - t))) == 0;
-                    const float f = s_pow[t + e0] * j.out_scale;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[tb][r] = sees ? o[tb][r] * f : 0.0f;
+                    for (int r = 0; r < 16; ++r) o[tb][r] = masked(o[tb][r], sees ? ones : 0u);
                 }
             }
             __syncthreads();
         }
-
-        if (mine) {
-            Frag vf[kKS];
-            uint32_t bad = 0;
-#pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) {
-                vf[ks] = O::col(&sV[ks * kDepth][c0], G::kVP, lane);
-                bad |= O::not_finite(vf[ks]);
+        // what lies before the last reset leaves nothing: P is formed, so those rows of k can go.  The
+        // last chunk of a walk may be short: its weights end with its last row.
+        if (resets || n < C) {
+            const int thread = 64 * w + lane;
+            if (resets) {
+                for (int p = thread; p < last * (DKP / O::kEpc); p += G::kThreads)
+                    *reinterpret_cast<u32x4*>(&sK[p / (DKP / O::kEpc)][p % (DKP / O::kEpc) * O::kEpc]) = u32x4{0, 0, 0, 0};
             }
-            if constexpr (!STATE) {
-                // ---- O^T += V^T P^T ----
-                // a row must not meet an infinity or NaN that it does not see, not even times 0: these are
-                // left out of the product and added where they are seen
-                const bool odd = __ballot(bad != 0) != 0;
+            if (n < C)
+                for (int i = thread; i < C; i += G::kThreads) s_leave[i] = i < n ? s_weight[i + C - n] : 0.0f;
+            __syncthreads();
+        }
+
+        Frag part[2][O::kParts], kf[2][kDB];
+        float wt[2][kHalf];
+        typename O::Weighing steps;
+        auto weights = [&](int ks) {
 #pragma unroll
-                for (int ks = 0; ks < kKS; ++ks) {
-                    Frag v = vf[ks];
-                    if (odd) v = O::finite_part(v);
+            for (int i = 0; i < kHalf; ++i) wt[ks & 1][i] = s_leave[ks * kDepth + kHalf * hl + i];
+        };
+        auto keys = [&](int ks) {
 #pragma unroll
-                    for (int tb = 0; tb < kTB; ++tb)
-                        if (ks < (tb + 1) * kSub)
-                            o[tb] = O::mma(v, O::row(&sP[32 * tb + l32][ks * kDepth + kHalf * hl]), o[tb]);
-                }
-                if (odd) {
+            for (int d = 0; d < kDB; ++d) kf[ks & 1][d] = O::col(&sK[ks * kDepth][32 * d], G::kKP, lane);
+        };
+        auto weigh = [&](auto ks_v, auto lo_v, auto hi_v) {  // steps [lo, hi) of it
+            constexpr int ks = decltype(ks_v)::value, lo = decltype(lo_v)::value, hi = decltype(hi_v)::value;
+            unroll<hi - lo>([&](auto t) {
+                O::template weigh<lo + decltype(t)::value>(vf[ks], wt[ks & 1], part[ks & 1], steps);
+            });
+        };
+        const std::integral_constant<int, 0> zero{};
+        const std::integral_constant<int, O::kSteps> all{};
+        weights(0);
+        const float f = s_pow[n - 1 + e0];  // the decay over the chunk
+        if constexpr (!STATE) {
+            // ---- O^T += V^T P^T ----
+            // a row must not meet an infinity or NaN that it does not see, not even times 0: these are
+            // left out of the product and added where they are seen
+            if (odd) {
+                const uint32_t ones = cold();
 #pragma unroll
-                    for (int tb = 0; tb < kTB; ++tb) {
-                        const int t = 32 * tb + l32;
-                        const uint64_t upto = resets & (~uint64_t(0) >> (63 - t));
-                        const int from = upto ? 63 - __builtin_clzll(upto) : 0;
-#pragma unroll 1
-                        for (int s = 0; s < 32 * (tb + 1); ++s) {
-                            const bool sees = s <= t && s >= from;
-                            const float p = O::widen(sP[t][s]);
+                for (int ks = 0; ks < kKS; ++ks) vf[ks] = O::finite_part(vf[ks], ones);
+            }
+            constexpr int kProducts = kTB == 2 ? 3 * kSub : kSub;
+            Frag pf[kProducts];
 #pragma unroll
-                            for (int r = 0; r < 16; ++r) {
-                                const float v = O::widen(sV[s][c0 + 8 * (r >> 2) + 4 * hl + (r & 3)]);
-                                o[tb][r] += sees && !(fabsf(v) < INFINITY) ? p * v : 0.0f;
-                            }
-                        }
-                    }
-                }
-                // ---- store: lane (t, 4 columns at a time) ----
+            for (int i = 0; i < kProducts; ++i) {
+                const int ks = i < 2 * kSub && kTB == 2 ? i / 2 : i - (kTB - 1) * kSub, tb = kTB == 2 && (i >= 2 * kSub || i % 2 == 1);
+                pf[i] = O::row(&sP[32 * tb + l32][ks * kDepth + kHalf * hl]);
+            }
+            keys(0);
+            weigh(zero, zero, all);  // while P's rows come
+            __builtin_amdgcn_sched_barrier(0);
+            unroll<kProducts>([&](auto i_v) {
+                constexpr int i = decltype(i_v)::value;
+                constexpr int ks = i < 2 * kSub && kTB == 2 ? i / 2 : i - (kTB - 1) * kSub, tb = kTB == 2 && (i >= 2 * kSub || i % 2 == 1);
+                o[tb] = O::mma(vf[ks], pf[i], o[tb]);
+                // the state's own decay beside these
+                constexpr int r0 = 16 * kDB * i / kProducts, r1 = 16 * kDB * (i + 1) / kProducts;
+                unroll<r1 - r0>([&](auto r_v) {
+                    constexpr int r = r0 + decltype(r_v)::value;
+                    st[r / 16][r % 16] *= f;
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if (odd) {
 #pragma unroll
                 for (int tb = 0; tb < kTB; ++tb) {
                     const int t = 32 * tb + l32;
-                    if (t >= n) continue;
-                    const int64_t at = ((b * L + token(t0 + t)) * H + h) * j.dv + v0;
+                    const uint64_t upto = resets & (~uint64_t(0) >> (63 - t));
+                    const int from = upto ? 63 - __builtin_clzll(upto) : 0;
+#pragma unroll 1
+                    for (int s = 0; s < 32 * (tb + 1); ++s) {
+                        const bool sees = s <= t && s >= from;
+                        const float p = O::widen(sP[t][s]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int c = c0 + 8 * q + 4 * hl;
-                        const float v[4] = {o[tb][4 * q], o[tb][4 * q + 1], o[tb][4 * q + 2], o[tb][4 * q + 3]};
-                        if (VEC) {
-                            if (c < vw) {
-                                if (j.out_f32) Ops<0>::store4(static_cast<float*>(j.out) + at + c, v);
-                                else O::store4(static_cast<E*>(j.out) + at + c, v);
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (c + e >= vw) continue;
-                                if (j.out_f32) static_cast<float*>(j.out)[at + c + e] = v[e];
-                                else O::store1(static_cast<E*>(j.out) + at + c + e, v[e]);
-                            }
+                        for (int r = 0; r < 16; ++r) {
+                            const float v = O::widen(sV[s][c0 + 8 * (r >> 2) + 4 * hl + (r & 3)]);
+                            o[tb][r] += sees && !(fabsf(v) < INFINITY) ? p * v : 0.0f;
                         }
                     }
                 }
+                columns();
             }
-
-            // ---- S = a^n S + K^T (w V) ----
-            const float f = resets ? 0.0f : s_pow[n - 1 + e0];
+            if (DT == 1 && j.out_f32) {
+                // sums over the heads that share k or q follow: a lane has 4 columns of row t at a time
+                const Rsrc b = rows(out, n);
+#pragma unroll
+                for (int tb = 0; tb < kTB; ++tb) {
+                    const int t = 32 * tb + l32;
+                    const uint32_t at = uint32_t(rev ? C - 1 - t : t) * lo + shift(out, n) + uint32_t(c0 + 4 * hl) * 4;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int c = 8 * (r >> 2) + (r & 3);
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[tb][r]), b,
+                                                              c0 + 4 * hl + c < ow ? at + 4 * c : kNowhere, 0, 0);
+                    }
+                }
+            } else {
+                // into the place of this wave's columns of v, which are in its registers: whole rows go
+                // out from there
+#pragma unroll
+                for (int tb = 0; tb < kTB; ++tb) {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const float x[4] = {o[tb][4 * q4], o[tb][4 * q4 + 1], o[tb][4 * q4 + 2], o[tb][4 * q4 + 3]};
+                        O::store4(&sV[32 * tb + l32][c0 + 8 * q4 + 4 * hl], x);
+                    }
+                }
+                out_rows = n;
+            }
+        } else {
+            keys(0);
+            weigh(zero, zero, all);
 #pragma unroll
             for (int d = 0; d < kDB; ++d) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) st[d][r] = resets ? 0.0f : st[d][r] * f;
-            }
-#pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) {
-                float wt[kHalf];
-#pragma unroll
-                for (int i = 0; i < kHalf; ++i) wt[i] = s_leave[ks * kDepth + kHalf * hl + i + C - n];
-                Frag v = vf[ks];
-                if (resets) v = O::drop_below(v, ks * kDepth + kHalf * hl, last);
-                Frag part[O::kParts];
-                O::split(v, wt, part);
-#pragma unroll
-                for (int d = 0; d < kDB; ++d) {
-                    Frag k = O::col(&sK[ks * kDepth][32 * d], G::kKP, lane);
-                    if (resets) k = O::drop_below(k, ks * kDepth + kHalf * hl, last);
-#pragma unroll
-                    for (int q = O::kParts - 1; q >= 0; --q) st[d] = O::mma(k, part[q], st[d]);
-                }
+                for (int r = 0; r < 16; ++r) st[d][r] *= f;
             }
         }
+
+        // ---- S = a^n S + K^T (w V) ----
+        if (odd || resets) {
+            const uint32_t ones = cold();
+            if (resets) {
+#pragma unroll
+                for (int ks = 0; ks < kKS; ++ks) vf[ks] = O::drop_below(vf[ks], ks * kDepth + kHalf * hl, last, ones);
+#pragma unroll
+                for (int d = 0; d < kDB; ++d) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) st[d][r] = masked(st[d][r], ~ones);
+                }
+            }
+            weigh(zero, zero, all);
+        }
+        // Each product is followed by a few steps of weighing the next rows: issued in this order, they
+        // run beside each other.  The smallest parts come first; neighbouring products are of different
+        // blocks of the state and do not wait for one another.
+        unroll<kKS>([&](auto ks_v) {
+            constexpr int ks = decltype(ks_v)::value, kProducts = O::kParts * kDB;
+            if constexpr (ks + 1 < kKS) {
+                weights(ks + 1);
+                keys(ks + 1);
+            }
+            unroll<kProducts>([&](auto i_v) {
+                constexpr int i = decltype(i_v)::value, q = O::kParts - 1 - i / kDB, d = i % kDB;
+                st[d] = O::mma(kf[ks & 1][d], part[ks & 1][q], st[d]);
+                if constexpr (ks + 1 < kKS)
+                    weigh(std::integral_constant<int, ks + 1>(), std::integral_constant<int, O::kSteps * i / kProducts>(),
+                          std::integral_constant<int, O::kSteps * (i + 1) / kProducts>());
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        });
         cut |= resets != 0;
         __syncthreads();
+        // whole rows of o; the same threads write the next chunk's rows of v there
+        if constexpr (!STATE) {
+#pragma unroll
+            for (int i = 0; i < G::kVPieces; ++i) fo[i] = *reinterpret_cast<const u32x4*>(&sV[vr + i * kVR][vc]);
+        }
+    }
+    if constexpr (!STATE) {
+        start_store();
+        unroll<kStores>(store_one);
     }
 
     if constexpr (STATE) {
@@ -536,25 +823,26 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
             j.keep[seg * a.batch * H + bh] = cut ? -1.0f : n == 0 ? 1.0f : float(exp(log_a * double(n)));
         }
     }
+    renew();
     // ---- the state after the last row ----
-    float* out = nullptr;
+    float* to = nullptr;
     int64_t oi = j.dv, oj = 1;
     float f = 1.0f;
     if (STATE) {
-        out = j.seg + (seg * a.batch * H + bh) * cells;
+        to = j.seg + (seg * a.batch * H + bh) * cells;
     } else if (j.h_last && seg == a.segs - 1) {
-        out = j.h_last + bh * cells;
+        to = j.h_last + bh * cells;
         oi = j.si;
         oj = j.sj;
         if (rev) f = pr && pr[0] ? -1.0f : s_pow[1];
     }
-    if (out && mine) {
+    if (to) {
 #pragma unroll
         for (int d = 0; d < kDB; ++d) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int i = 32 * d + 8 * (r >> 2) + 4 * hl + (r & 3);
-                if (i < j.dk && c0 + l32 < vw) out[i * oi + (v0 + c0 + l32) * oj] = f < 0.0f ? 0.0f : st[d][r] * f;
+                if (i < j.dk && c0 + l32 < vw) to[i * oi + (v0 + c0 + l32) * oj] = f < 0.0f ? 0.0f : st[d][r] * f;
             }
         }
     }

@@ -115,7 +115,10 @@ REFUSED = [
     # strides
     *[(f, {n: 127}, INVALID) for f in (lattn_fwd, lattn_bwd, lattn_step) for n in ("qs", "ks", "vs")],
     (lattn_bwd, dict(dos=159), INVALID),
-    *[(f, dict(qs=1 << 62), INVALID) for f in (lattn_fwd, lattn_bwd, lattn_step)],
+    *[(f, {n: (1 << 20) + 1}, UNSUPPORTED) for f in (lattn_fwd, lattn_bwd) for n in ("qs", "ks", "vs")],
+    (lattn_bwd, dict(dos=1 << 62), UNSUPPORTED),
+    (lattn_step, dict(qs=1 << 62), INVALID),
+    (lattn_fwd, dict(l=1 << 30), UNSUPPORTED),
     *[(f, dict(qs=255), INVALID) for f in (qknorm_fwd, qknorm_bwd)],
     *[(f, dict(ks=127), INVALID) for f in (qknorm_fwd, qknorm_bwd)],
     (sample, dict(xs=999), INVALID),
