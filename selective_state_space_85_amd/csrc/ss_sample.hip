@@ -1,14 +1,18 @@
 // gfx950 kernel of sampling from logits.  With the row's tokens in falling order of their logits
 // (equal ones by index) and w_j = exp((l_j - l_0) / T), every limit is a prefix of that order, and so
 // is what the random number passes over.  So no order is formed: each of top-k, top-p and the random
-// number asks for the place in the order at which a running count or sum first reaches a target,
-// and that is found by histograms.  Weights are fixed-point numbers of 64 bits: a row's sum fits, sums
-// are exact, and neither threads nor atomics change them by their order.
+// number asks for the place in the order at which a running count or sum first reaches a target.
+// Weights are fixed-point numbers of 64 bits: a row's sum fits, sums are exact, and neither threads nor
+// atomics change them by their order.
 //
-// One workgroup has one row.  Bins of equal width in the logit below the largest hold counts and
-// weights; their running sums answer which bin a place lies in.  The bin's tokens are copied to LDS
-// (or, if they are too many, found in the row again), and histograms over 8 bits at a time of the
-// logit's bits, then of the index, lead to the one token.
+// One workgroup has one row and reads it three times (from the caches, but for the first):
+//  1. the largest logit and the smallest;
+//  2. bins of equal width in the logit, with their weights.  Their running sums tell which bin a place
+//     lies in.  With a small top-k the bins have counts: the tokens that remain are weighed later;
+//  3. the tokens of the bins that the limits leave, to LDS, if they fit there.
+// A place is then found among the tokens of its bin: up to 64 of them, by one wave, a token to a lane,
+// each counting what comes before it.  More are first cut down by histograms over 8 bits of their logits
+// at a time and, where those are equal, of their indices.
 #include <hip/hip_runtime.h>
 
 #include "ss_attn_internal.h"
@@ -18,8 +22,9 @@ namespace ssk {
 namespace {
 
 constexpr int kThr = 1024;
-constexpr int kBins = 2048;   // coarse bins
-constexpr int kList = 4096;   // tokens of a bin that fit the LDS
+constexpr int kBins = 4096;   // coarse bins
+constexpr int kList = 4096;   // tokens that fit the LDS
+constexpr int kFew = 64;      // tokens of one wave
 constexpr int kRadix = 256;
 
 // Order-preserving bits of a logit: 0 for the ones that are never taken (NaN, -infinity).
@@ -35,38 +40,184 @@ __device__ __forceinline__ float logit_of(uint32_t k)
 }
 
 struct Shared {
-    uint64_t mass[kBins];   // running sums once formed
-    uint32_t count[kBins];
+    uint64_t mass[kBins];   // the bins' weights, running sums once formed
+    uint32_t count[kBins];  // the same of their tokens
     uint32_t key[kList], index[kList];
+    double root[64];        // 2^(i / 64)
     uint64_t rmass[kRadix];
-    uint32_t rcount[kRadix];
+    uint32_t few_key[kFew], few_index[kFew];
     uint64_t wave_mass[kThr / 64];
     uint32_t wave_count[kThr / 64];
-    uint64_t top[kThr / 64];
-    uint32_t low[kThr / 64];
-    uint32_t found, listed;
+    float top[kThr / 64], low[kThr / 64];
+    uint64_t found_mass;
+    uint32_t found, found_key, found_index, listed, few;
 };
 
-// The row and what its weights go by.
+// 8 or 4 elements at any alignment
+template <int DT>
+struct Piece;
+template <>
+struct Piece<0> {
+    static constexpr int kN = 4;
+    typedef float V __attribute__((ext_vector_type(4), aligned(4)));
+    V v;
+    __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+};
+template <>
+struct Piece<1> {
+    static constexpr int kN = 8;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+    V v;
+    __device__ __forceinline__ float operator[](int i) const
+    {
+        return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+    }
+};
+
+// The row, and what its weights go by.
 template <int DT>
 struct Row {
     const typename Elem<DT>::T* p;
-    int64_t n;
-    float top, scale;  // the largest logit; bins per unit of logit
-    double rate, unit; // 1 / T; the weight of the largest
-    bool infinite;
-    __device__ __forceinline__ uint32_t key(int64_t i) const { return key_of(Elem<DT>::load(p, i)); }
-    __device__ __forceinline__ int bin(float l) const
+    int n;
+    float least;  // the smallest logit that can be taken: the lowest number, or infinity if one is there
+    // what logits are multiplied with so that differences stay finite: 1, 1 / 4, or 0 for infinities, which
+    // are all equal then
+    float pre;
+    float top, scale;  // the largest logit; bins of counts per unit of logit
+    double rate;       // log2(e) / T; both go by logits times `pre`
+    int shift;         // the largest logit's weight is 2^shift
+    __device__ __forceinline__ float value(float l) const { return fminf(l, 3.402823466e38f) * pre; }
+    // the bin of a count
+    __device__ __forceinline__ int count_bin(float l) const { return int(fminf((top - value(l)) * scale, float(kBins - 1))); }
+    // The weight 2^shift exp((l - top) / T), rounded, and its bin: 2^t = 2^i root[j] 2^r with t = i + j / 64 + r,
+    // |r| <= 1 / 128, 2^r by its series, of which the first term left out is (ln 2 / 128)^6 / 720 = 3.5e-17.
+    // Bins are 1 / 64 of a halving wide: the weights of the last one are below 2^-63 of the largest, which is
+    // less than half a unit, whatever the row.
+    __device__ __forceinline__ uint64_t weight(float l, const double* root, int* bin) const
     {
-        const float f = (top - l) * scale;
-        return infinite ? (l < top ? kBins - 1 : 0) : f < float(kBins - 1) ? int(f) : kBins - 1;
+        constexpr double kGrid = 6755399441055744.0 / 64;  // 1.5 * 2^52 / 64: sums are multiples of 1 / 64
+        constexpr double kWhole = 4503599627370496.0;      // 2^52: sums are integers
+        const double t = fmax((double(value(l)) - double(top)) * rate, -1000.0);
+        const double g = t + kGrid;
+        const int n64 = int(__double_as_longlong(g));  // 64 t, rounded, in the low bits
+        const double r = t - (g - kGrid);
+        double s = fma(r, 0.0013333558146428441, 0.0096181291076284769);
+        s = fma(r, s, 0.055504108664821576);
+        s = fma(r, s, 0.24022650695910069);
+        s = fma(r, s, 0.69314718055994529) * r;
+        const double m = root[n64 & 63];
+        const double w = ldexp(fma(m, s, m), (n64 >> 6) + shift);
+        *bin = -n64 < kBins - 1 ? -n64 : kBins - 1;
+        return uint64_t(__double_as_longlong(w + kWhole)) & 0xfffffffffffffull;
     }
-    __device__ __forceinline__ uint64_t weight(float l) const
+    __device__ __forceinline__ int weight_bin(float l) const
     {
-        if (infinite) return l < top ? 0 : uint64_t(unit);
-        return uint64_t(rint(exp((double(l) - double(top)) * rate) * unit));
+        const double t = fmax((double(value(l)) - double(top)) * rate, -1000.0);
+        const int n64 = int(__double_as_longlong(t + 6755399441055744.0 / 64));
+        return -n64 < kBins - 1 ? -n64 : kBins - 1;
     }
 };
+
+// Some neighbouring pieces of the row, kThr pieces apart, of one thread.
+template <int DT, int N>
+struct Pieces {
+    Piece<DT> v[N];
+    int at;
+    float least;
+    // f(index, logit) for every token
+    template <typename F>
+    __device__ __forceinline__ void walk(F f)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < Piece<DT>::kN; ++e) f(uint32_t((at + i * kThr) * Piece<DT>::kN + e), v[i][e]);
+        }
+    }
+    // the weights and their bins, 0 for tokens that cannot be taken: four at a time without branches, so that
+    // one's table is read while another's series is formed
+    template <typename F>
+    __device__ __forceinline__ void weigh(const Row<DT>& r, const double* root, F f)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int q = 0; q < Piece<DT>::kN; q += 4) {
+                uint64_t w[4];
+                int b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float l = v[i][q + e];
+                    w[e] = r.weight(l >= least ? l : 0.0f, root, &b[e]);
+                    w[e] = l >= least ? w[e] : 0;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f(w[e], b[e]);
+            }
+        }
+    }
+};
+template <int DT>
+struct Single {
+    float l;
+    int at;
+    float least;
+    template <typename F>
+    __device__ __forceinline__ void walk(F f)
+    {
+        f(uint32_t(at), l);
+    }
+    template <typename F>
+    __device__ __forceinline__ void weigh(const Row<DT>& r, const double* root, F f)
+    {
+        int b;
+        const uint64_t w = r.weight(l >= least ? l : 0.0f, root, &b);
+        f(l >= least ? w : 0, b);
+    }
+};
+
+// Calls f with this thread's share of the row, some tokens at a time.
+template <int DT, typename F>
+__device__ __forceinline__ void each_few(const Row<DT>& r, F f)
+{
+    constexpr int kN = Piece<DT>::kN, kAhead = DT == 0 ? 4 : 2;
+    const int whole = r.n / kN;
+    auto load = [&](int at) { return Piece<DT>{*reinterpret_cast<const typename Piece<DT>::V*>(r.p + int64_t(at) * kN)}; };
+    int at = threadIdx.x;
+    for (; at + (kAhead - 1) * kThr < whole; at += kAhead * kThr) {
+        Pieces<DT, kAhead> v;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) v.v[i] = load(at + i * kThr);
+        v.at = at;
+        v.least = r.least;
+        f(v);
+    }
+#pragma unroll 1
+    for (; at < whole; at += kThr) {
+        Pieces<DT, 1> v{{load(at)}, at, r.least};
+        f(v);
+    }
+    const int last = whole * kN + threadIdx.x;
+    if (last < r.n) {
+        Single<DT> v{Elem<DT>::load(r.p, last), last, r.least};
+        f(v);
+    }
+}
+
+// Calls f(index, logit) for every token of the row, this thread's share of them: for all, and for those
+// that can be taken, not NaN and not -infinity.
+template <int DT, typename F>
+__device__ __forceinline__ void each_any(const Row<DT>& r, F f)
+{
+    each_few(r, [&](auto& v) { v.walk(f); });
+}
+template <int DT, typename F>
+__device__ __forceinline__ void each(const Row<DT>& r, F f)
+{
+    each_any(r, [&](uint32_t i, float l) {
+        if (l >= r.least) f(i, l);
+    });
+}
 
 // Inclusive running sums over a workgroup's threads.
 __device__ __forceinline__ void block_scan(Shared& s, uint64_t& m, uint32_t& c)
@@ -93,131 +244,230 @@ __device__ __forceinline__ void block_scan(Shared& s, uint64_t& m, uint32_t& c)
     __syncthreads();
 }
 
-// Calls f(index, key) for every token of the row that can be taken, this thread's share of them.
-template <int DT, typename F>
-__device__ __forceinline__ void each(const Row<DT>& r, F f)
+// Running sums of the bins' weights or counts, each thread's lying side by side.
+template <bool MASS>
+__device__ __forceinline__ void scan_bins(Shared& s)
 {
-    for (int64_t i = threadIdx.x; i < r.n; i += kThr) {
-        const uint32_t k = r.key(i);
-        if (k) f(uint32_t(i), k);
+    constexpr int kPer = kBins / kThr;
+    uint64_t m = 0, mm[kPer] = {};
+    uint32_t c = 0, cc[kPer] = {};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (MASS) m += mm[i] = s.mass[threadIdx.x * kPer + i];
+        else c += cc[i] = s.count[threadIdx.x * kPer + i];
     }
+    uint64_t before_m = m;
+    uint32_t before_c = c;
+    block_scan(s, before_m, before_c);
+    before_m -= m;
+    before_c -= c;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (MASS) s.mass[threadIdx.x * kPer + i] = before_m += mm[i];
+        else s.count[threadIdx.x * kPer + i] = before_c += cc[i];
+    }
+    __syncthreads();
 }
 
-// The place in the order at which the count (or the weights) first reaches `target`, 1 <= target <= all:
-// its key, the how-manieth of the tokens with that key it is, and the sum of the weights up to it.
-struct Place {
-    uint32_t key, nth;
-    uint64_t mass;
-    bool listed;  // whether the list holds its bin
-};
-
-template <int DT, bool MASS>
-__device__ Place find(Shared& s, const Row<DT>& r, uint64_t target)
+// The sum of v over the workgroup.
+__device__ __forceinline__ uint64_t block_sum(Shared& s, uint64_t v)
 {
-    // the bin
+    uint32_t none = 0;
+    block_scan(s, v, none);
+    if (threadIdx.x == kThr - 1) s.found_mass = v;
+    __syncthreads();
+    return s.found_mass;
+}
+
+// The bins' running counts, or weights; returns the sum of the weights that are at least `least`, if that
+// is not 0.
+template <int DT, bool MASS>
+__device__ __forceinline__ uint64_t fill_bins(Shared& s, const Row<DT>& r, uint64_t least)
+{
+    __syncthreads();
+    for (int b = threadIdx.x; b < kBins; b += kThr) {
+        if (MASS) s.mass[b] = 0;
+        else s.count[b] = 0;
+    }
+    __syncthreads();
+    uint64_t above = 0;
+    if (MASS) {
+        each_few(r, [&](auto& v) {
+            v.weigh(r, s.root, [&](uint64_t w, int b) {
+                if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[b]), w);
+                if (least) above += w >= least ? w : 0;
+            });
+        });
+    } else {
+        each(r, [&](uint32_t, float l) { atomicAdd(&s.count[r.count_bin(l)], 1u); });
+    }
+    __syncthreads();
+    scan_bins<MASS>(s);
+    return MASS && least ? block_sum(s, above) : 0;
+}
+
+// The bin in whose running sum `target` falls.
+template <bool MASS>
+__device__ __forceinline__ int bin_of(Shared& s, uint64_t target)
+{
     __syncthreads();
     for (int b = threadIdx.x; b < kBins; b += kThr) {
         const uint64_t before = b == 0 ? 0 : MASS ? s.mass[b - 1] : s.count[b - 1];
         const uint64_t upto = MASS ? s.mass[b] : s.count[b];
         if (before < target && target <= upto) s.found = uint32_t(b);
     }
+    __syncthreads();
+    return int(s.found);
+}
+
+// Copies the tokens whose logits are at least `limit`, which is not below `least`, to the list, and says
+// whether they fit there.
+template <int DT>
+__device__ __forceinline__ bool list_from(Shared& s, const Row<DT>& r, float limit)
+{
     if (threadIdx.x == 0) s.listed = 0;
     __syncthreads();
-    const int bin = int(s.found);
-    uint64_t mass = bin ? s.mass[bin - 1] : 0;        // of what lies before
-    uint64_t count = bin ? s.count[bin - 1] : 0;
-    const uint32_t in_bin = s.count[bin] - uint32_t(count);
-    Place at;
-    at.listed = in_bin <= kList;
-    if (at.listed) {
-        each(r, [&](uint32_t i, uint32_t k) {
-            if (r.bin(logit_of(k)) == bin) {
-                const uint32_t slot = atomicAdd(&s.listed, 1u);
-                s.key[slot] = k;
+    // the slots of several tokens at a time: a slot's number has to come back before it is written
+    each_few(r, [&](auto& v) {
+        uint32_t n = 0;
+        v.walk([&](uint32_t, float l) { n += l >= limit; });
+        if (n == 0) return;
+        uint32_t slot = atomicAdd(&s.listed, n);
+        v.walk([&](uint32_t i, float l) {
+            if (!(l >= limit)) return;
+            if (slot < kList) {
+                s.key[slot] = key_of(l);
                 s.index[slot] = i;
+            }
+            ++slot;
+        });
+    });
+    __syncthreads();
+    return s.listed <= kList;
+}
+// A logit below every one of the bins up to `bin`, for the list: that a few others are above it too
+// does no harm.  A bin's width is `width` logits.
+template <int DT>
+__device__ __forceinline__ float below(const Row<DT>& r, int bin, double width)
+{
+    if (bin == kBins - 1 || r.pre == 0.0f) return r.least;
+    const double l = (double(r.top) - (bin + 1) * width) / double(r.pre);
+    return fmaxf(float(l - (fabs(l) + fabs(double(r.top))) * 1e-6), r.least);
+}
+
+// A token, and the weights up to it in the order.
+struct Place {
+    uint32_t key, index;
+    uint64_t mass;
+};
+
+// The place at which the count (or the weights) first reaches `target`, 1 <= target <= all, by the bins'
+// running counts (or weights).  `listed`: the list holds the tokens that are left; a key of 0 there is
+// one that is not.  With counts, the weights up to the place are the caller's to find.
+template <int DT, bool MASS>
+__device__ __forceinline__ Place find(Shared& s, const Row<DT>& r, uint64_t target, bool listed)
+{
+    const int bin = bin_of<MASS>(s, target);
+    uint64_t before = bin == 0 ? 0 : MASS ? s.mass[bin - 1] : s.count[bin - 1];
+    // the tokens among which it lies: those of the bin whose key's bits from key_shift on are key_bits, and
+    // the index's from index_shift on
+    int key_shift = 32, index_shift = 32;
+    uint32_t key_bits = 0, index_bits = 0;
+    auto candidates = [&](auto f) {
+        auto test = [&](uint32_t i, uint32_t k, float l) {
+            if ((MASS ? r.weight_bin(l) : r.count_bin(l)) == bin && (key_shift == 32 || k >> key_shift == key_bits) &&
+                (index_shift == 32 || i >> index_shift == index_bits))
+                f(i, k, l);
+        };
+        if (listed) {
+            const uint32_t n = s.listed;
+            for (uint32_t j = threadIdx.x; j < n; j += kThr)
+                if (s.key[j]) test(s.index[j], s.key[j], logit_of(s.key[j]));
+        } else {
+            each(r, [&](uint32_t i, float l) { test(i, key_of(l), l); });
+        }
+    };
+    for (;;) {
+        if (threadIdx.x == 0) s.few = 0;
+        __syncthreads();
+        candidates([&](uint32_t i, uint32_t k, float) {
+            const uint32_t slot = atomicAdd(&s.few, 1u);
+            if (slot < kFew) {
+                s.few_key[slot] = k;
+                s.few_index[slot] = i;
             }
         });
         __syncthreads();
-    }
-    // 8 bits of the key at a time, the largest first
-    uint32_t prefix = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (threadIdx.x < kRadix) {
-            s.rmass[threadIdx.x] = 0;
-            s.rcount[threadIdx.x] = 0;
-        }
+        if (s.few <= kFew) break;
+        // the next 8 bits of the key, larger ones first, then of the index, smaller ones first
+        const bool by_key = key_shift > 0;
+        const int shift = by_key ? key_shift - 8 : index_shift - 8;
+        if (threadIdx.x < kRadix) s.rmass[threadIdx.x] = 0;
         __syncthreads();
-        auto add = [&](uint32_t, uint32_t k) {
-            if (shift < 24 && (k >> (shift + 8)) != prefix) return;
-            const int d = 255 - int(k >> shift & 255u);
-            atomicAdd(&s.rcount[d], 1u);
-            atomicAdd(reinterpret_cast<unsigned long long*>(&s.rmass[d]), r.weight(logit_of(k)));
-        };
-        if (at.listed) {
-            for (uint32_t i = threadIdx.x; i < in_bin; i += kThr) add(0, s.key[i]);
-        } else {
-            each(r, [&](uint32_t i, uint32_t k) {
-                if (r.bin(logit_of(k)) == bin) add(i, k);
-            });
-        }
+        candidates([&](uint32_t i, uint32_t k, float l) {
+            const uint32_t d = by_key ? 255u - (k >> shift & 255u) : i >> shift & 255u;
+            int b;
+            atomicAdd(reinterpret_cast<unsigned long long*>(&s.rmass[d]), MASS ? r.weight(l, s.root, &b) : 1ull);
+        });
         __syncthreads();
         uint64_t m = threadIdx.x < kRadix ? s.rmass[threadIdx.x] : 0;
-        uint32_t c = threadIdx.x < kRadix ? s.rcount[threadIdx.x] : 0;
-        const uint64_t own_m = m;
-        const uint32_t own_c = c;
-        block_scan(s, m, c);
-        const uint64_t upto = MASS ? mass + m : count + c, before = MASS ? upto - own_m : upto - own_c;
-        if (threadIdx.x < kRadix && before < target && target <= upto) {
+        uint32_t none = 0;
+        const uint64_t own = m;
+        block_scan(s, m, none);
+        if (threadIdx.x < kRadix && before + m - own < target && target <= before + m) {
             s.found = threadIdx.x;
-            s.wave_mass[0] = m - own_m;
-            s.wave_count[0] = c - own_c;
+            s.found_mass = m - own;
         }
         __syncthreads();
-        prefix = prefix << 8 | (255u - s.found);
-        mass += s.wave_mass[0];
-        count += s.wave_count[0];
+        const uint32_t d = s.found;
+        before += s.found_mass;
+        if (by_key) {
+            key_bits = key_bits << 8 | (255u - d);
+            key_shift = shift;
+        } else {
+            index_bits = index_bits << 8 | d;
+            index_shift = shift;
+        }
         __syncthreads();
     }
-    at.key = prefix;
-    const uint64_t w = r.weight(logit_of(prefix));
-    at.nth = uint32_t(MASS ? (target - mass + w - 1) / w : target - count);
-    at.mass = mass + at.nth * w;
-    return at;
+    if (threadIdx.x < 64) {
+        const int n = int(s.few), lane = threadIdx.x;
+        const uint32_t k = lane < n ? s.few_key[lane] : 0, i = lane < n ? s.few_index[lane] : 0xffffffffu;
+        int b;
+        const uint64_t w = lane >= n ? 0 : MASS ? r.weight(logit_of(k), s.root, &b) : 1;
+        const uint32_t wl = uint32_t(w), wh = uint32_t(w >> 32);
+        for (int t = 0; t < n; ++t) {
+            const uint32_t ok = __builtin_amdgcn_readlane(k, t), oi = __builtin_amdgcn_readlane(i, t);
+            const uint64_t ow = uint64_t(uint32_t(__builtin_amdgcn_readlane(wh, t))) << 32 | uint32_t(__builtin_amdgcn_readlane(wl, t));
+            before += ok > k || (ok == k && oi < i) ? ow : 0;
+        }
+        if (lane < n && before < target && target <= before + w) {
+            s.found_key = k;
+            s.found_index = i;
+            s.found_mass = before + w;
+        }
+    }
+    __syncthreads();
+    return {s.found_key, s.found_index, s.found_mass};
 }
 
-// The index of the nth token with this key.
+// The sums of the weights, and of those that are at least `least`, up to a place.
 template <int DT>
-__device__ uint32_t index_of(Shared& s, const Row<DT>& r, const Place& at)
+__device__ __forceinline__ void sums_upto(Shared& s, const Row<DT>& r, const Place& at, uint64_t least, uint64_t* all, uint64_t* above)
 {
-    const uint32_t in_list = s.listed;
-    uint32_t prefix = 0, before = 0;
-    for (int shift = 16; shift >= 0; shift -= 8) {
-        if (threadIdx.x < kRadix) s.rcount[threadIdx.x] = 0;
-        __syncthreads();
-        auto add = [&](uint32_t i, uint32_t k) {
-            if (k != at.key || (shift < 16 && (i >> (shift + 8)) != prefix)) return;
-            atomicAdd(&s.rcount[i >> shift & 255u], 1u);
-        };
-        if (at.listed) {
-            for (uint32_t i = threadIdx.x; i < in_list; i += kThr) add(s.index[i], s.key[i]);
-        } else {
-            each(r, add);
+    uint64_t m = 0, a = 0;
+    each(r, [&](uint32_t i, float l) {
+        const uint32_t k = key_of(l);
+        if (k > at.key || (k == at.key && i <= at.index)) {
+            int b;
+            const uint64_t v = r.weight(l, s.root, &b);
+            m += v;
+            a += v >= least ? v : 0;
         }
-        __syncthreads();
-        uint64_t m = 0;
-        uint32_t c = threadIdx.x < kRadix ? s.rcount[threadIdx.x] : 0;
-        const uint32_t own = c;
-        block_scan(s, m, c);
-        if (threadIdx.x < kRadix && before + c - own < at.nth && at.nth <= before + c) {
-            s.found = threadIdx.x;
-            s.wave_count[0] = c - own;
-        }
-        __syncthreads();
-        prefix = prefix << 8 | s.found;
-        before += s.wave_count[0];
-        __syncthreads();
-    }
-    return prefix;
+    });
+    *all = block_sum(s, m);
+    __syncthreads();
+    *above = block_sum(s, a);
 }
 
 template <int DT>
@@ -228,22 +478,20 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     Row<DT> r;
     r.p = static_cast<const typename Elem<DT>::T*>(a.logits) + row * a.ld;
-    r.n = a.vocab;
+    r.n = int(a.vocab);
+    if (threadIdx.x < 64) s.root[threadIdx.x] = exp2(threadIdx.x / 64.0);
 
-    // the largest logit with its first place, and the smallest
-    uint64_t top = 0;
-    uint32_t low = 0xffffffffu;
-    each(r, [&](uint32_t i, uint32_t k) {
-        const uint64_t v = uint64_t(k) << 32 | (0xffffffffu - i);
-        top = v > top ? v : top;
-        low = k < low ? k : low;
+    // the largest logit and the smallest
+    r.least = -3.402823466e38f;
+    float top = -INFINITY, low = INFINITY;
+    each_any(r, [&](uint32_t, float l) {
+        top = fmaxf(top, l);  // neither takes NaN
+        low = fminf(low, l > -INFINITY ? l : INFINITY);
     });
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-        const uint64_t ot = __shfl_xor(top, d);
-        const uint32_t ol = __shfl_xor(low, d);
-        top = ot > top ? ot : top;
-        low = ol < low ? ol : low;
+        top = fmaxf(top, __shfl_xor(top, d));
+        low = fminf(low, __shfl_xor(low, d));
     }
     if (lane == 0) {
         s.top[w] = top;
@@ -251,82 +499,97 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
     }
     __syncthreads();
     for (int i = 0; i < kThr / 64; ++i) {
-        top = s.top[i] > top ? s.top[i] : top;
-        low = s.low[i] < low ? s.low[i] : low;
+        top = fmaxf(top, s.top[i]);
+        low = fminf(low, s.low[i]);
     }
     const float t = a.temperature ? a.temperature[row] : a.temperature_all;
-    if (top == 0 || !(t > 0.0f)) {
-        if (threadIdx.x == 0) a.token[row] = top == 0 ? -1 : int64_t(0xffffffffu - uint32_t(top));
+    if (top == -INFINITY || !(t > 0.0f)) {
+        // none, or the first place of the largest
+        uint32_t where = 0xffffffffu;
+        if (threadIdx.x == 0) s.found = where;
+        __syncthreads();
+        each(r, [&](uint32_t i, float l) { where = l == top && i < where ? i : where; });
+        if (where != 0xffffffffu) atomicMin(&s.found, where);
+        __syncthreads();
+        if (threadIdx.x == 0) a.token[row] = top == -INFINITY ? -1 : int64_t(s.found);
         return;
     }
 
-    r.top = logit_of(uint32_t(top >> 32));
-    r.infinite = r.top == INFINITY;
-    r.rate = 1.0 / double(t);
-    // a row's weights sum to less than 2^63, and each fits a double's 52 bits
-    const int bits = 64 - __builtin_clzll(uint64_t(r.n));
-    const int shift = 62 - bits < 50 ? 62 - bits : 50;
-    r.unit = double(uint64_t(1) << shift);
-    // bins over what has a weight: exp(-64) of the largest is less than half a unit, whatever the row
-    const float depth = fminf(fminf(r.top - logit_of(low), 64.0f * t), 3.0e38f);
-    r.scale = depth > 0.0f ? float(kBins - 1) / depth : 0.0f;
-    if (!(r.scale < 3.0e38f)) r.scale = 3.0e38f;
+    // differences of logits up to 2^126 are finite
+    r.pre = fmaxf(fabsf(top), fabsf(low)) < 8.5e37f ? 1.0f : 0.25f;
+    if (top == INFINITY) {
+        r.least = INFINITY;
+        r.pre = 0.0f;
+        low = top;
+    }
+    r.top = r.value(top);
+    const double td = r.pre > 0.0f ? double(t) * double(r.pre) : 1.0;
+    r.rate = 1.4426950408889634 / td;
+    // a row's weights sum to less than 2^62, and each fits the 52 bits of a double
+    const int bits = 32 - __builtin_clz(uint32_t(r.n));
+    r.shift = 62 - bits < 50 ? 62 - bits : 50;
+    const uint64_t first = uint64_t(1) << r.shift;
+    // bins of counts over the logits that have a weight; the last one has those more than 64 T below the
+    // largest, whose weights, below exp(-63), are less than half a unit too
+    const float deep = float(fmin(double(r.top) - double(r.value(low)), 64.0 * td));
+    r.scale = deep > 0.0f ? fminf(float(kBins - 2) / deep, 3.0e38f) : 0.0f;
 
-    for (int b = threadIdx.x; b < kBins; b += kThr) {
-        s.mass[b] = 0;
-        s.count[b] = 0;
-    }
-    __syncthreads();
-    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all;
-    const double floor_w = min_p > 0.0f ? double(min_p) * r.unit : 0.0;
-    uint64_t above = 0;  // the weights that min_p leaves
-    each(r, [&](uint32_t, uint32_t k) {
-        const float l = logit_of(k);
-        const int b = r.bin(l);
-        const uint64_t v = r.weight(l);
-        atomicAdd(&s.count[b], 1u);
-        if (v) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[b]), v);
-        if (double(v) >= floor_w) above += v;
-    });
-    __syncthreads();
-    // running sums: each thread has neighbouring bins
-    {
-        constexpr int kPer = kBins / kThr;
-        uint64_t m = 0;
-        uint32_t c = 0;
-        for (int i = 0; i < kPer; ++i) {
-            m += s.mass[threadIdx.x * kPer + i];
-            c += s.count[threadIdx.x * kPer + i];
-        }
-        const uint64_t own_m = m;
-        const uint32_t own_c = c;
-        block_scan(s, m, c);
-        m -= own_m;
-        c -= own_c;
-        for (int i = 0; i < kPer; ++i) {
-            m += s.mass[threadIdx.x * kPer + i];
-            c += s.count[threadIdx.x * kPer + i];
-            s.mass[threadIdx.x * kPer + i] = m;
-            s.count[threadIdx.x * kPer + i] = c;
-        }
-        uint32_t none = 0;
-        block_scan(s, above, none);
-        if (threadIdx.x == kThr - 1) s.top[0] = above;
-        __syncthreads();
-        above = s.top[0];
-    }
-    uint64_t all = s.mass[kBins - 1];
     const int32_t k = a.top_k ? a.top_k[row] : a.top_k_all;
-    if (k > 0 && uint32_t(k) < s.count[kBins - 1]) all = find<DT, false>(s, r, uint64_t(k)).mass;
+    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all;
+    const uint64_t least = min_p > 0.0f ? uint64_t(ceil(fmin(double(min_p), 2.0) * double(first))) : 0;
+    bool listed = false;
+    uint64_t above = 0;  // the weights that min_p leaves
+    uint64_t all = 0;    // those that every limit so far leaves
+    if (k > 0 && k < r.n) {
+        // the bins' counts, and the last of the tokens that top_k leaves
+        fill_bins<DT, false>(s, r, 0);
+        const uint32_t can = s.count[kBins - 1];
+        const uint32_t keep = uint32_t(k) < can ? uint32_t(k) : can;
+        const int bin = bin_of<false>(s, keep);
+        if (bin < kBins - 1) {  // otherwise what top_k drops has no weight
+            if (s.count[bin] <= kList) listed = list_from(s, r, below(r, bin, r.scale > 0.0f ? 1.0 / double(r.scale) : 0.0));
+            const Place at = find<DT, false>(s, r, keep, listed);
+            if (listed) {
+                // the bins' weights from the list, without those that top_k drops
+                for (int b = threadIdx.x; b < kBins; b += kThr) s.mass[b] = 0;
+                __syncthreads();
+                for (uint32_t j = threadIdx.x; j < s.listed; j += kThr) {
+                    const uint32_t key = s.key[j];
+                    if (key < at.key || (key == at.key && s.index[j] > at.index)) {
+                        s.key[j] = 0;
+                    } else {
+                        int b;
+                        const uint64_t v = r.weight(logit_of(key), s.root, &b);
+                        atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[b]), v);
+                        above += v >= least ? v : 0;
+                    }
+                }
+                __syncthreads();
+                scan_bins<true>(s);
+                all = s.mass[kBins - 1];
+                above = block_sum(s, above);
+            } else {
+                sums_upto(s, r, at, least, &all, &above);
+            }
+        }
+    }
+    if (!listed) {
+        const uint64_t sum = fill_bins<DT, true>(s, r, least);
+        if (all == 0) {
+            all = s.mass[kBins - 1];
+            above = sum;
+        }
+    }
     const float p = a.top_p ? a.top_p[row] : a.top_p_all;
     if (p < 1.0f) {
         const double want = p > 0.0f ? ceil(double(p) * double(all)) : 1.0;
         uint64_t target = want > 1.0 ? uint64_t(want) : 1;
         target = target < all ? target : all;
-        all = find<DT, true>(s, r, target).mass;
+        // what is left, to the list if it fits: the token is among it
+        if (!listed) listed = list_from(s, r, below(r, bin_of<true>(s, target), 0.6931471805599453 / 64 * td));
+        all = find<DT, true>(s, r, target, listed).mass;
     }
     if (min_p > 0.0f) {
-        const uint64_t first = uint64_t(r.unit);
         const uint64_t kept = above > first ? above : first;
         all = kept < all ? kept : all;
     }
@@ -334,9 +597,8 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
     const double pass = u > 0.0f ? floor(double(u) * double(all)) : 0.0;
     uint64_t target = pass < double(all) ? uint64_t(pass) + 1 : all;
     target = target < all ? target : all;
-    const Place at = find<DT, true>(s, r, target);
-    const uint32_t token = index_of(s, r, at);
-    if (threadIdx.x == 0) a.token[row] = token;
+    const Place at = find<DT, true>(s, r, target, listed);
+    if (threadIdx.x == 0) a.token[row] = at.index;
 }
 
 }  // namespace
