@@ -31,20 +31,23 @@ bool lattn_sizes(const LattnDims& d)
 
 bool lattn_widths(const LattnDims& d) { return d.dk <= ssk::kLattnMaxDim && d.dv <= ssk::kLattnMaxDim; }
 
-// How a walk is cut into segments of the sequence.  With fewer workgroups than kLattnTarget, CUs
-// would idle; a cut costs a pass over k and v that forms the states between the segments.
-constexpr int64_t kLattnTarget = 512, kLattnMinSeg = 512, kLattnMaxSegs = 256;
+// How a walk is cut into segments of the sequence: so that there are about as many workgroups as the CUs
+// hold at once (bf16 two each, fp32 one), in segments of at least kLattnMinSeg rows.  The cut costs a
+// pass over k and v that forms the states between the segments, two fifths of a walk, and two launches:
+// in bf16 fewer than four segments do not pay for it.  Whole and cut, us, of 2048 rows in bf16: 16 heads 108
+// and 34, 64 heads 109 and 72, 128 heads 116 and 110 (in four), 200 heads 132 and 183 (in two); 16 heads of
+// 256 rows 19 and 25 (in two), of 512 rows 32 and 27 (in four).  fp32: 64 heads 435 and 188 (in four), 128
+// heads 436 and 346 (in two); 16 heads of 256 rows 60 and 54 (in two).
+constexpr int64_t kLattnMinSeg = 128, kLattnMaxSegs = 256;
 
-void lattn_plan(const LattnDims& d, int64_t walks, int64_t* len, int64_t* segs)
+void lattn_plan(const LattnDims& d, ss_dtype dtype, int64_t walks, int64_t* len, int64_t* segs)
 {
-    int64_t k = 1;
-    if (walks < kLattnTarget / 2) {
-        k = ceil_div(kLattnTarget, walks);
-        const int64_t most = d.seqlen / kLattnMinSeg;
-        k = k < most ? k : most;
-        k = k < kLattnMaxSegs ? k : kLattnMaxSegs;
-        k = k > 1 ? k : 1;
-    }
+    const int64_t target = dtype == SS_F32 ? 256 : 512, least = dtype == SS_F32 ? 2 : 4;
+    const int64_t most = d.seqlen / kLattnMinSeg;
+    int64_t k = target / walks;
+    k = k < most ? k : most;
+    k = k < kLattnMaxSegs ? k : kLattnMaxSegs;
+    if (k < least) k = 1;
     *len = ceil_div(ceil_div(d.seqlen, k), ssk::kLattnChunk) * ssk::kLattnChunk;
     *segs = ceil_div(d.seqlen, *len);
 }
@@ -55,13 +58,13 @@ struct LattnLayout {
     int64_t total;
 };
 
-bool lattn_layout(const LattnDims& d, bool back, LattnLayout* w)
+bool lattn_layout(const LattnDims& d, ss_dtype dtype, bool back, LattnLayout* w)
 {
     if (!lattn_sizes(d)) return false;
     const int jobs = back ? 3 : 1;
     int64_t walks;
     if (!mul(d.batch, d.heads, &walks)) return false;
-    lattn_plan(d, back ? 3 * walks : walks * ssk::lattn_slices(d.dv), &w->len, &w->segs);
+    lattn_plan(d, dtype, back ? 3 * walks : walks * ssk::lattn_slices(d.dv), &w->len, &w->segs);
     Regions r;
     int64_t n, f;
     if (!mul(w->segs, d.states(), &n) || !mul(w->segs, walks, &f)) return false;
@@ -92,7 +95,7 @@ size_t lattn_bytes(const LattnDims& d, ss_dtype dtype, bool back)
 {
     LattnLayout w;
     if (!known(dtype) || !lattn_sizes(d) || !lattn_widths(d)) return kBad;
-    return lattn_layout(d, back, &w) ? static_cast<size_t>(w.total) : kBad;
+    return lattn_layout(d, dtype, back, &w) ? static_cast<size_t>(w.total) : kBad;
 }
 
 ssk::LattnArgs lattn_args(const LattnDims& d, const LattnLayout& w, const float* log_decay, const uint8_t* reset)
@@ -137,7 +140,7 @@ ss_status ss_lattn_fwd(const void* q, int64_t q_row_stride, const void* k, int64
     if (q_row_stride < qk_heads * k_dim || k_row_stride < qk_heads * k_dim || v_row_stride < heads * v_dim)
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
-    if (!lattn_layout(d, false, &w)) return SS_ERR_INVALID_ARG;
+    if (!lattn_layout(d, dtype, false, &w)) return SS_ERR_INVALID_ARG;
     if (!lattn_grid_ok(d, w) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, heads * v_dim))
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
@@ -188,7 +191,7 @@ ss_status ss_lattn_bwd(const void* q, int64_t q_row_stride, const void* k, int64
         do_row_stride < heads * v_dim)
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
-    if (!lattn_layout(d, true, &w)) return SS_ERR_INVALID_ARG;
+    if (!lattn_layout(d, dtype, true, &w)) return SS_ERR_INVALID_ARG;
     if (!lattn_grid_ok(d, w) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, do_row_stride) ||
         lattn_too_wide(heads * k_dim, heads * v_dim, 0, 0))
         return SS_ERR_UNSUPPORTED;

@@ -45,40 +45,86 @@ __global__ __launch_bounds__(kShareThreads) void share_kernel(const float* part,
 }
 
 // ---- one token --------------------------------------------------------------------------
-// S <- a S + k v^T, o = scale S^T q.  A workgroup has one (batch row, head) and 64 columns of the
-// state; 16 threads side by side take 4 columns each, and the 16 groups of them every 16th row.
-constexpr int kStepThreads = 256, kStepCols = 64, kStepGroups = 16;
-template <int DT>
+// S <- a S + k v^T, o = scale S^T q: 8 bytes of the state's traffic per cell and nothing to speak of
+// beside it.  A workgroup has one (batch row, head) and 128 columns of the state, or fewer where there
+// are fewer; 32 threads side by side take 4 columns each, and the 8 groups of them every 8th row, all
+// of whose loads are issued before the first is used (ROWS of them at a time).  Their sums of o are
+// joined in order.
+constexpr int kStepThreads = 256, kStepCols = 128, kStepGroups = kStepThreads / (kStepCols / 4);
+template <int DT, bool VEC, int ROWS>
 __global__ __launch_bounds__(kStepThreads) void lattn_step_kernel(LattnStepArgs a)
 {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
     using T = typename Elem<DT>::T;
-    __shared__ float part[kStepGroups][kStepCols];
-    const int64_t tiles = (a.dv + kStepCols - 1) / kStepCols;
-    const int64_t c0 = blockIdx.x % tiles * kStepCols, bh = blockIdx.x / tiles;
+    __shared__ float part[kStepGroups][kStepCols + 4];
+    __shared__ float sk[kLattnMaxDim], sq[kLattnMaxDim];
+    const uint32_t tiles = uint32_t((a.dv + kStepCols - 1) / kStepCols);
+    const int dk = int(a.dk), dv = int(a.dv);
+    const int c0 = int(blockIdx.x % tiles) * kStepCols;
+    const int64_t bh = blockIdx.x / tiles;
     const int64_t b = bh / a.heads, h = bh % a.heads, hk = h / (a.heads / a.qk_heads);
-    const int col = threadIdx.x % 16 * 4, group = threadIdx.x / 16;
-    const T* const q = static_cast<const T*>(a.q) + b * a.q_ld + hk * a.dk;
-    const T* const k = static_cast<const T*>(a.k) + b * a.k_ld + hk * a.dk;
-    const T* const v = static_cast<const T*>(a.v) + b * a.v_ld + h * a.dv;
-    const float decay = expf(a.log_decay[h]);
-    float vv[4], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int e = 0; e < 4; ++e) vv[e] = c0 + col + e < a.dv ? Elem<DT>::load(v, c0 + col + e) : 0.0f;
-    for (int64_t i = group; i < a.dk; i += kStepGroups) {
-        const float kk = Elem<DT>::load(k, i), qq = Elem<DT>::load(q, i);
-        float* const s = a.h + (bh * a.dk + i) * a.dv + c0 + col;
-        for (int e = 0; e < 4; ++e) {
-            if (c0 + col + e >= a.dv) continue;
-            const float x = fmaf(decay, s[e], kk * vv[e]);
-            s[e] = x;
-            sum[e] = fmaf(qq, x, sum[e]);
+    const int col = c0 + threadIdx.x % (kStepCols / 4) * 4, group = threadIdx.x / (kStepCols / 4);
+    const T* const q = static_cast<const T*>(a.q) + b * a.q_ld + hk * dk;
+    const T* const k = static_cast<const T*>(a.k) + b * a.k_ld + hk * dk;
+    const T* const v = static_cast<const T*>(a.v) + b * a.v_ld + h * dv;
+    float* const s = a.h + (bh * dk + group) * dv + col;
+    const int64_t step = int64_t(kStepGroups) * dv;
+    f32x4 x[ROWS];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const float* const p = s + (i0 / kStepGroups + i) * step;
+            if constexpr (VEC) {
+                if (i0 + kStepGroups * i + group < dk && col < dv) x[i] = *reinterpret_cast<const f32x4*>(p);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i0 + kStepGroups * i + group < dk && col + e < dv) x[i][e] = p[e];
+            }
         }
+    };
+    load(0);
+    for (int i = threadIdx.x; i < dk; i += kStepThreads) {
+        sk[i] = Elem<DT>::load(k, i);
+        sq[i] = Elem<DT>::load(q, i);
     }
-    for (int e = 0; e < 4; ++e) part[group][col + e] = sum[e];
+    const float decay = float(exp(double(a.log_decay[h])));
+    f32x4 vv = {0.0f, 0.0f, 0.0f, 0.0f}, sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (col + e < dv) vv[e] = Elem<DT>::load(v, col + e);
     __syncthreads();
-    if (threadIdx.x < kStepCols && c0 + threadIdx.x < a.dv) {
-        float s = 0.0f;
-        for (int g = 0; g < kStepGroups; ++g) s += part[g][threadIdx.x];
-        Elem<DT>::store(static_cast<T*>(a.o), bh * a.dv + c0 + threadIdx.x, s * a.scale);
+    for (int i0 = 0;;) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int r = i0 + kStepGroups * i + group;
+            if (r >= dk) continue;
+            const float kk = sk[r], qq = sq[r];
+            float* const p = s + (i0 / kStepGroups + i) * step;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[i][e] = fmaf(decay, x[i][e], kk * vv[e]);
+                sum[e] = fmaf(qq, x[i][e], sum[e]);
+            }
+            if constexpr (VEC) {
+                if (col < dv) *reinterpret_cast<f32x4*>(p) = x[i];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < dv) p[e] = x[i][e];
+            }
+        }
+        i0 += kStepGroups * ROWS;
+        if (i0 >= dk) break;
+        load(i0);
+    }
+    *reinterpret_cast<f32x4*>(&part[group][col - c0]) = sum;
+    __syncthreads();
+    if (threadIdx.x < kStepCols && c0 + int(threadIdx.x) < dv) {
+        float o = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kStepGroups; ++g) o += part[g][threadIdx.x];
+        Elem<DT>::store(static_cast<T*>(a.o), bh * dv + c0 + threadIdx.x, o * a.scale);
     }
 }
 
@@ -121,12 +167,19 @@ hipError_t launch_lattn_share(const float* part, void* out, int64_t rows, int64_
     return hipGetLastError();
 }
 
-hipError_t launch_lattn_step(const LattnStepArgs& a, int dtype, hipStream_t stream)
+template <int DT>
+static hipError_t step_typed(const LattnStepArgs& a, hipStream_t stream)
 {
     const uint32_t grid = static_cast<uint32_t>(a.batch * a.heads * ((a.dv + kStepCols - 1) / kStepCols));
-    if (dtype == 0) lattn_step_kernel<0><<<grid, kStepThreads, 0, stream>>>(a);
-    else lattn_step_kernel<1><<<grid, kStepThreads, 0, stream>>>(a);
+    const bool vec = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.h) % 16 == 0;
+    if (vec) lattn_step_kernel<DT, true, 16><<<grid, kStepThreads, 0, stream>>>(a);
+    else lattn_step_kernel<DT, false, 8><<<grid, kStepThreads, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+hipError_t launch_lattn_step(const LattnStepArgs& a, int dtype, hipStream_t stream)
+{
+    return dtype == 0 ? step_typed<0>(a, stream) : step_typed<1>(a, stream);
 }
 
 }  // namespace ssk

@@ -273,6 +273,7 @@ __global__ __launch_bounds__(kSumCols * kSumRuns) void qknorm_sum_kernel(QknormA
     const float* const p = a.part + int64_t(blockIdx.y) * a.blocks * a.width;
     float v = 0.0f;
     if (col < a.width)
+#pragma unroll 8
         for (int64_t i = g; i < a.blocks; i += kSumRuns) v += p[i * a.width + col];
     run[g][c] = v;
     __syncthreads();

@@ -320,21 +320,21 @@ __device__ __forceinline__ int bin_of(Shared& s, uint64_t target)
     return int(s.found);
 }
 
-// Copies the tokens whose logits are at least `limit`, which is not below `least`, to the list, and says
-// whether they fit there.
+// Copies the tokens whose logits lie in [from, to], which holds nothing that cannot be taken, to the list,
+// and says whether they fit there.
 template <int DT>
-__device__ __forceinline__ bool list_from(Shared& s, const Row<DT>& r, float limit)
+__device__ __forceinline__ bool make_list(Shared& s, const Row<DT>& r, float from, float to)
 {
     if (threadIdx.x == 0) s.listed = 0;
     __syncthreads();
     // the slots of several tokens at a time: a slot's number has to come back before it is written
     each_few(r, [&](auto& v) {
         uint32_t n = 0;
-        v.walk([&](uint32_t, float l) { n += l >= limit; });
+        v.walk([&](uint32_t, float l) { n += l >= from && l <= to; });
         if (n == 0) return;
         uint32_t slot = atomicAdd(&s.listed, n);
         v.walk([&](uint32_t i, float l) {
-            if (!(l >= limit)) return;
+            if (!(l >= from && l <= to)) return;
             if (slot < kList) {
                 s.key[slot] = key_of(l);
                 s.index[slot] = i;
@@ -345,14 +345,17 @@ __device__ __forceinline__ bool list_from(Shared& s, const Row<DT>& r, float lim
     __syncthreads();
     return s.listed <= kList;
 }
-// A logit below every one of the bins up to `bin`, for the list: that a few others are above it too
-// does no harm.  A bin's width is `width` logits.
-template <int DT>
-__device__ __forceinline__ float below(const Row<DT>& r, int bin, double width)
+// The logit that lies `bins` bins below the largest, or, with up, one that is above it, else below, by what
+// rounding may move a bin's border: lists may hold a few tokens more than their bins.
+template <int DT, bool MASS>
+__device__ __forceinline__ float border(const Row<DT>& r, int bins, bool up)
 {
-    if (bin == kBins - 1 || r.pre == 0.0f) return r.least;
-    const double l = (double(r.top) - (bin + 1) * width) / double(r.pre);
-    return fmaxf(float(l - (fabs(l) + fabs(double(r.top))) * 1e-6), r.least);
+    if (r.pre == 0.0f) return INFINITY;
+    // log2(e) / rate is T
+    const double width = MASS ? 1.0 / 64 / r.rate : r.scale > 0.0f ? 1.0 / double(r.scale) : 0.0;
+    const double l = (double(r.top) - bins * width) / double(r.pre), slack = (fabs(l) + fabs(double(r.top))) * 1e-6;
+    if (up) return float(fmin(l + slack, 3.402823466e38));
+    return bins >= kBins ? r.least : fmaxf(float(fmax(l - slack, -3.402823466e38)), r.least);
 }
 
 // A token, and the weights up to it in the order.
@@ -362,12 +365,14 @@ struct Place {
 };
 
 // The place at which the count (or the weights) first reaches `target`, 1 <= target <= all, by the bins'
-// running counts (or weights).  `listed`: the list holds the tokens that are left; a key of 0 there is
-// one that is not.  With counts, the weights up to the place are the caller's to find.
+// running counts (or weights).  `listed`: the list holds the tokens that are left (a key of 0 there is one
+// that is not); otherwise it is overwritten.  With counts, the weights up to the place are the caller's to find.
 template <int DT, bool MASS>
 __device__ __forceinline__ Place find(Shared& s, const Row<DT>& r, uint64_t target, bool listed)
 {
     const int bin = bin_of<MASS>(s, target);
+    // without a list of all that is left, one of the bin
+    if (!listed) listed = make_list(s, r, border<DT, MASS>(r, bin + 1, false), border<DT, MASS>(r, bin - 1, true));
     uint64_t before = bin == 0 ? 0 : MASS ? s.mass[bin - 1] : s.count[bin - 1];
     // the tokens among which it lies: those of the bin whose key's bits from key_shift on are key_bits, and
     // the index's from index_shift on
@@ -547,7 +552,7 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
         const uint32_t keep = uint32_t(k) < can ? uint32_t(k) : can;
         const int bin = bin_of<false>(s, keep);
         if (bin < kBins - 1) {  // otherwise what top_k drops has no weight
-            if (s.count[bin] <= kList) listed = list_from(s, r, below(r, bin, r.scale > 0.0f ? 1.0 / double(r.scale) : 0.0));
+            if (s.count[bin] <= kList) listed = make_list(s, r, border<DT, false>(r, bin + 1, false), INFINITY);
             const Place at = find<DT, false>(s, r, keep, listed);
             if (listed) {
                 // the bins' weights from the list, without those that top_k drops
@@ -586,7 +591,7 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
         uint64_t target = want > 1.0 ? uint64_t(want) : 1;
         target = target < all ? target : all;
         // what is left, to the list if it fits: the token is among it
-        if (!listed) listed = list_from(s, r, below(r, bin_of<true>(s, target), 0.6931471805599453 / 64 * td));
+        if (!listed) listed = make_list(s, r, border<DT, true>(r, bin_of<true>(s, target) + 1, false), INFINITY);
         all = find<DT, true>(s, r, target, listed).mass;
     }
     if (min_p > 0.0f) {
