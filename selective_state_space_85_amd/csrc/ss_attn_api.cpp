@@ -88,7 +88,9 @@ bool lattn_too_wide(int64_t a, int64_t b, int64_t c, int64_t d)
 bool lattn_grid_ok(const LattnDims& d, const LattnLayout& w)
 {
     int64_t n;
-    return d.seqlen < (int64_t(1) << 30) && mul(d.batch * d.heads, w.segs, &n) && mul(n, 2, &n) && n <= INT32_MAX && launch_fits(n, 256);
+    // two slices of each of three walks, rounded up to 8
+    return d.seqlen < (int64_t(1) << 30) && mul(d.batch * d.heads, w.segs, &n) && mul(n, 6, &n) && n <= INT32_MAX - 24 &&
+           launch_fits(n + 24, 256);
 }
 
 size_t lattn_bytes(const LattnDims& d, ss_dtype dtype, bool back)

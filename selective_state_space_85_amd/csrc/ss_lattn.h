@@ -324,8 +324,10 @@ struct LattnShape {
     static constexpr int kVPieces = kC * 32 * NW / Ops<DT>::kEpc / kThreads;
 };
 
-// grid (slices * heads * batch * segments, jobs), slices fastest.
-// STATE: forms what each segment leaves in the state, from zero, and nothing else.
+// grid (units rounded up to 8, times jobs); units are slices * heads * batch * segments, slices fastest.
+// Workgroups go to the 8 XCDs in turn: the jobs of a unit, which read the same rows in the same order
+// (dk and dv), are 8 apart, on one XCD and its L2 (8 x 2048 x 40 heads of 128, gradients: 457 -> 448 us).
+// STATE: forms what each segment but the last leaves in the state, from zero, and nothing else.
 template <int DT, int DKP, int NW, bool VEC, bool STATE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0 || DKP == 256 || NW == 2 ? 1 : 2))) void lattn_kernel(LattnArgs a)
 {
@@ -346,7 +348,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
     __shared__ float s_weight[C];                // in_scale a^(C - 1 - s)
     __shared__ __align__(16) float s_leave[C];   // a chunk's weights: the same where it is whole
 
-    const LattnJob& j = a.job[blockIdx.y];
+    uint32_t x = blockIdx.x / (8 * a.jobs) * 8 + blockIdx.x % 8;
+    const LattnJob& j = a.job[blockIdx.x / 8 % a.jobs];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lane = tid & 63, l32 = lane & 31, hl = lane >> 5;
     // Hides from the compiler that addresses derived from the lane stay the same from chunk to chunk:
@@ -357,13 +360,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
         hl = lane >> 5;
     };
     const int slices = (j.dv + kLattnSlice - 1) / kLattnSlice;
-    uint32_t x = blockIdx.x;
     const int v0 = int(x % uint32_t(slices)) * kLattnSlice;
     x /= uint32_t(slices);
     const int64_t H = a.heads, L = a.seqlen;
     const int64_t h = x % uint32_t(H);
     x /= uint32_t(H);
     const int64_t b = x % uint32_t(a.batch), seg = x / uint32_t(a.batch);
+    if (seg >= (STATE ? a.segs - 1 : a.segs)) return;  // what the last segment leaves is not needed
     const int64_t row0 = seg * a.seg_len, row1 = row0 + a.seg_len < L ? row0 + a.seg_len : L;
     const int64_t bh = b * H + h, cells = int64_t(j.dk) * j.dv;
 
@@ -851,14 +854,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
 template <int DT, int DKP, int NW, bool VEC>
 hipError_t launch_shape(const LattnArgs& a, hipStream_t stream)
 {
-    const int64_t blocks = lattn_slices(a.job[0].dv) * a.heads * a.batch * a.segs;
-    const dim3 grid(static_cast<uint32_t>(blocks), static_cast<uint32_t>(a.jobs)), block(64 * NW);
+    const int64_t walks = lattn_slices(a.job[0].dv) * a.heads * a.batch;
+    auto grid = [&](int64_t segs) { return static_cast<uint32_t>((walks * segs + 7) / 8 * 8 * a.jobs); };
+    const dim3 block(64 * NW);
     if (a.segs > 1) {
-        lattn_kernel<DT, DKP, NW, VEC, true><<<grid, block, 0, stream>>>(a);
+        lattn_kernel<DT, DKP, NW, VEC, true><<<grid(a.segs - 1), block, 0, stream>>>(a);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         if (hipError_t e = launch_lattn_join(a, stream); e != hipSuccess) return e;
     }
-    lattn_kernel<DT, DKP, NW, VEC, false><<<grid, block, 0, stream>>>(a);
+    lattn_kernel<DT, DKP, NW, VEC, false><<<grid(a.segs), block, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -12,7 +12,7 @@ namespace {
 // What segment i leaves, T_i, and the decay over it, f_i, give the state before each:
 // S_0 = h0, S_{i+1} = f_i S_i + T_i (T_i alone where the segment has a reset).  One thread per cell of
 // the state; S_i takes T_i's place.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kAhead = 8;
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(LattnArgs a)
 {
     const LattnJob& j = a.job[blockIdx.z];
@@ -20,12 +20,27 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(LattnArgs a)
     for (int64_t c = int64_t(blockIdx.y) * kJoinThreads + threadIdx.x; c < cells; c += int64_t(gridDim.y) * kJoinThreads) {
         const int64_t i = c / j.dv, k = c % j.dv;
         float s = j.h0 ? j.h0[bh * cells + i * j.si + k * j.sj] : 0.0f;
-        for (int64_t g = 0; g < a.segs; ++g) {
-            float* const p = j.seg + (g * n + bh) * cells + c;
-            const float left = *p, f = j.keep[g * n + bh];
-            *p = s;
-            s = f < 0.0f ? left : fmaf(f, s, left);
+        float* p = j.seg + bh * cells + c;
+        const float* f = j.keep + bh;
+        // the last segment's T is not there, nor needed; kAhead of the others are read at a time
+        const int64_t last = a.segs - 1;
+        for (int64_t g = 0; g < last; g += kAhead) {
+            float left[kAhead], keep[kAhead];
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                left[e] = g + e < last ? p[e * n * cells] : 0.0f;
+                keep[e] = g + e < last ? f[e * n] : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                if (g + e >= last) continue;
+                p[e * n * cells] = s;
+                s = keep[e] < 0.0f ? left[e] : fmaf(keep[e], s, left[e]);
+            }
+            p += kAhead * n * cells;
+            f += kAhead * n;
         }
+        j.seg[(last * n + bh) * cells + c] = s;
     }
 }
 
