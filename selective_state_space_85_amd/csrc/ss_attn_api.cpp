@@ -31,18 +31,18 @@ bool lattn_sizes(const LattnDims& d)
 
 bool lattn_widths(const LattnDims& d) { return d.dk <= ssk::kLattnMaxDim && d.dv <= ssk::kLattnMaxDim; }
 
-// How a walk is cut into segments of the sequence: so that there are about as many workgroups as the CUs
-// hold at once (bf16 two each, fp32 one), in segments of at least kLattnMinSeg rows.  The cut costs a
-// pass over k and v that forms the states between the segments, two fifths of a walk, and two launches:
-// in bf16 fewer than four segments do not pay for it.  Whole and cut, us, of 2048 rows in bf16: 16 heads 108
-// and 34, 64 heads 109 and 72, 128 heads 116 and 110 (in four), 200 heads 132 and 183 (in two); 16 heads of
-// 256 rows 19 and 25 (in two), of 512 rows 32 and 27 (in four).  fp32: 64 heads 435 and 188 (in four), 128
-// heads 436 and 346 (in two); 16 heads of 256 rows 60 and 54 (in two).
+// How a walk is cut into segments of the sequence: so that there are two workgroups for each CU, in
+// segments of at least kLattnMinSeg rows.  The cut costs a pass over k and v that forms the states
+// between the segments, two fifths of a walk, and two launches: in bf16 fewer than four segments do not
+// pay for it, in fp32 fewer than three.  Whole and cut, us, of 2048 rows in bf16: 16 walks 108 and 34, 64
+// walks 109 and 72, 128 walks 116 and 110 (in four), 200 walks 132 and 183 (in two); 16 walks of 256 rows 19
+// and 25 (in two), of 512 rows 32 and 27 (in four).  fp32: 64 walks 310 and 127, 128 walks 310 and 237 (in
+// four), 192 walks 318 and 354 (in two), 200 walks 311 and 371 (in two).
 constexpr int64_t kLattnMinSeg = 128, kLattnMaxSegs = 256;
 
 void lattn_plan(const LattnDims& d, ss_dtype dtype, int64_t walks, int64_t* len, int64_t* segs)
 {
-    const int64_t target = dtype == SS_F32 ? 256 : 512, least = dtype == SS_F32 ? 2 : 4;
+    const int64_t target = 512, least = dtype == SS_F32 ? 3 : 4;
     const int64_t most = d.seqlen / kLattnMinSeg;
     int64_t k = target / walks;
     k = k < most ? k : most;

@@ -56,17 +56,17 @@ __device__ __forceinline__ uint32_t pack_named(float a, float b)
     return r;
 }
 
-// What a product of 32 x 32 blocks needs of an element type.  A fragment holds kDepth indices of the
-// contraction for 32 rows (or columns) of an operand: lane l has row l % 32 and, of the kDepth
-// indices, the kDepth / 2 ones from (l / 32) * kDepth / 2.
+// What a product of 32 x 32 blocks needs of an element type.  A fragment holds 16 indices of the
+// contraction for 32 rows (or columns) of an operand: lane l has row l % 32 and, of the 16 indices, the
+// 8 from l / 32 * 8.
 template <int DT>
 struct Ops;
 
 template <>
 struct Ops<1> {  // bf16
     using E = uint16_t;
-    using Frag = bf16x8;
-    static constexpr int kDepth = 16;
+    using Frag = bf16x8;   // an operand of a product
+    using VFrag = bf16x8;  // a fragment of v as it is
     static constexpr int kEpc = 8;  // elements per 16 bytes
     static __device__ __forceinline__ f32x16 mma(const Frag& a, const Frag& b, const f32x16& c)
     {
@@ -86,7 +86,24 @@ struct Ops<1> {  // bf16
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * pitch));
         return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
-    // rows [kDepth u, kDepth u + kDepth) of an accumulator block as a fragment, each value rounded to
+    static __device__ __forceinline__ VFrag vcol(const E* base, int pitch, int lane) { return col(base, pitch, lane); }
+    static __device__ __forceinline__ Frag operand(const VFrag& v) { return v; }
+    // rows of q, k or P in LDS
+    template <int R, int P>
+    struct Tile {
+        E m[R][P];
+        __device__ __forceinline__ void put(int r, int c, const u32x4& v) { *reinterpret_cast<u32x4*>(&m[r][c]) = v; }
+        __device__ __forceinline__ Frag row(int r, int c) const { return Ops::row(&m[r][c]); }
+        __device__ __forceinline__ Frag col(int r, int c, int lane) const { return Ops::col(&m[r][c], P, lane); }
+        __device__ __forceinline__ float value(int r, int c) const { return widen(m[r][c]); }
+        // 4 values that no matrix instruction wrote, each under a mask
+        __device__ __forceinline__ void store4(int r, int c, const float (&v)[4], const uint32_t (&k)[4])
+        {
+            *reinterpret_cast<u32x2*>(&m[r][c]) = u32x2{pack_named(masked(v[0], k[0]), masked(v[1], k[1])),
+                                                        pack_named(masked(v[2], k[2]), masked(v[3], k[3]))};
+        }
+    };
+    // rows [16 u, 16 u + 16) of an accumulator block as a fragment, each value rounded to
     // bf16.  Registers 8 u .. 8 u + 3 hold rows 0-3 (lower half of the wave) and 4-7 (upper half) of
     // these 16, the next four 8-11 and 12-15: one swap of halves gives the lower half 0-7, the upper 8-15.
     static __device__ __forceinline__ Frag from_acc(const f32x16& c, int u)
@@ -128,7 +145,7 @@ struct Ops<1> {  // bf16
     static constexpr int kParts = 3;
     // whether an element of column lane % 32 is infinite or NaN: times a matrix of zeros, they leave NaN
     template <int N>
-    static __device__ __forceinline__ bool not_finite(const Frag (&v)[N])
+    static __device__ __forceinline__ bool not_finite(const VFrag (&v)[N])
     {
         const Frag zero = __builtin_bit_cast(Frag, u32x4{0, 0, 0, 0});
         f32x16 c;
@@ -163,79 +180,176 @@ struct Ops<1> {  // bf16
     {
         *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     }
-    // of values that no matrix instruction wrote, each under a mask
-    static __device__ __forceinline__ void store4_masked(E* p, const float (&v)[4], const uint32_t (&m)[4])
-    {
-        *reinterpret_cast<u32x2*>(p) = u32x2{pack_named(masked(v[0], m[0]), masked(v[1], m[1])),
-                                             pack_named(masked(v[2], m[2]), masked(v[3], m[3]))};
-    }
 };
 
+// fp32 by three bf16 parts of each operand: the leading 8 bits of its 24, of what they leave, and the
+// rest, each cut off, not rounded, so that no part overflows and nothing is lost (below 2^-110 the last
+// bits are).  Of the nine products of parts the six that matter are formed, smallest first; what is left
+// out is below 2^-23 of a product, 2^-25 on average, and fp32 rounds one by up to 2^-24.  That is three
+// eighths of the time of the fp32 matrix instruction, which has a sixteenth of bf16's rate.  q, k and P
+// lie in LDS as their parts, v as it is.
 template <>
-struct Ops<0> {  // fp32: the fp32 matrix instruction, four of them to a fragment
+struct Ops<0> {
     using E = float;
-    using Frag = f32x4;
-    static constexpr int kDepth = 8;
+    struct Frag {
+        bf16x8 p[3];
+    };
+    struct VFrag {
+        float v[8];
+    };
     static constexpr int kEpc = 4;
     static __device__ __forceinline__ f32x16 mma(const Frag& a, const Frag& b, f32x16 c)
     {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
-        return c;
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
     }
-    static __device__ __forceinline__ Frag row(const E* p) { return *reinterpret_cast<const Frag*>(p); }
-    static __device__ __forceinline__ Frag col(const E* base, int pitch, int lane)
+    // blocks of 16 x 16: fragments of 32 indices, lane l has row l % 16 and 8 indices from l / 16 * 8; of the
+    // result rows l / 16 * 4 .. + 3 of column l % 16
+    static __device__ __forceinline__ f32x4 mma16(const Frag& a, const Frag& b, f32x4 c)
     {
-        const E* p = base + 4 * (lane >> 5) * pitch + (lane & 31);
-        return Frag{p[0], p[pitch], p[2 * pitch], p[3 * pitch]};
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[2], b.p[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[0], b.p[2], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[1], b.p[1], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[1], b.p[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[0], b.p[1], c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[0], b.p[0], c, 0, 0, 0);
     }
-    // accumulator registers 4 u .. 4 u + 3 hold rows 8 u .. 8 u + 3 in the lower half, the next in the upper
+    // the parts of x and y, packed, x in the low halves
+    static __device__ __forceinline__ void parts(float x, float y, uint32_t (&p)[3])
+    {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
+            p[q] = __builtin_amdgcn_perm(v, u, 0x07060302u);
+            x -= __uint_as_float(u & 0xffff0000u);
+            y -= __uint_as_float(v & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ Frag operand(const VFrag& v)
+    {
+        u32x4 r[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[3];
+            parts(v.v[2 * i], v.v[2 * i + 1], p);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) r[q][i] = p[q];
+        }
+        Frag f;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) f.p[q] = __builtin_bit_cast(bf16x8, r[q]);
+        return f;
+    }
+    template <int R, int P>
+    struct Tile {
+        uint16_t m[3][R][P];
+        __device__ __forceinline__ void put4(int r, int c, float x, float y, float z, float w)
+        {
+            uint32_t a[3], b[3];
+            parts(x, y, a);
+            parts(z, w, b);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x2*>(&m[q][r][c]) = u32x2{a[q], b[q]};
+        }
+        __device__ __forceinline__ void put(int r, int c, const u32x4& v)
+        {
+            put4(r, c, __uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
+        }
+        __device__ __forceinline__ void store4(int r, int c, const float (&v)[4], const uint32_t (&k)[4])
+        {
+            put4(r, c, masked(v[0], k[0]), masked(v[1], k[1]), masked(v[2], k[2]), masked(v[3], k[3]));
+        }
+        __device__ __forceinline__ Frag row(int r, int c) const
+        {
+            return Frag{Ops<1>::row(&m[0][r][c]), Ops<1>::row(&m[1][r][c]), Ops<1>::row(&m[2][r][c])};
+        }
+        __device__ __forceinline__ Frag col(int r, int c, int lane) const
+        {
+            return Frag{Ops<1>::col(&m[0][r][c], P, lane), Ops<1>::col(&m[1][r][c], P, lane), Ops<1>::col(&m[2][r][c], P, lane)};
+        }
+        __device__ __forceinline__ float value(int r, int c) const
+        {
+            return (Ops<1>::widen(m[2][r][c]) + Ops<1>::widen(m[1][r][c])) + Ops<1>::widen(m[0][r][c]);
+        }
+    };
+    static __device__ __forceinline__ VFrag vcol(const E* base, int pitch, int lane)
+    {
+        const E* p = base + 8 * (lane >> 5) * pitch + (lane & 31);
+        VFrag f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f.v[i] = p[i * pitch];
+        return f;
+    }
     static __device__ __forceinline__ Frag from_acc(const f32x16& c, int u)
     {
-        return Frag{c[4 * u], c[4 * u + 1], c[4 * u + 2], c[4 * u + 3]};
+        u32x4 r[3];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t x[3], y[3];
+            parts(c[8 * u + 2 * i], c[8 * u + 2 * i + 1], x);
+            parts(c[8 * u + 4 + 2 * i], c[8 * u + 4 + 2 * i + 1], y);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                const auto s = __builtin_amdgcn_permlane32_swap(x[q], y[q], false, false);
+                r[q][i] = s[0];
+                r[q][2 + i] = s[1];
+            }
+        }
+        Frag f;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) f.p[q] = __builtin_bit_cast(bf16x8, r[q]);
+        return f;
     }
+    // one operand of three parts, weighed two elements at a step
     static constexpr int kParts = 1;
     static constexpr int kSteps = 4;
     struct Weighing {};
     template <int I>
-    static __device__ __forceinline__ void weigh(const Frag& v, const float* w, Frag (&part)[1], Weighing&)
+    static __device__ __forceinline__ void weigh(const VFrag& v, const float* w, Frag (&part)[1], Weighing&)
     {
-        part[0][I] = v[I] * w[I];
+        uint32_t p[3];
+        parts(v.v[2 * I] * w[2 * I], v.v[2 * I + 1] * w[2 * I + 1], p);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            u32x4 r = __builtin_bit_cast(u32x4, part[0].p[q]);
+            r[I] = p[q];
+            part[0].p[q] = __builtin_bit_cast(bf16x8, r);
+        }
     }
     template <int N>
-    static __device__ __forceinline__ bool not_finite(const Frag (&v)[N])
+    static __device__ __forceinline__ bool not_finite(const VFrag (&v)[N])
     {
         float c = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c = fmaf(v[i][e], 0.0f, c);
+            for (int e = 0; e < 8; ++e) c = fmaf(v[i].v[e], 0.0f, c);
         }
         return !(c == 0.0f);
     }
-    static __device__ __forceinline__ Frag finite_part(Frag v, uint32_t ones)
+    static __device__ __forceinline__ VFrag finite_part(VFrag f, uint32_t ones)
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = __float_as_uint(v[i]);
-            v[i] = __uint_as_float(u & ((u & 0x7f800000u) == 0x7f800000u ? 0u : ones));
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t u = __float_as_uint(f.v[i]);
+            f.v[i] = __uint_as_float(u & ((u & 0x7f800000u) == 0x7f800000u ? 0u : ones));
         }
-        return v;
+        return f;
     }
-    static __device__ __forceinline__ Frag drop_below(Frag v, int index, int from, uint32_t ones)
+    static __device__ __forceinline__ VFrag drop_below(VFrag f, int index, int from, uint32_t ones)
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) & (index + i < from ? 0u : ones));
-        return v;
+        for (int i = 0; i < 8; ++i) f.v[i] = masked(f.v[i], index + i < from ? 0u : ones);
+        return f;
     }
     static __device__ __forceinline__ float widen(E v) { return v; }
     static __device__ __forceinline__ void store4(E* p, const float (&v)[4])
     {
         *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    }
-    static __device__ __forceinline__ void store4_masked(E* p, const float (&v)[4], const uint32_t (&m)[4])
-    {
-        *reinterpret_cast<f32x4*>(p) = f32x4{masked(v[0], m[0]), masked(v[1], m[1]), masked(v[2], m[2]), masked(v[3], m[3])};
     }
 };
 
@@ -314,14 +428,16 @@ __device__ __forceinline__ void unroll(F&& f)
 template <int DT, int DKP, int NW>
 struct LattnShape {
     static constexpr int kThreads = 64 * NW;
-    // fp32 rows of 256 elements: half a chunk at a time fits the LDS
-    static constexpr int kC = DT == 0 && DKP == 256 ? 32 : 64;
-    static constexpr int kPad = Ops<DT>::kEpc;
-    static constexpr int kKP = DKP + kPad;       // pitch of q and k rows
-    static constexpr int kVP = 32 * NW + kPad;   // of v rows
-    static constexpr int kPP = kC + kPad;        // of P rows
+    // three parts of every row in fp32: half a chunk at a time fits the LDS, with two workgroups beside each
+    // other up to 128 elements
+    static constexpr int kC = DT == 0 ? 32 : 64;
+    static constexpr int kKP = DKP + 8;                       // pitch of q and k rows
+    static constexpr int kVP = 32 * NW + Ops<DT>::kEpc;       // of v rows
+    static constexpr int kPP = kC + 8;                        // of P rows
     static constexpr int kQPieces = kC * DKP / Ops<DT>::kEpc / kThreads;
     static constexpr int kVPieces = kC * 32 * NW / Ops<DT>::kEpc / kThreads;
+    // two workgroups per CU, but where registers or LDS do not allow it
+    static constexpr int kWaves = DKP == 256 || NW == 2 ? 1 : 2;
 };
 
 // grid (units rounded up to 8, times jobs); units are slices * heads * batch * segments, slices fastest.
@@ -329,19 +445,20 @@ struct LattnShape {
 // (dk and dv), are 8 apart, on one XCD and its L2 (8 x 2048 x 40 heads of 128, gradients: 457 -> 448 us).
 // STATE: forms what each segment but the last leaves in the state, from zero, and nothing else.
 template <int DT, int DKP, int NW, bool VEC, bool STATE>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0 || DKP == 256 || NW == 2 ? 1 : 2))) void lattn_kernel(LattnArgs a)
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnShape<DT, DKP, NW>::kWaves))) void lattn_kernel(LattnArgs a)
 {
     using O = Ops<DT>;
     using E = typename O::E;
     using Frag = typename O::Frag;
+    using VFrag = typename O::VFrag;
     using G = LattnShape<DT, DKP, NW>;
-    constexpr int C = G::kC, kTB = C / 32, kDB = DKP / 32, kDepth = O::kDepth, kHalf = kDepth / 2;
+    constexpr int C = G::kC, kTB = C / 32, kDB = DKP / 32, kDepth = 16, kHalf = 8;
     constexpr int kKS = C / kDepth, kSub = 32 / kDepth;
 
-    __shared__ __align__(16) E sQ[STATE ? 1 : C][G::kKP];
-    __shared__ __align__(16) E sK[C][G::kKP];
+    __shared__ __align__(16) typename O::template Tile<STATE ? 1 : C, G::kKP> sQ;
+    __shared__ __align__(16) typename O::template Tile<C, G::kKP> sK;
     __shared__ __align__(16) E sV[C][G::kVP];
-    __shared__ __align__(16) E sP[STATE ? 1 : C][G::kPP];
+    __shared__ __align__(16) typename O::template Tile<STATE ? 1 : C, G::kPP> sP;
     __shared__ float s_enter[C + 1];    // out_scale a^j
     __shared__ float s_pow[C + 1];      // a^j
     __shared__ float s_pair[2 * C];              // pair_scale a^(C - 1 - x), 0 past C
@@ -494,14 +611,35 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
         }
     };
 
-    // Blocks of P^T: 0 is (s 0-31, t 0-31), 1 is (s 0-31, t 32-63), 2 is (s 32-63, t 32-63).  A wave left
-    // without one forms the last one too and writes the same numbers: every wave runs the same code.
-    constexpr int kBlocks = kTB == 2 ? 3 : 1, kRounds = (kBlocks + NW - 1) / NW;
+    // Blocks of P^T.  Of 64 rows, 32 x 32: (s 0-31, t 0-31), (s 0-31, t 32-63) and (s 32-63, t 32-63); a wave
+    // left without one forms the last one too and writes the same numbers, so that every wave runs the same
+    // code.  Of 32 rows, 16 x 16, all four.  A lane has column t = tb + lt of its block and, of its rows, four
+    // neighbouring ones at a time.
+    constexpr bool kWide = kTB == 2;
+    constexpr int kBlocks = kWide ? 3 : 4, kRounds = (kBlocks + NW - 1) / NW, kQuads = kWide ? 4 : 1;
 
-    // bit r: whether column t of a block on the diagonal sees the row s of register r
-    uint32_t diagonal = 0;
+    auto block = [&](int i, int& sb, int& tb) {
+        if constexpr (kWide) {
+            const int blk = w + i * NW < kBlocks ? w + i * NW : kBlocks - 1;
+            sb = blk == 2 ? 32 : 0;
+            tb = blk == 0 ? 0 : 32;
+        } else {
+            sb = (w + i * NW) / 2 * 16;
+            tb = (w + i * NW) % 2 * 16;
+        }
+    };
+    auto column = [&] { return kWide ? l32 : lane & 15; };
+    auto first_row = [&](int quad) { return kWide ? 8 * quad + 4 * hl : 4 * (lane >> 4); };
+    // a bit for each register of a block: whether row t comes after row s or is it
+    uint32_t causal[kRounds];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) diagonal |= (8 * (r >> 2) + 4 * hl + (r & 3) <= l32 ? 1u : 0u) << r;
+    for (int i = 0; i < kRounds; ++i) {
+        int sb, tb;
+        block(i, sb, tb);
+        causal[i] = 0;
+#pragma unroll
+        for (int r = 0; r < 4 * kQuads; ++r) causal[i] |= (sb + first_row(r / 4) + r % 4 <= tb + column() ? 1u : 0u) << r;
+    }
 
     const int left0 = int(row1 - row0);
     start_load(int(row0), left0 < C ? left0 : C);
@@ -513,8 +651,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
         // ---- the chunk into LDS, the next one's loads on their way ----
 #pragma unroll
         for (int i = 0; i < G::kQPieces; ++i) {
-            if constexpr (!STATE) *reinterpret_cast<u32x4*>(&sQ[qr + i * kQR][qc]) = fq[i];
-            *reinterpret_cast<u32x4*>(&sK[qr + i * kQR][qc]) = fk[i];
+            if constexpr (!STATE) sQ.put(qr + i * kQR, qc, fq[i]);
+            sK.put(qr + i * kQR, qc, fk[i]);
         }
 #pragma unroll
         for (int i = 0; i < G::kVPieces; ++i) *reinterpret_cast<u32x4*>(&sV[vr + i * kVR][vc]) = fv[i];
@@ -532,29 +670,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
         // that the last row's state has from outside
         const int e0 = rev && t0 == 0 ? 0 : 1;
 
-        Frag vf[kKS];  // this wave's columns of v
+        VFrag vf[kKS];  // this wave's columns of v
         auto columns = [&] {
 #pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) vf[ks] = O::col(&sV[ks * kDepth][c0], G::kVP, lane);
+            for (int ks = 0; ks < kKS; ++ks) vf[ks] = O::vcol(&sV[ks * kDepth][c0], G::kVP, lane);
         };
         columns();
         f32x16 o[kTB];
         bool odd = false;  // whether one of them is infinite or NaN
         if constexpr (!STATE) {
             // ---- P^T = K Q^T with its decays, into LDS as P (t, s); O^T = S^T Q^T ----
-            f32x16 p[kRounds];
-            uint32_t see[kRounds];
-            auto block = [&](int i, int& sb, int& tb) {
-                const int blk = w + i * NW < kBlocks ? w + i * NW : kBlocks - 1;
-                sb = blk == 2 ? 32 : 0;
-                tb = blk == 0 ? 0 : 32;
-            };
+            typedef std::conditional_t<kWide, f32x16, f32x4> Block;
+            Block p[kRounds];
+            uint32_t see[kRounds];  // the same for whether row t sees row s
 #pragma unroll
-            for (int i = 0; i < kRounds; ++i) {
-                int sb, tb;
-                block(i, sb, tb);
-                see[i] = sb == tb ? diagonal : 0xffffu;
-            }
+            for (int i = 0; i < kRounds; ++i) see[i] = causal[i];
+            const int lt = column();
             if (resets) {
                 cold();
 #pragma unroll
@@ -562,74 +693,74 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
                     int sb, tb;
                     block(i, sb, tb);
                     // the first row that row t sees
-                    const uint64_t upto = resets & (~uint64_t(0) >> (63 - tb - l32));
+                    const uint64_t upto = resets & (~uint64_t(0) >> (63 - tb - lt));
                     const int from = upto ? 63 - __builtin_clzll(upto) : 0;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (sb + 8 * (r >> 2) + 4 * hl + (r & 3) < from) see[i] &= ~(1u << r);
+                    for (int r = 0; r < 4 * kQuads; ++r)
+                        if (sb + first_row(r / 4) + r % 4 < from) see[i] &= ~(1u << r);
                 }
             }
             // four rows s of a block of P at a time
             auto pairs = [&](auto i_v) {
-                constexpr int i = decltype(i_v)::value / 4, q4 = decltype(i_v)::value % 4;
+                constexpr int i = decltype(i_v)::value / kQuads, quad = decltype(i_v)::value % kQuads;
                 int sb, tb;
                 block(i, sb, tb);
-                const int t = tb + l32, s = sb + 8 * q4 + 4 * hl;
+                const int t = tb + lt, s = sb + first_row(quad);
                 const float* const f = &s_pair[C - 1 - t + s];
                 float x[4];
                 uint32_t m[4];
                 // every product masked afterwards: a choice would become a branch
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[e] = p[i][4 * q4 + e] * f[e];
-                    m[e] = uint32_t(__builtin_amdgcn_sbfe(int(see[i]), 4 * q4 + e, 1));
+                    x[e] = p[i][4 * quad + e] * f[e];
+                    m[e] = uint32_t(__builtin_amdgcn_sbfe(int(see[i]), 4 * quad + e, 1));
                 }
-                O::store4_masked(&sP[t][s], x, m);
+                sP.store4(t, s, x, m);
             };
 #pragma unroll
             for (int tb = 0; tb < kTB; ++tb) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[tb][r] = 0.0f;
             }
-#pragma unroll
-            for (int i = 0; i < kRounds; ++i) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) p[i][r] = 0.0f;
-            }
             // every fragment is read some steps before its product
-            constexpr int kSteps = DKP / kDepth, kAhead = 3, kPieces = 4 * kRounds;
+            constexpr int kSteps = DKP / kDepth, kPieces = kQuads * kRounds;
             unroll<kRounds>([&](auto x_v) {
-                constexpr int x = decltype(x_v)::value;
+                constexpr int x = decltype(x_v)::value, kDeep = kWide ? 16 : 32, kTimes = DKP / kDeep, kAhead = kWide ? 3 : 1;
                 int sb, tb;
                 block(x, sb, tb);
                 Frag kq[kAhead + 1][2];
                 auto fetch = [&](int i) {
-                    kq[i % (kAhead + 1)][0] = O::row(&sK[sb + l32][kDepth * i + kHalf * hl]);
-                    kq[i % (kAhead + 1)][1] = O::row(&sQ[tb + l32][kDepth * i + kHalf * hl]);
+                    const int c = kDeep * i + (kWide ? 8 * hl : 8 * (lane >> 4));
+                    kq[i % (kAhead + 1)][0] = sK.row(sb + lt, c);
+                    kq[i % (kAhead + 1)][1] = sQ.row(tb + lt, c);
                 };
 #pragma unroll
+                for (int r = 0; r < 4 * kQuads; ++r) p[x][r] = 0.0f;
+#pragma unroll
                 for (int i = 0; i < kAhead; ++i) fetch(i);
-                unroll<kSteps>([&](auto i_v) {
+                unroll<kTimes>([&](auto i_v) {
                     constexpr int i = decltype(i_v)::value;
-                    if constexpr (i + kAhead < kSteps) fetch(i + kAhead);
-                    p[x] = O::mma(kq[i % (kAhead + 1)][0], kq[i % (kAhead + 1)][1], p[x]);
+                    if constexpr (i + kAhead < kTimes) fetch(i + kAhead);
+                    if constexpr (kWide) p[x] = O::mma(kq[i % (kAhead + 1)][0], kq[i % (kAhead + 1)][1], p[x]);
+                    else p[x] = O::mma16(kq[i % (kAhead + 1)][0], kq[i % (kAhead + 1)][1], p[x]);
                     __builtin_amdgcn_sched_barrier(0);
                 });
             });
-            Frag qf[3][kTB];
+            constexpr int kNext = DT == 1 ? 2 : 1;
+            Frag qf[kNext + 1][kTB];
             auto queries = [&](int i) {
 #pragma unroll
-                for (int tb = 0; tb < kTB; ++tb) qf[i % 3][tb] = O::row(&sQ[32 * tb + l32][kDepth * i + kHalf * hl]);
+                for (int tb = 0; tb < kTB; ++tb) qf[i % (kNext + 1)][tb] = sQ.row(32 * tb + l32, kDepth * i + kHalf * hl);
             };
-            queries(0);
-            queries(1);
+#pragma unroll
+            for (int i = 0; i < kNext; ++i) queries(i);
             // the products of S with, between them, the next chunk's loads and the rest of P
             unroll<kSteps>([&](auto i_v) {
                 constexpr int i = decltype(i_v)::value;
-                if constexpr (i + 2 < kSteps) queries(i + 2);
+                if constexpr (i + kNext < kSteps) queries(i + kNext);
                 const Frag s = O::from_acc(st[i / kSub], i % kSub);
 #pragma unroll
-                for (int tb = 0; tb < kTB; ++tb) o[tb] = O::mma(s, qf[i % 3][tb], o[tb]);
+                for (int tb = 0; tb < kTB; ++tb) o[tb] = O::mma(s, qf[i % (kNext + 1)][tb], o[tb]);
                 constexpr int m0 = kLoads * i / kSteps, m1 = kLoads * (i + 1) / kSteps;
                 unroll<m1 - m0>([&](auto m_v) { load_one(std::integral_constant<int, m0 + decltype(m_v)::value>()); });
                 constexpr int p0 = i < 2 ? 0 : kPieces * (i - 2) / (kSteps - 2), p1 = i < 2 ? 0 : kPieces * (i - 1) / (kSteps - 2);
@@ -660,23 +791,27 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
             const int thread = 64 * w + lane;
             if (resets) {
                 for (int p = thread; p < last * (DKP / O::kEpc); p += G::kThreads)
-                    *reinterpret_cast<u32x4*>(&sK[p / (DKP / O::kEpc)][p % (DKP / O::kEpc) * O::kEpc]) = u32x4{0, 0, 0, 0};
+                    sK.put(p / (DKP / O::kEpc), p % (DKP / O::kEpc) * O::kEpc, u32x4{0, 0, 0, 0});
             }
             if (n < C)
                 for (int i = thread; i < C; i += G::kThreads) s_leave[i] = i < n ? s_weight[i + C - n] : 0.0f;
             __syncthreads();
         }
 
-        Frag part[2][O::kParts], kf[2][kDB];
+        constexpr int kKeys = DT == 1 ? kDB : 1;  // fragments of k held for a step, and as many for the next
+        Frag part[2][O::kParts], kf[2][kKeys];
         float wt[2][kHalf];
         typename O::Weighing steps;
         auto weights = [&](int ks) {
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) wt[ks & 1][i] = s_leave[ks * kDepth + kHalf * hl + i];
         };
-        auto keys = [&](int ks) {
+        auto keys = [&](int step) {  // kKeys blocks of d of 16 rows
 #pragma unroll
-            for (int d = 0; d < kDB; ++d) kf[ks & 1][d] = O::col(&sK[ks * kDepth][32 * d], G::kKP, lane);
+            for (int e = 0; e < kKeys; ++e) {
+                const int at = step * kKeys + e;
+                kf[step & 1][e] = sK.col(at / kDB * kDepth, 32 * (at % kDB), lane);
+            }
         };
         auto weigh = [&](auto ks_v, auto lo_v, auto hi_v) {  // steps [lo, hi) of it
             constexpr int ks = decltype(ks_v)::value, lo = decltype(lo_v)::value, hi = decltype(hi_v)::value;
@@ -702,7 +837,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
 #pragma unroll
             for (int i = 0; i < kProducts; ++i) {
                 const int ks = i < 2 * kSub && kTB == 2 ? i / 2 : i - (kTB - 1) * kSub, tb = kTB == 2 && (i >= 2 * kSub || i % 2 == 1);
-                pf[i] = O::row(&sP[32 * tb + l32][ks * kDepth + kHalf * hl]);
+                pf[i] = sP.row(32 * tb + l32, ks * kDepth + kHalf * hl);
             }
             keys(0);
             weigh(zero, zero, all);  // while P's rows come
@@ -710,7 +845,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
             unroll<kProducts>([&](auto i_v) {
                 constexpr int i = decltype(i_v)::value;
                 constexpr int ks = i < 2 * kSub && kTB == 2 ? i / 2 : i - (kTB - 1) * kSub, tb = kTB == 2 && (i >= 2 * kSub || i % 2 == 1);
-                o[tb] = O::mma(vf[ks], pf[i], o[tb]);
+                o[tb] = O::mma(O::operand(vf[ks]), pf[i], o[tb]);
                 // the state's own decay beside these
                 constexpr int r0 = 16 * kDB * i / kProducts, r1 = 16 * kDB * (i + 1) / kProducts;
                 unroll<r1 - r0>([&](auto r_v) {
@@ -728,7 +863,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
 #pragma unroll 1
                     for (int s = 0; s < 32 * (tb + 1); ++s) {
                         const bool sees = s <= t && s >= from;
-                        const float p = O::widen(sP[t][s]);
+                        const float p = sP.value(t, s);
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
                             const float v = O::widen(sV[s][c0 + 8 * (r >> 2) + 4 * hl + (r & 3)]);
@@ -794,13 +929,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DT == 0
         // blocks of the state and do not wait for one another.
         unroll<kKS>([&](auto ks_v) {
             constexpr int ks = decltype(ks_v)::value, kProducts = O::kParts * kDB;
-            if constexpr (ks + 1 < kKS) {
-                weights(ks + 1);
-                keys(ks + 1);
-            }
+            if constexpr (ks + 1 < kKS) weights(ks + 1);
             unroll<kProducts>([&](auto i_v) {
                 constexpr int i = decltype(i_v)::value, q = O::kParts - 1 - i / kDB, d = i % kDB;
-                st[d] = O::mma(kf[ks & 1][d], part[ks & 1][q], st[d]);
+                constexpr int step = (ks * kDB + d) / kKeys;
+                if constexpr (q == O::kParts - 1 && d % kKeys == 0 && step + 1 < kKS * kDB / kKeys) keys(step + 1);
+                st[d] = O::mma(kf[step & 1][d % kKeys], part[ks & 1][q], st[d]);
                 if constexpr (ks + 1 < kKS)
                     weigh(std::integral_constant<int, ks + 1>(), std::integral_constant<int, O::kSteps * i / kProducts>(),
                           std::integral_constant<int, O::kSteps * (i + 1) / kProducts>());
