@@ -41,8 +41,10 @@ extern "C" {
  *               may be exactly h0
  * scale must be finite.  k_dim and v_dim above 256, row strides (and heads * k_dim, heads * v_dim)
  * above 2^20 elements and seqlen from 2^30 on are SS_ERR_UNSUPPORTED.
- * bf16: the state is fp32 throughout; it and the products q k^T are rounded to bf16 where they
- * enter a product with q or v.  A state that holds an infinity gives infinities or NaN.
+ * The state is fp32 throughout.  bf16: it and the products q k^T are rounded to bf16 where they
+ * enter a product with q or v.  fp32: products are formed from three bf16 parts of each operand,
+ * which hold its 24 bits.  An infinity in q, k, v or the state gives infinities or NaN in the rows
+ * and states that see it, and none in the others.
  */
 size_t ss_lattn_workspace_bytes(int64_t batch, int64_t seqlen, int64_t qk_heads, int64_t heads, int64_t k_dim,
                                 int64_t v_dim, ss_dtype dtype); /* 0: none needed */
@@ -104,8 +106,9 @@ ss_status ss_lattn_step(float* h, const void* q, int64_t q_row_stride, const voi
  *   pos      : (tokens,) int64
  *   inv_freq : (half_rotary,) fp32; NULL if half_rotary is 0
  *   qo, ko   : (tokens, q_heads, width), (tokens, k_heads, width) dtype outputs
- * width is at most 512 (SS_ERR_UNSUPPORTED above) and at least 2 half_rotary; eps is finite and
- * not negative.
+ * width is at most 512, q_heads and k_heads at most 2^24 (SS_ERR_UNSUPPORTED above); width is at least
+ * 2 half_rotary; eps is finite and not negative.  The mean of the squares is fp32: a head whose squares
+ * sum past its range is normed to 0.
  */
 ss_status ss_qknorm_fwd(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const float* w_q,
                         const float* w_k, const int64_t* pos, const float* inv_freq, float eps, int interleaved,

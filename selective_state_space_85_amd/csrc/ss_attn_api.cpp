@@ -323,7 +323,8 @@ ss_status qknorm_check(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
     if (!isfinite(eps) || eps < 0.0f) return SS_ERR_INVALID_ARG;
     if (q_ld < q_heads * width || k_ld < k_heads * width) return SS_ERR_INVALID_ARG;
     if (!known(dtype) || width > ssk::kQknormMaxDim) return SS_ERR_UNSUPPORTED;
-    if (tokens > INT32_MAX / 256) return SS_ERR_UNSUPPORTED;
+    if (tokens > INT32_MAX / 256 || q_heads > ssk::kQknormMaxHeads || k_heads > ssk::kQknormMaxHeads)
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype);
     if (!aligned(q, uintptr_t(es)) || !aligned(k, uintptr_t(es)) || !aligned(w_q, 4) || !aligned(w_k, 4) ||
         !aligned(pos, 8) || !aligned(inv_freq, 4))

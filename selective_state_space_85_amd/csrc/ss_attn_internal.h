@@ -76,6 +76,7 @@ hipError_t launch_lattn_step(const LattnStepArgs& a, int dtype, hipStream_t stre
 // ---- norms and rotation of queries and keys --------------------------------------------
 
 constexpr int kQknormMaxDim = 512;
+constexpr int64_t kQknormMaxHeads = int64_t(1) << 24;  // the heads of a tile's tokens are counted in 32 bits
 
 struct QknormSide {
     const void* x;   // (tokens, heads, width), rows ld apart

@@ -107,6 +107,8 @@ REFUSED = [
     *[(f, dict(half=v), INVALID) for f in (qknorm_fwd, qknorm_bwd) for v in (-1, 33)],
     *[(f, dict(w=513, qs=4096, ks=4096), UNSUPPORTED) for f in (qknorm_fwd, qknorm_bwd)],
     *[(f, dict(n=1 << 32), UNSUPPORTED) for f in (qknorm_fwd, qknorm_bwd)],
+    *[(f, dict(n=1, w=1, half=0, **{h: (1 << 24) + 1, s: 1 << 26}), UNSUPPORTED) for f in (qknorm_fwd, qknorm_bwd)
+      for h, s in (("hq", "qs"), ("hk", "ks"))],
     *[(f, dict(n=BIG, hq=BIG, qs=BIG), INVALID) for f in (qknorm_fwd, qknorm_bwd)],
     *[(sample, {n: v}, INVALID) for n in ("n", "v") for v in (0, -1)],
     (sample, dict(v=(1 << 24) + 1, xs=1 << 25), UNSUPPORTED),
