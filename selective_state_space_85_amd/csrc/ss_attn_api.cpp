@@ -32,23 +32,26 @@ bool lattn_sizes(const LattnDims& d)
 bool lattn_widths(const LattnDims& d) { return d.dk <= ssk::kLattnMaxDim && d.dv <= ssk::kLattnMaxDim; }
 
 // How a walk is cut into segments of the sequence: so that there are two workgroups for each CU, in
-// segments of at least kLattnMinSeg rows.  The cut costs a pass over k and v that forms the states
+// segments of at least two chunks of the kernel's.  The cut costs a pass over k and v that forms the states
 // between the segments, two fifths of a walk, and two launches: in bf16 fewer than four segments do not
 // pay for it, in fp32 fewer than three.  Whole and cut, us, of 2048 rows in bf16: 16 walks 108 and 34, 64
 // walks 109 and 72, 128 walks 116 and 110 (in four), 200 walks 132 and 183 (in two); 16 walks of 256 rows 19
 // and 25 (in two), of 512 rows 32 and 27 (in four).  fp32: 64 walks 310 and 127, 128 walks 310 and 237 (in
-// four), 192 walks 318 and 354 (in two), 200 walks 311 and 371 (in two).
-constexpr int64_t kLattnMinSeg = 128, kLattnMaxSegs = 256;
+// four), 192 walks 318 and 354 (in two), 200 walks 311 and 371 (in two).  Segments of one chunk and two, bf16:
+// 16 walks of 256 rows 23 and 20 (whole), of 512 rows 25 and 29, of 2048 rows 41 and 35; fp32: 16 walks of
+// 128 rows 30 and 25 (whole), of 2048 rows the same.  Of two chunks and four, fp32: 16 walks of 256 rows 31
+// and 43 (whole), of 512 rows 33 and 45, of 2048 rows 60 and 56.
+constexpr int64_t kLattnMaxSegs = 256;
 
 void lattn_plan(const LattnDims& d, ss_dtype dtype, int64_t walks, int64_t* len, int64_t* segs)
 {
-    const int64_t target = 512, least = dtype == SS_F32 ? 3 : 4;
-    const int64_t most = d.seqlen / kLattnMinSeg;
+    const int64_t target = 512, least = dtype == SS_F32 ? 3 : 4, chunk = ssk::lattn_chunk(dtype == SS_F32 ? 0 : 1);
+    const int64_t most = d.seqlen / (2 * chunk);
     int64_t k = target / walks;
     k = k < most ? k : most;
     k = k < kLattnMaxSegs ? k : kLattnMaxSegs;
     if (k < least) k = 1;
-    *len = ceil_div(ceil_div(d.seqlen, k), ssk::kLattnChunk) * ssk::kLattnChunk;
+    *len = ceil_div(ceil_div(d.seqlen, k), chunk) * chunk;
     *segs = ceil_div(d.seqlen, *len);
 }
 

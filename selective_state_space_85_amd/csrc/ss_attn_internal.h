@@ -11,7 +11,9 @@ namespace ssk {
 // ---- linear attention with a decay for each head ---------------------------------------
 
 constexpr int kLattnMaxDim = 256;
-constexpr int64_t kLattnChunk = 64;  // rows per chunk: the unit that sequences are cut in
+// rows per chunk, the unit that sequences are cut in: in fp32 the three parts of every row fit the LDS for 32,
+// with two workgroups beside each other up to 128 elements
+constexpr int lattn_chunk(int dtype) { return dtype == 0 ? 32 : 64; }
 
 // One walk over the sequence.  Forward, dq, dk and dv are the same operation
 //   o_t = sum over s up to t of a^(t - s) (q_t . k_s) v_s  (+ a^(t + 1) h0^T q_t)
@@ -41,7 +43,7 @@ struct LattnArgs {
     const float* log_decay;
     const uint8_t* reset;  // nullable
     int64_t batch, seqlen, heads;
-    int64_t seg_len, segs;  // rows of a segment (a multiple of kLattnChunk), segments
+    int64_t seg_len, segs;  // rows of a segment (a multiple of lattn_chunk), segments
 };
 // Columns of v that one workgroup takes.
 constexpr int kLattnSlice = 128;

@@ -428,9 +428,7 @@ __device__ __forceinline__ void unroll(F&& f)
 template <int DT, int DKP, int NW>
 struct LattnShape {
     static constexpr int kThreads = 64 * NW;
-    // three parts of every row in fp32: half a chunk at a time fits the LDS, with two workgroups beside each
-    // other up to 128 elements
-    static constexpr int kC = DT == 0 ? 32 : 64;
+    static constexpr int kC = lattn_chunk(DT);
     static constexpr int kKP = DKP + 8;                       // pitch of q and k rows
     static constexpr int kVP = 32 * NW + Ops<DT>::kEpc;       // of v rows
     static constexpr int kPP = kC + 8;                        // of P rows
