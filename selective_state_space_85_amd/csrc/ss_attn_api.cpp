@@ -31,8 +31,8 @@ bool lattn_sizes(const LattnDims& d)
 
 bool lattn_widths(const LattnDims& d) { return d.dk <= ssk::kLattnMaxDim && d.dv <= ssk::kLattnMaxDim; }
 
-// How a walk is cut into segments of the sequence: so that there are two workgroups for each CU, in
-// segments of at least two chunks of the kernel's.  The cut costs a pass over k and v that forms the states
+// How a walk is cut into segments of the sequence: so that a launch has as many workgroups as the CUs hold
+// beside each other, in segments of at least two chunks of the kernel's.  The cut costs a pass over k and v that forms the states
 // between the segments, two fifths of a walk, and two launches: in bf16 fewer than four segments do not
 // pay for it, in fp32 fewer than three.  Whole and cut, us, of 2048 rows in bf16: 16 walks 108 and 34, 64
 // walks 109 and 72, 128 walks 116 and 110 (in four), 200 walks 132 and 183 (in two); 16 walks of 256 rows 19
@@ -43,20 +43,30 @@ bool lattn_widths(const LattnDims& d) { return d.dk <= ssk::kLattnMaxDim && d.dv
 // and 43 (whole), of 512 rows 33 and 45, of 2048 rows 60 and 56.
 constexpr int64_t kLattnMaxSegs = 256;
 
-void lattn_plan(const LattnDims& d, ss_dtype dtype, int64_t walks, int64_t* len, int64_t* segs)
+struct LattnCut {
+    int64_t len, segs;  // rows of a segment, segments
+};
+
+// For a launch of `jobs` walks with widths dk and dv of each head.
+LattnCut lattn_cut(const LattnDims& d, ss_dtype dtype, int jobs, int64_t dk, int64_t dv)
 {
-    const int64_t target = 512, least = dtype == SS_F32 ? 3 : 4, chunk = ssk::lattn_chunk(dtype == SS_F32 ? 0 : 1);
+    const int dt = dtype == SS_F32 ? 0 : 1;
+    const int64_t walks = jobs * d.batch * d.heads * ssk::lattn_slices(dv);
+    const int64_t target = 256 * ssk::lattn_resident(dt, int(dk), int(dv)), least = dt == 0 ? 3 : 4, chunk = ssk::lattn_chunk(dt, int(dk), int(dv));
     const int64_t most = d.seqlen / (2 * chunk);
     int64_t k = target / walks;
     k = k < most ? k : most;
     k = k < kLattnMaxSegs ? k : kLattnMaxSegs;
     if (k < least) k = 1;
-    *len = ceil_div(ceil_div(d.seqlen, k), chunk) * chunk;
-    *segs = ceil_div(d.seqlen, *len);
+    const int64_t len = ceil_div(ceil_div(d.seqlen, k), chunk) * chunk;
+    return {len, ceil_div(d.seqlen, len)};
 }
 
+// Whether the backward's three walks, of widths (dk, dv) and (dv, dk), go in one launch.
+bool lattn_together(const LattnDims& d) { return ssk::lattn_class(int(d.dk), int(d.dv)) == ssk::lattn_class(int(d.dv), int(d.dk)); }
+
 struct LattnLayout {
-    int64_t len, segs;
+    LattnCut cut[3];  // of each walk: the forward's, or dv's, dk's and dq's
     int64_t seg[3], keep[3], part[2];
     int64_t total;
 };
@@ -64,16 +74,17 @@ struct LattnLayout {
 bool lattn_layout(const LattnDims& d, ss_dtype dtype, bool back, LattnLayout* w)
 {
     if (!lattn_sizes(d)) return false;
-    const int jobs = back ? 3 : 1;
-    int64_t walks;
-    if (!mul(d.batch, d.heads, &walks)) return false;
-    lattn_plan(d, dtype, back ? 3 * walks : walks * ssk::lattn_slices(d.dv), &w->len, &w->segs);
+    int64_t walks, n, f;
+    if (!mul(d.batch, d.heads, &walks) || !mul(walks, 6, &n)) return false;
+    const bool three = back && lattn_together(d);
+    w->cut[0] = lattn_cut(d, dtype, three ? 3 : 1, d.dk, d.dv);
+    w->cut[1] = w->cut[2] = three ? w->cut[0] : lattn_cut(d, dtype, 2, d.dv, d.dk);
     Regions r;
-    int64_t n, f;
-    if (!mul(w->segs, d.states(), &n) || !mul(w->segs, walks, &f)) return false;
-    for (int i = 0; i < jobs; ++i) {
-        w->seg[i] = r.add(w->segs > 1 ? n : 0, 4);
-        w->keep[i] = r.add(w->segs > 1 ? f : 0, 4);
+    for (int i = 0; i < (back ? 3 : 1); ++i) {
+        const int64_t segs = w->cut[i].segs;
+        if (!mul(segs, d.states(), &n) || !mul(segs, walks, &f)) return false;
+        w->seg[i] = r.add(segs > 1 ? n : 0, 4);
+        w->keep[i] = r.add(segs > 1 ? f : 0, 4);
     }
     for (int i = 0; i < 2; ++i) w->part[i] = r.add(back && d.share() > 1 ? d.batch * d.seqlen * d.heads * d.dk : 0, 4);
     w->total = r.at;
@@ -91,8 +102,9 @@ bool lattn_too_wide(int64_t a, int64_t b, int64_t c, int64_t d)
 bool lattn_grid_ok(const LattnDims& d, const LattnLayout& w)
 {
     int64_t n;
+    const int64_t segs = w.cut[0].segs > w.cut[1].segs ? w.cut[0].segs : w.cut[1].segs;
     // two slices of each of three walks, rounded up to 8
-    return d.seqlen < (int64_t(1) << 30) && mul(d.batch * d.heads, w.segs, &n) && mul(n, 6, &n) && n <= INT32_MAX - 24 &&
+    return d.seqlen < (int64_t(1) << 30) && mul(d.batch * d.heads, segs, &n) && mul(n, 6, &n) && n <= INT32_MAX - 24 &&
            launch_fits(n + 24, 256);
 }
 
@@ -103,7 +115,7 @@ size_t lattn_bytes(const LattnDims& d, ss_dtype dtype, bool back)
     return lattn_layout(d, dtype, back, &w) ? static_cast<size_t>(w.total) : kBad;
 }
 
-ssk::LattnArgs lattn_args(const LattnDims& d, const LattnLayout& w, const float* log_decay, const uint8_t* reset)
+ssk::LattnArgs lattn_args(const LattnDims& d, const LattnCut& cut, const float* log_decay, const uint8_t* reset)
 {
     ssk::LattnArgs a{};
     a.log_decay = log_decay;
@@ -111,8 +123,8 @@ ssk::LattnArgs lattn_args(const LattnDims& d, const LattnLayout& w, const float*
     a.batch = d.batch;
     a.seqlen = d.seqlen;
     a.heads = d.heads;
-    a.seg_len = w.len;
-    a.segs = w.segs;
+    a.seg_len = cut.len;
+    a.segs = cut.segs;
     return a;
 }
 
@@ -169,11 +181,11 @@ ss_status ss_lattn_fwd(const void* q, int64_t q_row_stride, const void* k, int64
     if (st != SS_OK) return st;
 
     char* const ws = static_cast<char*>(workspace);
-    ssk::LattnArgs a = lattn_args(d, w, log_decay, reset);
+    ssk::LattnArgs a = lattn_args(d, w.cut[0], log_decay, reset);
     ssk::LattnJob& j = a.job[0];
     j = {q, k, v, q_row_stride, k_row_stride, v_row_stride, int(d.share()), int(d.share()), 1, int(k_dim), int(v_dim),
          o, false, false, h0, h_last, v_dim, 1, scale, 1.0f, scale, nullptr, nullptr};
-    if (w.segs > 1) {
+    if (a.segs > 1) {
         j.seg = reinterpret_cast<float*>(ws + w.seg[0]);
         j.keep = reinterpret_cast<float*>(ws + w.keep[0]);
     }
@@ -237,20 +249,17 @@ ss_status ss_lattn_bwd(const void* q, int64_t q_row_stride, const void* k, int64
     const ssk::LattnJob jv = {k, q, d_o, k_row_stride, q_row_stride, do_row_stride, share, share, 1, ki, vi, dv, false,
                               true, dh_last, dh0, v_dim, 1, scale, scale, 1.0f, nullptr, nullptr};
     ssk::LattnJob jobs[] = {jv, jk, jq};
-    if (w.segs > 1)
-        for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 3; ++i)
+        if (w.cut[i].segs > 1) {
             jobs[i].seg = reinterpret_cast<float*>(ws + w.seg[i]);
             jobs[i].keep = reinterpret_cast<float*>(ws + w.keep[i]);
         }
     const int dt = dtype == SS_F32 ? 0 : 1;
-    // walks of the same class of widths in one launch
-    ssk::LattnArgs a = lattn_args(d, w, log_decay, reset);
-    const bool together = ssk::lattn_class(ki, vi) == ssk::lattn_class(vi, ki);
-    a.job[0] = jobs[0];
-    a.jobs = 1;
-    if (!together) {
+    ssk::LattnArgs a = lattn_args(d, w.cut[0], log_decay, reset);
+    a.job[a.jobs++] = jobs[0];
+    if (!lattn_together(d)) {
         if (const hipError_t e = ssk::launch_lattn(a, dt, stream); e != hipSuccess) return done(e);
-        a.jobs = 0;
+        a = lattn_args(d, w.cut[1], log_decay, reset);
     }
     a.job[a.jobs++] = jobs[1];
     a.job[a.jobs++] = jobs[2];

@@ -11,9 +11,11 @@ namespace ssk {
 // ---- linear attention with a decay for each head ---------------------------------------
 
 constexpr int kLattnMaxDim = 256;
-// rows per chunk, the unit that sequences are cut in: in fp32 the three parts of every row fit the LDS for 32,
-// with two workgroups beside each other up to 128 elements
-constexpr int lattn_chunk(int dtype) { return dtype == 0 ? 32 : 64; }
+// Rows per chunk, the unit that sequences are cut in, for widths dk and dv.  In fp32 the three parts of every
+// row fit the LDS for 32, with two workgroups beside each other up to 128 elements.  In bf16 a state above
+// 128 x 128 for each four waves, or 64 x 64 for each two, leaves registers for 32 rows with two waves on a
+// SIMD (32768 x 8 heads of 256: 459 -> 340 us forward; of 128 and 64: 100 -> 84; of 128, where both fit: 114).
+constexpr int lattn_chunk(int dtype, int dk, int dv) { return dtype == 0 || dk > 128 || (dk > 64 && dv <= 64) ? 32 : 64; }
 
 // One walk over the sequence.  Forward, dq, dk and dv are the same operation
 //   o_t = sum over s up to t of a^(t - s) (q_t . k_s) v_s  (+ a^(t + 1) h0^T q_t)
@@ -51,6 +53,11 @@ inline int64_t lattn_slices(int64_t dv) { return (dv + kLattnSlice - 1) / kLattn
 
 // Jobs of one launch have the same class of widths (lattn_class).
 inline int lattn_class(int dk, int dv) { return (dk <= 64 ? 0 : dk <= 128 ? 1 : 2) + 3 * (dv <= 64 ? 0 : int(lattn_slices(dv))); }
+// Workgroups of a class that a CU holds beside each other.
+inline int64_t lattn_resident(int dtype, int dk, int dv)
+{
+    return dtype == 0 ? (dk > 128 ? 1 : 2) : dk <= 128 && dv <= 64 ? 4 : 2;
+}
 hipError_t launch_lattn(const LattnArgs& a, int dtype, hipStream_t stream);
 // its parts: the element types' instantiations (vec: every row is whole 16-byte chunks), and the
 // states before the segments from what each segment leaves

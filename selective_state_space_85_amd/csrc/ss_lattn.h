@@ -72,6 +72,12 @@ struct Ops<1> {  // bf16
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
+    // blocks of 16 x 16: fragments of 32 indices, lane l has row l % 16 and 8 indices from l / 16 * 8; of the
+    // result rows l / 16 * 4 .. + 3 of column l % 16
+    static __device__ __forceinline__ f32x4 mma16(const Frag& a, const Frag& b, const f32x4& c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
     // contraction along a row of LDS: p is this lane's row at its first index
     static __device__ __forceinline__ Frag row(const E* p) { return *reinterpret_cast<const Frag*>(p); }
     // contraction down the columns: rows from `base`, column lane % 32.  Within a group of 16 lanes the
@@ -207,8 +213,6 @@ struct Ops<0> {
         c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], c, 0, 0, 0);
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
     }
-    // blocks of 16 x 16: fragments of 32 indices, lane l has row l % 16 and 8 indices from l / 16 * 8; of the
-    // result rows l / 16 * 4 .. + 3 of column l % 16
     static __device__ __forceinline__ f32x4 mma16(const Frag& a, const Frag& b, f32x4 c)
     {
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[2], b.p[0], c, 0, 0, 0);
@@ -428,14 +432,14 @@ __device__ __forceinline__ void unroll(F&& f)
 template <int DT, int DKP, int NW>
 struct LattnShape {
     static constexpr int kThreads = 64 * NW;
-    static constexpr int kC = lattn_chunk(DT);
+    static constexpr int kC = lattn_chunk(DT, DKP, 32 * NW);
     static constexpr int kKP = DKP + 8;                       // pitch of q and k rows
     static constexpr int kVP = 32 * NW + Ops<DT>::kEpc;       // of v rows
     static constexpr int kPP = kC + 8;                        // of P rows
     static constexpr int kQPieces = kC * DKP / Ops<DT>::kEpc / kThreads;
     static constexpr int kVPieces = kC * 32 * NW / Ops<DT>::kEpc / kThreads;
-    // two workgroups per CU, but where registers or LDS do not allow it
-    static constexpr int kWaves = DKP == 256 || NW == 2 ? 1 : 2;
+    // waves on a SIMD: two, but where their registers do not allow it
+    static constexpr int kWaves = (DKP == 256 && (DT == 0 || NW == 2)) || (DKP == 128 && DT == 0 && NW == 2) ? 1 : 2;
 };
 
 // grid (units rounded up to 8, times jobs); units are slices * heads * batch * segments, slices fastest.
@@ -796,7 +800,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
             __syncthreads();
         }
 
-        constexpr int kKeys = DT == 1 ? kDB : 1;  // fragments of k held for a step, and as many for the next
+        constexpr int kKeys = DT == 0 ? 1 : kDB > 4 ? 2 : kDB;  // fragments of k held for a step, and as many for the next
         Frag part[2][O::kParts], kf[2][kKeys];
         float wt[2][kHalf];
         typename O::Weighing steps;
@@ -929,9 +933,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
             constexpr int ks = decltype(ks_v)::value, kProducts = O::kParts * kDB;
             if constexpr (ks + 1 < kKS) weights(ks + 1);
             unroll<kProducts>([&](auto i_v) {
-                constexpr int i = decltype(i_v)::value, q = O::kParts - 1 - i / kDB, d = i % kDB;
+                constexpr int i = decltype(i_v)::value, group = i / (O::kParts * kKeys), at = i % (O::kParts * kKeys);
+                constexpr int q = O::kParts - 1 - at / kKeys, d = group * kKeys + at % kKeys;
                 constexpr int step = (ks * kDB + d) / kKeys;
-                if constexpr (q == O::kParts - 1 && d % kKeys == 0 && step + 1 < kKS * kDB / kKeys) keys(step + 1);
+                if constexpr (at == 0 && step + 1 < kKS * kDB / kKeys) keys(step + 1);
                 st[d] = O::mma(kf[step & 1][d % kKeys], part[ks & 1][q], st[d]);
                 if constexpr (ks + 1 < kKS)
                     weigh(std::integral_constant<int, ks + 1>(), std::integral_constant<int, O::kSteps * i / kProducts>(),
