@@ -368,12 +368,25 @@ __device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), short(0), int(bytes), 0x00020000);
 }
 
-// 16 bytes of a row.  VEC: the host has checked that rows are whole 16-byte chunks, and `at` is kNowhere
-// past the width; otherwise element by element, `left` of them.
-template <int DT, bool VEC>
-__device__ __forceinline__ u32x4 load_piece(Rsrc r, uint32_t at, int left)
+// How rows are read.  kWhole: the host has checked that they are whole 16-byte chunks at such addresses.
+// kAny: bf16 at any address, of 8 elements and more.  kSingle: element by element (8 x 2048 x 32 heads of 125
+// in bf16: 707 us, 297 by kAny; of 128 by kWhole 143).
+enum Access { kSingle, kWhole, kAny };
+
+// 16 bytes of a row; `at` is kNowhere past the width.  kSingle: the `left` elements there are.  kAny: the
+// aligned 16 bytes from the word at which they begin, and the next word where they do not begin with a
+// word; a row's last piece ends with the row, so that nothing else of memory is touched.
+struct Piece {
+    u32x4 v;
+    uint32_t x;
+};
+template <int DT, Access ACC>
+__device__ __forceinline__ Piece load_piece(Rsrc r, uint32_t at, int left)
 {
-    if constexpr (VEC) return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+    if constexpr (ACC == kWhole) return {__builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0), 0};
+    if constexpr (ACC == kAny)
+        return {__builtin_amdgcn_raw_buffer_load_b128(r, at & ~3u, 0, 0),
+                uint32_t(__builtin_amdgcn_raw_buffer_load_b32(r, at & 2u ? (at & ~3u) + 16u : kNowhere, 0, 0))};
     u32x4 v;
     if constexpr (DT == 0) {
 #pragma unroll
@@ -386,14 +399,35 @@ __device__ __forceinline__ u32x4 load_piece(Rsrc r, uint32_t at, int left)
             v[i] = lo | hi << 16;
         }
     }
-    return v;
+    return {v, 0};
+}
+// The piece's 8 elements.  kAny: without what lies before them, the half of a word and the `over` elements by
+// which the piece was moved to end with its row; zeros come in behind.
+template <Access ACC>
+__device__ __forceinline__ u32x4 elements(const Piece& p, uint32_t at, int over)
+{
+    if constexpr (ACC != kAny) return p.v;
+    const uint32_t half = at << 3 & 16u, odd = uint32_t(over) << 4 & 16u;
+    const uint32_t raw[5] = {p.v[0], p.v[1], p.v[2], p.v[3], p.x & 0xffffu};
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbit(raw[i + 1], raw[i], half);
+    w[4] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], odd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = over & 2 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = over & 4 ? (i < 2 ? w[i + 2] : 0u) : w[i];
+    return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-// The same as a store.
-template <int DT, bool VEC>
+// The same as a store.  kAny: element by element too.  Words and their halves at the ends, out of pieces
+// moved as they are for loads, cost more than they save: 8 x 2048 x 32 heads of 125 297 -> 390 us.
+template <int DT, Access ACC>
 __device__ __forceinline__ void store_piece(Rsrc r, uint32_t at, int left, const u32x4& v)
 {
-    if constexpr (VEC) {
+    if constexpr (ACC == kWhole) {
         __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
     } else if constexpr (DT == 0) {
 #pragma unroll
@@ -429,10 +463,11 @@ __device__ __forceinline__ void unroll(F&& f)
 }
 
 // The geometry of one instantiation.  Rows in LDS are padded by 16 bytes.
-template <int DT, int DKP, int NW>
+template <int DT, int DKP, int NW, Access ACC>
 struct LattnShape {
     static constexpr int kThreads = 64 * NW;
-    static constexpr int kC = lattn_chunk(DT, DKP, 32 * NW);
+    // rows at any address take a register more for each piece on its way
+    static constexpr int kC = ACC == kAny ? 32 : lattn_chunk(DT, DKP, 32 * NW);
     static constexpr int kKP = DKP + 8;                       // pitch of q and k rows
     static constexpr int kVP = 32 * NW + Ops<DT>::kEpc;       // of v rows
     static constexpr int kPP = kC + 8;                        // of P rows
@@ -446,14 +481,14 @@ struct LattnShape {
 // Workgroups go to the 8 XCDs in turn: the jobs of a unit, which read the same rows in the same order
 // (dk and dv), are 8 apart, on one XCD and its L2 (8 x 2048 x 40 heads of 128, gradients: 457 -> 448 us).
 // STATE: forms what each segment but the last leaves in the state, from zero, and nothing else.
-template <int DT, int DKP, int NW, bool VEC, bool STATE>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnShape<DT, DKP, NW>::kWaves))) void lattn_kernel(LattnArgs a)
+template <int DT, int DKP, int NW, Access ACC, bool STATE>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnShape<DT, DKP, NW, ACC>::kWaves))) void lattn_kernel(LattnArgs a)
 {
     using O = Ops<DT>;
     using E = typename O::E;
     using Frag = typename O::Frag;
     using VFrag = typename O::VFrag;
-    using G = LattnShape<DT, DKP, NW>;
+    using G = LattnShape<DT, DKP, NW, ACC>;
     constexpr int C = G::kC, kTB = C / 32, kDB = DKP / 32, kDepth = 16, kHalf = 8;
     constexpr int kKS = C / kDepth, kSub = 32 / kDepth;
 
@@ -504,7 +539,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     constexpr uint32_t kEs = sizeof(E);
     const char* const pq = static_cast<const char*>(j.q) + (b * L * j.q_ld + (h / j.q_share) * j.dk) * kEs;
     const char* const pk = static_cast<const char*>(j.k) + (b * L * j.k_ld + (h / j.k_share) * j.dk) * kEs;
-    const char* const pv = static_cast<const char*>(j.v) + (b * L * j.v_ld + (h / j.v_share) * j.dv + v0) * kEs;
+    const char* const pv = static_cast<const char*>(j.v) + (b * L * j.v_ld + (h / j.v_share) * j.dv) * kEs;
     const uint32_t lq = uint32_t(j.q_ld) * kEs, lk = uint32_t(j.k_ld) * kEs, lv = uint32_t(j.v_ld) * kEs;
     const uint32_t oes = j.out_f32 ? 4 : kEs, lo = uint32_t(H * j.dv) * oes;
     char* const po = static_cast<char*>(j.out) + (b * L * H * j.dv + h * j.dv + v0) * oes;
@@ -522,12 +557,24 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     };
     auto next = [&](Side& s) { s.at += (rev ? -int64_t(C) : int64_t(C)) * int64_t(s.ld); };
     // n of its rows as a buffer, and what to add to the offset of row r in a whole chunk, which is
-    // (rev ? C - 1 - r : r) rows: a short chunk lacks its last rows, from the end the lowest in memory
+    // (rev ? C - 1 - r : r) rows: a short chunk lacks its last rows, from the end the lowest in memory.  The
+    // buffer begins and ends with a word.
     auto rows = [&](const Side& s, int n) {
         const uint32_t miss = uint32_t(C - n) * s.ld;
-        return buffer_of(s.at + (rev ? miss : 0u), n > 0 ? uint32_t(C - 1) * s.ld + s.width - miss : 0);
+        const char* p = s.at + (rev ? miss : 0u);
+        uint32_t bytes = n > 0 ? uint32_t(C - 1) * s.ld + s.width - miss : 0;
+        if constexpr (ACC == kAny) {
+            const uint32_t half = uint32_t(reinterpret_cast<uintptr_t>(p)) & 2u;
+            p -= half;
+            bytes = n > 0 ? (bytes + half + 3u) & ~3u : 0;
+        }
+        return buffer_of(p, bytes);
     };
-    auto shift = [&](const Side& s, int n) { return rev ? 0u - uint32_t(C - n) * s.ld : 0u; };
+    auto shift = [&](const Side& s, int n) {
+        uint32_t by = rev ? 0u - uint32_t(C - n) * s.ld : 0u;
+        if constexpr (ACC == kAny) by += uint32_t(reinterpret_cast<uintptr_t>(s.at) + (rev ? uint32_t(C - n) * s.ld : 0u)) & 2u;
+        return by;
+    };
 
     const int c0 = 32 * w;  // this wave's columns of v; past the width they are zeros and nothing is stored
 
@@ -550,31 +597,37 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     constexpr int kQR = G::kThreads / kQC, kVR = G::kThreads / kVC;  // rows that the threads load at once
     static_assert(G::kThreads % kQC == 0 && G::kThreads % kVC == 0, "a thread's pieces lie in one column");
     const int qr = tid / kQC, qc = tid % kQC * O::kEpc, vr = tid / kVC, vc = tid % kVC * O::kEpc;
-    u32x4 fq[STATE ? 1 : G::kQPieces], fk[G::kQPieces], fv[G::kVPieces];
+    Piece fq[STATE ? 1 : G::kQPieces], fk[G::kQPieces], fv[G::kVPieces];
     uint32_t flag = 0;
     const Rsrc rr = buffer_of(pr, pr ? uint32_t(L) : 0);
-    Side q = side(pq, lq, j.dk * kEs, int(row0)), k = side(pk, lk, j.dk * kEs, int(row0)), v = side(pv, lv, vw * kEs, int(row0));
+    Side q = side(pq, lq, j.dk * kEs, int(row0)), k = side(pk, lk, j.dk * kEs, int(row0)), v = side(pv, lv, j.dv * kEs, int(row0));
     // results go out a chunk later: the first time nothing does
     Side out = side(po, lo, ow * oes, int(row0) - C);
     u32x4 fo[STATE ? 1 : G::kVPieces];
     int out_rows = 0;
-    // a thread's first piece of a whole chunk, and the bytes to the next
+    // a thread's first piece of a whole chunk, and the bytes to the next; by how much a piece is moved to end
+    // with its row
     auto first = [&](const Side& s, int r, int c, int width) {
         return (c < width ? uint32_t(c) * kEs : kNowhere) + uint32_t(rev ? C - 1 - r : r) * s.ld;
     };
+    auto past = [&](int c, int width) { return ACC == kAny && c < width && c + 8 > width ? c + 8 - width : 0; };
+    const int q_past = past(qc, j.dk), v_past = past(v0 + vc, j.dv);
     auto step = [&](const Side& s, int r) { return rev ? 0u - r * s.ld : r * s.ld; };
-    const uint32_t oq = first(q, qr, qc, j.dk), ok = first(k, qr, qc, j.dk), ov = first(v, vr, vc, vw);
+    const uint32_t oq = first(q, qr, qc, j.dk) - q_past * kEs, ok = first(k, qr, qc, j.dk) - q_past * kEs;
+    const uint32_t ov = first(v, vr, v0 + vc, j.dv) - v_past * kEs;
     const uint32_t oo = first(out, vr, vc, ow);
     // The stores and loads of a chunk, one piece at a time, so that they go out between products.  Stores
     // come first: a wait for loads then waits for no store that was issued behind them.
     struct Moves {
         Rsrc out, q, k, v;
         uint32_t ao, aq, ak, av, so, sq, sk, sv;
+        int out_rows, rows;
     } mv;
     auto start_store = [&] {
         mv.out = rows(out, out_rows);
         mv.ao = oo + shift(out, out_rows);
         mv.so = step(out, kVR);
+        mv.out_rows = out_rows;
         next(out);
     };
     auto start_load = [&](int t0, int n) {
@@ -591,25 +644,28 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
         mv.sq = step(q, kQR);
         mv.sk = step(k, kQR);
         mv.sv = step(v, kVR);
+        mv.rows = n;
         next(q);
         next(k);
         next(v);
     };
     constexpr int kStores = G::kVPieces, kLoads = (STATE ? 1 : 2) * G::kQPieces + G::kVPieces;
+    // kAny: the words at a buffer's ends hold elements of rows that are not there
+    auto there = [&](uint32_t at, int row, int n) { return ACC == kAny && row >= n ? kNowhere : at; };
     auto store_one = [&](auto i_v) {
         constexpr int i = decltype(i_v)::value;
-        store_piece<DT, VEC>(mv.out, mv.ao + i * mv.so, ow - vc, fo[i]);
+        store_piece<DT, ACC>(mv.out, there(mv.ao + i * mv.so, vr + i * kVR, mv.out_rows), ow - vc, fo[i]);
     };
     auto load_one = [&](auto i_v) {
         constexpr int i = decltype(i_v)::value;
         if constexpr (i < G::kVPieces) {
-            fv[i] = load_piece<DT, VEC>(mv.v, mv.av + i * mv.sv, vw - vc);
+            fv[i] = load_piece<DT, ACC>(mv.v, there(mv.av + i * mv.sv, vr + i * kVR, mv.rows), vw - vc);
         } else if constexpr (i < G::kVPieces + G::kQPieces) {
             constexpr int p = i - G::kVPieces;
-            fk[p] = load_piece<DT, VEC>(mv.k, mv.ak + p * mv.sk, j.dk - qc);
+            fk[p] = load_piece<DT, ACC>(mv.k, there(mv.ak + p * mv.sk, qr + p * kQR, mv.rows), j.dk - qc);
         } else {
             constexpr int p = i - G::kVPieces - G::kQPieces;
-            fq[p] = load_piece<DT, VEC>(mv.q, mv.aq + p * mv.sq, j.dk - qc);
+            fq[p] = load_piece<DT, ACC>(mv.q, there(mv.aq + p * mv.sq, qr + p * kQR, mv.rows), j.dk - qc);
         }
     };
 
@@ -653,11 +709,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
         // ---- the chunk into LDS, the next one's loads on their way ----
 #pragma unroll
         for (int i = 0; i < G::kQPieces; ++i) {
-            if constexpr (!STATE) sQ.put(qr + i * kQR, qc, fq[i]);
-            sK.put(qr + i * kQR, qc, fk[i]);
+            if constexpr (!STATE) sQ.put(qr + i * kQR, qc, elements<ACC>(fq[i], mv.aq + i * mv.sq, q_past));
+            sK.put(qr + i * kQR, qc, elements<ACC>(fk[i], mv.ak + i * mv.sk, q_past));
         }
 #pragma unroll
-        for (int i = 0; i < G::kVPieces; ++i) *reinterpret_cast<u32x4*>(&sV[vr + i * kVR][vc]) = fv[i];
+        for (int i = 0; i < G::kVPieces; ++i) *reinterpret_cast<u32x4*>(&sV[vr + i * kVR][vc]) = elements<ACC>(fv[i], mv.av + i * mv.sv, v_past);
         const uint64_t resets = __ballot(flag != 0);
         const int last = resets ? 63 - __builtin_clzll(resets) : 0;  // the last reset's row: what is before leaves nothing
         if constexpr (!STATE) {
@@ -988,18 +1044,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     }
 }
 
-template <int DT, int DKP, int NW, bool VEC>
+template <int DT, int DKP, int NW, Access ACC>
 hipError_t launch_shape(const LattnArgs& a, hipStream_t stream)
 {
     const int64_t walks = lattn_slices(a.job[0].dv) * a.heads * a.batch;
     auto grid = [&](int64_t segs) { return static_cast<uint32_t>((walks * segs + 7) / 8 * 8 * a.jobs); };
     const dim3 block(64 * NW);
     if (a.segs > 1) {
-        lattn_kernel<DT, DKP, NW, VEC, true><<<grid(a.segs - 1), block, 0, stream>>>(a);
+        lattn_kernel<DT, DKP, NW, ACC, true><<<grid(a.segs - 1), block, 0, stream>>>(a);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         if (hipError_t e = launch_lattn_join(a, stream); e != hipSuccess) return e;
     }
-    lattn_kernel<DT, DKP, NW, VEC, false><<<grid(a.segs), block, 0, stream>>>(a);
+    lattn_kernel<DT, DKP, NW, ACC, false><<<grid(a.segs), block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -1008,9 +1064,15 @@ template <int DT>
 hipError_t launch_typed(const LattnArgs& a, bool vec, hipStream_t stream)
 {
     const int dk = a.job[0].dk, dv = a.job[0].dv;
+    // rows of 8 elements and more
+    bool any = DT == 1;
+    for (int i = 0; i < a.jobs; ++i) any = any && a.job[i].dk >= 8 && a.job[i].dv >= 8;
     auto go = [&](auto dkp, auto nw) {
         constexpr int kD = decltype(dkp)::value, kW = decltype(nw)::value;
-        return vec ? launch_shape<DT, kD, kW, true>(a, stream) : launch_shape<DT, kD, kW, false>(a, stream);
+        if (vec) return launch_shape<DT, kD, kW, kWhole>(a, stream);
+        if constexpr (DT == 1)
+            if (any) return launch_shape<DT, kD, kW, kAny>(a, stream);
+        return launch_shape<DT, kD, kW, kSingle>(a, stream);
     };
     using std::integral_constant;
     auto by_dv = [&](auto dkp) {

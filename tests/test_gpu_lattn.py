@@ -100,6 +100,12 @@ CASES = [
     (BF16, 1, 2111, 2, 2, 64, 64, True, 0.001, 8),
     (BF16, 1, 1600, 1, 2, 128, 128, True, 0.002, 0),
     (F32, 2, 1090, 1, 1, 128, 256, False, 0.002, 0),
+    (BF16, 2, 129, 1, 3, 91, 101, True, 0.05, 3),     # rows at any address
+    (BF16, 1, 2100, 1, 2, 77, 250, True, 0.001, 1),
+    (BF16, 2, 70, 2, 2, 8, 9, True, 0.1, 1),
+    (BF16, 1, 96, 1, 1, 255, 130, True, None, 0),
+    (BF16, 2, 65, 2, 2, 128, 128, True, 0.1, 1),
+    (BF16, 2, 40, 1, 2, 7, 64, True, 0.1, 0),
 ]
 
 
@@ -257,6 +263,27 @@ def test_what_a_row_does_not_see(ss, dtype, bad, l, at):
         assert torch.equal(g[n][:, at + 1:], want[n][:, at + 1:]), n
         if at:
             assert torch.equal(g["dq"][:, :at], want["dq"][:, :at])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("l,dk,dv", [(37, 9, 11), (101, 125, 127), (33, 31, 130), (65, 7, 8), (70, 201, 9)])
+def test_rows_beside_a_sequence(ss, dtype, l, dk, dv):
+    """One head of an odd width: a sequence's last row ends within a word of memory, of which the other
+    half belongs to the next sequence.  What that holds is not seen."""
+    say("lattn beside", dtype, l, dk, dv)
+    args, extra, normal = make(dtype, 3, l, 1, 1, dk, dv, 11, h0=True)
+    do, dh = normal(3, l, 1, dv), normal(3, 1, dk, dv, dtype=F32)
+    o, last = ss.lattn_fwd(**args, **extra, return_last_state=True)
+    g = ss.lattn_bwd(**args, **extra, do=do, dh_last=dh, want_dh0=True)
+    for n in "qkv":
+        args[n][0], args[n][2] = float("nan"), float("nan")
+    do[0], do[2] = float("nan"), float("nan")
+    o2, last2 = ss.lattn_fwd(**args, **extra, return_last_state=True)
+    g2 = ss.lattn_bwd(**args, **extra, do=do, dh_last=dh, want_dh0=True)
+    assert torch.isfinite(o[1]).all()
+    assert torch.equal(o[1], o2[1]) and torch.equal(last[1], last2[1])
+    for n in g:
+        assert torch.equal(g[n][1], g2[n][1]), n
 
 
 def test_state_dropped_at_a_reset(ss):
