@@ -13,10 +13,25 @@
 //   O^T = S^T Q^T, times a^(t + 1), + V^T P^T     (v columns x t)
 //   S   = a^C S + K^T (w V)
 // A block of the state in accumulators (rows dk, columns v) is the operand S^T as it stands, up to
-// a swap between the halves of a wave (bf16) or as it is (fp32).
+// a swap between the halves of a wave.  In bf16, S and P are rounded where they become operands: of the
+// output that leaves a relative error of 0.0023 with the rounding of the output itself, 0.0017 alone;
+// w V goes in as three bf16 parts, since what is rounded on its way into the state would stay there.
 //
 // Resets cut the sequence: row t sees the rows from the last reset up to t, and the state only if
 // none lies in the chunk before or at t.  A chunk's resets are one 64-bit mask.
+//
+// What bounds it: with heads of 128 and 64 rows in bf16 a wave has 82 matrix instructions of 32 cycles
+// to a chunk, some 560 vector instructions beside them, and some 80 KB of LDS traffic
+// to the wave.  Two workgroups on a CU take 6.8 us for a chunk each at the 1.6-1.8 GHz that the card then runs at,
+// of which the matrix cores are busy 40-45%.  bf16, heads of 128:
+//   131072 x 16 heads, forward: states between segments 247-289 us (1.07 GB read, 3.7-4.3 TB/s), joined 15,
+//     main pass 465-535 (2.15 GB, 4.0-4.6 TB/s)
+//   8 x 2048 x 40 heads: forward 205-217 us, 320 walks on 256 CUs (256 of them, of 32 heads: 143); gradients,
+//     960 walks in one launch, 409-443 us
+// fp32, 3 x 1021 x 12 heads of 72 and 91: 21 + 9 + 39 us forward, 40 + 9 + 88 + 10 for the gradients.
+// Tried and not kept in bf16: chunks of 32 rows with three workgroups on a CU (28 registers in memory: 8 x
+// 2048 x 32 heads 141 -> 285 us) or with two (141 -> 153), rows padded by 32 bytes more in LDS, loads before
+// the barrier instead of among the products, P's products among those of S.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -473,8 +488,9 @@ struct LattnShape {
     static constexpr int kPP = kC + 8;                        // of P rows
     static constexpr int kQPieces = kC * DKP / Ops<DT>::kEpc / kThreads;
     static constexpr int kVPieces = kC * 32 * NW / Ops<DT>::kEpc / kThreads;
-    // waves on a SIMD: two, but where their registers do not allow it
-    static constexpr int kWaves = (DKP == 256 && (DT == 0 || NW == 2)) || (DKP == 128 && DT == 0 && NW == 2) ? 1 : 2;
+    // waves on a SIMD: two, but where their registers do not allow it (8 x 2048 x 32 heads of 201 in bf16:
+    // 1053 us with two and 34 registers in memory, 811 with one)
+    static constexpr int kWaves = (DKP == 256 && (DT == 0 || NW == 2 || ACC != kWhole)) || (DKP == 128 && DT == 0 && NW == 2) ? 1 : 2;
 };
 
 // grid (units rounded up to 8, times jobs); units are slices * heads * batch * segments, slices fastest.

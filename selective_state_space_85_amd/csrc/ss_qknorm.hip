@@ -10,6 +10,12 @@
 // all heads, then its groups of lanes walk the tile's heads in the order in which they lie in memory.
 // The angle is a number of turns, reduced in 64 bits before it is rounded: a product of a position
 // and a frequency in 32 bits would be off by whole turns far into a long context.
+//
+// What bounds it: HBM, each input read and each output written once.  bf16: 131072 tokens of 16 + 4 heads of
+// 128 forward 256 us, 5.2 TB/s; 16384 tokens of 40 + 40 heads forward 134 us, 5.0 TB/s, backward 217 + 5 us,
+// 4.6 TB/s.  One token 4.2 us, the latency of its angles and of one row.  fp32 of an odd pairing, 3063 tokens of
+// 12 + 4 heads of 90: 11 us forward, 18 + 4 backward, three rounds of latency for each workgroup.  In the
+// backward, loading the next row before the sums of this one: 217 -> 338 us.
 #include <hip/hip_runtime.h>
 
 #include "ss_attn_internal.h"
