@@ -19,6 +19,8 @@ from .lm import _call, _code, _dtype, _gpu, _need, _on, _p, _size, _space
 def _heads(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     """Token stride of a tensor (tokens..., heads, width) whose heads lie side by side and whose
     tokens lie evenly apart."""
+    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return shape[-2] * shape[-1]
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if t.dtype != dtype:
@@ -26,8 +28,6 @@ def _heads(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     h, w = shape[-2], shape[-1]
-    if t.is_contiguous():
-        return h * w
     st = t.stride()
     row = (w == 1 or st[-1] == 1) and (h == 1 or st[-2] == w)
     if len(shape) == 4:
@@ -42,9 +42,14 @@ def _heads(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     return ld
 
 
-def _shared(q: torch.Tensor, v: torch.Tensor) -> None:
-    if q.shape[-2] == 0 or v.shape[-2] % q.shape[-2] != 0:
-        raise ValueError("v's %d heads are not a multiple of q's %d" % (v.shape[-2], q.shape[-2]))
+def _shared(qk_heads: int, heads: int) -> None:
+    if qk_heads == 0 or heads % qk_heads != 0:
+        raise ValueError("v's %d heads are not a multiple of q's %d" % (heads, qk_heads))
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous result of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _flags(reset: Optional[torch.Tensor], shape, dev) -> None:
@@ -73,11 +78,11 @@ def _attention(q, k, v, log_decay, scale, h0, reset, fn):
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("%s: q, k and v must be (batch, seqlen, heads, width)" % fn)
     dev, dt = _gpu(q, fn), _dtype(q)
-    nb, nl, hk, dk = q.shape
+    shape, dtype = q.shape, q.dtype
+    nb, nl, hk, dk = shape
     nh, dv = v.shape[2], v.shape[3]
-    _shared(q, v)
-    lds = (_heads(q, "q", q.shape, q.dtype, dev), _heads(k, "k", q.shape, q.dtype, dev),
-           _heads(v, "v", (nb, nl, nh, dv), q.dtype, dev))
+    _shared(hk, nh)
+    lds = (_heads(q, "q", shape, dtype, dev), _heads(k, "k", shape, dtype, dev), _heads(v, "v", (nb, nl, nh, dv), dtype, dev))
     _need(log_decay, "log_decay", (nh,), torch.float32, dev)
     if h0 is not None:
         _need(h0, "h0", (nb, nh, dk, dv), torch.float32, dev)
@@ -102,7 +107,7 @@ def lattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     may be h0 itself)."""
     dev, dt, (nb, nl, hk, nh, dk, dv), (lq, lk, lv), scale = _attention(q, k, v, log_decay, scale, h0, reset, "lattn_fwd")
     if out is None:
-        out = q.new_empty((nb, nl, nh, dv))
+        out = _like(v)
     else:
         _need(out, "out", (nb, nl, nh, dv), q.dtype, dev)
     if h_last is None and return_last_state:
@@ -130,7 +135,7 @@ def lattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     ldo = _heads(do, "do", (nb, nl, nh, dv), q.dtype, dev)
     if dh_last is not None:
         _need(dh_last, "dh_last", (nb, nh, dk, dv), torch.float32, dev)
-    g = {"dq": q.new_empty(q.shape), "dk": q.new_empty(q.shape), "dv": q.new_empty((nb, nl, nh, dv))}
+    g = {"dq": _like(q), "dk": _like(k), "dv": _like(v)}
     if want_dh0:
         g["dh0"] = torch.empty((nb, nh, dk, dv), dtype=torch.float32, device=dev)
     lib = _attn.load()
@@ -150,18 +155,19 @@ def lattn_step(h: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("lattn_step: q, k and v must be (batch, heads, width)")
     dev, dt = _gpu(q, "lattn_step"), _dtype(q)
-    nb, hk, dk = q.shape
+    shape, dtype = q.shape, q.dtype
+    nb, hk, dk = shape
     nh, dv = v.shape[1], v.shape[2]
-    _shared(q, v)
-    lq = _heads(q, "q", q.shape, q.dtype, dev)
-    lk = _heads(k, "k", q.shape, q.dtype, dev)
-    lv = _heads(v, "v", (nb, nh, dv), q.dtype, dev)
+    _shared(hk, nh)
+    lq = _heads(q, "q", shape, dtype, dev)
+    lk = _heads(k, "k", shape, dtype, dev)
+    lv = _heads(v, "v", (nb, nh, dv), dtype, dev)
     _need(h, "h", (nb, nh, dk, dv), torch.float32, dev)
     _need(log_decay, "log_decay", (nh,), torch.float32, dev)
     if out is None:
-        out = q.new_empty((nb, nh, dv))
+        out = _like(v)
     else:
-        _need(out, "out", (nb, nh, dv), q.dtype, dev)
+        _need(out, "out", (nb, nh, dv), dtype, dev)
     with _on(dev) as stream:
         st = _attn.load().ss_lattn_step(_p(h), _p(q), lq, _p(k), lk, _p(v), lv, _p(log_decay),
                                         dk ** -0.5 if scale is None else scale, _p(out), nb, hk, nh, dk, dv, dt, stream)
@@ -178,22 +184,27 @@ def qknorm_bwd_workspace_bytes(tokens: int, q_heads: int, k_heads: int, width: i
 
 def _norm(q, k, w_q, w_k, pos, inv_freq, fn):
     """The checks of both directions: device, type code, sizes and row strides."""
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    shape, dtype = q.shape, q.dtype
+    if len(shape) == 4:
+        nb, nl, hq, width = shape
+        lead, n = (nb, nl), nb * nl
+    elif len(shape) == 3:
+        n, hq, width = shape
+        lead = (n,)
+    if len(shape) not in (3, 4) or k.dim() != len(shape):
         raise ValueError("%s: q and k must be (tokens, heads, width) or (batch, seqlen, heads, width)" % fn)
-    dev, dt = _gpu(q, fn), _dtype(q)
-    lead, width = q.shape[:-2], q.shape[-1]
-    lq = _heads(q, "q", q.shape, q.dtype, dev)
-    lk = _heads(k, "k", lead + (k.shape[-2], width), q.dtype, dev)
+    dev, dt = _gpu(q, fn), _code(dtype)
+    hk = k.shape[-2]
+    lq = _heads(q, "q", shape, dtype, dev)
+    lk = _heads(k, "k", lead + (hk, width), dtype, dev)
     _need(w_q, "w_q", (width,), torch.float32, dev)
     _need(w_k, "w_k", (width,), torch.float32, dev)
     _need(pos, "pos", lead, torch.int64, dev)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must have one axis")
-    _need(inv_freq, "inv_freq", inv_freq.shape, torch.float32, dev)
-    n = 1
-    for s in lead:
-        n *= s
-    return dev, dt, lq, lk, (n, q.shape[-2], k.shape[-2], width, inv_freq.shape[0])
+    half = inv_freq.shape[0]
+    _need(inv_freq, "inv_freq", (half,), torch.float32, dev)
+    return dev, dt, lq, lk, (n, hq, hk, width, half)
 
 
 def qknorm_fwd(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor, w_k: torch.Tensor, pos: torch.Tensor,
@@ -208,7 +219,7 @@ def qknorm_fwd(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor, w_k: torch.T
     (n,) float32, n at most W / 2 (n = 0: norms alone).  Pairs are (i, i + n), or (2 i, 2 i + 1) with
     ``interleaved``.  ``out``: contiguous tensors of q's and k's shapes.  Returns (qo, ko)."""
     dev, dt, lq, lk, sizes = _norm(q, k, w_q, w_k, pos, inv_freq, "qknorm_fwd")
-    qo, ko = (q.new_empty(q.shape), k.new_empty(k.shape)) if out is None else out
+    qo, ko = (_like(q), _like(k)) if out is None else out
     if out is not None:
         _need(qo, "out[0]", q.shape, q.dtype, dev)
         _need(ko, "out[1]", k.shape, q.dtype, dev)
@@ -227,7 +238,7 @@ def qknorm_bwd(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor, w_k: torch.T
     dev, dt, lq, lk, sizes = _norm(q, k, w_q, w_k, pos, inv_freq, "qknorm_bwd")
     _need(dqo, "dqo", q.shape, q.dtype, dev)
     _need(dko, "dko", k.shape, q.dtype, dev)
-    g = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape),
+    g = {"dq": _like(q), "dk": _like(k),
          "dw_q": torch.empty(w_q.shape, dtype=torch.float32, device=dev),
          "dw_k": torch.empty(w_k.shape, dtype=torch.float32, device=dev)}
     lib = _attn.load()
