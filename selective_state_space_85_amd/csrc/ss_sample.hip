@@ -88,6 +88,9 @@ struct Row {
     // are all equal then
     float pre;
     float top, scale;  // the largest logit; bins of counts per unit of logit
+    // a logit whose weight is 0 in place of all below it, NaN and -infinity too; plain: it is there and `pre` is 1
+    float floor;
+    bool plain;
     double rate;       // log2(e) / T; both go by logits times `pre`
     int shift;         // the largest logit's weight is 2^shift
     __device__ __forceinline__ float value(float l) const { return fminf(l, 3.402823466e38f) * pre; }
@@ -97,11 +100,13 @@ struct Row {
     // |r| <= 1 / 128, 2^r by its series, of which the first term left out is (ln 2 / 128)^6 / 720 = 3.5e-17.
     // Bins are 1 / 64 of a halving wide: the weights of the last one are below 2^-63 of the largest, which is
     // less than half a unit, whatever the row.
+    template <bool PLAIN = false>
     __device__ __forceinline__ uint64_t weight(float l, const double* root, int* bin) const
     {
         constexpr double kGrid = 6755399441055744.0 / 64;  // 1.5 * 2^52 / 64: sums are multiples of 1 / 64
         constexpr double kWhole = 4503599627370496.0;      // 2^52: sums are integers
-        const double t = fmax((double(value(l)) - double(top)) * rate, -1000.0);
+        const double t = PLAIN ? (double(fmaxf(l, floor)) - double(top)) * rate
+                               : fmax((double(value(l)) - double(top)) * rate, -1000.0);
         const double g = t + kGrid;
         const int n64 = int(__double_as_longlong(g));  // 64 t, rounded, in the low bits
         const double r = t - (g - kGrid);
@@ -140,7 +145,7 @@ struct Pieces {
     }
     // the weights and their bins, 0 for tokens that cannot be taken: four at a time without branches, so that
     // one's table is read while another's series is formed
-    template <typename F>
+    template <bool PLAIN, typename F>
     __device__ __forceinline__ void weigh(const Row<DT>& r, const double* root, F f)
     {
 #pragma unroll
@@ -152,8 +157,8 @@ struct Pieces {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float l = v[i][q + e];
-                    w[e] = r.weight(l >= least ? l : 0.0f, root, &b[e]);
-                    w[e] = l >= least ? w[e] : 0;
+                    w[e] = r.template weight<PLAIN>(PLAIN || l >= least ? l : 0.0f, root, &b[e]);
+                    if (!PLAIN) w[e] = l >= least ? w[e] : 0;
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f(w[e], b[e]);
@@ -171,7 +176,7 @@ struct Single {
     {
         f(uint32_t(at), l);
     }
-    template <typename F>
+    template <bool PLAIN, typename F>
     __device__ __forceinline__ void weigh(const Row<DT>& r, const double* root, F f)
     {
         int b;
@@ -296,12 +301,12 @@ __device__ __forceinline__ uint64_t fill_bins(Shared& s, const Row<DT>& r, uint6
     __syncthreads();
     uint64_t above = 0;
     if (MASS) {
-        each_few(r, [&](auto& v) {
-            v.weigh(r, s.root, [&](uint64_t w, int b) {
-                if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[b]), w);
-                if (least) above += w >= least ? w : 0;
-            });
-        });
+        auto add = [&](uint64_t w, int b) {
+            if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[b]), w);
+            if (least) above += w >= least ? w : 0;
+        };
+        if (r.plain) each_few(r, [&](auto& v) { v.template weigh<true>(r, s.root, add); });
+        else each_few(r, [&](auto& v) { v.template weigh<false>(r, s.root, add); });
     } else {
         each(r, [&](uint32_t, float l) { atomicAdd(&s.count[r.count_bin(l)], 1u); });
     }
@@ -331,12 +336,24 @@ __device__ __forceinline__ bool make_list(Shared& s, const Row<DT>& r, float fro
 {
     if (threadIdx.x == 0) s.listed = 0;
     __syncthreads();
-    // the slots of several tokens at a time: a slot's number has to come back before it is written
+    // A wave's slots at a time: of at most 16 tokens a thread, the sums over the lanes before it by the bits
+    // of their numbers.  One addition for each thread's takes the time of 64.
     each_few(r, [&](auto& v) {
         uint32_t n = 0;
         v.walk([&](uint32_t, float l) { n += l >= from && l <= to; });
+        if (__ballot(n != 0) == 0) return;
+        uint32_t slot = 0, all = 0;
+#pragma unroll
+        for (int b = 0; b < 5; ++b) {
+            const uint64_t m = __ballot(n >> b & 1);
+            slot += __builtin_amdgcn_mbcnt_hi(uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0)) << b;
+            all += uint32_t(__builtin_popcountll(m)) << b;
+        }
+        const uint64_t here = __ballot(true);
+        uint32_t base = 0;
+        if ((here & ((uint64_t(1) << (threadIdx.x & 63)) - 1)) == 0) base = atomicAdd(&s.listed, all);
+        slot += __builtin_amdgcn_readfirstlane(base);
         if (n == 0) return;
-        uint32_t slot = atomicAdd(&s.listed, n);
         v.walk([&](uint32_t i, float l) {
             if (!(l >= from && l <= to)) return;
             if (slot < kList) {
@@ -460,6 +477,38 @@ __device__ __forceinline__ Place find(Shared& s, const Row<DT>& r, uint64_t targ
     return {s.found_key, s.found_index, s.found_mass};
 }
 
+// The list's running counts in place of the row's.
+template <int DT>
+__device__ __forceinline__ void count_list(Shared& s, const Row<DT>& r)
+{
+    __syncthreads();
+    for (int b = threadIdx.x; b < kBins; b += kThr) s.count[b] = 0;
+    __syncthreads();
+    const uint32_t n = s.listed;
+    for (uint32_t j = threadIdx.x; j < n; j += kThr)
+        if (s.key[j]) atomicAdd(&s.count[r.count_bin(logit_of(s.key[j]))], 1u);
+    __syncthreads();
+    scan_bins<false>(s);
+}
+
+// Lists tokens among which the first `k` are, without counting the row: those that are at least the k-th of
+// the threads' largest logits, `own`.  About -kThr ln(1 - k / kThr) of them, if the large ones lie anywhere.
+// Says whether there are k threads with one and the tokens fit the list.
+template <int DT>
+__device__ __forceinline__ bool shortlist(Shared& s, const Row<DT>& r, float own, uint32_t k)
+{
+    __syncthreads();
+    s.key[threadIdx.x] = own >= r.least ? key_of(own) : 0u;
+    s.index[threadIdx.x] = threadIdx.x;
+    if (threadIdx.x == 0) s.listed = kThr;
+    count_list(s, r);
+    if (s.count[kBins - 1] < k) return false;
+    const Place at = find<DT, false>(s, r, k, true);
+    if (!make_list(s, r, logit_of(at.key), INFINITY)) return false;
+    count_list(s, r);
+    return true;
+}
+
 // The sums of the weights, and of those that are at least `least`, up to a place.
 template <int DT>
 __device__ __forceinline__ void sums_upto(Shared& s, const Row<DT>& r, const Place& at, uint64_t least, uint64_t* all, uint64_t* above)
@@ -497,6 +546,7 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
         top = fmaxf(top, l);  // neither takes NaN
         low = fminf(low, l > -INFINITY ? l : INFINITY);
     });
+    const float own = top;  // this thread's largest
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         top = fmaxf(top, __shfl_xor(top, d));
@@ -534,6 +584,11 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
     r.top = r.value(top);
     const double td = r.pre > 0.0f ? double(t) * double(r.pre) : 1.0;
     r.rate = 1.4426950408889634 / td;
+    // at 100 T below the largest logit, which rounding moves by less than half of that, or the next number
+    // below it: less than 2^-70 of the largest weight
+    r.floor = float(double(r.top) - 100.0 * td);
+    if (!(r.floor < r.top)) r.floor = logit_of(key_of(r.top) - 1);
+    r.plain = r.pre == 1.0f && (double(r.floor) - double(r.top)) * r.rate >= -1000.0;
     // a row's weights sum to less than 2^62, and each fits the 52 bits of a double
     const int bits = 32 - __builtin_clz(uint32_t(r.n));
     r.shift = 62 - bits < 50 ? 62 - bits : 50;
@@ -551,12 +606,14 @@ __global__ __launch_bounds__(kThr) void sample_kernel(SampleArgs a)
     uint64_t all = 0;    // those that every limit so far leaves
     if (k > 0 && k < r.n) {
         // the bins' counts, and the last of the tokens that top_k leaves
-        fill_bins<DT, false>(s, r, 0);
+        const bool few = k <= kThr / 8 * 7 && shortlist(s, r, own, uint32_t(k));
+        if (!few) fill_bins<DT, false>(s, r, 0);
         const uint32_t can = s.count[kBins - 1];
         const uint32_t keep = uint32_t(k) < can ? uint32_t(k) : can;
         const int bin = bin_of<false>(s, keep);
         if (bin < kBins - 1) {  // otherwise what top_k drops has no weight
-            if (s.count[bin] <= kList) listed = make_list(s, r, border<DT, false>(r, bin + 1, false), INFINITY);
+            if (few) listed = true;
+            else if (s.count[bin] <= kList) listed = make_list(s, r, border<DT, false>(r, bin + 1, false), INFINITY);
             const Place at = find<DT, false>(s, r, keep, listed);
             if (listed) {
                 // the bins' weights from the list, without those that top_k drops
