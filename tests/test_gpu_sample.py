@@ -97,6 +97,37 @@ def test_numbers_at_the_ends(ss):
         assert ss.sample(tiny, u, temperature=t).tolist() == want(tiny, u, temperature=t), t
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_where_the_largest_lie(ss, dtype):
+    """The largest logits in a few threads' share of the row, in order, all equal, few that can be taken at all."""
+    say("sample places", dtype)
+    v = 20011
+    l, u = logits(dtype, 8, v, 6)
+    at = torch.arange(v, device="cuda")
+    l[0, at % 8192 < 8] += 30.0
+    l[1] = l[1].sort(descending=True).values
+    l[2] = l[2].sort().values
+    l[3, 900:] = -float("inf")
+    l[4, 40:] = float("nan")
+    l[5] = 1.25
+    l[6, 100:] = 1.25
+    l[7, :5000] = 9.0
+    for k in (1, 2, 39, 41, 300, 895, 896, 897, 2000, 5000, 20010):
+        for kw in (dict(), dict(temperature=0.2, top_p=0.9), dict(temperature=3.0, min_p=0.3)):
+            assert ss.sample(l, u, top_k=k, **kw).tolist() == want(l, u, top_k=k, **kw), (k, kw)
+
+
+def test_temperatures_beside_the_logits_steps(ss):
+    """Temperatures from far below a step of the largest logit's to far above the logits' span."""
+    say("sample steps")
+    l, u = logits(F32, 6, 3000, 7)
+    for scale in (1.0, 1e6, 1e12, 1e30):
+        for t in (1e-30, 1e-3, 0.0625, 1.0, 1e6, 1e30, 3e38):
+            for kw in (dict(), dict(top_k=20), dict(top_p=0.6)):
+                x = l * scale + scale
+                assert ss.sample(x, u, temperature=t, **kw).tolist() == want(x, u, temperature=t, **kw), (scale, t, kw)
+
+
 def test_masked_logits(ss):
     """-infinity, the type's lowest value, +infinity and NaN; rows of which nothing is left."""
     say("sample masks")
