@@ -8,15 +8,18 @@
 // One workgroup has one row and reads it three times (from the caches, but for the first):
 //  1. the largest logit and the smallest;
 //  2. bins of equal width in the logit, with their weights.  Their running sums tell which bin a place
-//     lies in.  With a small top-k the bins have counts: the tokens that remain are weighed later;
+//     lies in.  With a small top-k no bins of the row are needed: the tokens that are at least the k-th largest
+//     of the threads' own maxima hold the first k, fit the LDS, and are binned by count, then by weight;
 //  3. the tokens of the bins that the limits leave, to LDS, if they fit there.
 // A place is then found among the tokens of its bin: up to 64 of them, by one wave, a token to a lane,
 // each counting what comes before it.  More are first cut down by histograms over 8 bits of their logits
 // at a time and, where those are equal, of their indices.
 //
-// What bounds it: one workgroup's passes, scans and barriers, not bytes: one row of 50257 in bf16 takes 32 us
-// (89 by histograms over the logits' bits alone), 64 rows of 131072 35 us, a row to a CU, 256 rows of 50257 in
-// fp32 with settings of their own 65 us (140 with every limit's own pass over the row).
+// What bounds it: one workgroup's passes, scans and barriers, not bytes.  One row of 50257 in bf16, nucleus: 30
+// us, of which 3 for the largest logit, 15 for the weights' bins (some 40 instructions and an LDS addition for
+// each of 49 tokens a thread), 5-7 for the list, 2-3 for a place.  64 rows of 131072, top-k of 50 and nucleus,
+// a row to a CU: 30 us (35 with counts of the whole row, and 23 of them for those).  256 rows of 50257 in fp32
+// with settings of their own: 56 us, a workgroup to a CU (104 registers a thread).
 #include <hip/hip_runtime.h>
 
 #include "ss_attn_internal.h"
