@@ -28,7 +28,7 @@
 //     main pass 465-535 (2.15 GB, 4.0-4.6 TB/s)
 //   8 x 2048 x 40 heads: forward 205-217 us, 320 walks on 256 CUs (256 of them, of 32 heads: 143); gradients,
 //     960 walks in one launch, 409-443 us
-// fp32, 3 x 1021 x 12 heads of 72 and 91: 21 + 9 + 39 us forward, 40 + 9 + 88 + 10 for the gradients.
+// fp32, 3 x 1021 x 12 heads of 72 and 91: 16 + 7 + 33 us forward, 29 + 10 + 74 + 10 for the gradients.
 // Tried and not kept in bf16: chunks of 32 rows with three workgroups on a CU (28 registers in memory: 8 x
 // 2048 x 32 heads 141 -> 285 us) or with two (141 -> 153), rows padded by 32 bytes more in LDS, loads before
 // the barrier instead of among the products, P's products among those of S.
@@ -384,8 +384,9 @@ __device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes)
 }
 
 // How rows are read.  kWhole: the host has checked that they are whole 16-byte chunks at such addresses.
-// kAny: bf16 at any address, of 8 elements and more.  kSingle: element by element (8 x 2048 x 32 heads of 125
-// in bf16: 707 us, 297 by kAny; of 128 by kWhole 143).
+// kAny: at any address, of 16 bytes and more.  kSingle: element by element (8 x 2048 x 32 heads of 125
+// in bf16: 707 us, 297 by kAny; of 128 by kWhole 143; 3 x 1021 x 12 heads of 72 and 91 in fp32 with their
+// gradients: 186 and 163).
 enum Access { kSingle, kWhole, kAny };
 
 // 16 bytes of a row; `at` is kNowhere past the width.  kSingle: the `left` elements there are.  kAny: the
@@ -399,6 +400,7 @@ template <int DT, Access ACC>
 __device__ __forceinline__ Piece load_piece(Rsrc r, uint32_t at, int left)
 {
     if constexpr (ACC == kWhole) return {__builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0), 0};
+    if constexpr (ACC == kAny && DT == 0) return {__builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0), 0};
     if constexpr (ACC == kAny)
         return {__builtin_amdgcn_raw_buffer_load_b128(r, at & ~3u, 0, 0),
                 uint32_t(__builtin_amdgcn_raw_buffer_load_b32(r, at & 2u ? (at & ~3u) + 16u : kNowhere, 0, 0))};
@@ -416,12 +418,20 @@ __device__ __forceinline__ Piece load_piece(Rsrc r, uint32_t at, int left)
     }
     return {v, 0};
 }
-// The piece's 8 elements.  kAny: without what lies before them, the half of a word and the `over` elements by
+// The piece's elements.  kAny: without what lies before them, the half of a word and the `over` elements by
 // which the piece was moved to end with its row; zeros come in behind.
-template <Access ACC>
+template <int DT, Access ACC>
 __device__ __forceinline__ u32x4 elements(const Piece& p, uint32_t at, int over)
 {
     if constexpr (ACC != kAny) return p.v;
+    if constexpr (DT == 0) {
+        u32x4 w = p.v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = over & 1 ? (i < 3 ? w[i + 1] : 0u) : w[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = over & 2 ? (i < 2 ? w[i + 2] : 0u) : w[i];
+        return w;
+    }
     const uint32_t half = at << 3 & 16u, odd = uint32_t(over) << 4 & 16u;
     const uint32_t raw[5] = {p.v[0], p.v[1], p.v[2], p.v[3], p.x & 0xffffu};
     uint32_t w[5];
@@ -486,11 +496,14 @@ struct LattnShape {
     static constexpr int kKP = DKP + 8;                       // pitch of q and k rows
     static constexpr int kVP = 32 * NW + Ops<DT>::kEpc;       // of v rows
     static constexpr int kPP = kC + 8;                        // of P rows
-    static constexpr int kQPieces = kC * DKP / Ops<DT>::kEpc / kThreads;
+    // q and k are loaded as if they had a power of two of columns; the products go by DKP (8 x 512 x 32 heads of
+    // 96 in fp32: 84 -> 77 us for 96 beside 128, of 160: 290 -> 232 for 192 beside 256)
+    static constexpr int kLoad = DKP <= 64 ? 64 : DKP <= 128 ? 128 : 256;
+    static constexpr int kQPieces = kC * kLoad / Ops<DT>::kEpc / kThreads;
     static constexpr int kVPieces = kC * 32 * NW / Ops<DT>::kEpc / kThreads;
     // waves on a SIMD: two, but where their registers do not allow it (8 x 2048 x 32 heads of 201 in bf16:
-    // 1053 us with two and 34 registers in memory, 811 with one)
-    static constexpr int kWaves = (DKP == 256 && (DT == 0 || NW == 2 || ACC != kWhole)) || (DKP == 128 && DT == 0 && NW == 2) ? 1 : 2;
+    // 1053 us with two and 34 registers in memory, 811 with one; of 177, which fit two: 821 with one, 668)
+    static constexpr int kWaves = (DKP > 128 && (DT == 0 || NW == 2 || (ACC != kWhole && DKP == 256))) || (DKP > 64 && DT == 0 && NW == 2) ? 1 : 2;
 };
 
 // grid (units rounded up to 8, times jobs); units are slices * heads * batch * segments, slices fastest.
@@ -609,7 +622,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     }
 
     // ---- a chunk's operands, loaded one chunk ahead ----
-    constexpr int kQC = DKP / O::kEpc, kVC = 32 * NW / O::kEpc;  // 16-byte pieces of a row
+    constexpr int kQC = G::kLoad / O::kEpc, kVC = 32 * NW / O::kEpc;  // 16-byte pieces of a row
     constexpr int kQR = G::kThreads / kQC, kVR = G::kThreads / kVC;  // rows that the threads load at once
     static_assert(G::kThreads % kQC == 0 && G::kThreads % kVC == 0, "a thread's pieces lie in one column");
     const int qr = tid / kQC, qc = tid % kQC * O::kEpc, vr = tid / kVC, vc = tid % kVC * O::kEpc;
@@ -626,7 +639,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     auto first = [&](const Side& s, int r, int c, int width) {
         return (c < width ? uint32_t(c) * kEs : kNowhere) + uint32_t(rev ? C - 1 - r : r) * s.ld;
     };
-    auto past = [&](int c, int width) { return ACC == kAny && c < width && c + 8 > width ? c + 8 - width : 0; };
+    auto past = [&](int c, int width) { return ACC == kAny && c < width && c + O::kEpc > width ? c + O::kEpc - width : 0; };
     const int q_past = past(qc, j.dk), v_past = past(v0 + vc, j.dv);
     auto step = [&](const Side& s, int r) { return rev ? 0u - r * s.ld : r * s.ld; };
     const uint32_t oq = first(q, qr, qc, j.dk) - q_past * kEs, ok = first(k, qr, qc, j.dk) - q_past * kEs;
@@ -667,7 +680,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     };
     constexpr int kStores = G::kVPieces, kLoads = (STATE ? 1 : 2) * G::kQPieces + G::kVPieces;
     // kAny: the words at a buffer's ends hold elements of rows that are not there
-    auto there = [&](uint32_t at, int row, int n) { return ACC == kAny && row >= n ? kNowhere : at; };
+    auto there = [&](uint32_t at, int row, int n) { return DT == 1 && ACC == kAny && row >= n ? kNowhere : at; };
     auto store_one = [&](auto i_v) {
         constexpr int i = decltype(i_v)::value;
         store_piece<DT, ACC>(mv.out, there(mv.ao + i * mv.so, vr + i * kVR, mv.out_rows), ow - vc, fo[i]);
@@ -725,11 +738,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
         // ---- the chunk into LDS, the next one's loads on their way ----
 #pragma unroll
         for (int i = 0; i < G::kQPieces; ++i) {
-            if constexpr (!STATE) sQ.put(qr + i * kQR, qc, elements<ACC>(fq[i], mv.aq + i * mv.sq, q_past));
-            sK.put(qr + i * kQR, qc, elements<ACC>(fk[i], mv.ak + i * mv.sk, q_past));
+            if (G::kLoad != DKP && qc >= DKP) break;
+            if constexpr (!STATE) sQ.put(qr + i * kQR, qc, elements<DT, ACC>(fq[i], mv.aq + i * mv.sq, q_past));
+            sK.put(qr + i * kQR, qc, elements<DT, ACC>(fk[i], mv.ak + i * mv.sk, q_past));
         }
 #pragma unroll
-        for (int i = 0; i < G::kVPieces; ++i) *reinterpret_cast<u32x4*>(&sV[vr + i * kVR][vc]) = elements<ACC>(fv[i], mv.av + i * mv.sv, v_past);
+        for (int i = 0; i < G::kVPieces; ++i) *reinterpret_cast<u32x4*>(&sV[vr + i * kVR][vc]) = elements<DT, ACC>(fv[i], mv.av + i * mv.sv, v_past);
         const uint64_t resets = __ballot(flag != 0);
         const int last = resets ? 63 - __builtin_clzll(resets) : 0;  // the last reset's row: what is before leaves nothing
         if constexpr (!STATE) {
@@ -1075,27 +1089,30 @@ hipError_t launch_shape(const LattnArgs& a, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Jobs of one launch have the same widths up to the padding that chooses the instantiation.
+// Jobs of one launch have the same class of widths; the widest chooses the padding of q and k.
 template <int DT>
 hipError_t launch_typed(const LattnArgs& a, bool vec, hipStream_t stream)
 {
-    const int dk = a.job[0].dk, dv = a.job[0].dv;
-    // rows of 8 elements and more
-    bool any = DT == 1;
-    for (int i = 0; i < a.jobs; ++i) any = any && a.job[i].dk >= 8 && a.job[i].dv >= 8;
+    const int dv = a.job[0].dv;
+    int dk = 0;
+    for (int i = 0; i < a.jobs; ++i) dk = a.job[i].dk > dk ? a.job[i].dk : dk;
+    // rows of 16 bytes and more
+    bool any = true;
+    for (int i = 0; i < a.jobs; ++i) any = any && a.job[i].dk >= Ops<DT>::kEpc && a.job[i].dv >= Ops<DT>::kEpc;
     auto go = [&](auto dkp, auto nw) {
         constexpr int kD = decltype(dkp)::value, kW = decltype(nw)::value;
         if (vec) return launch_shape<DT, kD, kW, kWhole>(a, stream);
-        if constexpr (DT == 1)
-            if (any) return launch_shape<DT, kD, kW, kAny>(a, stream);
+        if (any) return launch_shape<DT, kD, kW, kAny>(a, stream);
         return launch_shape<DT, kD, kW, kSingle>(a, stream);
     };
     using std::integral_constant;
     auto by_dv = [&](auto dkp) {
         return dv <= 64 ? go(dkp, integral_constant<int, 2>()) : go(dkp, integral_constant<int, 4>());
     };
-    return dk <= 64 ? by_dv(integral_constant<int, 64>())
-                    : dk <= 128 ? by_dv(integral_constant<int, 128>()) : by_dv(integral_constant<int, 256>());
+    return dk <= 64    ? by_dv(integral_constant<int, 64>())
+           : dk <= 96  ? by_dv(integral_constant<int, 96>())
+           : dk <= 128 ? by_dv(integral_constant<int, 128>())
+           : dk <= 192 ? by_dv(integral_constant<int, 192>()) : by_dv(integral_constant<int, 256>());
 }
 
 }  // namespace

@@ -106,6 +106,12 @@ CASES = [
     (BF16, 1, 96, 1, 1, 255, 130, True, None, 0),
     (BF16, 2, 65, 2, 2, 128, 128, True, 0.1, 1),
     (BF16, 2, 40, 1, 2, 7, 64, True, 0.1, 0),
+    (F32, 2, 70, 1, 2, 96, 65, True, 0.1, 0),         # widths between the powers of two
+    (BF16, 1, 150, 1, 2, 80, 96, True, 0.05, 0),
+    (F32, 1, 77, 1, 1, 191, 150, True, 0.1, 2),
+    (BF16, 2, 130, 1, 1, 192, 136, True, 0.02, 0),
+    (BF16, 1, 1500, 1, 2, 160, 40, True, 0.002, 8),
+    (BF16, 1, 600, 1, 1, 97, 193, True, 0.01, 1),
 ]
 
 
