@@ -98,14 +98,22 @@ bool lattn_too_wide(int64_t a, int64_t b, int64_t c, int64_t d)
     return a > kLattnMaxStride || b > kLattnMaxStride || c > kLattnMaxStride || d > kLattnMaxStride;
 }
 
-// Whether the walks' launches fit a grid, and a sequence's rows their counters.
-bool lattn_grid_ok(const LattnDims& d, const LattnLayout& w)
+// Whether a launch of `jobs` walks of width dv fits a grid.
+bool lattn_fits(const LattnDims& d, int64_t dv, int jobs, int64_t segs)
 {
     int64_t n;
-    const int64_t segs = w.cut[0].segs > w.cut[1].segs ? w.cut[0].segs : w.cut[1].segs;
-    // two slices of each of three walks, rounded up to 8
-    return d.seqlen < (int64_t(1) << 30) && mul(d.batch * d.heads, segs, &n) && mul(n, 6, &n) && n <= INT32_MAX - 24 &&
-           launch_fits(n + 24, 256);
+    // counted as the kernel's launch does, which then cannot overflow
+    return mul(d.batch * d.heads, segs, &n) && n <= UINT32_MAX &&
+           launch_fits(ssk::lattn_groups(d.batch, d.heads, dv, jobs, segs), 64 * ssk::lattn_waves(dv));
+}
+
+// Whether every launch of a direction fits a grid, and a sequence's rows their counters.
+bool lattn_grid_ok(const LattnDims& d, const LattnLayout& w, bool back)
+{
+    if (d.seqlen >= int64_t(1) << 30) return false;
+    if (!back) return lattn_fits(d, d.dv, 1, w.cut[0].segs);
+    if (lattn_together(d)) return lattn_fits(d, d.dv, 3, w.cut[0].segs);
+    return lattn_fits(d, d.dv, 1, w.cut[0].segs) && lattn_fits(d, d.dk, 2, w.cut[1].segs);
 }
 
 size_t lattn_bytes(const LattnDims& d, ss_dtype dtype, bool back)
@@ -158,7 +166,7 @@ ss_status ss_lattn_fwd(const void* q, int64_t q_row_stride, const void* k, int64
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
     if (!lattn_layout(d, dtype, false, &w)) return SS_ERR_INVALID_ARG;
-    if (!lattn_grid_ok(d, w) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, heads * v_dim))
+    if (!lattn_grid_ok(d, w, false) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, heads * v_dim))
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {q, k, v, o};
@@ -209,7 +217,7 @@ ss_status ss_lattn_bwd(const void* q, int64_t q_row_stride, const void* k, int64
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
     if (!lattn_layout(d, dtype, true, &w)) return SS_ERR_INVALID_ARG;
-    if (!lattn_grid_ok(d, w) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, do_row_stride) ||
+    if (!lattn_grid_ok(d, w, true) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, do_row_stride) ||
         lattn_too_wide(heads * k_dim, heads * v_dim, 0, 0))
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
@@ -283,7 +291,8 @@ ss_status ss_lattn_step(float* h, const void* q, int64_t q_row_stride, const voi
     if (q_row_stride < qk_heads * k_dim || k_row_stride < qk_heads * k_dim || v_row_stride < heads * v_dim)
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
-    if (batch * heads > INT32_MAX / 4 || !launch_fits(4 * batch * heads, 256)) return SS_ERR_UNSUPPORTED;
+    if (batch * heads > UINT32_MAX || !launch_fits(ssk::lattn_step_groups(batch, heads, v_dim), ssk::kStepThreads))
+        return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype);
     const void* elems[] = {q, k, v, o};
     for (const void* p : elems)
@@ -335,7 +344,9 @@ ss_status qknorm_check(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
     if (!isfinite(eps) || eps < 0.0f) return SS_ERR_INVALID_ARG;
     if (q_ld < q_heads * width || k_ld < k_heads * width) return SS_ERR_INVALID_ARG;
     if (!known(dtype) || width > ssk::kQknormMaxDim) return SS_ERR_UNSUPPORTED;
-    if (tokens > INT32_MAX / 256 || q_heads > ssk::kQknormMaxHeads || k_heads > ssk::kQknormMaxHeads)
+    // the backward, whose launch does not grow with the tokens, takes what the forward does
+    if (!launch_fits(ssk::qknorm_tiles(tokens, half, false), ssk::kQknormThreads) || q_heads > ssk::kQknormMaxHeads ||
+        k_heads > ssk::kQknormMaxHeads)
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype);
     if (!aligned(q, uintptr_t(es)) || !aligned(k, uintptr_t(es)) || !aligned(w_q, 4) || !aligned(w_k, 4) ||

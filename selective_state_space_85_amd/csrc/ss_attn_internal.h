@@ -51,6 +51,14 @@ struct LattnArgs {
 constexpr int kLattnSlice = 128;
 inline int64_t lattn_slices(int64_t dv) { return (dv + kLattnSlice - 1) / kLattnSlice; }
 
+// Waves of a workgroup, 32 columns of v each.
+inline int lattn_waves(int64_t dv) { return dv <= 64 ? 2 : 4; }
+// Workgroups of a launch of `jobs` walks over `segs` segments: whole eights of them (lattn_kernel).
+inline int64_t lattn_groups(int64_t batch, int64_t heads, int64_t dv, int jobs, int64_t segs)
+{
+    return (lattn_slices(dv) * heads * batch * segs + 7) / 8 * 8 * jobs;
+}
+
 // Jobs of one launch have the same class of widths (lattn_class).
 inline int lattn_class(int dk, int dv) { return (dk <= 64 ? 0 : dk <= 128 ? 1 : 2) + 3 * (dv <= 64 ? 0 : int(lattn_slices(dv))); }
 // Workgroups of a class that a CU holds beside each other.
@@ -69,6 +77,13 @@ hipError_t launch_lattn_join(const LattnArgs& a, hipStream_t stream);
 hipError_t launch_lattn_share(const float* part, void* out, int64_t rows, int64_t heads, int64_t share, int64_t width,
                               int dtype, hipStream_t stream);
 
+// One token: workgroups of kStepThreads for each kStepCols columns of a head's state.
+constexpr int kStepThreads = 256, kStepCols = 128;
+inline int64_t lattn_step_groups(int64_t batch, int64_t heads, int64_t dv)
+{
+    return batch * heads * ((dv + kStepCols - 1) / kStepCols);
+}
+
 struct LattnStepArgs {
     float* h;
     const void* q;
@@ -86,6 +101,27 @@ hipError_t launch_lattn_step(const LattnStepArgs& a, int dtype, hipStream_t stre
 
 constexpr int kQknormMaxDim = 512;
 constexpr int64_t kQknormMaxHeads = int64_t(1) << 24;  // the heads of a tile's tokens are counted in 32 bits
+
+constexpr int kQknormThreads = 256;
+constexpr int kQknormAngles = 1024;   // of a workgroup's tile of tokens
+constexpr int kQknormTile = 16;       // tokens of a tile at most
+
+// Tokens of a tile: as many as its angles allow, fewer where that would leave CUs without work: 2048
+// tiles forward (16384 tokens of 40 + 40 heads of 128: 142 us in 1024 tiles, 134 in 2048), 1024 backward
+// (221 and 216 there, and 3 us more for the sums of 2048 workgroups).
+inline int64_t qknorm_tile(int64_t tokens, int64_t half, bool back)
+{
+    int64_t n = half ? kQknormAngles / half : kQknormTile;
+    n = n < kQknormTile ? n : kQknormTile;
+    const int64_t even = back ? tokens / 1024 : tokens / 2048 + (tokens % 2048 != 0);
+    n = n < even ? n : even;
+    return n > 1 ? n : 1;
+}
+inline int64_t qknorm_tiles(int64_t tokens, int64_t half, bool back)
+{
+    const int64_t tile = qknorm_tile(tokens, half, back);
+    return tokens / tile + (tokens % tile != 0);
+}
 
 struct QknormSide {
     const void* x;   // (tokens, heads, width), rows ld apart

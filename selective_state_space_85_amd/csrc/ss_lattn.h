@@ -1077,8 +1077,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
 template <int DT, int DKP, int NW, Access ACC>
 hipError_t launch_shape(const LattnArgs& a, hipStream_t stream)
 {
-    const int64_t walks = lattn_slices(a.job[0].dv) * a.heads * a.batch;
-    auto grid = [&](int64_t segs) { return static_cast<uint32_t>((walks * segs + 7) / 8 * 8 * a.jobs); };
+    auto grid = [&](int64_t segs) { return static_cast<uint32_t>(lattn_groups(a.batch, a.heads, a.job[0].dv, a.jobs, segs)); };
     const dim3 block(64 * NW);
     if (a.segs > 1) {
         lattn_kernel<DT, DKP, NW, ACC, true><<<grid(a.segs - 1), block, 0, stream>>>(a);
@@ -1107,7 +1106,7 @@ hipError_t launch_typed(const LattnArgs& a, bool vec, hipStream_t stream)
     };
     using std::integral_constant;
     auto by_dv = [&](auto dkp) {
-        return dv <= 64 ? go(dkp, integral_constant<int, 2>()) : go(dkp, integral_constant<int, 4>());
+        return lattn_waves(dv) == 2 ? go(dkp, integral_constant<int, 2>()) : go(dkp, integral_constant<int, 4>());
     };
     return dk <= 64    ? by_dv(integral_constant<int, 64>())
            : dk <= 96  ? by_dv(integral_constant<int, 96>())

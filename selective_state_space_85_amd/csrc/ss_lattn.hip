@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kShareThreads) void share_kernel(const float* part,
 // of whose loads are issued before the first is used (ROWS of them at a time).  Their sums of o are
 // joined in order.  256 sequences of 40 heads of 128 x 128: 1.34 GB in 275 us, 4.9 TB/s, a large copy's rate
 // (490 us with a load and a store in turn); one sequence: 6.5 us, the latency of one round of loads.
-constexpr int kStepThreads = 256, kStepCols = 128, kStepGroups = kStepThreads / (kStepCols / 4);
+constexpr int kStepGroups = kStepThreads / (kStepCols / 4);
 template <int DT, bool VEC, int ROWS>
 __global__ __launch_bounds__(kStepThreads) void lattn_step_kernel(LattnStepArgs a)
 {
@@ -186,7 +186,7 @@ hipError_t launch_lattn_share(const float* part, void* out, int64_t rows, int64_
 template <int DT>
 static hipError_t step_typed(const LattnStepArgs& a, hipStream_t stream)
 {
-    const uint32_t grid = static_cast<uint32_t>(a.batch * a.heads * ((a.dv + kStepCols - 1) / kStepCols));
+    const uint32_t grid = static_cast<uint32_t>(lattn_step_groups(a.batch, a.heads, a.dv));
     const bool vec = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.h) % 16 == 0;
     if (vec) lattn_step_kernel<DT, true, 16><<<grid, kStepThreads, 0, stream>>>(a);
     else lattn_step_kernel<DT, false, 8><<<grid, kStepThreads, 0, stream>>>(a);

@@ -27,10 +27,6 @@ namespace {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kNormThreads = 256;
-constexpr int kTable = 1024;     // angles of a tile
-constexpr int kMaxTokens = 16;   // tokens of a tile
-
 // four neighbouring elements, in fp32
 __device__ __forceinline__ void load4(const float* p, float (&v)[4])
 {
@@ -141,7 +137,7 @@ private:
 __device__ __forceinline__ void fill_table(const QknormArgs& a, float2* table, int64_t t0, int n)
 {
     const int half = int(a.half);
-    for (int i = threadIdx.x; i < n * half; i += kNormThreads) {
+    for (int i = threadIdx.x; i < n * half; i += kQknormThreads) {
         const double turns = double(a.pos[t0 + i / half]) * double(a.inv_freq[i % half]) * 0.15915494309189535;
         float s, c;
         sincospif(2.0f * float(turns - rint(turns)), &s, &c);
@@ -158,10 +154,10 @@ __device__ __forceinline__ float group_sum(float v)
 }
 
 template <int DT, bool VEC, bool INTER, int GL>
-__global__ __launch_bounds__(kNormThreads) void qknorm_fwd_kernel(QknormArgs a, int tile)
+__global__ __launch_bounds__(kQknormThreads) void qknorm_fwd_kernel(QknormArgs a, int tile)
 {
     using T = typename Elem<DT>::T;
-    __shared__ float2 table[kTable];
+    __shared__ float2 table[kQknormAngles];
     const int64_t t0 = int64_t(blockIdx.x) * tile;
     const int n = int(a.tokens - t0 < tile ? a.tokens - t0 : tile);
     const int width = int(a.width), half = int(a.half);
@@ -175,7 +171,7 @@ __global__ __launch_bounds__(kNormThreads) void qknorm_fwd_kernel(QknormArgs a, 
         float wa[4], wb[4];
         sl.load(s.w, wa, wb);
         // every lane of a group has the same row, and with it the same way through the loop
-        for (int row = threadIdx.x / GL; row < n * heads; row += kNormThreads / GL) {
+        for (int row = threadIdx.x / GL; row < n * heads; row += kQknormThreads / GL) {
             const int t = row / heads, h = row % heads;
             float xa[4], xb[4], c[4], sn[4];
             sl.load(static_cast<const T*>(s.x) + (t0 + t) * s.ld + int64_t(h) * width, xa, xb);
@@ -197,11 +193,11 @@ __global__ __launch_bounds__(kNormThreads) void qknorm_fwd_kernel(QknormArgs a, 
 }
 
 template <int DT, bool VEC, bool INTER, int GL>
-__global__ __launch_bounds__(kNormThreads) void qknorm_bwd_kernel(QknormArgs a, int tile)
+__global__ __launch_bounds__(kQknormThreads) void qknorm_bwd_kernel(QknormArgs a, int tile)
 {
     using T = typename Elem<DT>::T;
-    constexpr int kGroups = kNormThreads / GL;
-    __shared__ float2 table[kTable];
+    constexpr int kGroups = kQknormThreads / GL;
+    __shared__ float2 table[kQknormAngles];
     __shared__ float sums[kGroups][8 * GL];
     const int width = int(a.width), half = int(a.half);
     const Slots<DT, VEC, INTER, GL> sl(width, half);
@@ -265,7 +261,7 @@ __global__ __launch_bounds__(kNormThreads) void qknorm_bwd_kernel(QknormArgs a, 
             sl.store(&sums[group][0], da[i], db[i]);
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < width; c += kNormThreads) {
+        for (int c = threadIdx.x; c < width; c += kQknormThreads) {
             float v = 0.0f;
             for (int g = 0; g < kGroups; ++g) v += sums[g][c];
             a.part[(i * int64_t(gridDim.x) + blockIdx.x) * width + c] = v;
@@ -299,27 +295,15 @@ bool runs_of_four(const void* p, int64_t ld, int64_t es)
     return reinterpret_cast<uintptr_t>(p) % uintptr_t(4 * es) == 0 && ld % 4 == 0;
 }
 
-// Tokens of a tile: as many as its table holds, fewer where that would leave CUs without work: 2048
-// tiles forward (16384 tokens of 40 + 40 heads of 128: 142 us in 1024 tiles, 134 in 2048), 1024 backward
-// (221 and 216 there, and 3 us more for the sums of 2048 workgroups).
-int tile_tokens(const QknormArgs& a, bool back)
-{
-    int64_t n = a.half ? kTable / a.half : kMaxTokens;
-    n = n < kMaxTokens ? n : kMaxTokens;
-    const int64_t even = back ? a.tokens / 1024 : (a.tokens + 2047) / 2048;
-    n = n < even ? n : even;
-    return int(n > 1 ? n : 1);
-}
-
 template <int DT, bool VEC, bool INTER>
 hipError_t launch(const QknormArgs& a, bool back, hipStream_t stream)
 {
-    const int tile = tile_tokens(a, back);
-    const uint32_t tiles = uint32_t((a.tokens + tile - 1) / tile);
+    const int tile = int(qknorm_tile(a.tokens, a.half, back));
+    const uint32_t tiles = uint32_t(qknorm_tiles(a.tokens, a.half, false));
     auto go = [&](auto gl) {
         constexpr int GL = decltype(gl)::value;
-        if (back) qknorm_bwd_kernel<DT, VEC, INTER, GL><<<uint32_t(a.blocks), kNormThreads, 0, stream>>>(a, tile);
-        else qknorm_fwd_kernel<DT, VEC, INTER, GL><<<tiles, kNormThreads, 0, stream>>>(a, tile);
+        if (back) qknorm_bwd_kernel<DT, VEC, INTER, GL><<<uint32_t(a.blocks), kQknormThreads, 0, stream>>>(a, tile);
+        else qknorm_fwd_kernel<DT, VEC, INTER, GL><<<tiles, kQknormThreads, 0, stream>>>(a, tile);
         return hipGetLastError();
     };
     using std::integral_constant;
