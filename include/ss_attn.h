@@ -39,8 +39,8 @@ extern "C" {
  *   o         : (batch, seqlen, heads, v_dim) dtype output
  *   h_last    : (batch, heads, k_dim, v_dim) fp32 output, the state after the last row, or NULL;
  *               may be exactly h0
- * scale must be finite.  k_dim and v_dim above 256, row strides (and heads * k_dim, heads * v_dim)
- * above 2^20 elements and seqlen from 2^30 on are SS_ERR_UNSUPPORTED.
+ * scale must be finite.  k_dim and v_dim above 256, heads * k_dim, heads * v_dim and, where seqlen is
+ * above 1, row strides above 2^20 elements, and seqlen from 2^30 on are SS_ERR_UNSUPPORTED.
  * The state is fp32 throughout.  bf16: it and the products q k^T are rounded to bf16 where they
  * enter a product with q or v.  fp32: products are formed from three bf16 parts of each operand,
  * which hold its 24 bits.  An infinity in q, k, v or the state gives infinities or NaN in the rows

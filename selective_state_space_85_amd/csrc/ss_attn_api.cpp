@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "ss_attn.h"
 #include "ss_attn_internal.h"
 #include "ss_host.h"
@@ -91,11 +93,14 @@ bool lattn_layout(const LattnDims& d, ss_dtype dtype, bool back, LattnLayout* w)
     return r.ok;
 }
 
-// Rows' strides that the kernels' 32-bit offsets over a chunk take, in elements.
+// Rows' strides that the kernels' 32-bit offsets over a chunk take, in elements: the inputs', which a
+// sequence of one row has none of, and the outputs' (row, 0 where there is no second one).
 constexpr int64_t kLattnMaxStride = int64_t(1) << 20;
-bool lattn_too_wide(int64_t a, int64_t b, int64_t c, int64_t d)
+bool lattn_too_wide(int64_t seqlen, std::initializer_list<int64_t> in, int64_t row, int64_t other)
 {
-    return a > kLattnMaxStride || b > kLattnMaxStride || c > kLattnMaxStride || d > kLattnMaxStride;
+    for (const int64_t ld : in)
+        if (seqlen > 1 && ld > kLattnMaxStride) return true;
+    return row > kLattnMaxStride || other > kLattnMaxStride;
 }
 
 // Whether a launch of `jobs` walks of width dv fits a grid.
@@ -166,7 +171,7 @@ ss_status ss_lattn_fwd(const void* q, int64_t q_row_stride, const void* k, int64
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
     if (!lattn_layout(d, dtype, false, &w)) return SS_ERR_INVALID_ARG;
-    if (!lattn_grid_ok(d, w, false) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, heads * v_dim))
+    if (!lattn_grid_ok(d, w, false) || lattn_too_wide(seqlen, {q_row_stride, k_row_stride, v_row_stride}, heads * v_dim, 0))
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {q, k, v, o};
@@ -217,8 +222,8 @@ ss_status ss_lattn_bwd(const void* q, int64_t q_row_stride, const void* k, int64
         return SS_ERR_INVALID_ARG;
     if (!known(dtype) || !lattn_widths(d)) return SS_ERR_UNSUPPORTED;
     if (!lattn_layout(d, dtype, true, &w)) return SS_ERR_INVALID_ARG;
-    if (!lattn_grid_ok(d, w, true) || lattn_too_wide(q_row_stride, k_row_stride, v_row_stride, do_row_stride) ||
-        lattn_too_wide(heads * k_dim, heads * v_dim, 0, 0))
+    if (!lattn_grid_ok(d, w, true) ||
+        lattn_too_wide(seqlen, {q_row_stride, k_row_stride, v_row_stride, do_row_stride}, heads * k_dim, heads * v_dim))
         return SS_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = batch * seqlen;
     const void* elems[] = {q, k, v, d_o, dq, dk, dv};

@@ -569,7 +569,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(LattnSh
     const char* const pq = static_cast<const char*>(j.q) + (b * L * j.q_ld + (h / j.q_share) * j.dk) * kEs;
     const char* const pk = static_cast<const char*>(j.k) + (b * L * j.k_ld + (h / j.k_share) * j.dk) * kEs;
     const char* const pv = static_cast<const char*>(j.v) + (b * L * j.v_ld + (h / j.v_share) * j.dv) * kEs;
-    const uint32_t lq = uint32_t(j.q_ld) * kEs, lk = uint32_t(j.k_ld) * kEs, lv = uint32_t(j.v_ld) * kEs;
+    // the stride of a single row lies between sequences alone, and may be any
+    const bool single = L == 1;
+    const uint32_t lq = uint32_t(single ? j.dk : j.q_ld) * kEs, lk = uint32_t(single ? j.dk : j.k_ld) * kEs;
+    const uint32_t lv = uint32_t(single ? j.dv : j.v_ld) * kEs;
     const uint32_t oes = j.out_f32 ? 4 : kEs, lo = uint32_t(H * j.dv) * oes;
     char* const po = static_cast<char*>(j.out) + (b * L * H * j.dv + h * j.dv + v0) * oes;
     const int vw = j.dv - v0;  // columns from here on

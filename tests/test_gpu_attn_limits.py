@@ -6,7 +6,7 @@ from gpu_util import say
 
 pytestmark = pytest.mark.gpu
 
-F32 = torch.float32
+F32, BF16 = torch.float32, torch.bfloat16
 
 
 @pytest.fixture(scope="module")
@@ -100,3 +100,31 @@ def test_norms_of_many_tokens(ss):
         e = float((g["dw_" + name].double() - dw).norm()) / scale
         say("   dw_%s %.2e" % (name, e))
         assert e <= tol + 2.0 ** -24 * (256 + 32 + 16 + 64) ** 0.5, name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (72, 91), (3, 40), (256, 5)])
+def test_one_row_of_long_sequences(ss, dtype, dk, dv):
+    """One row each of sequences that lie more than 2^20 elements apart, read in place."""
+    say("lattn one row", dtype, dk, dv)
+    b, l, hk, h, wide = 3, 40, 2, 4, 32768
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    rows = torch.full((b, l, wide), float("nan"), dtype=dtype, device="cuda")
+    rows[:, 17:18] = normal(gen, b, 1, wide).to(dtype)
+    row, at, views = rows[:, 17:18], 0, []
+    for heads, width in ((hk, dk), (hk, dk), (h, dv), (h, dv)):
+        views.append(row[..., at:at + heads * width].unflatten(-1, (heads, width)))
+        at += (heads * width + 7) // 8 * 8  # the same alignment as by themselves
+    decay = -torch.rand((h,), generator=gen, device="cuda")
+    h0, dh = normal(gen, b, h, dk, dv), normal(gen, b, h, dk, dv)
+
+    def both(q, k, v, do):
+        o, last = ss.lattn_fwd(q, k, v, decay, h0=h0, return_last_state=True)
+        return {"o": o, "h_last": last, **ss.lattn_bwd(q, k, v, decay, do, h0=h0, dh_last=dh, want_dh0=True)}
+
+    assert row.stride(0) > 1 << 20
+    got, want = both(*views), both(*(t.contiguous() for t in views))
+    # the same numbers, however the rows are read
+    for n in want:
+        assert torch.isfinite(want[n]).all() and torch.equal(got[n], want[n]), n
