@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kStepThreads) void lattn_step_kernel(LattnStepArgs 
 {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     using T = typename Elem<DT>::T;
-    __shared__ float part[kStepGroups][kStepCols + 4];
+    __shared__ __align__(16) float part[kStepGroups][kStepCols + 4];
     __shared__ float sk[kLattnMaxDim], sq[kLattnMaxDim];
     const uint32_t tiles = uint32_t((a.dv + kStepCols - 1) / kStepCols);
     const int dk = int(a.dk), dv = int(a.dv);

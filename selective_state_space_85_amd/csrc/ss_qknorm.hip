@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kQknormThreads) void qknorm_bwd_kernel(QknormArgs a
     using T = typename Elem<DT>::T;
     constexpr int kGroups = kQknormThreads / GL;
     __shared__ float2 table[kQknormAngles];
-    __shared__ float sums[kGroups][8 * GL];
+    __shared__ __align__(16) float sums[kGroups][8 * GL];
     const int width = int(a.width), half = int(a.half);
     const Slots<DT, VEC, INTER, GL> sl(width, half);
     const int group = threadIdx.x / GL;
@@ -253,13 +253,7 @@ __global__ __launch_bounds__(kQknormThreads) void qknorm_bwd_kernel(QknormArgs a
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         __syncthreads();
-        if (VEC) {
-            if (sl.live()) {
-                sl.store(&sums[group][0], da[i], db[i]);
-            }
-        } else {
-            sl.store(&sums[group][0], da[i], db[i]);
-        }
+        sl.store(&sums[group][0], da[i], db[i]);
         __syncthreads();
         for (int c = threadIdx.x; c < width; c += kQknormThreads) {
             float v = 0.0f;
