@@ -249,38 +249,39 @@ __global__ __launch_bounds__(kQknormThreads) void qknorm_bwd_kernel(QknormArgs a
             }
         }
     }
-    // the groups' sums of dw, joined in order
+    // The groups' sums of dw, joined in order.  These joins and the next kernel's are in 64 bits, beside which
+    // the rest of either does not notice them: in 32 each addition would round all that is summed so far.
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         __syncthreads();
         sl.store(&sums[group][0], da[i], db[i]);
         __syncthreads();
         for (int c = threadIdx.x; c < width; c += kQknormThreads) {
-            float v = 0.0f;
-            for (int g = 0; g < kGroups; ++g) v += sums[g][c];
-            a.part[(i * int64_t(gridDim.x) + blockIdx.x) * width + c] = v;
+            double v = 0.0;
+            for (int g = 0; g < kGroups; ++g) v += double(sums[g][c]);
+            a.part[(i * int64_t(gridDim.x) + blockIdx.x) * width + c] = float(v);
         }
     }
 }
 
-// dw[c] = sum of the workgroups' sums: 64 columns x 16 runs of workgroups, the runs joined in order.
+// dw[c] = sum of the workgroups' sums: 16 columns x 64 runs of workgroups, the runs joined in order.
 constexpr int kSumCols = 16, kSumRuns = 64;
 __global__ __launch_bounds__(kSumCols * kSumRuns) void qknorm_sum_kernel(QknormArgs a)
 {
-    __shared__ float run[kSumRuns][kSumCols];
+    __shared__ double run[kSumRuns][kSumCols];
     const int c = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
     const int64_t col = int64_t(blockIdx.x) * kSumCols + c;
     const float* const p = a.part + int64_t(blockIdx.y) * a.blocks * a.width;
-    float v = 0.0f;
+    double v = 0.0;
     if (col < a.width)
 #pragma unroll 8
-        for (int64_t i = g; i < a.blocks; i += kSumRuns) v += p[i * a.width + col];
+        for (int64_t i = g; i < a.blocks; i += kSumRuns) v += double(p[i * a.width + col]);
     run[g][c] = v;
     __syncthreads();
     if (g == 0 && col < a.width) {
-        float s = 0.0f;
+        double s = 0.0;
         for (int i = 0; i < kSumRuns; ++i) s += run[i][c];
-        a.side[blockIdx.y].dw[col] = s;
+        a.side[blockIdx.y].dw[col] = float(s);
     }
 }
 
