@@ -47,6 +47,11 @@ def _shared(qk_heads: int, heads: int) -> None:
         raise ValueError("v's %d heads are not a multiple of q's %d" % (heads, qk_heads))
 
 
+def _scale(scale: Optional[float], k_dim: int) -> float:
+    """The one given, or k_dim ** -0.5 (heads without a width have none; the library refuses them)."""
+    return scale if scale is not None else k_dim ** -0.5 if k_dim else 1.0
+
+
 def _like(t: torch.Tensor) -> torch.Tensor:
     """A contiguous result of t's shape and type."""
     return torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -87,7 +92,7 @@ def _attention(q, k, v, log_decay, scale, h0, reset, fn):
     if h0 is not None:
         _need(h0, "h0", (nb, nh, dk, dv), torch.float32, dev)
     _flags(reset, (nb, nl), dev)
-    return dev, dt, (nb, nl, hk, nh, dk, dv), lds, dk ** -0.5 if scale is None else scale
+    return dev, dt, (nb, nl, hk, nh, dk, dv), lds, _scale(scale, dk)
 
 
 def lattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
@@ -170,7 +175,7 @@ def lattn_step(h: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
         _need(out, "out", (nb, nh, dv), dtype, dev)
     with _on(dev) as stream:
         st = _attn.load().ss_lattn_step(_p(h), _p(q), lq, _p(k), lk, _p(v), lv, _p(log_decay),
-                                        dk ** -0.5 if scale is None else scale, _p(out), nb, hk, nh, dk, dv, dt, stream)
+                                        _scale(scale, dk), _p(out), nb, hk, nh, dk, dv, dt, stream)
     _call("ss_lattn_step", st)
     return out
 
