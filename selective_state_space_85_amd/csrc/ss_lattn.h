@@ -385,7 +385,7 @@ __device__ __forceinline__ Rsrc buffer_of(const void* p, uint32_t bytes)
 
 // How rows are read.  kWhole: the host has checked that they are whole 16-byte chunks at such addresses.
 // kAny: at any address, of 16 bytes and more.  kSingle: element by element (8 x 2048 x 32 heads of 125
-// in bf16: 707 us, 297 by kAny; of 128 by kWhole 143; 3 x 1021 x 12 heads of 72 and 91 in fp32 with their
+// in bf16: 707 us, 222 by kAny; of 128 by kWhole 134; 3 x 1021 x 12 heads of 72 and 91 in fp32 with their
 // gradients: 186 and 163).
 enum Access { kSingle, kWhole, kAny };
 
@@ -432,23 +432,26 @@ __device__ __forceinline__ u32x4 elements(const Piece& p, uint32_t at, int over)
         for (int i = 0; i < 4; ++i) w[i] = over & 2 ? (i < 2 ? w[i + 2] : 0u) : w[i];
         return w;
     }
+    // By masks, each move into words of its own: of `over & 2 ? w[i + 1] : w[i]` the compiler makes an index
+    // into w, which then lies in memory.
     const uint32_t half = at << 3 & 16u, odd = uint32_t(over) << 4 & 16u;
+    const uint32_t two = over & 2 ? 0xffffffffu : 0u, four = over & 4 ? 0xffffffffu : 0u;
     const uint32_t raw[5] = {p.v[0], p.v[1], p.v[2], p.v[3], p.x & 0xffffu};
-    uint32_t w[5];
+    uint32_t x[5], y[5], z[6];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbit(raw[i + 1], raw[i], half);
-    w[4] = 0;
+    for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_alignbit(raw[i + 1], raw[i], half);
+    x[4] = y[4] = z[4] = z[5] = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], odd);
+    for (int i = 0; i < 4; ++i) y[i] = __builtin_amdgcn_alignbit(x[i + 1], x[i], odd);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = over & 2 ? w[i + 1] : w[i];
+    for (int i = 0; i < 4; ++i) z[i] = (y[i + 1] & two) | (y[i] & ~two);
+    u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = over & 4 ? (i < 2 ? w[i + 2] : 0u) : w[i];
-    return u32x4{w[0], w[1], w[2], w[3]};
+    for (int i = 0; i < 4; ++i) w[i] = (z[i + 2] & four) | (z[i] & ~four);
+    return w;
 }
 
-// The same as a store.  kAny: element by element too.  Words and their halves at the ends, out of pieces
-// moved as they are for loads, cost more than they save: 8 x 2048 x 32 heads of 125 297 -> 390 us.
+// The same as a store.  kAny: element by element too.
 template <int DT, Access ACC>
 __device__ __forceinline__ void store_piece(Rsrc r, uint32_t at, int left, const u32x4& v)
 {
@@ -501,8 +504,8 @@ struct LattnShape {
     static constexpr int kLoad = DKP <= 64 ? 64 : DKP <= 128 ? 128 : 256;
     static constexpr int kQPieces = kC * kLoad / Ops<DT>::kEpc / kThreads;
     static constexpr int kVPieces = kC * 32 * NW / Ops<DT>::kEpc / kThreads;
-    // waves on a SIMD: two, but where their registers do not allow it (8 x 2048 x 32 heads of 201 in bf16:
-    // 1053 us with two and 34 registers in memory, 811 with one; of 177, which fit two: 821 with one, 668)
+    // waves on a SIMD: two, but where their registers do not allow it (8 x 2048 x 32 heads of 201 in bf16: 833 us
+    // with two and 28 registers in memory, 667 with one; of 177, which fit two: 587 with one, 405)
     static constexpr int kWaves = (DKP > 128 && (DT == 0 || NW == 2 || (ACC != kWhole && DKP == 256))) || (DKP > 64 && DT == 0 && NW == 2) ? 1 : 2;
 };
 
