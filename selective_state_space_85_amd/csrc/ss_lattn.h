@@ -506,7 +506,7 @@ struct LattnShape {
     static constexpr int kVPieces = kC * 32 * NW / Ops<DT>::kEpc / kThreads;
     // waves on a SIMD: two, but where their registers do not allow it (8 x 2048 x 32 heads of 201 in bf16: 833 us
     // with two and 28 registers in memory, 667 with one; of 177, which fit two: 587 with one, 405)
-    static constexpr int kWaves = (DKP > 128 && (DT == 0 || NW == 2 || (ACC != kWhole && DKP == 256))) || (DKP > 64 && DT == 0 && NW == 2) ? 1 : 2;
+    static constexpr int kWaves = (DKP > 128 && (DT == 0 || NW == 2 || (ACC == kAny && DKP == 256))) || (DKP > 64 && DT == 0 && NW == 2) ? 1 : 2;
 };
 
 // grid (units rounded up to 8, times jobs); units are slices * heads * batch * segments, slices fastest.
@@ -1108,7 +1108,9 @@ hipError_t launch_typed(const LattnArgs& a, bool vec, hipStream_t stream)
         constexpr int kD = decltype(dkp)::value, kW = decltype(nw)::value;
         if (vec) return launch_shape<DT, kD, kW, kWhole>(a, stream);
         if (any) return launch_shape<DT, kD, kW, kAny>(a, stream);
-        return launch_shape<DT, kD, kW, kSingle>(a, stream);
+        // rows of less than 16 bytes: beside v of more than 64 columns only those of q and k, so of up to 64
+        if constexpr (kW == 2 || kD == 64) return launch_shape<DT, kD, kW, kSingle>(a, stream);
+        return hipErrorInvalidValue;
     };
     using std::integral_constant;
     auto by_dv = [&](auto dkp) {
