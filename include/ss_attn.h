@@ -108,7 +108,9 @@ ss_status ss_lattn_step(float* h, const void* q, int64_t q_row_stride, const voi
  *   qo, ko   : (tokens, q_heads, width), (tokens, k_heads, width) dtype outputs
  * width is at most 512, q_heads and k_heads at most 2^24 (SS_ERR_UNSUPPORTED above); width is at least
  * 2 half_rotary; eps is finite and not negative.  The mean of the squares is fp32: a head whose squares
- * sum past its range is normed to 0.
+ * sum past its range is normed to 0, with gradient 0; squares below its range (of elements below 2^-63)
+ * lose bits or count as 0, so that a head of such elements is normed by eps, and with eps 0 to infinities
+ * or NaN, as a head of zeros then is to NaN.
  */
 ss_status ss_qknorm_fwd(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const float* w_q,
                         const float* w_k, const int64_t* pos, const float* inv_freq, float eps, int interleaved,
