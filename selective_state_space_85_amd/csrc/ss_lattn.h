@@ -14,7 +14,10 @@
 //   S   = a^C S + K^T (w V)
 // A block of the state in accumulators (rows dk, columns v) is the operand S^T as it stands, up to
 // a swap between the halves of a wave.  In bf16, S and P are rounded where they become operands: of the
-// output that leaves a relative error of 0.0023 with the rounding of the output itself, 0.0017 alone;
+// output that leaves a relative error of 0.0023 with the rounding of the output itself, 0.0017 alone.  As two
+// bf16 parts each they leave that alone, in mostly 13-43% more time: 8 x 2048 x 40 heads of 128 forward 237 -> 288 us
+// and backward 481 -> 580, 131072 x 16 heads 758 -> 860, 8 x 2048 x 32 heads of 64 forward 95 -> 123 (S alone in
+// two parts 259, 530, 811 and 97, P alone 259, 527, 803 and 119).  What is rounded there is gone with its row;
 // w V goes in as three bf16 parts, since what is rounded on its way into the state would stay there.
 //
 // Resets cut the sequence: row t sees the rows from the last reset up to t, and the state only if
@@ -22,12 +25,12 @@
 //
 // What bounds it: with heads of 128 and 64 rows in bf16 a wave has 82 matrix instructions of 32 cycles
 // to a chunk, some 560 vector instructions beside them, and some 80 KB of LDS traffic
-// to the wave.  Two workgroups on a CU take 6.8 us for a chunk each at the 1.6-1.8 GHz that the card then runs at,
-// of which the matrix cores are busy 40-45%.  bf16, heads of 128:
-//   131072 x 16 heads, forward: states between segments 247-289 us (1.07 GB read, 3.7-4.3 TB/s), joined 15,
-//     main pass 465-535 (2.15 GB, 4.0-4.6 TB/s)
-//   8 x 2048 x 40 heads: forward 205-217 us, 320 walks on 256 CUs (256 of them, of 32 heads: 143); gradients,
-//     960 walks in one launch, 409-443 us
+// to the wave.  Two workgroups on a CU take 7-9 us for a chunk each at the 1.75-2.05 GHz that the card then runs at,
+// of which the matrix cores are busy 36-38% and vector instructions are issued in 40%.  bf16, heads of 128:
+//   131072 x 16 heads, forward: states between segments 242-333 us (1.07 GB read, 3.2-4.4 TB/s), joined 15,
+//     main pass 457-612 (2.15 GB, 3.5-4.7 TB/s)
+//   8 x 2048 x 40 heads: forward 206-234 us, 320 walks on 256 CUs (256 of them, of 32 heads: 130-156); gradients,
+//     960 walks in one launch, 409-471 us; queries and keys shared by four heads: 726-802, and 2 x 86 for the sums
 // fp32, 3 x 1021 x 12 heads of 72 and 91: 16 + 7 + 33 us forward, 29 + 10 + 74 + 10 for the gradients.
 // Tried and not kept in bf16: chunks of 32 rows with three workgroups on a CU (28 registers in memory: 8 x
 // 2048 x 32 heads 141 -> 285 us) or with two (141 -> 153), rows padded by 32 bytes more in LDS, loads before

@@ -19,7 +19,7 @@
 // us, of which 3 for the largest logit, 15 for the weights' bins (some 40 instructions and an LDS addition for
 // each of 49 tokens a thread), 5-7 for the list, 2-3 for a place.  64 rows of 131072, top-k of 50 and nucleus,
 // a row to a CU: 30 us (35 with counts of the whole row, and 23 of them for those).  256 rows of 50257 in fp32
-// with settings of their own: 56 us, a workgroup to a CU (104 registers a thread).
+// with settings of their own: 56 us, a workgroup to a CU (85 KB of LDS, 94 registers a thread).
 #include <hip/hip_runtime.h>
 
 #include "ss_attn_internal.h"
